@@ -441,6 +441,101 @@ fg_status fp8_cast_per_token_ue8m0_bf16(const uint16_t* x, int64_t ldx, uint8_t*
 fg_status fp8_cast_per_block_ue8m0_bf16(const uint16_t* w, int64_t ldw, uint8_t* q, int32_t* sb,
                                         int N, int K, void* stream);
 
+/*
+ * 8-bit-integer products and the gated feed-forward block.  Operands are
+ * signed bytes with an fp32 scale per row (a token of the activations, an
+ * output channel of the weights), or BF16.  All matrices are row-major with
+ * their last dimension contiguous.
+ *
+ * Workspace of the calls that take one, where not stated otherwise: as
+ * gemm_fp8_nt_ws's (256-byte aligned, its first 64 KiB zero before first use
+ * and left zero by every call, not shared by calls that overlap in time), and
+ * of fg_nt_workspace_max_bytes() bytes, or NULL and 0.  It lets calls whose
+ * output tiles cannot occupy the device split K over workgroups; partials are
+ * added in a fixed order, so results are reproducible.  One workspace may
+ * serve these calls and gemm_fp8_nt_ws on one stream.
+ */
+
+/*
+ * Cast of each row to signed bytes, for either operand of gemm_int8_nt:
+ *     s[m] = max(max_k |x[m, k]|, 1e-4f) / 127     (fp32, correctly rounded)
+ *     q    = rint(x / s[m])                        (fp32 division, nearest-even; |q| <= 127)
+ *   x   device fp32 (or bf16) [M, K], row stride ldx elements (ldx >= K, 16-byte aligned rows)
+ *   q   device [M, K], packed, 16-byte aligned
+ *   s   device fp32 [M]
+ * K % 16 == 0.  Input values must be finite.  K == 0 writes nothing.
+ */
+fg_status int8_cast_per_row(const float* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream);
+fg_status int8_cast_per_row_bf16(const uint16_t* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream);
+
+/*
+ * D[m,n] = bf16( sa[m] * sb[n] * sum_k A[m,k] * B[n,k] ), the sum exact in int32.
+ *   A   device [M, K] int8, row stride lda bytes (lda >= K, lda % 16 == 0, A 16-byte aligned)
+ *   sa  device fp32 [M]
+ *   B   device [N, K] int8, row stride ldb bytes (ldb >= K, ldb % 16 == 0, B 16-byte aligned)
+ *   sb  device fp32 [N]
+ *   D   device [M, N] bf16, row stride ldd elements (ldd >= N); only D[0:M, 0:N] is written
+ * M, N >= 0 arbitrary, K % 16 == 0, K <= 131056 (the sum of more products may
+ * leave int32; FG_EUNSUPPORTED).  K == 0 writes D = sa * sb * 0.  Rows of
+ * at most 4 MiB.  The product is scaled as (sum * sa[m]) * sb[n] in fp32 and
+ * rounded once.  Allocates nothing.
+ */
+fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
+                       uint16_t* D, int64_t ldd, int M, int N, int K, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
+/* Activations of the gated block: act(x) = x / (1 + exp(-y)), y = x (SiLU) or
+ * y = 2 sqrt(2/pi) (x + 0.044715 x^3) (the tanh form of GELU). */
+typedef enum { FG_ACT_SILU = 0, FG_ACT_GELU_TANH = 1 } fg_activation;
+
+/*
+ * Gated feed-forward block: both projections, the activation and the product
+ * in one kernel,
+ *     g = X . W[0:F]^T,  u = X . W[F:2F]^T,  H = bf16( act(g) * u ).
+ *   X   device [M, K] bf16, row stride ldx elements (ldx >= K, ldx % 8 == 0, X 16-byte aligned)
+ *   W   device [2F, K] bf16, gate rows then up rows, row stride ldw elements (as ldx)
+ *   H   device [M, F] bf16, row stride ldh elements (ldh >= F); written
+ *   P   NULL, or device fp32 [M, 2F] (row stride ldp >= 2F): receives [g u] for the backward pass
+ * M, F >= 0 arbitrary, K % 8 == 0 (K == 0: g = u = 0), rows of at most 4 MiB.
+ * g and u are accumulated in fp32 and not rounded before the activation.
+ */
+fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, uint16_t* H, int64_t ldh,
+                         float* P, int64_t ldp, int M, int F, int K, int activation, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, given dH:
+ *     dg = dH * u * act'(g),  du = dH * act(g),
+ *     dX = bf16( [dg du] . W ),  dW = bf16( [dg du]^T . X ).
+ *   dH  device [M, F] bf16, row stride lddh
+ *   X, W as in the forward call
+ *   P   the forward call's pre-activations [g u], or NULL: they are recomputed from X and W
+ *   dX  device [M, K] bf16, row stride lddx, or NULL (not wanted)
+ *   dW  device [2F, K] bf16, row stride lddw, or NULL (not wanted)
+ *   workspace  device, 256-byte aligned, fg_gated_ffn_backward_workspace_bytes(M, F) bytes; holds
+ *       [dg du] in bf16 and needs no initialisation; in use until the call's work has finished
+ * dX and dW accumulate in fp32 over the bf16 pair [dg du].  M == 0 writes
+ * dW = 0, F == 0 writes dX = 0.  F <= 2^20.  Outputs may not overlap inputs.
+ */
+fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16_t* X, int64_t ldx,
+                                  const uint16_t* W, int64_t ldw, const float* P, int64_t ldp, uint16_t* dX,
+                                  int64_t lddx, uint16_t* dW, int64_t lddw, int M, int F, int K, int activation,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gated_ffn_bf16_backward; -1 for sizes it rejects. */
+int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F);
+
+/*
+ * The gated block on 8-bit integers (serving):
+ *     g = sx * sw[0:F] * (X . W[0:F]^T),  u likewise with rows F..2F-1,  H = bf16( act(g) * u ).
+ *   X, sx, W, sw  as A, sa, B, sb of gemm_int8_nt, W and sw of 2F rows
+ *   H             device [M, F] bf16, row stride ldh (ldh >= F); written
+ * M, F >= 0 arbitrary; K as in gemm_int8_nt.
+ */
+fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const int8_t* W, int64_t ldw,
+                         const float* sw, uint16_t* H, int64_t ldh, int M, int F, int K, int activation,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Row alignment of each expert segment in the contiguous layout: 128. */
 int fg_get_mk_alignment_for_contiguous_layout(void);
 

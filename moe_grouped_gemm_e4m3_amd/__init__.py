@@ -16,6 +16,7 @@ Layouts (Kb = ceil(K/128), Nb = ceil(N/128)):
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -48,6 +49,12 @@ __all__ = [
     "fp8_cast_per_token_ue8m0",
     "fp8_cast_per_block_ue8m0",
     "empty_activation_scales_ue8m0",
+    "int8_cast_per_row",
+    "gemm_int8_nt",
+    "gated_ffn_bf16",
+    "gated_ffn_bf16_backward",
+    "gated_ffn_backward_workspace_bytes",
+    "gated_ffn_int8",
     "get_mk_alignment_for_contiguous_layout",
     "set_num_cus",
     "get_num_cus",
@@ -89,6 +96,14 @@ _SIGNATURES = {
     "fp8_cast_per_block_bf16": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
     "fp8_cast_per_token_ue8m0_bf16": (_I, [_P, _I64, _P, _P, _I64, _I, _I, _P]),
     "fp8_cast_per_block_ue8m0_bf16": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
+    "int8_cast_per_row": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
+    "int8_cast_per_row_bf16": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
+    "gemm_int8_nt": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _P, _I64, _P]),
+    "gated_ffn_bf16": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
+    "gated_ffn_bf16_backward": (
+        _I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
+    "fg_gated_ffn_backward_workspace_bytes": (_I64, [_I, _I]),
+    "gated_ffn_int8": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
     "fg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "fg_set_num_cus": (None, [_I]),
     "fg_get_num_cus": (_I, []),
@@ -621,6 +636,180 @@ def fp8_cast_per_block_ue8m0(w, q=None, sb=None, stream=None):
         raise ValueError("q and sb must be contiguous")
     _call("fp8_cast_per_block_ue8m0" + sfx, _ptr(w), _ld(w), _ptr(q), _ptr(sb), N, K, _stream(stream))
     return q, sb
+
+
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int) -> int:
+    """Row stride of a [rows, cols] CUDA matrix of `dtype` with contiguous rows."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+    return t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _row_scales(t: torch.Tensor, name: str, rows: int) -> int:
+    if t.dtype != torch.float32 or not t.is_cuda:
+        raise TypeError(f"{name} must be a float32 CUDA tensor")
+    if t.shape != (rows,) or (rows > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous [{rows}] vector, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _activation(name: str) -> int:
+    act = ACTIVATIONS.get(name)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
+    return act
+
+
+def _one_device(*ts):
+    """All tensors of a call (None skipped) lie on the current device, where its kernels run."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, the current device is {dev}")
+
+
+def _on_stream(stream):
+    """Context in which torch allocates and fills on the stream a call runs on,
+    so that memory it makes for the call is ordered with the call's kernels."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _split_workspace(workspace, device, stream):
+    """(pointer, bytes) of a call's split-K workspace: the given one or the stream's."""
+    if workspace is None:
+        workspace = _NT_WS.get((device.index, _stream(stream)))
+        if workspace is None:
+            with _on_stream(stream):
+                workspace = nt_workspace(device, stream)
+    return _byte_workspace(workspace)
+
+
+def _byte_workspace(workspace: torch.Tensor):
+    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
+    n = workspace.numel()
+    return (workspace.data_ptr() if n else None), n
+
+
+def int8_cast_per_row(x, q=None, s=None, stream=None):
+    """Signed 8-bit codes and one scale for each row of fp32 or bf16 x [M, K]:
+    s[m] = max(max |x[m]|, 1e-4) / 127, q = rint(x / s).  A row is a token of
+    activations or an output channel of weights.  -> (q int8 [M, K], s fp32 [M])."""
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    bf16 = x.dtype == torch.bfloat16
+    ldx = _matrix(x, "x", torch.bfloat16 if bf16 else torch.float32, M, K)
+    if q is None or s is None:
+        with _on_stream(stream):
+            q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else q
+            s = torch.empty(M, dtype=torch.float32, device=x.device) if s is None else s
+    if _matrix(q, "q", torch.int8, M, K) != K and M > 1:
+        raise ValueError("q must be contiguous")
+    _one_device(x, q, s)
+    _call("int8_cast_per_row_bf16" if bf16 else "int8_cast_per_row", x.data_ptr(), ldx, q.data_ptr(),
+          _row_scales(s, "s", M), M, K, _stream(stream))
+    return q, s
+
+
+def gemm_int8_nt(A, sa, B, sb, D, stream=None, workspace=None):
+    """D[M,N] = bf16(sa[m] sb[n] (A . B^T)) for int8 A [M, K], B [N, K] and
+    fp32 scales for each row of A and of B; the integer sum is exact.  Few
+    rows may split K over workgroups in `workspace` (default: the stream's
+    cached one, see nt_workspace; an empty one: no split)."""
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A and B must be matrices")
+    M, K = A.shape
+    N = B.shape[0]
+    lda, ldb = _matrix(A, "A", torch.int8, M, K), _matrix(B, "B", torch.int8, N, K)
+    ldd = _matrix(D, "D", torch.bfloat16, M, N)
+    _one_device(D, A, sa, B, sb, workspace)
+    ws, ws_bytes = _split_workspace(workspace, D.device, stream)
+    _call("gemm_int8_nt", A.data_ptr(), lda, _row_scales(sa, "sa", M), B.data_ptr(), ldb, _row_scales(sb, "sb", N),
+          D.data_ptr(), ldd, M, N, K, ws, ws_bytes, _stream(stream))
+    return D
+
+
+def gated_ffn_int8(X, sx, W, sw, H, activation="silu", stream=None, workspace=None):
+    """H[M,F] = bf16(act(g) u) from int8 X [M, K] and W [2F, K] (gate rows,
+    then up rows) with fp32 row scales: g = sx sw (X . W[:F]^T), u likewise.
+    activation: "silu" or "gelu_tanh".  Workspace as for gemm_int8_nt."""
+    if X.dim() != 2 or H.dim() != 2:
+        raise ValueError("X and H must be matrices")
+    M, K = X.shape
+    F = H.shape[1]
+    ldx, ldw = _matrix(X, "X", torch.int8, M, K), _matrix(W, "W", torch.int8, 2 * F, K)
+    ldh = _matrix(H, "H", torch.bfloat16, M, F)
+    _one_device(H, X, sx, W, sw, workspace)
+    ws, ws_bytes = _split_workspace(workspace, H.device, stream)
+    _call("gated_ffn_int8", X.data_ptr(), ldx, _row_scales(sx, "sx", M), W.data_ptr(), ldw,
+          _row_scales(sw, "sw", 2 * F), H.data_ptr(), ldh, M, F, K, _activation(activation), ws, ws_bytes,
+          _stream(stream))
+    return H
+
+
+def gated_ffn_bf16(X, W, H, P=None, activation="silu", stream=None, workspace=None):
+    """H[M,F] = bf16(act(X . W[:F]^T) * (X . W[F:]^T)) for bf16 X [M, K] and
+    W [2F, K] (gate rows, then up rows), in one kernel.  P: fp32 [M, 2F],
+    receives the pre-activations for gated_ffn_bf16_backward.  activation:
+    "silu" or "gelu_tanh".  Workspace as for gemm_int8_nt."""
+    if X.dim() != 2 or H.dim() != 2:
+        raise ValueError("X and H must be matrices")
+    M, K = X.shape
+    F = H.shape[1]
+    bf16 = torch.bfloat16
+    ldx, ldw, ldh = _matrix(X, "X", bf16, M, K), _matrix(W, "W", bf16, 2 * F, K), _matrix(H, "H", bf16, M, F)
+    ldp = 0 if P is None else _matrix(P, "P", torch.float32, M, 2 * F)
+    _one_device(H, X, W, P, workspace)
+    ws, ws_bytes = _split_workspace(workspace, H.device, stream)
+    _call("gated_ffn_bf16", X.data_ptr(), ldx, W.data_ptr(), ldw, H.data_ptr(), ldh, _ptr(P), ldp, M, F, K,
+          _activation(activation), ws, ws_bytes, _stream(stream))
+    return H
+
+
+def gated_ffn_backward_workspace_bytes(M: int, F: int) -> int:
+    """Device workspace bytes gated_ffn_bf16_backward needs."""
+    n = load_library().fg_gated_ffn_backward_workspace_bytes(M, F)
+    if n < 0:
+        raise ValueError(f"sizes {(M, F)} not accepted")
+    return n
+
+
+def gated_ffn_bf16_backward(dH, X, W, dX, dW, P=None, activation="silu", stream=None, workspace=None):
+    """Gradients of gated_ffn_bf16: dX [M, K] and dW [2F, K] (bf16, either may
+    be None) from dH [M, F], X and W.  P: the forward pass's pre-activations;
+    without them they are recomputed from X and W.  The workspace
+    (gated_ffn_backward_workspace_bytes) comes from torch's allocator if not
+    given.  -> (dX, dW)."""
+    if X.dim() != 2 or dH.dim() != 2:
+        raise ValueError("X and dH must be matrices")
+    M, K = X.shape
+    F = dH.shape[1]
+    bf16 = torch.bfloat16
+    lddh, ldx, ldw = _matrix(dH, "dH", bf16, M, F), _matrix(X, "X", bf16, M, K), _matrix(W, "W", bf16, 2 * F, K)
+    ldp = 0 if P is None else _matrix(P, "P", torch.float32, M, 2 * F)
+    lddx = 0 if dX is None else _matrix(dX, "dX", bf16, M, K)
+    lddw = 0 if dW is None else _matrix(dW, "dW", bf16, 2 * F, K)
+    _one_device(dH, X, W, P, dX, dW, workspace)
+    act = _activation(activation)
+    if workspace is None:
+        with _on_stream(stream):
+            workspace = torch.empty(gated_ffn_backward_workspace_bytes(M, F), dtype=torch.uint8, device=dH.device)
+    ws, ws_bytes = _byte_workspace(workspace)
+    _call("gated_ffn_bf16_backward", dH.data_ptr(), lddh, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(P), ldp,
+          _ptr(dX), lddx, _ptr(dW), lddw, M, F, K, act, ws, ws_bytes, _stream(stream))
+    return dX, dW
 
 
 def get_mk_alignment_for_contiguous_layout() -> int:

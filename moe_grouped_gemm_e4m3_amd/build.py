@@ -38,6 +38,7 @@ HIPCC_FLAGS = [
 SOURCES = [
     ("fp8gemm.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("ue8m0.hip", []),
+    ("linear.hip", []),
 ]
 
 

@@ -29,6 +29,7 @@
 #include "skinny_kernel.hpp"
 #include "transpose_kernel.hpp"
 #include "check_kernel.hpp"
+#include "host_common.hpp"
 
 #define FG_TRY(x)                    \
   do {                               \
@@ -886,6 +887,34 @@ static fg_status launch_cast_per_token(const T* x, int64_t ldx, uint8_t* q, void
   if (e != hipSuccess) return fail(FG_EHIP, "%s launch: %s", name, hipGetErrorString(e));
   return FG_OK;
 }
+
+namespace fg {
+
+void clear_error() { g_err.clear(); }
+
+fg_status set_error(fg_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return st;
+}
+
+fg_status usable_cus(int* cus) {
+  FG_TRY(device_cus(cus));
+  if (g_num_cus_cap > 0 && g_num_cus_cap < *cus) *cus = g_num_cus_cap;
+  return FG_OK;
+}
+
+fg_status require_ptr(const void* p, uintptr_t align, const char* name) { return check_ptr(p, align, name); }
+
+fg_status require_ld(int64_t ld, int64_t row, int64_t mult, const char* name) {
+  return check_ld(ld, row, mult, name);
+}
+
+}  // namespace fg
 
 extern "C" {
 

@@ -1,0 +1,256 @@
+// linear.hip -- C entry points of the 8-bit-integer products and the gated
+// feed-forward block (linear_kernel.hpp): argument checks, plans, launches.
+// Nothing is launched after a failed check; nothing is allocated.
+
+#include "host_common.hpp"
+#include "linear_kernel.hpp"
+
+#define FG_TRY(x)                   \
+  do {                              \
+    fg_status st__ = (x);           \
+    if (st__ != FG_OK) return st__; \
+  } while (0)
+
+namespace fg {
+namespace {
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;  // buffer offsets inside a tile are 32-bit
+// |sum| <= 128 * 128 * K must stay below 2^31
+constexpr int kMaxInt8K = (1 << 17) - 16;
+constexpr int kPairAlign = 64;  // columns of each half of the gradient pair
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+fg_status launched(const char* what) {
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return set_error(FG_EHIP, "%s launch: %s", what, hipGetErrorString(e));
+  return FG_OK;
+}
+
+template <int E, bool TA = false, bool TB = false>
+fg_status launch_linear(const LinearParams& p, void* stream, const char* what) {
+  const int64_t cols = E == kEpiGatedGrad ? p.half : p.N;
+  const int64_t tiles = ((p.M + 63) / 64) * ((cols + 63) / 64);
+  if (tiles > (1 << 23)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
+  hipLaunchKernelGGL((linear_kernel<E, TA, TB>), dim3((unsigned)tiles), dim3(256), 0, (hipStream_t)stream, p);
+  return launched(what);
+}
+
+// Sizes every entry point shares; *empty when there is no output element.
+fg_status check_sizes(int M, int N, int K, int mult, bool* empty) {
+  *empty = false;
+  if (M < 0 || N < 0 || K < 0) return set_error(FG_EINVAL, "negative size: %d rows, %d columns, K=%d", M, N, K);
+  if (K % mult) return set_error(FG_EALIGN, "K=%d is not a multiple of %d", K, mult);
+  if (M == 0 || N == 0) {
+    *empty = true;
+    return FG_OK;
+  }
+  if (M > kMaxRows || N > kMaxRows / 2) return set_error(FG_EUNSUPPORTED, "more than 2^30 rows");
+  return FG_OK;
+}
+
+fg_status check_operand(const void* ptr, int64_t ld, int64_t cols, int item, const char* name, const char* ld_name) {
+  FG_TRY(require_ptr(ptr, 16, name));
+  FG_TRY(require_ld(ld, cols, 16 / item, ld_name));
+  if (ld * item > kMaxRowBytes) return set_error(FG_EUNSUPPORTED, "%s=%lld: rows above 4 MiB", ld_name, (long long)ld);
+  return FG_OK;
+}
+
+fg_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
+  if (bytes < 0) return set_error(FG_EINVAL, "workspace_bytes=%lld is negative", (long long)bytes);
+  if (!ws && bytes > 0) return set_error(FG_EINVAL, "workspace is NULL");
+  if (ws && ((uintptr_t)ws & 255)) return set_error(FG_EALIGN, "workspace is not 256-byte aligned");
+  if (bytes < need)
+    return set_error(FG_EINVAL, "workspace_bytes=%lld is smaller than the %lld needed", (long long)bytes,
+                     (long long)need);
+  return FG_OK;
+}
+
+// The workspace of a K split: none, or one that serves every plan.
+fg_status check_split_workspace(const void* ws, int64_t bytes) {
+  return check_workspace(ws, bytes, ws ? fg_nt_workspace_max_bytes() : 0);
+}
+
+fg_status check_activation(int act) {
+  if (act != FG_ACT_SILU && act != FG_ACT_GELU_TANH) return set_error(FG_EINVAL, "activation=%d is not known", act);
+  return FG_OK;
+}
+
+int64_t pair_cols(int F) { return 2 * round_up(F, kPairAlign); }
+
+int64_t backward_bytes(int M, int F) { return round_up((int64_t)M * pair_cols(F) * 2, 256); }
+
+template <typename T>
+fg_status cast_rows(const T* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream, const char* what) {
+  clear_error();
+  if (M < 0 || K < 0) return set_error(FG_EINVAL, "negative size M=%d K=%d", M, K);
+  if (K % 16) return set_error(FG_EALIGN, "K=%d is not a multiple of 16", K);
+  if (M == 0 || K == 0) return FG_OK;
+  FG_TRY(require_ptr(x, 16, "x"));
+  FG_TRY(require_ptr(q, 16, "q"));
+  FG_TRY(require_ptr(s, 4, "s"));
+  FG_TRY(require_ld(ldx, K, 16 / (int)sizeof(T), "ldx"));
+  hipLaunchKernelGGL((int8_cast_kernel<T>), dim3((unsigned)(M < (1 << 20) ? M : 1 << 20)), dim3(256), 0,
+                     (hipStream_t)stream, x, ldx, q, s, M, K);
+  return launched(what);
+}
+
+}  // namespace
+}  // namespace fg
+
+using namespace fg;
+
+extern "C" {
+
+fg_status int8_cast_per_row(const float* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream) {
+  return cast_rows(x, ldx, q, s, M, K, stream, "int8_cast_per_row");
+}
+
+fg_status int8_cast_per_row_bf16(const uint16_t* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream) {
+  return cast_rows(x, ldx, q, s, M, K, stream, "int8_cast_per_row_bf16");
+}
+
+fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
+                       uint16_t* D, int64_t ldd, int M, int N, int K, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
+  clear_error();
+  bool empty;
+  FG_TRY(check_sizes(M, N, K, 16, &empty));
+  if (empty) return FG_OK;
+  if (K > kMaxInt8K) return set_error(FG_EUNSUPPORTED, "K=%d: sums of more than %d products", K, kMaxInt8K);
+  FG_TRY(require_ptr(D, 2, "D"));
+  FG_TRY(require_ld(ldd, N, 1, "ldd"));
+  FG_TRY(require_ptr(sa, 4, "sa"));
+  FG_TRY(require_ptr(sb, 4, "sb"));
+  if (K > 0) {
+    FG_TRY(check_operand(A, lda, K, 1, "A", "lda"));
+    FG_TRY(check_operand(B, ldb, K, 1, "B", "ldb"));
+  }
+  FG_TRY(check_split_workspace(workspace, workspace_bytes));
+  LinearParams p{};
+  p.A = (const uint8_t*)A; p.lda = lda; p.B = (const uint8_t*)B; p.ldb = ldb; p.sa = sa; p.sb = sb;
+  p.D = D; p.ldd = ldd; p.M = M; p.N = N; p.K = K;
+  return launch_linear<kEpiInt8>(p, stream, "gemm_int8_nt");
+}
+
+fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const int8_t* W, int64_t ldw,
+                         const float* sw, uint16_t* H, int64_t ldh, int M, int F, int K, int activation,
+                         void* workspace, int64_t workspace_bytes, void* stream) {
+  clear_error();
+  bool empty;
+  FG_TRY(check_sizes(M, F, K, 16, &empty));
+  FG_TRY(check_activation(activation));
+  if (empty) return FG_OK;
+  if (K > kMaxInt8K) return set_error(FG_EUNSUPPORTED, "K=%d: sums of more than %d products", K, kMaxInt8K);
+  FG_TRY(require_ptr(H, 2, "H"));
+  FG_TRY(require_ld(ldh, F, 1, "ldh"));
+  FG_TRY(require_ptr(sx, 4, "sx"));
+  FG_TRY(require_ptr(sw, 4, "sw"));
+  if (K > 0) {
+    FG_TRY(check_operand(X, ldx, K, 1, "X", "ldx"));
+    FG_TRY(check_operand(W, ldw, K, 1, "W", "ldw"));
+  }
+  FG_TRY(check_split_workspace(workspace, workspace_bytes));
+  LinearParams p{};
+  p.A = (const uint8_t*)X; p.lda = ldx; p.B = (const uint8_t*)W; p.ldb = ldw; p.sa = sx; p.sb = sw;
+  p.D = H; p.ldd = ldh; p.M = M; p.N = F; p.K = K; p.act = activation;
+  return launch_linear<kEpiGatedInt8>(p, stream, "gated_ffn_int8");
+}
+
+fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, uint16_t* H, int64_t ldh,
+                         float* P, int64_t ldp, int M, int F, int K, int activation, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+  clear_error();
+  bool empty;
+  FG_TRY(check_sizes(M, F, K, 8, &empty));
+  FG_TRY(check_activation(activation));
+  if (empty) return FG_OK;
+  FG_TRY(require_ptr(H, 2, "H"));
+  FG_TRY(require_ld(ldh, F, 1, "ldh"));
+  if (P) {
+    FG_TRY(require_ptr(P, 4, "P"));
+    FG_TRY(require_ld(ldp, 2 * (int64_t)F, 1, "ldp"));
+  }
+  if (K > 0) {
+    FG_TRY(check_operand(X, ldx, K, 2, "X", "ldx"));
+    FG_TRY(check_operand(W, ldw, K, 2, "W", "ldw"));
+  }
+  FG_TRY(check_split_workspace(workspace, workspace_bytes));
+  LinearParams p{};
+  p.A = (const uint8_t*)X; p.lda = 2 * ldx; p.B = (const uint8_t*)W; p.ldb = 2 * ldw;
+  p.D = H; p.ldd = ldh; p.P = P; p.ldp = ldp; p.M = M; p.N = F; p.K = K; p.act = activation;
+  return launch_linear<kEpiGated>(p, stream, "gated_ffn_bf16");
+}
+
+fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16_t* X, int64_t ldx,
+                                  const uint16_t* W, int64_t ldw, const float* P, int64_t ldp, uint16_t* dX,
+                                  int64_t lddx, uint16_t* dW, int64_t lddw, int M, int F, int K, int activation,
+                                  void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* what = "gated_ffn_bf16_backward";
+  clear_error();
+  if (M < 0 || F < 0 || K < 0) return set_error(FG_EINVAL, "negative size M=%d F=%d K=%d", M, F, K);
+  if (K % 8) return set_error(FG_EALIGN, "K=%d is not a multiple of 8", K);
+  FG_TRY(check_activation(activation));
+  // no gradient element is asked for: dX is M x K, dW 2F x K
+  if (K == 0 || ((!dX || M == 0) && (!dW || F == 0))) return FG_OK;
+  if (M > kMaxRows || F > kMaxRows / 4) return set_error(FG_EUNSUPPORTED, "more than 2^30 rows");
+  FG_TRY(check_workspace(workspace, workspace_bytes, M > 0 && F > 0 ? backward_bytes(M, F) : 0));
+  if (dX && M > 0) {
+    FG_TRY(require_ptr(dX, 2, "dX"));
+    FG_TRY(require_ld(lddx, K, 1, "lddx"));
+  }
+  if (dW && F > 0) {
+    FG_TRY(require_ptr(dW, 2, "dW"));
+    FG_TRY(require_ld(lddw, K, 1, "lddw"));
+  }
+  LinearParams p{};
+  p.act = activation;
+  p.F = F;
+  p.half = (int)(pair_cols(F) / 2);
+  const int64_t pair_ld = pair_cols(F);
+  if (M > 0 && F > 0) {
+    FG_TRY(require_ptr(dH, 2, "dH"));
+    FG_TRY(require_ld(lddh, F, 1, "lddh"));
+    FG_TRY(check_operand(X, ldx, K, 2, "X", "ldx"));
+    FG_TRY(check_operand(W, ldw, K, 2, "W", "ldw"));
+    if (pair_ld * 2 > kMaxRowBytes) return set_error(FG_EUNSUPPORTED, "F=%d: rows above 4 MiB", F);
+    if (P) {
+      FG_TRY(require_ptr(P, 4, "P"));
+      FG_TRY(require_ld(ldp, 2 * (int64_t)F, 1, "ldp"));
+    }
+    LinearParams g = p;
+    g.A = (const uint8_t*)X; g.lda = 2 * ldx; g.B = (const uint8_t*)W; g.ldb = 2 * ldw;
+    g.dH = dH; g.lddh = lddh; g.P = const_cast<float*>(P); g.ldp = ldp;
+    g.D = (uint16_t*)workspace; g.ldd = pair_ld;
+    g.M = M; g.N = F; g.K = K;
+    if (P) {
+      hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)((g.half + 255) / 256), (unsigned)(M < 65535 ? M : 65535)),
+                         dim3(256), 0, (hipStream_t)stream, g);
+      FG_TRY(launched(what));
+    } else {
+      FG_TRY((launch_linear<kEpiGatedGrad>(g, stream, what)));
+    }
+  }
+  // With M or F of zero the reductions below are empty and write zeros.
+  if (dX && M > 0) {
+    LinearParams g = p;
+    g.A = (const uint8_t*)workspace; g.lda = 2 * pair_ld; g.B = (const uint8_t*)W; g.ldb = 2 * ldw;
+    g.D = dX; g.ldd = lddx; g.M = M; g.N = K; g.K = F > 0 ? (int)pair_ld : 0;
+    FG_TRY((launch_linear<kEpiBf16, false, true>(g, stream, what)));
+  }
+  if (dW && F > 0) {
+    LinearParams g = p;
+    g.A = (const uint8_t*)workspace; g.lda = 2 * pair_ld; g.B = (const uint8_t*)X; g.ldb = 2 * ldx;
+    g.D = dW; g.ldd = lddw; g.M = (int)pair_ld; g.N = K; g.K = M;
+    FG_TRY((launch_linear<kEpiBf16, true, true>(g, stream, what)));
+  }
+  return FG_OK;
+}
+
+int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F) {
+  if (M < 0 || F < 0 || M > kMaxRows || F > kMaxRows / 4) return -1;
+  return M > 0 && F > 0 ? backward_bytes(M, F) : 0;
+}
+
+}  // extern "C"
