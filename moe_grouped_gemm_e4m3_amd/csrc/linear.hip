@@ -2,8 +2,10 @@
 // feed-forward block (linear_kernel.hpp): argument checks, plans, launches.
 // Nothing is launched after a failed check; nothing is allocated.
 
+#include <algorithm>
+
 #include "host_common.hpp"
-#include "linear_kernel.hpp"
+#include "linear_tile.hpp"
 
 #define FG_TRY(x)                   \
   do {                              \
@@ -28,13 +30,31 @@ fg_status launched(const char* what) {
   return FG_OK;
 }
 
-template <int E, bool TA = false, bool TB = false>
-fg_status launch_linear(const LinearParams& p, void* stream, const char* what) {
-  const int64_t cols = E == kEpiGatedGrad ? p.half : p.N;
-  const int64_t tiles = ((p.M + 63) / 64) * ((cols + 63) / 64);
-  if (tiles > (1 << 23)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
-  hipLaunchKernelGGL((linear_kernel<E, TA, TB>), dim3((unsigned)tiles), dim3(256), 0, (hipStream_t)stream, p);
+template <class C>
+fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, const char* what) {
+  p.nk = (int)std::max<int64_t>(1, ((int64_t)p.K * C::ES + 127) / 128);
+  const int64_t tm = ((int64_t)p.M + C::BM - 1) / C::BM, tn = (cols + C::OUT_N - 1) / C::OUT_N;
+  if (tm * tn >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
+  p.tiles_m = (int)tm;
+  p.tiles_n = (int)tn;
+  p.num_tiles = (int)(tm * tn);
+  p.group_m = 8;
+  const int grid = std::min(cus * C::OCC, p.num_tiles);
+  hipLaunchKernelGGL((linear_tile_kernel<C>), dim3((unsigned)grid), dim3(C::THREADS), 0, (hipStream_t)stream, p);
   return launched(what);
+}
+
+template <int E, bool TA = false, bool TB = false>
+fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
+  int cus = 0;
+  FG_TRY(usable_cus(&cus));
+  const int64_t cols = E == kEpiGatedGrad ? p.half : p.N;
+  using Big = LinearTile<E, 256, 256, 2, 4, TA, TB>;
+  using Small = LinearTile<E, 128, 128, 2, 2, TA, TB>;
+  // the large tile once there are enough of them to keep half the CUs busy
+  if ((((int64_t)p.M + 255) / 256) * ((cols + Big::OUT_N - 1) / Big::OUT_N) * 2 > cus)
+    return launch_tile<Big>(p, cus, cols, stream, what);
+  return launch_tile<Small>(p, cus, cols, stream, what);
 }
 
 // Sizes every entry point shares; *empty when there is no output element.

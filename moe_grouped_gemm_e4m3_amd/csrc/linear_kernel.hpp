@@ -15,6 +15,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gemm_kernel.hpp"
 
 namespace fg {
@@ -51,6 +53,9 @@ struct LinearParams {
   // As the reduction axis (dX) or the output rows (dW) index r stands for
   // hidden unit r < F of the first half and r - half of the second.
   int F, half;
+  // slices of the reduction and output tiles of the persistent grid (linear_tile.hpp)
+  int nk;
+  int tiles_m, tiles_n, num_tiles, group_m;
 };
 
 // Row of W (or dW) for column r of the gradient pair; -1 for a padding column.
@@ -84,125 +89,18 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16x2(v, 0.f) & 0xffff); }
 
-// One output element from its accumulators (b: the up product of a gated form).
-template <int E>
-__device__ __forceinline__ void store_one(const LinearParams& p, int m, int n, float a, float b) {
-  if (m >= p.M) return;
-  if (E == kEpiGatedGrad) {
-    if (n >= p.half) return;
-    float dg = 0.f, du = 0.f;
-    if (n < p.N) gated_grad(to_f32(p.dH[(int64_t)m * p.lddh + n]), a, b, p.act, dg, du);
-    p.D[(int64_t)m * p.ldd + n] = bf16_bits(dg);
-    p.D[(int64_t)m * p.ldd + p.half + n] = bf16_bits(du);
-    return;
-  }
-  if (n >= p.N) return;
-  if (epi_int8(E)) {
-    a = a * p.sa[m] * p.sb[n];
-    if (epi_gated(E)) b = b * p.sa[m] * p.sb[p.N + n];
-  }
-  if (epi_gated(E)) {
-    if (E == kEpiGated && p.P) {
-      p.P[(int64_t)m * p.ldp + n] = a;
-      p.P[(int64_t)m * p.ldp + p.N + n] = b;
-    }
-    a = gated_value(a, b, p.act);
-  }
-  p.D[(int64_t)m * p.ldd + n] = bf16_bits(a);
-}
-
-// A 64 x 64 output tile per workgroup of four waves; operands go through LDS
-// element by element with every index checked.
-template <int E, bool TA, bool TB>
-__global__ __launch_bounds__(256) void linear_kernel(LinearParams p) {
-  constexpr int ES = epi_int8(E) ? 1 : 2;     // bytes of an operand element
-  constexpr int KT = 64 / ES;                 // reduction elements of a slice
-  constexpr int NB = epi_gated(E) ? 2 : 1;
-  __shared__ __attribute__((aligned(16))) uint8_t sA[64 * 80];
-  __shared__ __attribute__((aligned(16))) uint8_t sB[NB][64 * 80];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tiles_n = ((E == kEpiGatedGrad ? p.half : p.N) + 63) / 64;
-  const int m0 = (int)(blockIdx.x / tiles_n) * 64, n0 = (int)(blockIdx.x % tiles_n) * 64;
-
-  auto get = [&](const uint8_t* base, int64_t ld, bool t, int64_t row, int64_t k) {
-    const uint8_t* s = base + (t ? k * ld + row * ES : row * ld + k * ES);
-    return ES == 1 ? (int)*s : (int)*(const uint16_t*)s;
-  };
-  f32x4 facc[NB][4];
-  i32x4 iacc[NB][4];
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      facc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      iacc[b][t] = i32x4{0, 0, 0, 0};
-    }
-  for (int k0 = 0; k0 < p.K; k0 += KT) {
-    for (int i = threadIdx.x; i < 64 * KT; i += 256) {
-      // neighbouring threads take neighbouring elements of the stored rows
-      const int ra = TA ? i & 63 : i / KT, ka = TA ? i >> 6 : i % KT;
-      const int rb = TB ? i & 63 : i / KT, kb = TB ? i >> 6 : i % KT;
-      int v = 0;
-      if (m0 + ra < p.M && k0 + ka < p.K) v = get(p.A, p.lda, TA, m0 + ra, k0 + ka);
-      if (ES == 1) sA[ra * 80 + ka] = (uint8_t)v;
-      else *(uint16_t*)(sA + ra * 80 + 2 * ka) = (uint16_t)v;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        int64_t row = n0 + rb, k = k0 + kb;
-        bool ok = n0 + rb < p.N && k < p.K;
-        if (TB && ok && p.F > 0 && !TA) {  // dX: the reduction runs over the gradient pair
-          k = pair_row(p, (int)k);
-          ok = k >= 0;
-        }
-        v = ok ? get(p.B, p.ldb, TB, row + (int64_t)b * p.N, k) : 0;
-        if (ES == 1) sB[b][rb * 80 + kb] = (uint8_t)v;
-        else *(uint16_t*)(sB[b] + rb * 80 + 2 * kb) = (uint16_t)v;
-      }
-    }
-    __syncthreads();
-    const int at = (lane & 15) * 80 + (lane >> 4) * 16;
-    const i32x4 a = *(const i32x4*)(sA + wave * 16 * 80 + at);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const i32x4 w = *(const i32x4*)(sB[b] + t * 16 * 80 + at);
-        if (epi_int8(E))
-          iacc[b][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, a, iacc[b][t], 0, 0, 0);
-        else
-          facc[b][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w),
-                                                               __builtin_bit_cast(bf16x8, a), facc[b][t], 0, 0, 0);
-      }
-    __syncthreads();
-  }
-  // lane: row lane % 16, four consecutive columns 4 (lane / 16)
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int m = m0 + wave * 16 + (lane & 15), n = n0 + t * 16 + 4 * (lane >> 4) + r;
-      const float a = epi_int8(E) ? (float)iacc[0][t][r] : facc[0][t][r];
-      const float b = epi_int8(E) ? (float)iacc[NB - 1][t][r] : facc[NB - 1][t][r];
-      if (TA && m < p.M) {  // dW: the output rows are the gradient pair's columns
-        const int row = pair_row(p, m);
-        if (row >= 0 && n < p.N) p.D[(int64_t)row * p.ldd + n] = bf16_bits(a);
-      } else {
-        store_one<E>(p, m, n, a, b);
-      }
-    }
-}
-
 // [dg du] from the kept pre-activations P = [g u], one element a thread.
 static __global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p) {
   const int n = blockIdx.x * 256 + threadIdx.x;
   if (n >= p.half) return;
   for (int m = blockIdx.y; m < p.M; m += gridDim.y) {
-    float g = 0.f, u = 0.f;
+    float dg = 0.f, du = 0.f;
     if (n < p.N) {
-      g = p.P[(int64_t)m * p.ldp + n];
-      u = p.P[(int64_t)m * p.ldp + p.N + n];
+      const float* prow = p.P + (int64_t)m * p.ldp;
+      gated_grad(to_f32(p.dH[(int64_t)m * p.lddh + n]), prow[n], prow[p.N + n], p.act, dg, du);
     }
-    store_one<kEpiGatedGrad>(p, m, n, g, u);
+    p.D[(int64_t)m * p.ldd + n] = bf16_bits(dg);
+    p.D[(int64_t)m * p.ldd + p.half + n] = bf16_bits(du);
   }
 }
 
