@@ -446,14 +446,10 @@ fg_status fp8_cast_per_block_ue8m0_bf16(const uint16_t* w, int64_t ldw, uint8_t*
  * signed bytes with an fp32 scale per row (a token of the activations, an
  * output channel of the weights), or BF16.  All matrices are row-major with
  * their last dimension contiguous.
- *
- * Workspace of the calls that take one, where not stated otherwise: as
- * gemm_fp8_nt_ws's (256-byte aligned, its first 64 KiB zero before first use
- * and left zero by every call, not shared by calls that overlap in time), and
- * of fg_nt_workspace_max_bytes() bytes, or NULL and 0.  It lets calls whose
- * output tiles cannot occupy the device split K over workgroups; partials are
- * added in a fixed order, so results are reproducible.  One workspace may
- * serve these calls and gemm_fp8_nt_ws on one stream.
+ * These calls split no reduction over workgroups and need no workspace, but
+ * for the backward pass's intermediate.  Their plans depend only on the
+ * arguments, the device and the CU cap, and sums have a fixed order, so
+ * results are reproducible.
  */
 
 /*
@@ -481,8 +477,7 @@ fg_status int8_cast_per_row_bf16(const uint16_t* x, int64_t ldx, int8_t* q, floa
  * rounded once.  Allocates nothing.
  */
 fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
-                       uint16_t* D, int64_t ldd, int M, int N, int K, void* workspace, int64_t workspace_bytes,
-                       void* stream);
+                       uint16_t* D, int64_t ldd, int M, int N, int K, void* stream);
 
 /* Activations of the gated block: act(x) = x / (1 + exp(-y)), y = x (SiLU) or
  * y = 2 sqrt(2/pi) (x + 0.044715 x^3) (the tanh form of GELU). */
@@ -500,8 +495,7 @@ typedef enum { FG_ACT_SILU = 0, FG_ACT_GELU_TANH = 1 } fg_activation;
  * g and u are accumulated in fp32 and not rounded before the activation.
  */
 fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, uint16_t* H, int64_t ldh,
-                         float* P, int64_t ldp, int M, int F, int K, int activation, void* workspace,
-                         int64_t workspace_bytes, void* stream);
+                         float* P, int64_t ldp, int M, int F, int K, int activation, void* stream);
 
 /*
  * Its gradients, given dH:
@@ -534,7 +528,7 @@ int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F);
  */
 fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const int8_t* W, int64_t ldw,
                          const float* sw, uint16_t* H, int64_t ldh, int M, int F, int K, int activation,
-                         void* workspace, int64_t workspace_bytes, void* stream);
+                         void* stream);
 
 /* Row alignment of each expert segment in the contiguous layout: 128. */
 int fg_get_mk_alignment_for_contiguous_layout(void);

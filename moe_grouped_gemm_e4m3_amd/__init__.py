@@ -98,12 +98,12 @@ _SIGNATURES = {
     "fp8_cast_per_block_ue8m0_bf16": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
     "int8_cast_per_row": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
     "int8_cast_per_row_bf16": (_I, [_P, _I64, _P, _P, _I, _I, _P]),
-    "gemm_int8_nt": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _P, _I64, _P]),
-    "gated_ffn_bf16": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
+    "gemm_int8_nt": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _P]),
+    "gated_ffn_bf16": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P]),
     "gated_ffn_bf16_backward": (
         _I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
     "fg_gated_ffn_backward_workspace_bytes": (_I64, [_I, _I]),
-    "gated_ffn_int8": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
+    "gated_ffn_int8": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _P]),
     "fg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "fg_set_num_cus": (None, [_I]),
     "fg_get_num_cus": (_I, []),
@@ -685,16 +685,6 @@ def _on_stream(stream):
     return torch.cuda.stream(stream)
 
 
-def _split_workspace(workspace, device, stream):
-    """(pointer, bytes) of a call's split-K workspace: the given one or the stream's."""
-    if workspace is None:
-        workspace = _NT_WS.get((device.index, _stream(stream)))
-        if workspace is None:
-            with _on_stream(stream):
-                workspace = nt_workspace(device, stream)
-    return _byte_workspace(workspace)
-
-
 def _byte_workspace(workspace: torch.Tensor):
     if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
@@ -723,47 +713,42 @@ def int8_cast_per_row(x, q=None, s=None, stream=None):
     return q, s
 
 
-def gemm_int8_nt(A, sa, B, sb, D, stream=None, workspace=None):
+def gemm_int8_nt(A, sa, B, sb, D, stream=None):
     """D[M,N] = bf16(sa[m] sb[n] (A . B^T)) for int8 A [M, K], B [N, K] and
-    fp32 scales for each row of A and of B; the integer sum is exact.  Few
-    rows may split K over workgroups in `workspace` (default: the stream's
-    cached one, see nt_workspace; an empty one: no split)."""
+    fp32 scales for each row of A and of B; the integer sum is exact."""
     if A.dim() != 2 or B.dim() != 2:
         raise ValueError("A and B must be matrices")
     M, K = A.shape
     N = B.shape[0]
     lda, ldb = _matrix(A, "A", torch.int8, M, K), _matrix(B, "B", torch.int8, N, K)
     ldd = _matrix(D, "D", torch.bfloat16, M, N)
-    _one_device(D, A, sa, B, sb, workspace)
-    ws, ws_bytes = _split_workspace(workspace, D.device, stream)
+    _one_device(D, A, sa, B, sb)
     _call("gemm_int8_nt", A.data_ptr(), lda, _row_scales(sa, "sa", M), B.data_ptr(), ldb, _row_scales(sb, "sb", N),
-          D.data_ptr(), ldd, M, N, K, ws, ws_bytes, _stream(stream))
+          D.data_ptr(), ldd, M, N, K, _stream(stream))
     return D
 
 
-def gated_ffn_int8(X, sx, W, sw, H, activation="silu", stream=None, workspace=None):
+def gated_ffn_int8(X, sx, W, sw, H, activation="silu", stream=None):
     """H[M,F] = bf16(act(g) u) from int8 X [M, K] and W [2F, K] (gate rows,
     then up rows) with fp32 row scales: g = sx sw (X . W[:F]^T), u likewise.
-    activation: "silu" or "gelu_tanh".  Workspace as for gemm_int8_nt."""
+    activation: "silu" or "gelu_tanh"."""
     if X.dim() != 2 or H.dim() != 2:
         raise ValueError("X and H must be matrices")
     M, K = X.shape
     F = H.shape[1]
     ldx, ldw = _matrix(X, "X", torch.int8, M, K), _matrix(W, "W", torch.int8, 2 * F, K)
     ldh = _matrix(H, "H", torch.bfloat16, M, F)
-    _one_device(H, X, sx, W, sw, workspace)
-    ws, ws_bytes = _split_workspace(workspace, H.device, stream)
+    _one_device(H, X, sx, W, sw)
     _call("gated_ffn_int8", X.data_ptr(), ldx, _row_scales(sx, "sx", M), W.data_ptr(), ldw,
-          _row_scales(sw, "sw", 2 * F), H.data_ptr(), ldh, M, F, K, _activation(activation), ws, ws_bytes,
-          _stream(stream))
+          _row_scales(sw, "sw", 2 * F), H.data_ptr(), ldh, M, F, K, _activation(activation), _stream(stream))
     return H
 
 
-def gated_ffn_bf16(X, W, H, P=None, activation="silu", stream=None, workspace=None):
+def gated_ffn_bf16(X, W, H, P=None, activation="silu", stream=None):
     """H[M,F] = bf16(act(X . W[:F]^T) * (X . W[F:]^T)) for bf16 X [M, K] and
     W [2F, K] (gate rows, then up rows), in one kernel.  P: fp32 [M, 2F],
     receives the pre-activations for gated_ffn_bf16_backward.  activation:
-    "silu" or "gelu_tanh".  Workspace as for gemm_int8_nt."""
+    "silu" or "gelu_tanh"."""
     if X.dim() != 2 or H.dim() != 2:
         raise ValueError("X and H must be matrices")
     M, K = X.shape
@@ -771,10 +756,9 @@ def gated_ffn_bf16(X, W, H, P=None, activation="silu", stream=None, workspace=No
     bf16 = torch.bfloat16
     ldx, ldw, ldh = _matrix(X, "X", bf16, M, K), _matrix(W, "W", bf16, 2 * F, K), _matrix(H, "H", bf16, M, F)
     ldp = 0 if P is None else _matrix(P, "P", torch.float32, M, 2 * F)
-    _one_device(H, X, W, P, workspace)
-    ws, ws_bytes = _split_workspace(workspace, H.device, stream)
+    _one_device(H, X, W, P)
     _call("gated_ffn_bf16", X.data_ptr(), ldx, W.data_ptr(), ldw, H.data_ptr(), ldh, _ptr(P), ldp, M, F, K,
-          _activation(activation), ws, ws_bytes, _stream(stream))
+          _activation(activation), _stream(stream))
     return H
 
 

@@ -3,9 +3,10 @@
 // Nothing is launched after a failed check; nothing is allocated.
 
 #include <algorithm>
+#include <cmath>
 
 #include "host_common.hpp"
-#include "linear_tile.hpp"
+#include "linear_fewrow.hpp"
 
 #define FG_TRY(x)                   \
   do {                              \
@@ -30,9 +31,14 @@ fg_status launched(const char* what) {
   return FG_OK;
 }
 
+// ---------------------------------------------------------------------------
+// Plans.  Each candidate's time is estimated from its tiles and slices with
+// costs measured on MI355X (256 CUs; microseconds; int8 and bf16 slices cost
+// the same, both are 128 bytes and 2048 MFMA cycles on the 256 x 256 tile),
+// and the cheapest runs.  The estimates only rank candidates.
+
 template <class C>
 fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, const char* what) {
-  p.nk = (int)std::max<int64_t>(1, ((int64_t)p.K * C::ES + 127) / 128);
   const int64_t tm = ((int64_t)p.M + C::BM - 1) / C::BM, tn = (cols + C::OUT_N - 1) / C::OUT_N;
   if (tm * tn >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
   p.tiles_m = (int)tm;
@@ -44,17 +50,92 @@ fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, cons
   return launched(what);
 }
 
+// Output tiles of BM rows and BN weight rows.
+double tile_count(const LinearParams& p, int64_t cols, bool gated, int bm, int bn) {
+  const int out_n = gated ? bn / 2 : bn;
+  return (double)(((int64_t)p.M + bm - 1) / bm) * (double)((cols + out_n - 1) / out_n);
+}
+
+// One tile per CU and round: `idle` a slice with few CUs at work, `busy` with
+// all of them (clock and cache contention).
+double tile_us(double tiles, int cus, int nk, double idle, double busy) {
+  const double load = tiles < cus ? tiles / cus : 1.0;
+  return 3.0 + ceil(tiles / cus) * (nk * (idle + (busy - idle) * load) + 1.5);
+}
+
+// Two workgroups per CU: a round that leaves one workgroup per CU is cheaper.
+double tile2_us(double tiles, int cus, int nk, double one, double two) {
+  const double full = floor(tiles / (2 * cus)), rest = tiles - full * 2 * cus;
+  return 3.0 + full * (nk * two + 1.5) + (rest > 0 ? nk * (rest > cus ? two : one) + 1.5 : 0);
+}
+
+template <class C>
+fg_status launch_fewrow(const LinearParams& p, void* stream, const char* what) {
+  const int64_t parts = ((int64_t)p.M + C::ROWS - 1) / C::ROWS, tiles = ((int64_t)p.N + C::OUT_N - 1) / C::OUT_N;
+  if (parts * tiles >= (1 << 23)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
+  hipLaunchKernelGGL((fewrow_kernel<C>), dim3((unsigned)(parts * tiles)), dim3(C::THREADS), 0, (hipStream_t)stream, p,
+                     (int)parts);
+  return launched(what);
+}
+
+// A few-row workgroup fetches its rows' slices at about 80 GB/s; a launch's
+// rounds each add about 2 us of latency.
+double fewrow_us(const LinearParams& p, bool gated, int cus, int mf, int cf) {
+  const double parts = (double)((p.M + 16 * mf - 1) / (16 * mf)), out_n = gated ? 8 * cf : 16 * cf;
+  const double groups = parts * ceil(p.N / out_n), bytes = (double)p.nk * 128 * (std::min(p.M, 16 * mf) + 16 * cf);
+  return 1.0 + ceil(groups / cus) * (2.0 + bytes / 80e3);
+}
+
 template <int E, bool TA = false, bool TB = false>
 fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
   int cus = 0;
   FG_TRY(usable_cus(&cus));
+  constexpr bool gated = epi_gated(E);
   const int64_t cols = E == kEpiGatedGrad ? p.half : p.N;
-  using Big = LinearTile<E, 256, 256, 2, 4, TA, TB>;
-  using Small = LinearTile<E, 128, 128, 2, 2, TA, TB>;
-  // the large tile once there are enough of them to keep half the CUs busy
-  if ((((int64_t)p.M + 255) / 256) * ((cols + Big::OUT_N - 1) / Big::OUT_N) * 2 > cus)
-    return launch_tile<Big>(p, cus, cols, stream, what);
-  return launch_tile<Small>(p, cus, cols, stream, what);
+  p.nk = (int)std::max<int64_t>(1, ((int64_t)p.K * (epi_int8(E) ? 1 : 2) + 127) / 128);
+  // 256 x 256: 1.2 us a slice alone, 1.7 with every CU at work (4096 x 4096 x
+  // 7168 int8 95 us).  128 x 128, two workgroups of four waves: 0.66 alone,
+  // 1.0 for both (112 us on that shape); one of eight waves with four stages:
+  // 0.48 and 0.58 (34 us on 1000 x 4096 x 7168, 71 on 256 x 256 tiles).
+  // 64 x 64 with eight stages: 0.33 (20 us on 256 x 4096 x 7168, 27 on
+  // 128 x 128 tiles).
+  const double big = tile_us(tile_count(p, cols, gated, 256, 256), cus, p.nk, 1.2, 1.7);
+  const double mid2 = tile2_us(tile_count(p, cols, gated, 128, 128), cus, p.nk, 0.66, 1.0);
+  const double mid = tile_us(tile_count(p, cols, gated, 128, 128), cus, p.nk, 0.48, 0.58);
+  const double small = tile_us(tile_count(p, cols, gated, 64, 64), cus, p.nk, 0.33, 0.33);
+  const double tile = std::min(std::min(big, mid2), std::min(mid, small));
+  if constexpr (!TA && !TB && E != kEpiGatedGrad) {
+    if (p.M <= 256) {
+      static const int shapes[][2] = {{1, 1}, {1, 2}, {2, 1}, {2, 2}, {4, 1}, {4, 2}, {4, 4}};
+      int best = -1;
+      double least = tile;
+      for (int i = 0; i < 7; ++i) {
+        const double t = fewrow_us(p, gated, cus, shapes[i][0], shapes[i][1]);
+        if (t < least) {
+          least = t;
+          best = i;
+        }
+      }
+      switch (best) {
+        case 0:
+          // long chains of slices are shared out over eight waves (1 x 2112 x
+          // 7168 5.1 us against 6.1, 1 x 2048 x 1024 3.1 against 2.8)
+          if (p.nk >= 32) return launch_fewrow<FewRow<E, 1, 1, 8, 2>>(p, stream, what);
+          return launch_fewrow<FewRow<E, 1, 1, 4, 2>>(p, stream, what);
+        case 1: return launch_fewrow<FewRow<E, 1, 2, 4, 2>>(p, stream, what);
+        case 2: return launch_fewrow<FewRow<E, 2, 1, 4, 3>>(p, stream, what);
+        case 3: return launch_fewrow<FewRow<E, 2, 2, 4, 2>>(p, stream, what);
+        case 4: return launch_fewrow<FewRow<E, 4, 1, 4, 2>>(p, stream, what);
+        case 5: return launch_fewrow<FewRow<E, 4, 2, 4, 2>>(p, stream, what);
+        case 6: return launch_fewrow<FewRow<E, 4, 4, 4, 2>>(p, stream, what);
+        default: break;
+      }
+    }
+  }
+  if (tile == big) return launch_tile<LinearTile<E, 256, 256, 4, 2, 2, TA, TB>>(p, cus, cols, stream, what);
+  if (tile == mid2) return launch_tile<LinearTile<E, 128, 128, 2, 2, 2, TA, TB>>(p, cus, cols, stream, what);
+  if (tile == mid) return launch_tile<LinearTile<E, 128, 128, 4, 2, 4, TA, TB>>(p, cus, cols, stream, what);
+  return launch_tile<LinearTile<E, 64, 64, 2, 2, 8, TA, TB>>(p, cus, cols, stream, what);
 }
 
 // Sizes every entry point shares; *empty when there is no output element.
@@ -85,11 +166,6 @@ fg_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
     return set_error(FG_EINVAL, "workspace_bytes=%lld is smaller than the %lld needed", (long long)bytes,
                      (long long)need);
   return FG_OK;
-}
-
-// The workspace of a K split: none, or one that serves every plan.
-fg_status check_split_workspace(const void* ws, int64_t bytes) {
-  return check_workspace(ws, bytes, ws ? fg_nt_workspace_max_bytes() : 0);
 }
 
 fg_status check_activation(int act) {
@@ -132,8 +208,7 @@ fg_status int8_cast_per_row_bf16(const uint16_t* x, int64_t ldx, int8_t* q, floa
 }
 
 fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
-                       uint16_t* D, int64_t ldd, int M, int N, int K, void* workspace, int64_t workspace_bytes,
-                       void* stream) {
+                       uint16_t* D, int64_t ldd, int M, int N, int K, void* stream) {
   clear_error();
   bool empty;
   FG_TRY(check_sizes(M, N, K, 16, &empty));
@@ -147,7 +222,6 @@ fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8
     FG_TRY(check_operand(A, lda, K, 1, "A", "lda"));
     FG_TRY(check_operand(B, ldb, K, 1, "B", "ldb"));
   }
-  FG_TRY(check_split_workspace(workspace, workspace_bytes));
   LinearParams p{};
   p.A = (const uint8_t*)A; p.lda = lda; p.B = (const uint8_t*)B; p.ldb = ldb; p.sa = sa; p.sb = sb;
   p.D = D; p.ldd = ldd; p.M = M; p.N = N; p.K = K;
@@ -156,7 +230,7 @@ fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8
 
 fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const int8_t* W, int64_t ldw,
                          const float* sw, uint16_t* H, int64_t ldh, int M, int F, int K, int activation,
-                         void* workspace, int64_t workspace_bytes, void* stream) {
+                         void* stream) {
   clear_error();
   bool empty;
   FG_TRY(check_sizes(M, F, K, 16, &empty));
@@ -171,7 +245,6 @@ fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const in
     FG_TRY(check_operand(X, ldx, K, 1, "X", "ldx"));
     FG_TRY(check_operand(W, ldw, K, 1, "W", "ldw"));
   }
-  FG_TRY(check_split_workspace(workspace, workspace_bytes));
   LinearParams p{};
   p.A = (const uint8_t*)X; p.lda = ldx; p.B = (const uint8_t*)W; p.ldb = ldw; p.sa = sx; p.sb = sw;
   p.D = H; p.ldd = ldh; p.M = M; p.N = F; p.K = K; p.act = activation;
@@ -179,8 +252,7 @@ fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const in
 }
 
 fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, uint16_t* H, int64_t ldh,
-                         float* P, int64_t ldp, int M, int F, int K, int activation, void* workspace,
-                         int64_t workspace_bytes, void* stream) {
+                         float* P, int64_t ldp, int M, int F, int K, int activation, void* stream) {
   clear_error();
   bool empty;
   FG_TRY(check_sizes(M, F, K, 8, &empty));
@@ -196,7 +268,6 @@ fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
     FG_TRY(check_operand(X, ldx, K, 2, "X", "ldx"));
     FG_TRY(check_operand(W, ldw, K, 2, "W", "ldw"));
   }
-  FG_TRY(check_split_workspace(workspace, workspace_bytes));
   LinearParams p{};
   p.A = (const uint8_t*)X; p.lda = 2 * ldx; p.B = (const uint8_t*)W; p.ldb = 2 * ldw;
   p.D = H; p.ldd = ldh; p.P = P; p.ldp = ldp; p.M = M; p.N = F; p.K = K; p.act = activation;

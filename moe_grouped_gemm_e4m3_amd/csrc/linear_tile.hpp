@@ -9,22 +9,24 @@ namespace fg {
 // A BM x BN output tile (gated: BN / 2 hidden units, gate and up columns) per
 // workgroup of WAVES_M x WAVES_N waves.  A slice is 128 bytes of the
 // reduction: 64 bf16 or 128 int8.
-template <int E_, int BM_, int BN_, int WAVES_M_, int WAVES_N_, bool TA_ = false, bool TB_ = false>
+template <int E_, int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, bool TA_ = false, bool TB_ = false>
 struct LinearTile {
   static constexpr int E = E_, BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
+  static constexpr int STAGES = STAGES_;  // slices in LDS
   static constexpr bool TA = TA_, TB = TB_;
   static constexpr bool INT8 = epi_int8(E), GATED = epi_gated(E);
   static constexpr int ES = INT8 ? 1 : 2;
   static constexpr int NW = WAVES_M * WAVES_N, THREADS = NW * 64;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, SM = WM / 16, SN = WN / 16;
-  static constexpr int STAGE = (BM + BN) * 128;
-  static constexpr int LDS_BYTES = 2 * STAGE;
+  static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;  // a stage: A rows, then B rows
+  static constexpr int LDS_BYTES = STAGES * STAGE;
   static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads per wave and slice
   static constexpr int OUT_N = GATED ? BN / 2 : BN;         // output columns of a tile
   // two workgroups share a CU where LDS and registers allow it
   static constexpr int OCC = 2 * LDS_BYTES <= 160 * 1024 ? 2 : 1;
   static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads");
-  static_assert(SN % 2 == 0, "column blocks are stored in pairs");
+  static_assert(LDS_BYTES <= 160 * 1024 && STAGES >= 2 && (STAGES - 1) * (LA + LB) < 64, "stages");
+  static_assert(!GATED || SN % 2 == 0, "gate and up blocks come in pairs");
   static_assert(!INT8 || (!TA && !TB), "bytes are staged K-major");
 };
 
@@ -58,96 +60,99 @@ __device__ __forceinline__ int mn_swz(int r) {
   return (((r & 3) | ((r >> 1) & 12)) << 1) & (CH - 1);
 }
 
-// N loads of an operand stored K-major: 8 stage rows of 128 bytes each.
-template <int N, bool CLIP>
-__device__ __forceinline__ void issue_k_major(__amdgpu_buffer_rsrc_t rs, int64_t ld, int row0, int srow0, int k0,
-                                              int kbytes, uint8_t* dst, int lane) {
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int r = 8 * j + (lane >> 3);
-    const int c = (lane & 7) ^ swz16(srow0 + r);
-    int v = (row0 + r) * (int)ld + c * 16;
-    if (CLIP) v = k_clip(v, k0 + c * 16, kbytes);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + j * 1024), 16, v, k0,
-                                             0, 0);
-  }
+// 16-byte chunk swizzle of K-major stage rows.  A 128-bit LDS read is served
+// 16 lanes at a time, lanes 0-3, 12-15, 20-23 and 24-27 together: with the
+// row's low 3 bits those lanes' chunks lie in 16 different bank groups
+// (measured: no conflicts; an XOR with bit 3 as well has two on every read).
+__device__ __forceinline__ int lin_swz(int row) {
+  return row & 7;
 }
 
-// N loads of an operand stored MN-major: 1 KiB of whole stage rows each.
-template <int N, int COLS>
-__device__ __forceinline__ void issue_mn_major(__amdgpu_buffer_rsrc_t rs, int64_t ld, int q0, int cols_left,
-                                               uint8_t* dst, int lane) {
-  constexpr int CH = COLS / 8, RPL = 64 / CH;  // chunks per row, rows per load
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int r = (q0 + j) * RPL + lane / CH;
-    const int c = (lane % CH) ^ mn_swz<CH>(r);
-    const int v = c * 8 < cols_left ? r * (int)ld + c * 16 : kOobOffset;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + j * 1024), 16, v, 0,
+// The loads of one operand, slice after slice and tile after tile, into the
+// LDS stages: 1 KiB each, straight into LDS, shared out over the waves.  Past
+// the workgroup's last tile they load zeros and touch no memory: every slice
+// issues the same number of loads, which the main loop's waits count on.
+template <class C, bool IS_A>
+struct Loader {
+  static constexpr bool MN = IS_A ? C::TA : C::TB;
+  static constexpr bool PAIRED = !IS_A && C::GATED;  // gate and up rows
+  static constexpr int N = IS_A ? C::LA : C::LB;     // loads per wave
+  static constexpr int COLS = IS_A ? C::BM : C::BN;
+  LinearWork t;
+  int kb;                         // slice of tile t
+  int dst;                        // LDS offset of its stage
+  __amdgpu_buffer_rsrc_t rs, ru;  // its range (K-major: the tile's rows; gated: gate and up rows)
+  int cols;                       // rows (MN-major: columns) of the operand from the tile's first on
+  bool empty;                     // nothing to read: every offset is out of range
+
+  __device__ __forceinline__ Loader(const LinearParams& p, const LinearWork& first) : t(first), kb(0) {
+    dst = IS_A ? 0 : C::A_BYTES;
+    range(p);
+  }
+  __device__ __forceinline__ void range(const LinearParams& p) {
+    const uint8_t* base = IS_A ? p.A : p.B;
+    const int64_t ld = IS_A ? p.lda : p.ldb;
+    const int first = IS_A ? t.m0 : t.n0;
+    cols = (IS_A ? p.M : p.N) - first;
+    // no tile, or one of a gradient pair's padding columns alone
+    empty = t.w < 0 || cols <= 0;
+    if constexpr (MN) {
+      // reduction rows from this slice on; of W they are the hidden units of
+      // one half of the gradient pair
+      int64_t row = (int64_t)kb * 64, left = p.K - row;
+      if (!IS_A && !C::TA && p.F > 0) {
+        const int h = row >= p.half ? 1 : 0;
+        const int f = (int)row - h * p.half;
+        row = (int64_t)h * p.F + f;
+        left = p.F - f;
+      }
+      empty = empty || left <= 0;
+      rs = make_rsrc(base + row * ld + (int64_t)first * 2,
+                     empty ? 0 : (min(left, (int64_t)64) - 1) * ld + (int64_t)cols * 2);
+    } else {
+      const int64_t bytes = empty ? 0 : (int64_t)(cols - 1) * ld + p.K * C::ES;
+      rs = make_rsrc(base + (int64_t)first * ld, bytes);
+      if (PAIRED) ru = make_rsrc(base + (int64_t)(p.N + first) * ld, bytes);
+    }
+  }
+  // Load j of this wave's N of the slice, into its stage (lds + dst).
+  __device__ __forceinline__ void issue(const LinearParams& p, uint8_t* stage, int j, int wave, int lane) const {
+    const int64_t ld = IS_A ? p.lda : p.ldb;
+    const int q = wave * N + j;
+    __amdgpu_buffer_rsrc_t r = rs;
+    int v, k = 0;
+    if constexpr (MN) {  // whole stage rows of COLS columns
+      constexpr int CH = COLS / 8;  // chunks per row
+      const int row = q * (64 / CH) + lane / CH;
+      const int c = (lane % CH) ^ mn_swz<CH>(row);
+      v = c * 8 < cols ? row * (int)ld + c * 16 : kOobOffset;
+    } else {  // 8 stage rows of 128 bytes
+      int row = q * 8;
+      if constexpr (PAIRED) {  // stage rows: 16 gate rows, 16 up rows of the same hidden units, ...
+        row = (q >> 2) * 16 + (q & 1) * 8;
+        if ((q >> 1) & 1) r = ru;
+      }
+      const int r8 = lane >> 3, c = ((lane & 7) ^ lin_swz(r8)) * 16;
+      v = k_clip((row + r8) * (int)ld + c, kb * 128 + c, p.K * C::ES);
+      // the scalar offset counts against the range's end, which an empty
+      // range has at 0: it must not pass it
+      k = empty ? 0 : kb * 128;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(stage + q * 1024), 16, v, k,
                                              0, 0);
   }
-}
-
-// All loads of slice kb of tile t into `stage`, shared out over the waves.
-template <class C>
-__device__ __forceinline__ void issue_linear_slice(const LinearParams& p, const LinearWork& t, int kb, uint8_t* stage,
-                                                   int wave, int lane) {
-  const int kbytes = C::TA ? 0 : p.K * C::ES, k0 = kb * 128;
-  const bool clip = k0 + 128 > kbytes;
-  uint8_t* a_dst = stage + wave * C::LA * 1024;
-  uint8_t* b_dst = stage + C::BM * 128 + wave * C::LB * 1024;
-  if constexpr (C::TA) {
-    const int left = p.K - kb * 64;
-    const __amdgpu_buffer_rsrc_t ra = make_rsrc(p.A + (int64_t)kb * 64 * p.lda + (int64_t)t.m0 * 2,
-                                                left > 0 ? (int64_t)(left - 1) * p.lda + (int64_t)(p.M - t.m0) * 2 : 0);
-    issue_mn_major<C::LA, C::BM>(ra, p.lda, wave * C::LA, p.M - t.m0, a_dst, lane);
-  } else {
-    const __amdgpu_buffer_rsrc_t ra =
-        make_rsrc(p.A + (int64_t)t.m0 * p.lda, (int64_t)(p.M - t.m0 - 1) * p.lda + kbytes);
-    if (clip)
-      issue_k_major<C::LA, true>(ra, p.lda, wave * C::LA * 8, wave * C::LA * 8, k0, kbytes, a_dst, lane);
-    else
-      issue_k_major<C::LA, false>(ra, p.lda, wave * C::LA * 8, wave * C::LA * 8, k0, kbytes, a_dst, lane);
-  }
-  if constexpr (C::TB) {
-    // reduction rows of B: of W, hidden units of one half of the gradient
-    // pair; otherwise B's own rows
-    int64_t row = (int64_t)kb * 64;
-    int left = p.K - kb * 64;
-    if (!C::TA && p.F > 0) {
-      const int h = row >= p.half ? 1 : 0;
-      const int f = (int)row - h * p.half;
-      row = (int64_t)h * p.F + f;
-      left = p.F - f;
+  __device__ __forceinline__ void advance(const LinearParams& p, int grid) {
+    constexpr int FIRST = IS_A ? 0 : C::A_BYTES;
+    dst = dst == FIRST + (C::STAGES - 1) * C::STAGE ? FIRST : dst + C::STAGE;
+    if (++kb == p.nk) {
+      kb = 0;
+      if (t.w >= 0) t = linear_work<C>(p, t.w + grid);
+      range(p);
+    } else if (MN) {
+      range(p);
     }
-    const __amdgpu_buffer_rsrc_t rb =
-        make_rsrc(p.B + row * p.ldb + (int64_t)t.n0 * 2,
-                  left > 0 ? (int64_t)(min(left, 64) - 1) * p.ldb + (int64_t)(p.N - t.n0) * 2 : 0);
-    issue_mn_major<C::LB, C::BN>(rb, p.ldb, wave * C::LB, p.N - t.n0, b_dst, lane);
-  } else if constexpr (C::GATED) {
-    // stage rows: 16 gate rows, 16 up rows of the same hidden units, ...
-    const int64_t bytes = (int64_t)(p.N - t.n0 - 1) * p.ldb + kbytes;
-    const uint8_t* base = p.B + (int64_t)t.n0 * p.ldb;
-    const __amdgpu_buffer_rsrc_t rg = make_rsrc(base, bytes), ru = make_rsrc(base + (int64_t)p.N * p.ldb, bytes);
-#pragma unroll
-    for (int j = 0; j < C::LB; ++j) {
-      const int q = wave * C::LB + j;  // 8 stage rows
-      const int unit = (q >> 2) * 16 + (q & 1) * 8;
-      const __amdgpu_buffer_rsrc_t rb = (q >> 1) & 1 ? ru : rg;
-      if (clip)
-        issue_k_major<1, true>(rb, p.ldb, unit, q * 8, k0, kbytes, b_dst + j * 1024, lane);
-      else
-        issue_k_major<1, false>(rb, p.ldb, unit, q * 8, k0, kbytes, b_dst + j * 1024, lane);
-    }
-  } else {
-    const __amdgpu_buffer_rsrc_t rb =
-        make_rsrc(p.B + (int64_t)t.n0 * p.ldb, (int64_t)(p.N - t.n0 - 1) * p.ldb + kbytes);
-    if (clip)
-      issue_k_major<C::LB, true>(rb, p.ldb, wave * C::LB * 8, wave * C::LB * 8, k0, kbytes, b_dst, lane);
-    else
-      issue_k_major<C::LB, false>(rb, p.ldb, wave * C::LB * 8, wave * C::LB * 8, k0, kbytes, b_dst, lane);
   }
-}
+};
 
 // Fragments of half h (64 bytes of the reduction) of a slice: lane l holds
 // row l % 16, bytes [16 (l / 16), +16) of the half.
@@ -155,36 +160,34 @@ template <int COLS, bool MN, int N>
 struct FragReader {
   int off;   // K-major: byte offset of the first fragment's chunk for half 0
   int row0;  // MN-major: first column block of the wave
-  __device__ __forceinline__ FragReader(int area, int first_row, int lane) {
+  __device__ __forceinline__ FragReader(int first_row, int lane) {
     const int l16 = lane & 15, q = lane >> 4;
     if (MN) {
       // lane i of group q reads reduction rows 8 q + i / 4 (and 4 further),
       // columns 4 (i % 4) .. +3 of the block; the transposing read hands it
       // column i of the four rows
-      off = area + (8 * q + (l16 >> 2)) * COLS * 2 + (l16 & 1) * 8;
+      off = (8 * q + (l16 >> 2)) * COLS * 2 + (l16 & 1) * 8;
       row0 = (first_row >> 4) * 2 + ((l16 >> 1) & 1);
     } else {
       const int r = first_row + l16;
-      off = area + r * 128 + ((q ^ swz16(r)) << 4);
+      off = r * 128 + ((q ^ lin_swz(r)) << 4);
       row0 = 0;
     }
   }
-  __device__ __forceinline__ void read(const uint8_t* st, int h, int lane, i32x4 (&f)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if constexpr (MN) {
-        typedef short s16x4 __attribute__((ext_vector_type(4)));
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const int r = 8 * (lane >> 4) + ((lane & 15) >> 2);  // row within the half
-        const int chunk = ((row0 + 2 * i) ^ mn_swz<COLS / 8>(r)) << 4;
-        const uint8_t* a = st + off + h * 32 * COLS * 2 + chunk;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * COLS * 2));
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        f[i] = __builtin_bit_cast(i32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-      } else {
-        f[i] = *(const i32x4*)(st + (off ^ (h * 64)) + i * 2048);
-      }
+  // Fragment i of half h of the slice in stage st.
+  __device__ __forceinline__ void read(const uint8_t* st, int h, int lane, int i, i32x4 (&f)[N]) const {
+    if constexpr (MN) {
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef short s16x8 __attribute__((ext_vector_type(8)));
+      typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+      const int r = 8 * (lane >> 4) + ((lane & 15) >> 2);  // row within the half
+      const int chunk = ((row0 + 2 * i) ^ mn_swz<COLS / 8>(r)) << 4;
+      const uint8_t* a = st + off + h * 32 * COLS * 2 + chunk;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * COLS * 2));
+      f[i] = __builtin_bit_cast(i32x4, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      f[i] = *(const i32x4*)(st + (off ^ (h * 64)) + i * 2048);
     }
   }
 };
@@ -199,9 +202,8 @@ struct LinearAcc {
 #pragma unroll
       for (int j = 0; j < C::SN; ++j) v[i][j] = V{0, 0, 0, 0};
   }
-  __device__ __forceinline__ void mma(const i32x4 (&a)[C::SM], const i32x4 (&b)[C::SN]) {
-#pragma unroll
-    for (int j = 0; j < C::SN; ++j)
+  // column block j with every row block
+  __device__ __forceinline__ void mma(const i32x4 (&a)[C::SM], const i32x4 (&b)[C::SN], int j) {
 #pragma unroll
       for (int i = 0; i < C::SM; ++i) {
         if constexpr (C::INT8)
@@ -243,6 +245,19 @@ __device__ __forceinline__ void store_pair(uint16_t* row, int n0, int n_end, boo
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (n + e < n_end) row[n + e] = (uint16_t)((uint32_t)w[e >> 1] >> ((e & 1) * 16));
+  }
+}
+
+// Columns [n, n + 4) of an output row.
+__device__ __forceinline__ void store_quad(uint16_t* row, int n, int n_end, bool ok, uint32_t a0, uint32_t a1) {
+  if (!ok || n >= n_end) return;
+  if (n + 4 <= n_end && ((uintptr_t)(row + n) & 7) == 0) {
+    *(uint2*)(row + n) = make_uint2(a0, a1);
+  } else {
+    const uint32_t w[2] = {a0, a1};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < n_end) row[n + e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
   }
 }
 
@@ -347,27 +362,72 @@ __device__ __forceinline__ void store_linear(const LinearParams& p, const Linear
       if constexpr (C::E == kEpiGatedGrad)
         store_pair(row + p.half, nw + j * 16, n_end, ok, vec, lane, lo2[j], hi2[j], lo2[j + 1], hi2[j + 1]);
     }
-    static_assert(NB % 2 == 0, "output blocks are stored in pairs");
+    if constexpr (NB % 2 == 1) {  // the last block alone: 8 bytes a lane
+      store_quad(row, nw + (NB - 1) * 16 + 4 * kq, n_end, ok, lo[NB - 1], hi[NB - 1]);
+      if constexpr (C::E == kEpiGatedGrad)
+        store_quad(row + p.half, nw + (NB - 1) * 16 + 4 * kq, n_end, ok, lo2[NB - 1], hi2[NB - 1]);
+    }
   }
 }
 
-// Waits of the main loop: this wave's LDS reads and direct-to-LDS loads are
-// done, then the workgroup meets.
+// Wait until this wave's LDS reads are done and at most N of its vector
+// memory operations are outstanding (they complete in issue order), then meet
+// the other waves.
+template <int N>
 __device__ __forceinline__ void linear_sync() {
   __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// The reduction runs in 128-byte slices through two LDS stages.  A slice's
+// One half of a slice: the MFMAs on fragments (a, b), and between them the
+// reads of the next half's fragments (na, nb) from stages st_a and st_b and
+// LOAD, the loads of a later slice into ld_a and ld_b, spread evenly: issued together they would fill the memory pipe's queue and hold up
+// the MFMAs behind them.  No two of the four stages overlap here, and the
+// compiler is told so: it would otherwise wait for the loads before it reads.
+template <class C, int H, bool LOAD>
+__device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>& acc, const i32x4 (&a)[C::SM],
+                                            const i32x4 (&b)[C::SN], i32x4 (&na)[C::SM], i32x4 (&nb)[C::SN],
+                                            const FragReader<C::BM, C::TA, C::SM>& ra,
+                                            const FragReader<C::BN, C::TB, C::SN>& rb, const uint8_t* __restrict st_a,
+                                            const uint8_t* __restrict st_b, const Loader<C, true>& la,
+                                            const Loader<C, false>& lb, uint8_t* __restrict ld_a,
+                                            uint8_t* __restrict ld_b, int wave, int lane) {
+  constexpr int READS = (C::SM + C::SN + C::SN - 1) / C::SN;
+  constexpr int LOADS = LOAD ? C::LA + C::LB : 0;
+#pragma unroll
+  for (int j = 0; j < C::SN; ++j) {
+#pragma unroll
+    for (int i = j * READS; i < (j + 1) * READS && i < C::SM + C::SN; ++i) {
+      if (i < C::SM)
+        ra.read(st_a, H, lane, i, na);
+      else
+        rb.read(st_b, H, lane, i - C::SM, nb);
+    }
+#pragma unroll
+    for (int r = 0; r < LOADS; ++r) {
+      if (r * C::SN / LOADS != j) continue;
+      if (r < C::LB)
+        lb.issue(p, ld_b, r, wave, lane);
+      else
+        la.issue(p, ld_a, r - C::LB, wave, lane);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    acc.mma(a, b, j);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The reduction runs in 128-byte slices through STAGES LDS stages.  A slice's
 // fragments are read in halves, each one half ahead of the MFMAs that use it,
 // so no MFMA waits for an LDS read that was just issued; one barrier a slice
 // lies between the two halves, where every wave has read all of the current
-// stage and the next slice (loaded a whole slice earlier) has landed.  The
-// loads run two slices ahead and go on into the workgroup's next tile.
+// stage and the next slice has landed.  The loads run STAGES slices ahead
+// (into the workgroup's next tile too) and are issued in the half after the
+// barrier that frees their stage.
 template <class C>
 __global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_kernel(LinearParams p) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS_BYTES];
@@ -377,52 +437,49 @@ __global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_ke
   const int grid = gridDim.x;
   const int nk = p.nk;
 
-  int w = xcd_local_id(blockIdx.x, grid);
-  LinearWork cur = linear_work<C>(p, w);
+  LinearWork cur = linear_work<C>(p, xcd_local_id(blockIdx.x, grid));
   if (cur.w < 0) return;
-  LinearWork ld = cur;  // where the loads are: slice ld_kb of tile ld
-  int ld_kb = 0;
-  auto load_next = [&](uint8_t* stage) {
-    if (ld.w < 0) return;
-    issue_linear_slice<C>(p, ld, ld_kb, stage, wave, lane);
-    if (++ld_kb == nk) {
-      ld_kb = 0;
-      ld = linear_work<C>(p, ld.w + grid);
-    }
-  };
+  Loader<C, true> la(p, cur);
+  Loader<C, false> lb(p, cur);
 
-  const FragReader<C::BM, C::TA, C::SM> ra(0, wm * C::WM, lane);
-  const FragReader<C::BN, C::TB, C::SN> rb(C::BM * 128, wn * C::WN, lane);
+  const FragReader<C::BM, C::TA, C::SM> ra(wm * C::WM, lane);
+  const FragReader<C::BN, C::TB, C::SN> rb(wn * C::WN, lane);
   i32x4 a0[C::SM], b0[C::SN], a1[C::SM], b1[C::SN];
   LinearAcc<C> acc;
   acc.zero();
 
-  load_next(lds);
-  linear_sync();
-  load_next(lds + C::STAGE);
-  ra.read(lds, 0, lane, a0);
-  rb.read(lds, 0, lane, b0);
-  int s = 0;
+#pragma unroll
+  for (int i = 0; i < C::STAGES; ++i) {
+#pragma unroll
+    for (int j = 0; j < C::LA; ++j) la.issue(p, lds + la.dst, j, wave, lane);
+    la.advance(p, grid);
+#pragma unroll
+    for (int j = 0; j < C::LB; ++j) lb.issue(p, lds + lb.dst, j, wave, lane);
+    lb.advance(p, grid);
+  }
+  linear_sync<(C::STAGES - 1) * (C::LA + C::LB)>();
+#pragma unroll
+  for (int i = 0; i < C::SM; ++i) ra.read(lds, 0, lane, i, a0);
+#pragma unroll
+  for (int i = 0; i < C::SN; ++i) rb.read(lds + C::A_BYTES, 0, lane, i, b0);
+  int s = 0;  // stage of the current slice
   while (cur.w >= 0) {
     for (int kb = 0; kb < nk; ++kb) {
-      uint8_t* st = lds + s * C::STAGE;
-      rb.read(st, 1, lane, b1);
-      ra.read(st, 1, lane, a1);
-      __builtin_amdgcn_sched_barrier(0);
-      acc.mma(a0, b0);
-      linear_sync();
-      s ^= 1;
-      load_next(st);
-      rb.read(lds + s * C::STAGE, 0, lane, b0);
-      ra.read(lds + s * C::STAGE, 0, lane, a0);
-      __builtin_amdgcn_sched_barrier(0);
-      acc.mma(a1, b1);
-      __builtin_amdgcn_sched_barrier(0);
+      linear_half<C, 1, false>(p, acc, a0, b0, a1, b1, ra, rb, lds + s, lds + C::A_BYTES + s, la, lb, nullptr, nullptr,
+                               wave, lane);
+      linear_sync<(C::STAGES - 2) * (C::LA + C::LB)>();
+      s = s == (C::STAGES - 1) * C::STAGE ? 0 : s + C::STAGE;
+      linear_half<C, 0, true>(p, acc, a1, b1, a0, b0, ra, rb, lds + s, lds + C::A_BYTES + s, la, lb, lds + la.dst,
+                              lds + lb.dst, wave, lane);
+      lb.advance(p, grid);
+      la.advance(p, grid);
     }
     store_linear<C>(p, cur, acc, wm, wn, lane);
     acc.zero();
     cur = linear_work<C>(p, cur.w + grid);
   }
+  // no load may still be writing LDS when the workgroup ends
+  __builtin_amdgcn_s_waitcnt(0);
 }
 
 }  // namespace fg

@@ -146,18 +146,6 @@ def test_forward_nan_and_inf_stay_in_their_rows_and_units(gpu_lib, M):
     assert_within(got[np.ix_(rows, cols)], ref.gated(g, u, "silu"), ref.gated_bound(g, u, eg, eu, "silu"), "others")
 
 
-@pytest.mark.gpu
-def test_forward_without_a_workspace(gpu_lib):
-    none = torch.empty(0, dtype=torch.uint8, device="cuda")
-    for M, F, K in ((1, 260, 4096), (40, 132, 4096), (300, 150, 2048)):
-        X, W, _ = block(M, F, K, 5)
-        out = Output(M, F)
-        gpu_lib.gated_ffn_bf16(X.cuda(), W.cuda(), out.t, workspace=none)
-        out.check_untouched()
-        g, u, eg, eu = ref.pre_activations(f64(X), f64(W))
-        assert_within(out.f64(), ref.gated(g, u, "silu"), ref.gated_bound(g, u, eg, eu, "silu"), "H")
-
-
 # ---- backward -------------------------------------------------------------
 
 GRAD_SHAPES = [
@@ -309,14 +297,13 @@ def lib():
     (dict(act=-1), 1, "activation"), (dict(X=None), 1, "X is NULL"), (dict(W=Q + 8), 2, "W is not 16-byte"),
     (dict(H=None), 1, "H is NULL"), (dict(H=Q + 1), 2, "H is not"), (dict(ldx=504), 1, "ldx=504"),
     (dict(ldw=516), 2, "ldw=516"), (dict(ldh=60), 1, "ldh=60"), (dict(ldp=100), 1, "ldp=100"),
-    (dict(P=Q + 2), 2, "P is not"), (dict(ldw=(1 << 21) + 8), 3, "4 MiB"), (dict(ws=Q + 64), 2, "256-byte"),
-    (dict(wsb=100), 1, "smaller"), (dict(ws=None), 1, "workspace is NULL"),
+    (dict(P=Q + 2), 2, "P is not"), (dict(ldw=(1 << 21) + 8), 3, "4 MiB"),
 ])
 def test_forward_refusals(lib, kw, status, needle):
-    a = dict(X=Q, ldx=512, W=Q, ldw=512, H=Q, ldh=64, P=Q, ldp=128, M=64, F=64, K=512, act=0, ws=Q, wsb=1 << 24)
+    a = dict(X=Q, ldx=512, W=Q, ldw=512, H=Q, ldh=64, P=Q, ldp=128, M=64, F=64, K=512, act=0)
     a.update(kw)
     st = lib.gated_ffn_bf16(a["X"], a["ldx"], a["W"], a["ldw"], a["H"], a["ldh"], a["P"], a["ldp"], a["M"], a["F"],
-                            a["K"], a["act"], a["ws"], a["wsb"], None)
+                            a["K"], a["act"], None)
     assert st == status, lib.fg_last_error()
     assert needle in lib.fg_last_error().decode()
 
@@ -345,10 +332,10 @@ def test_backward_refusals(lib, kw, status, needle):
     (dict(K=131072, ldx=131072, ldw=131072), 3, "131056"),
 ])
 def test_int8_forward_refusals(lib, kw, status, needle):
-    a = dict(X=Q, ldx=512, sx=Q, W=Q, ldw=512, sw=Q, H=Q, ldh=64, M=64, F=64, K=512, act=0, ws=Q, wsb=1 << 24)
+    a = dict(X=Q, ldx=512, sx=Q, W=Q, ldw=512, sw=Q, H=Q, ldh=64, M=64, F=64, K=512, act=0)
     a.update(kw)
     st = lib.gated_ffn_int8(a["X"], a["ldx"], a["sx"], a["W"], a["ldw"], a["sw"], a["H"], a["ldh"], a["M"], a["F"],
-                            a["K"], a["act"], a["ws"], a["wsb"], None)
+                            a["K"], a["act"], None)
     assert st == status, lib.fg_last_error()
     assert needle in lib.fg_last_error().decode()
 

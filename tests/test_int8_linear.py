@@ -105,20 +105,6 @@ def test_gemm_matches_float64(gpu_lib, M, N, K, pads):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("M,N,K", [(1, 520, 4096), (40, 264, 8192), (300, 300, 2048)])
-def test_gemm_without_a_workspace_gives_the_same_bits(gpu_lib, M, N, K):
-    """The sums are exact integers, so a split of K cannot change a bit."""
-    A, sa = (torch.from_numpy(t).cuda() for t in codes(M, K, 3))
-    B, sb = (torch.from_numpy(t).cuda() for t in codes(N, K, 4))
-    split, whole = Output(M, N), Output(M, N)
-    gpu_lib.gemm_int8_nt(A, sa, B, sb, split.t)
-    gpu_lib.gemm_int8_nt(A, sa, B, sb, whole.t, workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
-    split.check_untouched()
-    whole.check_untouched()
-    assert torch.equal(split.t.view(torch.int16), whole.t.view(torch.int16))
-
-
-@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 33, 260])
 def test_gemm_extreme_codes_do_not_overflow(gpu_lib, M):
     """The largest sums K allows: every product 128 * 128, or of alternating sign."""
@@ -260,15 +246,14 @@ def lib():
     (dict(sa=None), 1, "sa is NULL"), (dict(sb=None), 1, "sb is NULL"), (dict(A=P + 8), 2, "A is not 16-byte"),
     (dict(B=P + 4), 2, "B is not 16-byte"), (dict(D=P + 1), 2, "D is not 2-byte"), (dict(sa=P + 2), 2, "sa is not"),
     (dict(lda=500), 1, "lda=500"), (dict(ldb=520), 2, "ldb=520"), (dict(ldd=100), 1, "ldd=100"),
-    (dict(lda=(1 << 22) + 16), 3, "4 MiB"), (dict(ws=P + 16, wsb=1 << 24), 2, "256-byte"),
-    (dict(ws=None, wsb=64), 1, "workspace is NULL"), (dict(wsb=-1), 1, "negative"), (dict(wsb=4096), 1, "smaller"),
+    (dict(lda=(1 << 22) + 16), 3, "4 MiB"),
     (dict(M=(1 << 30) + 1), 3, "2^30"),
 ])
 def test_gemm_refusals(lib, kw, status, needle):
-    a = dict(A=P, lda=512, sa=P, B=P, ldb=512, sb=P, D=P, ldd=256, M=64, N=256, K=512, ws=P, wsb=1 << 24)
+    a = dict(A=P, lda=512, sa=P, B=P, ldb=512, sb=P, D=P, ldd=256, M=64, N=256, K=512)
     a.update(kw)
     st = lib.gemm_int8_nt(a["A"], a["lda"], a["sa"], a["B"], a["ldb"], a["sb"], a["D"], a["ldd"], a["M"], a["N"],
-                          a["K"], a["ws"], a["wsb"], None)
+                          a["K"], None)
     assert st == status, lib.fg_last_error()
     assert needle in lib.fg_last_error().decode()
 
@@ -287,8 +272,8 @@ def test_cast_refusals(lib, kw, status, needle):
 
 
 def test_empty_calls_need_no_pointers(lib):
-    assert lib.gemm_int8_nt(None, 0, None, None, 0, None, None, 0, 0, 256, 512, None, 0, None) == 0
-    assert lib.gemm_int8_nt(None, 0, None, None, 0, None, None, 0, 64, 0, 512, None, 0, None) == 0
+    assert lib.gemm_int8_nt(None, 0, None, None, 0, None, None, 0, 0, 256, 512, None) == 0
+    assert lib.gemm_int8_nt(None, 0, None, None, 0, None, None, 0, 64, 0, 512, None) == 0
     assert lib.int8_cast_per_row(None, 0, None, None, 0, 512, None) == 0
 
 
@@ -320,5 +305,3 @@ def test_wrappers_reject_shapes_and_strides(gpu_lib):
                 lambda: gpu_lib.gemm_int8_nt(q, s.double(), q, s, d)):
         with pytest.raises(TypeError):
             bad()
-    with pytest.raises(gpu_lib.FP8GemmError, match="smaller"):
-        gpu_lib.gemm_int8_nt(q, s, q, s, d, workspace=torch.zeros(4096, dtype=torch.uint8, device="cuda"))
