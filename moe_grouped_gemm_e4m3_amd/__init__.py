@@ -641,23 +641,38 @@ def fp8_cast_per_block_ue8m0(w, q=None, sb=None, stream=None):
 ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
 
 
-def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int) -> int:
-    """Row stride of a [rows, cols] CUDA matrix of `dtype` with contiguous rows."""
-    if t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a {str(dtype)[6:]} CUDA tensor")
+# The wrappers below are called where a kernel takes a few microseconds, so
+# their checks are kept to a few attribute reads per tensor.
+
+
+def _device() -> int:
+    """The current device; every tensor of a call must be on it."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+
+
+def _matrix(t: torch.Tensor, name: str, dtype: torch.dtype, rows: int, cols: int, dev: int) -> int:
+    """Row stride of a [rows, cols] matrix of `dtype` on device `dev` with contiguous rows."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {str(dtype)[6:]} tensor on the current CUDA device, got {t.dtype} on {t.device}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have unit stride in its last dimension")
-    return t.stride(0) if rows > 1 else max(cols, 1)
+    return ld if rows > 1 else max(cols, 1)  # a single row's stride is arbitrary in torch
 
 
-def _row_scales(t: torch.Tensor, name: str, rows: int) -> int:
-    if t.dtype != torch.float32 or not t.is_cuda:
-        raise TypeError(f"{name} must be a float32 CUDA tensor")
+def _row_scales(t: torch.Tensor, name: str, rows: int, dev: int) -> int:
+    if t.dtype is not torch.float32 or t.get_device() != dev:
+        raise TypeError(f"{name} must be a float32 tensor on the current CUDA device, got {t.dtype} on {t.device}")
     if t.shape != (rows,) or (rows > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous [{rows}] vector, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The HIP stream of a call (None: torch's current one)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _activation(name: str) -> int:
@@ -665,14 +680,6 @@ def _activation(name: str) -> int:
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {name!r}")
     return act
-
-
-def _one_device(*ts):
-    """All tensors of a call (None skipped) lie on the current device, where its kernels run."""
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, the current device is {dev}")
 
 
 def _on_stream(stream):
@@ -699,17 +706,17 @@ def int8_cast_per_row(x, q=None, s=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
     M, K = x.shape
-    bf16 = x.dtype == torch.bfloat16
-    ldx = _matrix(x, "x", torch.bfloat16 if bf16 else torch.float32, M, K)
+    dev = _device()
+    bf16 = x.dtype is torch.bfloat16
+    ldx = _matrix(x, "x", torch.bfloat16 if bf16 else torch.float32, M, K, dev)
     if q is None or s is None:
         with _on_stream(stream):
             q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else q
             s = torch.empty(M, dtype=torch.float32, device=x.device) if s is None else s
-    if _matrix(q, "q", torch.int8, M, K) != K and M > 1:
+    if _matrix(q, "q", torch.int8, M, K, dev) != K and M > 1:
         raise ValueError("q must be contiguous")
-    _one_device(x, q, s)
     _call("int8_cast_per_row_bf16" if bf16 else "int8_cast_per_row", x.data_ptr(), ldx, q.data_ptr(),
-          _row_scales(s, "s", M), M, K, _stream(stream))
+          _row_scales(s, "s", M, dev), M, K, _raw_stream(stream, dev))
     return q, s
 
 
@@ -720,11 +727,11 @@ def gemm_int8_nt(A, sa, B, sb, D, stream=None):
         raise ValueError("A and B must be matrices")
     M, K = A.shape
     N = B.shape[0]
-    lda, ldb = _matrix(A, "A", torch.int8, M, K), _matrix(B, "B", torch.int8, N, K)
-    ldd = _matrix(D, "D", torch.bfloat16, M, N)
-    _one_device(D, A, sa, B, sb)
-    _call("gemm_int8_nt", A.data_ptr(), lda, _row_scales(sa, "sa", M), B.data_ptr(), ldb, _row_scales(sb, "sb", N),
-          D.data_ptr(), ldd, M, N, K, _stream(stream))
+    dev = _device()
+    lda, ldb = _matrix(A, "A", torch.int8, M, K, dev), _matrix(B, "B", torch.int8, N, K, dev)
+    ldd = _matrix(D, "D", torch.bfloat16, M, N, dev)
+    _call("gemm_int8_nt", A.data_ptr(), lda, _row_scales(sa, "sa", M, dev), B.data_ptr(), ldb,
+          _row_scales(sb, "sb", N, dev), D.data_ptr(), ldd, M, N, K, _raw_stream(stream, dev))
     return D
 
 
@@ -736,11 +743,12 @@ def gated_ffn_int8(X, sx, W, sw, H, activation="silu", stream=None):
         raise ValueError("X and H must be matrices")
     M, K = X.shape
     F = H.shape[1]
-    ldx, ldw = _matrix(X, "X", torch.int8, M, K), _matrix(W, "W", torch.int8, 2 * F, K)
-    ldh = _matrix(H, "H", torch.bfloat16, M, F)
-    _one_device(H, X, sx, W, sw)
-    _call("gated_ffn_int8", X.data_ptr(), ldx, _row_scales(sx, "sx", M), W.data_ptr(), ldw,
-          _row_scales(sw, "sw", 2 * F), H.data_ptr(), ldh, M, F, K, _activation(activation), _stream(stream))
+    dev = _device()
+    ldx, ldw = _matrix(X, "X", torch.int8, M, K, dev), _matrix(W, "W", torch.int8, 2 * F, K, dev)
+    ldh = _matrix(H, "H", torch.bfloat16, M, F, dev)
+    _call("gated_ffn_int8", X.data_ptr(), ldx, _row_scales(sx, "sx", M, dev), W.data_ptr(), ldw,
+          _row_scales(sw, "sw", 2 * F, dev), H.data_ptr(), ldh, M, F, K, _activation(activation),
+          _raw_stream(stream, dev))
     return H
 
 
@@ -753,12 +761,12 @@ def gated_ffn_bf16(X, W, H, P=None, activation="silu", stream=None):
         raise ValueError("X and H must be matrices")
     M, K = X.shape
     F = H.shape[1]
-    bf16 = torch.bfloat16
-    ldx, ldw, ldh = _matrix(X, "X", bf16, M, K), _matrix(W, "W", bf16, 2 * F, K), _matrix(H, "H", bf16, M, F)
-    ldp = 0 if P is None else _matrix(P, "P", torch.float32, M, 2 * F)
-    _one_device(H, X, W, P)
+    bf16, dev = torch.bfloat16, _device()
+    ldx, ldw = _matrix(X, "X", bf16, M, K, dev), _matrix(W, "W", bf16, 2 * F, K, dev)
+    ldh = _matrix(H, "H", bf16, M, F, dev)
+    ldp = 0 if P is None else _matrix(P, "P", torch.float32, M, 2 * F, dev)
     _call("gated_ffn_bf16", X.data_ptr(), ldx, W.data_ptr(), ldw, H.data_ptr(), ldh, _ptr(P), ldp, M, F, K,
-          _activation(activation), _stream(stream))
+          _activation(activation), _raw_stream(stream, dev))
     return H
 
 
@@ -780,19 +788,19 @@ def gated_ffn_bf16_backward(dH, X, W, dX, dW, P=None, activation="silu", stream=
         raise ValueError("X and dH must be matrices")
     M, K = X.shape
     F = dH.shape[1]
-    bf16 = torch.bfloat16
-    lddh, ldx, ldw = _matrix(dH, "dH", bf16, M, F), _matrix(X, "X", bf16, M, K), _matrix(W, "W", bf16, 2 * F, K)
-    ldp = 0 if P is None else _matrix(P, "P", torch.float32, M, 2 * F)
-    lddx = 0 if dX is None else _matrix(dX, "dX", bf16, M, K)
-    lddw = 0 if dW is None else _matrix(dW, "dW", bf16, 2 * F, K)
-    _one_device(dH, X, W, P, dX, dW, workspace)
+    bf16, dev = torch.bfloat16, _device()
+    lddh, ldx = _matrix(dH, "dH", bf16, M, F, dev), _matrix(X, "X", bf16, M, K, dev)
+    ldw = _matrix(W, "W", bf16, 2 * F, K, dev)
+    ldp = 0 if P is None else _matrix(P, "P", torch.float32, M, 2 * F, dev)
+    lddx = 0 if dX is None else _matrix(dX, "dX", bf16, M, K, dev)
+    lddw = 0 if dW is None else _matrix(dW, "dW", bf16, 2 * F, K, dev)
     act = _activation(activation)
     if workspace is None:
         with _on_stream(stream):
             workspace = torch.empty(gated_ffn_backward_workspace_bytes(M, F), dtype=torch.uint8, device=dH.device)
     ws, ws_bytes = _byte_workspace(workspace)
     _call("gated_ffn_bf16_backward", dH.data_ptr(), lddh, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(P), ldp,
-          _ptr(dX), lddx, _ptr(dW), lddw, M, F, K, act, ws, ws_bytes, _stream(stream))
+          _ptr(dX), lddx, _ptr(dW), lddw, M, F, K, act, ws, ws_bytes, _raw_stream(stream, dev))
     return dX, dW
 
 

@@ -187,8 +187,16 @@ fg_status cast_rows(const T* x, int64_t ldx, int8_t* q, float* s, int M, int K, 
   FG_TRY(require_ptr(q, 16, "q"));
   FG_TRY(require_ptr(s, 4, "s"));
   FG_TRY(require_ld(ldx, K, 16 / (int)sizeof(T), "ldx"));
-  hipLaunchKernelGGL((int8_cast_kernel<T>), dim3((unsigned)(M < (1 << 20) ? M : 1 << 20)), dim3(256), 0,
-                     (hipStream_t)stream, x, ldx, q, s, M, K);
+  const int pieces = K / (16 / (int)sizeof(T));
+  const dim3 grid((unsigned)std::min(M, 1 << 20));
+  // Two pieces a thread while they hold the row (4096 x 7168 bf16: 512 threads
+  // 15.0 us, 5.9 TB/s; 4096 x 1024: 256 threads 5.7 us), four of a longer one.
+  if (pieces <= 512)
+    hipLaunchKernelGGL((int8_cast_kernel<T, 256, 2>), grid, dim3(256), 0, (hipStream_t)stream, x, ldx, q, s, M, K);
+  else if (pieces <= 1024)
+    hipLaunchKernelGGL((int8_cast_kernel<T, 512, 2>), grid, dim3(512), 0, (hipStream_t)stream, x, ldx, q, s, M, K);
+  else
+    hipLaunchKernelGGL((int8_cast_kernel<T, 512, 4>), grid, dim3(512), 0, (hipStream_t)stream, x, ldx, q, s, M, K);
   return launched(what);
 }
 
@@ -316,8 +324,9 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
     g.D = (uint16_t*)workspace; g.ldd = pair_ld;
     g.M = M; g.N = F; g.K = K;
     if (P) {
-      hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)((g.half + 255) / 256), (unsigned)(M < 65535 ? M : 65535)),
-                         dim3(256), 0, (hipStream_t)stream, g);
+      const int64_t blocks = ((int64_t)M * (g.half / 8) + 255) / 256;
+      hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16)), dim3(256), 0,
+                         (hipStream_t)stream, g);
       FG_TRY(launched(what));
     } else {
       FG_TRY((launch_linear<kEpiGatedGrad>(g, stream, what)));

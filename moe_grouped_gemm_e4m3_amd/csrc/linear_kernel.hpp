@@ -89,39 +89,155 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16x2(v, 0.f) & 0xffff); }
 
-// [dg du] from the kept pre-activations P = [g u], one element a thread.
+// [dg du] from the kept pre-activations P = [g u], eight columns a thread.
+// Bound by HBM: 10 bytes in and 4 out for each hidden unit and row.
 static __global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p) {
-  const int n = blockIdx.x * 256 + threadIdx.x;
-  if (n >= p.half) return;
-  for (int m = blockIdx.y; m < p.M; m += gridDim.y) {
-    float dg = 0.f, du = 0.f;
-    if (n < p.N) {
-      const float* prow = p.P + (int64_t)m * p.ldp;
-      gated_grad(to_f32(p.dH[(int64_t)m * p.lddh + n]), prow[n], prow[p.N + n], p.act, dg, du);
+  const int per_row = p.half / 8;
+  const int64_t total = (int64_t)p.M * per_row;
+  const bool vec = (p.N & 3) == 0 && (p.ldp & 3) == 0 && ((uintptr_t)p.P & 15) == 0 && (p.lddh & 7) == 0 &&
+                   ((uintptr_t)p.dH & 15) == 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / per_row;
+    const int n = (int)(i - m * per_row) * 8;
+    const float* gp = p.P + m * p.ldp + n;
+    const float* up = gp + p.N;
+    const uint16_t* hp = p.dH + m * p.lddh + n;
+    float g[8], u[8], h[8];
+    if (vec && n + 8 <= p.N) {
+      const f32x4 g0 = *(const f32x4*)gp, g1 = *(const f32x4*)(gp + 4);
+      const f32x4 u0 = *(const f32x4*)up, u1 = *(const f32x4*)(up + 4);
+      const uint4 hv = *(const uint4*)hp;
+      const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        g[r] = g0[r];
+        g[4 + r] = g1[r];
+        u[r] = u0[r];
+        u[4 + r] = u1[r];
+        h[2 * r] = __uint_as_float(hw[r] << 16);
+        h[2 * r + 1] = __uint_as_float(hw[r] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const bool in = n + r < p.N;  // padding columns hold zeros
+        g[r] = in ? gp[r] : 0.f;
+        u[r] = in ? up[r] : 0.f;
+        h[r] = in ? to_f32(hp[r]) : 0.f;
+      }
     }
-    p.D[(int64_t)m * p.ldd + n] = bf16_bits(dg);
-    p.D[(int64_t)m * p.ldd + p.half + n] = bf16_bits(du);
+    uint32_t dg[4], du[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float a0, b0, a1, b1;
+      gated_grad(h[2 * r], g[2 * r], u[2 * r], p.act, a0, b0);
+      gated_grad(h[2 * r + 1], g[2 * r + 1], u[2 * r + 1], p.act, a1, b1);
+      dg[r] = pack_bf16x2(a0, a1);
+      du[r] = pack_bf16x2(b0, b1);
+    }
+    uint16_t* dst = p.D + m * p.ldd + n;
+    *(uint4*)dst = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+    *(uint4*)(dst + p.half) = make_uint4(du[0], du[1], du[2], du[3]);
+  }
+}
+
+// The 16-byte piece of a row at src as fp32 values.
+__device__ __forceinline__ void widen(const uint4& u, float (&x)[4], const float*) {
+  x[0] = __uint_as_float(u.x);
+  x[1] = __uint_as_float(u.y);
+  x[2] = __uint_as_float(u.z);
+  x[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void widen(const uint4& u, float (&x)[8], const uint16_t*) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// rint(x / s) of V values, packed into bytes.  x * (1 / s) differs from the
+// rounded quotient by less than 127 * 3 * 2^-24 < 3e-5, so both round to the
+// same integer unless the product lies that close to a half; only then are
+// the values divided (about 1 piece in 600; a division is some ten
+// instructions, and with one for every value the cast is not bound by HBM).
+template <int V>
+__device__ __forceinline__ void int8_codes(const float (&x)[V], float s, float inv, uint32_t (&out)[V / 4]) {
+  float q[V], far = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float t = x[i] * inv;
+    q[i] = __builtin_rintf(t);
+    far = fmaxf(far, fabsf(t - q[i]));
+  }
+  if (far > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = __builtin_rintf(x[i] / s);
+  }
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    out[i] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[i] |= ((uint32_t)(int)q[4 * i + j] & 0xffu) << (8 * j);
   }
 }
 
 // int8 codes and scale of each row: s = max(amax, 1e-4) / 127, q = rint(x / s).
-template <typename T>
-__global__ __launch_bounds__(256) void int8_cast_kernel(const T* x, int64_t ldx, int8_t* q, float* s, int M, int K) {
-  __shared__ float red[4];
+// One workgroup a row.  The first PIECES 16-byte pieces of each thread stay in
+// registers between the two passes, so a row of up to PIECES * THREADS * 16
+// bytes is read once; of a longer row the rest is read again.
+template <typename T, int THREADS, int PIECES>
+__global__ __launch_bounds__(THREADS) void int8_cast_kernel(const T* __restrict__ x, int64_t ldx,
+                                                            int8_t* __restrict__ q, float* __restrict__ s, int M,
+                                                            int K) {
+  constexpr int V = 16 / sizeof(T), WAVES = THREADS / 64;
+  __shared__ float red[WAVES];
+  const int tid = threadIdx.x, pieces = K / V;
   for (int m = blockIdx.x; m < M; m += gridDim.x) {
-    const T* row = x + (int64_t)m * ldx;
+    const uint4* row = (const uint4*)(x + (int64_t)m * ldx);
+    uint4 v[PIECES];
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) {
+      const int i = tid + j * THREADS;
+      v[j] = i < pieces ? row[i] : make_uint4(0, 0, 0, 0);
+    }
     float amax = 0.f;
-    for (int k = threadIdx.x; k < K; k += 256) amax = fmaxf(amax, fabsf(to_f32(row[k])));
+    auto take = [&](const uint4& u) {
+      float f[V];
+      widen(u, f, (const T*)nullptr);
+#pragma unroll
+      for (int i = 0; i < V; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    };
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) take(v[j]);
+    for (int i = tid + PIECES * THREADS; i < pieces; i += THREADS) take(row[i]);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor(amax, o, 64));
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
+    if ((tid & 63) == 0) red[tid >> 6] = amax;
     __syncthreads();
-    amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float sc = fmaxf(amax, 1e-4f) / 127.0f;
-    if (threadIdx.x == 0) s[m] = sc;
-    for (int k = threadIdx.x; k < K; k += 256)
-      q[(int64_t)m * K + k] = (int8_t)(int)__builtin_rintf(to_f32(row[k]) / sc);
-    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) amax = fmaxf(amax, red[w]);
+    const float sc = fmaxf(amax, 1e-4f) / 127.0f, inv = 1.0f / sc;
+    if (tid == 0) s[m] = sc;
+    uint32_t* dst = (uint32_t*)(q + (int64_t)m * K);
+    auto put = [&](const uint4& u, int i) {
+      float f[V];
+      uint32_t c[V / 4];
+      widen(u, f, (const T*)nullptr);
+      int8_codes<V>(f, sc, inv, c);
+      if constexpr (V == 8)
+        *(uint2*)(dst + 2 * i) = make_uint2(c[0], c[1]);
+      else
+        dst[i] = c[0];
+    };
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j) {
+      const int i = tid + j * THREADS;
+      if (i < pieces) put(v[j], i);
+    }
+    for (int i = tid + PIECES * THREADS; i < pieces; i += THREADS) put(row[i], i);
+    __syncthreads();  // red is free again
   }
 }
 

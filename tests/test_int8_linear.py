@@ -67,6 +67,25 @@ def test_cast_ties_go_to_even(gpu_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_cast_near_ties(gpu_lib, dtype):
+    """Values a few units in the last place around every half step of many
+    scales: the rounding is that of the fp32 quotient, exactly."""
+    rows, K = 400, 512
+    gen = torch.Generator().manual_seed(0)
+    amax = (torch.rand(rows, generator=gen) * 4 + 0.01).to(dtype).float()
+    half = torch.arange(K) % 254 - 126.5
+    x = half[None, :] * (amax / 127)[:, None]
+    ulps = torch.randint(-3, 4, (rows, K), generator=gen, dtype=torch.int32)
+    x = (x.view(torch.int32) + ulps).view(torch.float32)
+    x = x.to(dtype).float().clamp(-amax[:, None], amax[:, None])
+    x[:, 7] = amax
+    q, s = gpu_lib.int8_cast_per_row(x.to(dtype).cuda())
+    want_q, want_s = ref.int8_cast(x.numpy())
+    assert np.array_equal(s.cpu().numpy(), want_s) and np.array_equal(q.cpu().numpy(), want_q)
+
+
+@pytest.mark.gpu
 def test_cast_writes_only_its_outputs(gpu_lib):
     x = torch.randn(3, 48, device="cuda")
     q = torch.full((4, 48), 99, dtype=torch.int8, device="cuda")
