@@ -446,16 +446,15 @@ fg_status fp8_cast_per_block_ue8m0_bf16(const uint16_t* w, int64_t ldw, uint8_t*
  * signed bytes with an fp32 scale per row (a token of the activations, an
  * output channel of the weights), or BF16.  All matrices are row-major with
  * their last dimension contiguous.
- * These calls split no reduction over workgroups and need no workspace, but
- * for the backward pass's intermediate.  Their plans depend only on the
+ * Only the backward pass needs a workspace.  Their plans depend only on the
  * arguments, the device and the CU cap, and sums have a fixed order, so
  * results are reproducible.
  */
 
 /*
  * Cast of each row to signed bytes, for either operand of gemm_int8_nt:
- *     s[m] = max(max_k |x[m, k]|, 1e-4f) / 127     (fp32, correctly rounded)
- *     q    = rint(x / s[m])                        (fp32 division, nearest-even; |q| <= 127)
+ *     s[m] = max(max_k |x[m, k]|, 1e-4f) * (1.0f / 127.0f)    (fp32)
+ *     q    = rint(x / s[m])                                   (fp32 division, nearest-even; |q| <= 127)
  *   x   device fp32 (or bf16) [M, K], row stride ldx elements (ldx >= K, 16-byte aligned rows)
  *   q   device [M, K], packed, 16-byte aligned
  *   s   device fp32 [M]
@@ -506,8 +505,9 @@ fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
  *   P   the forward call's pre-activations [g u], or NULL: they are recomputed from X and W
  *   dX  device [M, K] bf16, row stride lddx, or NULL (not wanted)
  *   dW  device [2F, K] bf16, row stride lddw, or NULL (not wanted)
- *   workspace  device, 256-byte aligned, fg_gated_ffn_backward_workspace_bytes(M, F) bytes; holds
- *       [dg du] in bf16 and needs no initialisation; in use until the call's work has finished
+ *   workspace  device, 256-byte aligned, fg_gated_ffn_backward_workspace_bytes(M, F, K) bytes; holds
+ *       [dg du] in bf16 and, where dX is small, fp32 partials of its sum over 2F; needs no
+ *       initialisation; in use until the call's work has finished
  * dX and dW accumulate in fp32 over the bf16 pair [dg du].  M == 0 writes
  * dW = 0, F == 0 writes dX = 0.  F <= 2^20.  Outputs may not overlap inputs.
  */
@@ -517,7 +517,7 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of gated_ffn_bf16_backward; -1 for sizes it rejects. */
-int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F);
+int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F, int K);
 
 /*
  * The gated block on 8-bit integers (serving):

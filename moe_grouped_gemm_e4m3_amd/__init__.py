@@ -102,7 +102,7 @@ _SIGNATURES = {
     "gated_ffn_bf16": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P]),
     "gated_ffn_bf16_backward": (
         _I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
-    "fg_gated_ffn_backward_workspace_bytes": (_I64, [_I, _I]),
+    "fg_gated_ffn_backward_workspace_bytes": (_I64, [_I, _I, _I]),
     "gated_ffn_int8": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _P]),
     "fg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "fg_set_num_cus": (None, [_I]),
@@ -701,7 +701,7 @@ def _byte_workspace(workspace: torch.Tensor):
 
 def int8_cast_per_row(x, q=None, s=None, stream=None):
     """Signed 8-bit codes and one scale for each row of fp32 or bf16 x [M, K]:
-    s[m] = max(max |x[m]|, 1e-4) / 127, q = rint(x / s).  A row is a token of
+    s[m] = max(max |x[m]|, 1e-4) * (1 / 127) in fp32, q = rint(x / s).  A row is a token of
     activations or an output channel of weights.  -> (q int8 [M, K], s fp32 [M])."""
     if x.dim() != 2:
         raise ValueError("x must be [M, K]")
@@ -770,11 +770,11 @@ def gated_ffn_bf16(X, W, H, P=None, activation="silu", stream=None):
     return H
 
 
-def gated_ffn_backward_workspace_bytes(M: int, F: int) -> int:
+def gated_ffn_backward_workspace_bytes(M: int, F: int, K: int) -> int:
     """Device workspace bytes gated_ffn_bf16_backward needs."""
-    n = load_library().fg_gated_ffn_backward_workspace_bytes(M, F)
+    n = load_library().fg_gated_ffn_backward_workspace_bytes(M, F, K)
     if n < 0:
-        raise ValueError(f"sizes {(M, F)} not accepted")
+        raise ValueError(f"sizes {(M, F, K)} not accepted")
     return n
 
 
@@ -797,7 +797,7 @@ def gated_ffn_bf16_backward(dH, X, W, dX, dW, P=None, activation="silu", stream=
     act = _activation(activation)
     if workspace is None:
         with _on_stream(stream):
-            workspace = torch.empty(gated_ffn_backward_workspace_bytes(M, F), dtype=torch.uint8, device=dH.device)
+            workspace = torch.empty(gated_ffn_backward_workspace_bytes(M, F, K), dtype=torch.uint8, device=dH.device)
     ws, ws_bytes = _byte_workspace(workspace)
     _call("gated_ffn_bf16_backward", dH.data_ptr(), lddh, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(P), ldp,
           _ptr(dX), lddx, _ptr(dW), lddw, M, F, K, act, ws, ws_bytes, _raw_stream(stream, dev))

@@ -38,12 +38,12 @@ fg_status launched(const char* what) {
 // and the cheapest runs.  The estimates only rank candidates.
 
 template <class C>
-fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, const char* what) {
+fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, const char* what, int splits = 1) {
   const int64_t tm = ((int64_t)p.M + C::BM - 1) / C::BM, tn = (cols + C::OUT_N - 1) / C::OUT_N;
-  if (tm * tn >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
+  if (tm * tn * splits >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
   p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
-  p.num_tiles = (int)(tm * tn);
+  p.num_tiles = (int)(tm * tn) * splits;
   p.group_m = 8;
   const int grid = std::min(cus * C::OCC, p.num_tiles);
   hipLaunchKernelGGL((linear_tile_kernel<C>), dim3((unsigned)grid), dim3(C::THREADS), 0, (hipStream_t)stream, p);
@@ -57,10 +57,10 @@ double tile_count(const LinearParams& p, int64_t cols, bool gated, int bm, int b
 }
 
 // One tile per CU and round: `idle` a slice with few CUs at work, `busy` with
-// all of them (clock and cache contention).
-double tile_us(double tiles, int cus, int nk, double idle, double busy) {
+// all of them (clock and cache contention), `store` for the epilogue.
+double tile_us(double tiles, int cus, int nk, double idle, double busy, double store) {
   const double load = tiles < cus ? tiles / cus : 1.0;
-  return 3.0 + ceil(tiles / cus) * (nk * (idle + (busy - idle) * load) + 1.5);
+  return 3.0 + ceil(tiles / cus) * (nk * (idle + (busy - idle) * load) + store);
 }
 
 // Two workgroups per CU: a round that leaves one workgroup per CU is cheaper.
@@ -86,6 +86,38 @@ double fewrow_us(const LinearParams& p, bool gated, int cus, int mf, int cf) {
   return 1.0 + ceil(groups / cus) * (2.0 + bytes / 80e3);
 }
 
+// Splits of the reduction over workgroups (dX alone: its reduction is the
+// long axis 2 F).  The fp32 partials of at most kMaxSplits splits and
+// kMaxPartialBytes go to the workspace and a second launch adds them.
+constexpr int kMaxSplits = 16;
+constexpr int64_t kMaxPartialBytes = (int64_t)32 << 20;
+
+// Workspace bytes for the partials of an M x N output: none where fewer than
+// two fit.
+int64_t partial_bytes(int64_t M, int64_t N) {
+  const int64_t one = M * N * 4;
+  if (2 * one > kMaxPartialBytes) return 0;
+  return round_up(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one) * one, 256);
+}
+
+struct SplitPlan {
+  double us;
+  int splits, nk;  // slices of a split (even)
+};
+
+SplitPlan plan_split(const LinearParams& p, int cus, int bm, int bn, double idle, double busy) {
+  const double tiles = tile_count(p, p.N, false, bm, bn);
+  const int64_t one = (int64_t)p.M * p.N * 4;
+  const int most = (int)std::min<int64_t>(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one), (int64_t)(cus / tiles));
+  SplitPlan s{1e30, 1, p.nk};
+  if (2 * one > kMaxPartialBytes || most < 2) return s;
+  s.nk = (int)round_up((p.nk + most - 1) / most, 2);
+  s.splits = (p.nk + s.nk - 1) / s.nk;
+  // the partials are written and read at about 4 TB/s; the second launch is 4 us
+  s.us = tile_us(tiles * s.splits, cus, s.nk, idle, busy, 1.5) + 4.0 + 2.0 * s.splits * one / 4e6;
+  return s;
+}
+
 template <int E, bool TA = false, bool TB = false>
 fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
   int cus = 0;
@@ -93,17 +125,25 @@ fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
   constexpr bool gated = epi_gated(E);
   const int64_t cols = E == kEpiGatedGrad ? p.half : p.N;
   p.nk = (int)std::max<int64_t>(1, ((int64_t)p.K * (epi_int8(E) ? 1 : 2) + 127) / 128);
-  // 256 x 256: 1.2 us a slice alone, 1.7 with every CU at work (4096 x 4096 x
-  // 7168 int8 95 us).  128 x 128, two workgroups of four waves: 0.66 alone,
-  // 1.0 for both (112 us on that shape); one of eight waves with four stages:
-  // 0.48 and 0.58 (34 us on 1000 x 4096 x 7168, 71 on 256 x 256 tiles).
-  // 64 x 64 with eight stages: 0.33 (20 us on 256 x 4096 x 7168, 27 on
-  // 128 x 128 tiles).
-  const double big = tile_us(tile_count(p, cols, gated, 256, 256), cus, p.nk, 1.2, 1.7);
-  const double mid2 = tile2_us(tile_count(p, cols, gated, 128, 128), cus, p.nk, 0.66, 1.0);
-  const double mid = tile_us(tile_count(p, cols, gated, 128, 128), cus, p.nk, 0.48, 0.58);
-  const double small = tile_us(tile_count(p, cols, gated, 64, 64), cus, p.nk, 0.33, 0.33);
-  const double tile = std::min(std::min(big, mid2), std::min(mid, small));
+  // 256 rows by 256, 224, 192 or 160: 1.2, 1.1, 1.0 and 0.92 us a slice with
+  // few CUs at work, 1.45, 1.36, 1.15 and 1.02 with all, which the chip's power
+  // limits (int8 4096 x 7168 x 16384: 380 us with 256 columns, 364 with 224;
+  // 4096 x 2112 x 7168: 80 with 256, 63 with 160).  128 x 128, two workgroups
+  // of four waves: 0.66 alone, 1.0 for both (112 us on 4096 x 4096 x 7168, 92
+  // on 256 x 256); one of eight waves with four stages: 0.48 and 0.58 (34 us
+  // on 1000 x 4096 x 7168, 71 on 256 x 256).  64 x 64 with eight waves in two
+  // groups: 0.22 (16 us on 256 x 4096 x 7168, 27 on 128 x 128), 0.34 where
+  // operands are MN-major.
+  auto count = [&](int bm, int bn) { return tile_count(p, cols, gated, bm, bn); };
+  const double w256 = tile_us(count(256, 256), cus, p.nk, 1.2, 1.45, 4.0);
+  const double w224 = gated ? 1e30 : tile_us(count(256, 224), cus, p.nk, 1.1, 1.36, 4.0);
+  const double w192 = gated ? tile_us(count(256, 192), cus, p.nk, 1.0, 1.15, 4.0) : 1e30;
+  const double w160 = gated ? 1e30 : tile_us(count(256, 160), cus, p.nk, 0.92, 1.02, 3.5);
+  const double mid2 = tile2_us(count(128, 128), cus, p.nk, 0.66, 1.0);
+  const double mid = tile_us(count(128, 128), cus, p.nk, 0.48, 0.58, 1.5);
+  const double small_slice = TA || TB ? 0.34 : 0.22;
+  const double small = tile_us(count(64, 64), cus, p.nk, small_slice, small_slice, 1.5);
+  const double tile = std::min({w256, w224, w192, w160, mid2, mid, small});
   if constexpr (!TA && !TB && E != kEpiGatedGrad) {
     if (p.M <= 256) {
       static const int shapes[][2] = {{1, 1}, {1, 2}, {2, 1}, {2, 2}, {4, 1}, {4, 2}, {4, 4}};
@@ -132,10 +172,33 @@ fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
       }
     }
   }
-  if (tile == big) return launch_tile<LinearTile<E, 256, 256, 4, 2, 2, TA, TB>>(p, cus, cols, stream, what);
-  if (tile == mid2) return launch_tile<LinearTile<E, 128, 128, 2, 2, 2, TA, TB>>(p, cus, cols, stream, what);
-  if (tile == mid) return launch_tile<LinearTile<E, 128, 128, 4, 2, 4, TA, TB>>(p, cus, cols, stream, what);
-  return launch_tile<LinearTile<E, 64, 64, 2, 2, 8, TA, TB>>(p, cus, cols, stream, what);
+  if constexpr (E == kEpiBf16 && TB && !TA) {
+    // 251 x 1016 with 178 slices: 60 us on 64 64 x 64 tiles, a quarter of the
+    // device; split four ways 25 us with the addition.
+    const SplitPlan a = plan_split(p, cus, 64, 64, 0.34, 0.34), b = plan_split(p, cus, 128, 128, 0.5, 0.6);
+    const SplitPlan& s = a.us <= b.us ? a : b;
+    if (p.P && s.us < tile) {
+      p.split_nk = s.nk;
+      if (a.us <= b.us)
+        FG_TRY((launch_tile<LinearTile<kEpiPartial, 64, 64, 2, 2, 2, 4, TA, TB>>(p, cus, cols, stream, what, s.splits)));
+      else
+        FG_TRY((launch_tile<LinearTile<kEpiPartial, 128, 128, 4, 2, 1, 4, TA, TB>>(p, cus, cols, stream, what, s.splits)));
+      const int64_t blocks = ((int64_t)p.M * (p.N / 4) + 255) / 256;
+      hipLaunchKernelGGL(add_partials_kernel, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16)), dim3(256), 0,
+                         (hipStream_t)stream, p, s.splits);
+      return launched(what);
+    }
+  }
+  if (tile == w256) return launch_tile<LinearTile<E, 256, 256, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+  if constexpr (gated) {
+    if (tile == w192) return launch_tile<LinearTile<E, 256, 192, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+  } else {
+    if (tile == w224) return launch_tile<LinearTile<E, 256, 224, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+    if (tile == w160) return launch_tile<LinearTile<E, 256, 160, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+  }
+  if (tile == mid2) return launch_tile<LinearTile<E, 128, 128, 2, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+  if (tile == mid) return launch_tile<LinearTile<E, 128, 128, 4, 2, 1, 4, TA, TB>>(p, cus, cols, stream, what);
+  return launch_tile<LinearTile<E, 64, 64, 2, 2, 2, 4, TA, TB>>(p, cus, cols, stream, what);
 }
 
 // Sizes every entry point shares; *empty when there is no output element.
@@ -175,7 +238,9 @@ fg_status check_activation(int act) {
 
 int64_t pair_cols(int F) { return 2 * round_up(F, kPairAlign); }
 
-int64_t backward_bytes(int M, int F) { return round_up((int64_t)M * pair_cols(F) * 2, 256); }
+// The gradient pair, then dX's partials.
+int64_t pair_bytes(int M, int F) { return round_up((int64_t)M * pair_cols(F) * 2, 256); }
+int64_t backward_bytes(int M, int F, int K) { return pair_bytes(M, F) + partial_bytes(M, K); }
 
 template <typename T>
 fg_status cast_rows(const T* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream, const char* what) {
@@ -279,7 +344,8 @@ fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
   LinearParams p{};
   p.A = (const uint8_t*)X; p.lda = 2 * ldx; p.B = (const uint8_t*)W; p.ldb = 2 * ldw;
   p.D = H; p.ldd = ldh; p.P = P; p.ldp = ldp; p.M = M; p.N = F; p.K = K; p.act = activation;
-  return launch_linear<kEpiGated>(p, stream, "gated_ffn_bf16");
+  return P ? launch_linear<kEpiGatedKeep>(p, stream, "gated_ffn_bf16")
+           : launch_linear<kEpiGated>(p, stream, "gated_ffn_bf16");
 }
 
 fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16_t* X, int64_t ldx,
@@ -294,7 +360,7 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
   // no gradient element is asked for: dX is M x K, dW 2F x K
   if (K == 0 || ((!dX || M == 0) && (!dW || F == 0))) return FG_OK;
   if (M > kMaxRows || F > kMaxRows / 4) return set_error(FG_EUNSUPPORTED, "more than 2^30 rows");
-  FG_TRY(check_workspace(workspace, workspace_bytes, M > 0 && F > 0 ? backward_bytes(M, F) : 0));
+  FG_TRY(check_workspace(workspace, workspace_bytes, M > 0 && F > 0 ? backward_bytes(M, F, K) : 0));
   if (dX && M > 0) {
     FG_TRY(require_ptr(dX, 2, "dX"));
     FG_TRY(require_ld(lddx, K, 1, "lddx"));
@@ -325,8 +391,11 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
     g.M = M; g.N = F; g.K = K;
     if (P) {
       const int64_t blocks = ((int64_t)M * (g.half / 8) + 255) / 256;
-      hipLaunchKernelGGL(gated_grad_kernel, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16)), dim3(256), 0,
-                         (hipStream_t)stream, g);
+      const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 16));
+      if (activation == FG_ACT_SILU)
+        hipLaunchKernelGGL((gated_grad_kernel<kActSilu>), grid, dim3(256), 0, (hipStream_t)stream, g);
+      else
+        hipLaunchKernelGGL((gated_grad_kernel<kActGeluTanh>), grid, dim3(256), 0, (hipStream_t)stream, g);
       FG_TRY(launched(what));
     } else {
       FG_TRY((launch_linear<kEpiGatedGrad>(g, stream, what)));
@@ -337,6 +406,7 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
     LinearParams g = p;
     g.A = (const uint8_t*)workspace; g.lda = 2 * pair_ld; g.B = (const uint8_t*)W; g.ldb = 2 * ldw;
     g.D = dX; g.ldd = lddx; g.M = M; g.N = K; g.K = F > 0 ? (int)pair_ld : 0;
+    if (F > 0 && partial_bytes(M, K) > 0) g.P = (float*)((uint8_t*)workspace + pair_bytes(M, F));
     FG_TRY((launch_linear<kEpiBf16, false, true>(g, stream, what)));
   }
   if (dW && F > 0) {
@@ -348,9 +418,9 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
   return FG_OK;
 }
 
-int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F) {
-  if (M < 0 || F < 0 || M > kMaxRows || F > kMaxRows / 4) return -1;
-  return M > 0 && F > 0 ? backward_bytes(M, F) : 0;
+int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F, int K) {
+  if (M < 0 || F < 0 || K < 0 || M > kMaxRows || F > kMaxRows / 4 || K > kMaxRows) return -1;
+  return M > 0 && F > 0 && K > 0 ? backward_bytes(M, F, K) : 0;
 }
 
 }  // extern "C"

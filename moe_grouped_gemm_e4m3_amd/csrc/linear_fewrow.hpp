@@ -61,9 +61,12 @@ __device__ __forceinline__ void fewrow_store(const LinearParams& p, int m, int n
     a[r] = C::INT8 ? x[r] * sa * sg[r] : x[r];
     if (C::GATED) b[r] = C::INT8 ? y[r] * sa * su[r] : y[r];
   }
-  if constexpr (C::E == kEpiGated) {
-    if (p.P) {
-      float* prow = p.P + (int64_t)m * p.ldp;
+  if constexpr (C::E == kEpiGatedKeep) {
+    float* prow = p.P + (int64_t)m * p.ldp;
+    if (n + 4 <= p.N) {
+      *(f32x4_at4*)(prow + n) = f32x4{a[0], a[1], a[2], a[3]};
+      *(f32x4_at4*)(prow + p.N + n) = f32x4{b[0], b[1], b[2], b[3]};
+    } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (n + r < p.N) {
@@ -74,11 +77,12 @@ __device__ __forceinline__ void fewrow_store(const LinearParams& p, int m, int n
   }
   if constexpr (C::GATED) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) a[r] = gated_value(a[r], b[r], p.act);
+    for (int r = 0; r < 4; ++r)
+      a[r] = p.act == kActSilu ? gated_value<kActSilu>(a[r], b[r]) : gated_value<kActGeluTanh>(a[r], b[r]);
   }
   uint16_t* dst = p.D + (int64_t)m * p.ldd + n;
-  if (n + 4 <= p.N && ((uintptr_t)dst & 7) == 0) {
-    *(uint2*)dst = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+  if (n + 4 <= p.N) {
+    *(uint2_at2*)dst = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r)

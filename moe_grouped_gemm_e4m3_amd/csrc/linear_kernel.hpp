@@ -22,15 +22,24 @@
 namespace fg {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// Vectors at addresses that are aligned to their elements only (rows of any
+// stride): the compiler makes one access of them, which the hardware takes at
+// any address.
+typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
+typedef uint2 uint2_at2 __attribute__((aligned(2)));
+typedef uint4 uint4_at2 __attribute__((aligned(2)));
+typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 
 enum LinearEpi {
   kEpiInt8,       // D = bf16(sa sb acc)
   kEpiBf16,       // D = bf16(acc)
-  kEpiGated,      // D = bf16(act(g) u), optionally P = [g u] in fp32
+  kEpiPartial,    // P[split] = acc, [M, N] in fp32: one split of the reduction
+  kEpiGated,      // D = bf16(act(g) u)
   kEpiGatedInt8,  // the same with g, u = sa sb acc
   kEpiGatedGrad,  // D = bf16([dg du]) from g, u and dH
+  kEpiGatedKeep,  // kEpiGated and P = [g u] in fp32
 };
-constexpr bool epi_gated(int e) { return e == kEpiGated || e == kEpiGatedInt8 || e == kEpiGatedGrad; }
+constexpr bool epi_gated(int e) { return e >= kEpiGated; }
 constexpr bool epi_int8(int e) { return e == kEpiInt8 || e == kEpiGatedInt8; }
 
 enum { kActSilu = 0, kActGeluTanh = 1 };
@@ -43,7 +52,7 @@ struct LinearParams {
   const float *sa, *sb;  // int8 scales
   uint16_t* D;
   int64_t ldd;  // elements
-  float* P;     // gated: pre-activations [M, 2N] or NULL
+  float* P;     // pre-activations [M, 2N] (kEpiGatedKeep: written)
   int64_t ldp;
   const uint16_t* dH;  // gradient: [M, N]
   int64_t lddh;
@@ -53,8 +62,9 @@ struct LinearParams {
   // As the reduction axis (dX) or the output rows (dW) index r stands for
   // hidden unit r < F of the first half and r - half of the second.
   int F, half;
-  // slices of the reduction and output tiles of the persistent grid (linear_tile.hpp)
-  int nk;
+  // slices of the reduction (kEpiPartial: and of one split, an even number)
+  // and output tiles of the persistent grid (linear_tile.hpp)
+  int nk, split_nk;
   int tiles_m, tiles_n, num_tiles, group_m;
 };
 
@@ -65,22 +75,27 @@ __device__ __forceinline__ int pair_row(const LinearParams& p, int r) {
   return f < p.F ? h * p.F + f : -1;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.f + __expf(-x)); }
-
-// act(g) = g s with s = sigmoid(y(g)); silu: y = g; gelu (tanh form):
-// y = 2 c (g + a g^3), c = sqrt(2 / pi).
-constexpr float kGelu2C = 1.5957691216057308f, kGeluA = 0.044715f;
-__device__ __forceinline__ float act_gate(float g, int act) {
-  return sigmoid(act == kActSilu ? g : kGelu2C * (g + kGeluA * g * g * g));
+// act(g) = g s with s = 1 / (1 + exp(-y(g))); silu: y = g; gelu (tanh form):
+// y = 2 c (g + a g^3), c = sqrt(2 / pi).  The factors of y and log2(e) are one
+// constant.  exp overflows to infinity for far negative y, and s is then 0.
+constexpr float kLog2e = 1.4426950408889634f, kGelu2C = 1.5957691216057308f, kGeluA = 0.044715f;
+template <int ACT>
+__device__ __forceinline__ float act_gate(float g) {
+  const float z = ACT == kActSilu ? -kLog2e * g : g * __builtin_fmaf(-kLog2e * kGelu2C * kGeluA, g * g, -kLog2e * kGelu2C);
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z));
 }
-__device__ __forceinline__ float gated_value(float g, float u, int act) { return g * act_gate(g, act) * u; }
+template <int ACT>
+__device__ __forceinline__ float gated_value(float g, float u) {
+  return g * act_gate<ACT>(g) * u;
+}
 
 // dg = dH u act'(g), du = dH act(g), act'(g) = s + g s (1 - s) y'(g).  Where
 // s (1 - s) has underflowed the last term is 0 (y' may have overflowed there).
-__device__ __forceinline__ void gated_grad(float dh, float g, float u, int act, float& dg, float& du) {
-  const float s = act_gate(g, act);
+template <int ACT>
+__device__ __forceinline__ void gated_grad(float dh, float g, float u, float& dg, float& du) {
+  const float s = act_gate<ACT>(g);
   const float t = s * (1.f - s);
-  const float slope = act == kActSilu ? 1.f : kGelu2C * (1.f + 3.f * kGeluA * g * g);
+  const float slope = ACT == kActSilu ? 1.f : kGelu2C * (1.f + 3.f * kGeluA * g * g);
   dg = dh * u * (s + (t == 0.f ? 0.f : g * t * slope));
   du = dh * g * s;
 }
@@ -91,11 +106,10 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)(pack_
 
 // [dg du] from the kept pre-activations P = [g u], eight columns a thread.
 // Bound by HBM: 10 bytes in and 4 out for each hidden unit and row.
-static __global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p) {
+template <int ACT>
+__global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p) {
   const int per_row = p.half / 8;
   const int64_t total = (int64_t)p.M * per_row;
-  const bool vec = (p.N & 3) == 0 && (p.ldp & 3) == 0 && ((uintptr_t)p.P & 15) == 0 && (p.lddh & 7) == 0 &&
-                   ((uintptr_t)p.dH & 15) == 0;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / per_row;
     const int n = (int)(i - m * per_row) * 8;
@@ -103,10 +117,10 @@ static __global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p) 
     const float* up = gp + p.N;
     const uint16_t* hp = p.dH + m * p.lddh + n;
     float g[8], u[8], h[8];
-    if (vec && n + 8 <= p.N) {
-      const f32x4 g0 = *(const f32x4*)gp, g1 = *(const f32x4*)(gp + 4);
-      const f32x4 u0 = *(const f32x4*)up, u1 = *(const f32x4*)(up + 4);
-      const uint4 hv = *(const uint4*)hp;
+    if (n + 8 <= p.N) {
+      const f32x4 g0 = *(const f32x4_at4*)gp, g1 = *(const f32x4_at4*)(gp + 4);
+      const f32x4 u0 = *(const f32x4_at4*)up, u1 = *(const f32x4_at4*)(up + 4);
+      const uint4 hv = *(const uint4_at2*)hp;
       const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -130,14 +144,30 @@ static __global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p) 
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       float a0, b0, a1, b1;
-      gated_grad(h[2 * r], g[2 * r], u[2 * r], p.act, a0, b0);
-      gated_grad(h[2 * r + 1], g[2 * r + 1], u[2 * r + 1], p.act, a1, b1);
+      gated_grad<ACT>(h[2 * r], g[2 * r], u[2 * r], a0, b0);
+      gated_grad<ACT>(h[2 * r + 1], g[2 * r + 1], u[2 * r + 1], a1, b1);
       dg[r] = pack_bf16x2(a0, a1);
       du[r] = pack_bf16x2(b0, b1);
     }
     uint16_t* dst = p.D + m * p.ldd + n;
     *(uint4*)dst = make_uint4(dg[0], dg[1], dg[2], dg[3]);
     *(uint4*)(dst + p.half) = make_uint4(du[0], du[1], du[2], du[3]);
+  }
+}
+
+// D = bf16(sum of `splits` partials P), added in split order, four columns a
+// thread (N % 4 == 0).
+static __global__ __launch_bounds__(256) void add_partials_kernel(LinearParams p, int splits) {
+  const int per_row = p.N / 4;
+  const int64_t quads = (int64_t)p.M * per_row;
+  const f32x4* src = (const f32x4*)p.P;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
+    f32x4 s = src[i];
+#pragma unroll 4
+    for (int k = 1; k < splits; ++k) s += src[k * quads + i];
+    const int64_t m = i / per_row;
+    *(uint2_at2*)(p.D + m * p.ldd + (i - m * per_row) * 4) =
+        make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
   }
 }
 
@@ -183,7 +213,7 @@ __device__ __forceinline__ void int8_codes(const float (&x)[V], float s, float i
   }
 }
 
-// int8 codes and scale of each row: s = max(amax, 1e-4) / 127, q = rint(x / s).
+// int8 codes and scale of each row: s = max(amax, 1e-4) (1 / 127), q = rint(x / s).
 // One workgroup a row.  The first PIECES 16-byte pieces of each thread stay in
 // registers between the two passes, so a row of up to PIECES * THREADS * 16
 // bytes is read once; of a longer row the rest is read again.
@@ -218,7 +248,7 @@ __global__ __launch_bounds__(THREADS) void int8_cast_kernel(const T* __restrict_
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) amax = fmaxf(amax, red[w]);
-    const float sc = fmaxf(amax, 1e-4f) / 127.0f, inv = 1.0f / sc;
+    const float sc = fmaxf(amax, 1e-4f) * (1.0f / 127.0f), inv = 1.0f / sc;
     if (tid == 0) s[m] = sc;
     uint32_t* dst = (uint32_t*)(q + (int64_t)m * K);
     auto put = [&](const uint4& u, int i) {

@@ -7,44 +7,61 @@
 namespace fg {
 
 // A BM x BN output tile (gated: BN / 2 hidden units, gate and up columns) per
-// workgroup of WAVES_M x WAVES_N waves.  A slice is 128 bytes of the
-// reduction: 64 bf16 or 128 int8.
-template <int E_, int BM_, int BN_, int WAVES_M_, int WAVES_N_, int STAGES_, bool TA_ = false, bool TB_ = false>
+// workgroup of KG groups of WAVES_M x WAVES_N waves.  A slice is 128 bytes of
+// the reduction: 64 bf16 or 128 int8.  The main loop takes KG slices a step,
+// one for each group; the groups' sums are added at the end of a tile.
+template <int E_, int BM_, int BN_, int WAVES_M_, int WAVES_N_, int KG_, int STAGES_, bool TA_ = false,
+          bool TB_ = false>
 struct LinearTile {
   static constexpr int E = E_, BM = BM_, BN = BN_, WAVES_M = WAVES_M_, WAVES_N = WAVES_N_;
-  static constexpr int STAGES = STAGES_;  // slices in LDS
+  static constexpr int KG = KG_, STAGES = STAGES_;  // slices of a step, steps in LDS
   static constexpr bool TA = TA_, TB = TB_;
   static constexpr bool INT8 = epi_int8(E), GATED = epi_gated(E);
   static constexpr int ES = INT8 ? 1 : 2;
-  static constexpr int NW = WAVES_M * WAVES_N, THREADS = NW * 64;
+  static constexpr int GW = WAVES_M * WAVES_N, NW = GW * KG, THREADS = NW * 64;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, SM = WM / 16, SN = WN / 16;
-  static constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;  // a stage: A rows, then B rows
-  static constexpr int LDS_BYTES = STAGES * STAGE;
-  static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads per wave and slice
+  // B rows of a stage: BN rounded up to whole loads of every wave (MN-major:
+  // to a power of two); what lies past BN loads as zeros without touching
+  // memory and is not read
+  static constexpr int BROWS = TB ? (BN > 128 ? 256 : BN) : (BN + 8 * GW - 1) / (8 * GW) * (8 * GW);
+  // a stage: for each slice its A rows, then its B rows
+  static constexpr int A_BYTES = BM * 128, SLICE = (BM + BROWS) * 128, STAGE = KG * SLICE;
+  static constexpr int SUMS = (KG - 1) * BM * BN * 4;  // the further groups' accumulators
+  static constexpr int LDS_BYTES = STAGES * STAGE + SUMS;
+  static constexpr int LA = BM / 8 / GW, LB = BROWS / 8 / GW;  // 1 KiB loads per wave and step
   static constexpr int OUT_N = GATED ? BN / 2 : BN;         // output columns of a tile
   // two workgroups share a CU where LDS and registers allow it
   static constexpr int OCC = 2 * LDS_BYTES <= 160 * 1024 ? 2 : 1;
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads");
+  static_assert(BM % (8 * GW) == 0 && BROWS % (8 * GW) == 0, "loads");
   static_assert(LDS_BYTES <= 160 * 1024 && STAGES >= 2 && (STAGES - 1) * (LA + LB) < 64, "stages");
+  static_assert(WM % 16 == 0 && WN % 16 == 0 && BN % WAVES_N == 0, "wave tile");
   static_assert(!GATED || SN % 2 == 0, "gate and up blocks come in pairs");
   static_assert(!INT8 || (!TA && !TB), "bytes are staged K-major");
 };
 
-// One output tile: its place, and where its operands' first rows lie.
+// One output tile: its place, and its slices of the reduction.
 struct LinearWork {
   int w;  // tile id, < 0: none
   int m0, n0;
+  int kb0, kb1;
 };
 
 template <class C>
 __device__ __forceinline__ LinearWork linear_work(const LinearParams& p, int w) {
   LinearWork t;
   t.w = -1;
-  t.m0 = t.n0 = 0;
+  t.m0 = t.n0 = t.kb0 = 0;
+  t.kb1 = p.nk;
   if (w < p.num_tiles) {
+    t.w = w;
+    if (C::E == kEpiPartial) {  // every tile of one split, then the next split's
+      const int tiles = p.tiles_m * p.tiles_n, split = w / tiles;
+      w -= split * tiles;
+      t.kb0 = split * p.split_nk;
+      t.kb1 = min(p.nk, t.kb0 + p.split_nk);
+    }
     int tm, tn;
     raster(w, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-    t.w = w;
     t.m0 = tm * C::BM;
     t.n0 = tn * C::OUT_N;
   }
@@ -52,11 +69,13 @@ __device__ __forceinline__ LinearWork linear_work(const LinearParams& p, int w) 
 }
 
 // 16-byte chunk swizzle of MN-major stage rows (one row per reduction index,
-// CH chunks of 8 columns): a transposing fragment read takes, per group of 16
-// lanes, 4 rows at one pair of chunks, and its four groups take rows 8 apart;
-// moving the pair by (row % 4) + 4 (row / 8 % 4) spreads them over the banks.
+// CH chunks of 8 columns): a transposing fragment read takes, for each half of
+// the wave, rows 8 q + j (j < 4, two q) at one pair of chunks.  Moving the pair
+// by j and q lays those eight 32-byte pieces in different banks; a row of 8
+// chunks is half the banks, so its own parity already parts neighbours.
 template <int CH>
 __device__ __forceinline__ int mn_swz(int r) {
+  if (CH == 8) return (r & 2) | ((r >> 1) & 4);
   return (((r & 3) | ((r >> 1) & 12)) << 1) & (CH - 1);
 }
 
@@ -77,18 +96,22 @@ struct Loader {
   static constexpr bool MN = IS_A ? C::TA : C::TB;
   static constexpr bool PAIRED = !IS_A && C::GATED;  // gate and up rows
   static constexpr int N = IS_A ? C::LA : C::LB;     // loads per wave
-  static constexpr int COLS = IS_A ? C::BM : C::BN;
+  static constexpr int ROWS = IS_A ? C::BM : C::BN, COLS = IS_A ? C::BM : C::BROWS;
   LinearWork t;
-  int kb;                         // slice of tile t
-  int dst;                        // LDS offset of its stage
-  __amdgpu_buffer_rsrc_t rs, ru;  // its range (K-major: the tile's rows; gated: gate and up rows)
-  int cols;                       // rows (MN-major: columns) of the operand from the tile's first on
-  bool empty;                     // nothing to read: every offset is out of range
+  int kb;     // first slice of the step in tile t
+  int dst;    // LDS offset of its stage
+  // the ranges read (K-major: the tile's rows, gated: gate and up rows;
+  // MN-major: each slice's reduction rows)
+  __amdgpu_buffer_rsrc_t rs[MN ? C::KG : PAIRED ? 2 : 1];
+  int cols;   // rows (MN-major: columns) of the operand from the tile's first on
+  bool empty; // nothing to read: every offset is out of range
+  const uint8_t* from;  // MN-major: the operand at the tile's first column
 
-  __device__ __forceinline__ Loader(const LinearParams& p, const LinearWork& first) : t(first), kb(0) {
+  __device__ __forceinline__ Loader(const LinearParams& p, const LinearWork& first) : t(first), kb(first.kb0) {
     dst = IS_A ? 0 : C::A_BYTES;
     range(p);
   }
+  // Ranges of the step at slice kb of tile t.
   __device__ __forceinline__ void range(const LinearParams& p) {
     const uint8_t* base = IS_A ? p.A : p.B;
     const int64_t ld = IS_A ? p.lda : p.ldb;
@@ -97,59 +120,71 @@ struct Loader {
     // no tile, or one of a gradient pair's padding columns alone
     empty = t.w < 0 || cols <= 0;
     if constexpr (MN) {
-      // reduction rows from this slice on; of W they are the hidden units of
-      // one half of the gradient pair
-      int64_t row = (int64_t)kb * 64, left = p.K - row;
-      if (!IS_A && !C::TA && p.F > 0) {
-        const int h = row >= p.half ? 1 : 0;
-        const int f = (int)row - h * p.half;
-        row = (int64_t)h * p.F + f;
-        left = p.F - f;
-      }
-      empty = empty || left <= 0;
-      rs = make_rsrc(base + row * ld + (int64_t)first * 2,
-                     empty ? 0 : (min(left, (int64_t)64) - 1) * ld + (int64_t)cols * 2);
+      from = empty ? base : base + (int64_t)first * 2;
+      slices(p);
     } else {
       const int64_t bytes = empty ? 0 : (int64_t)(cols - 1) * ld + p.K * C::ES;
-      rs = make_rsrc(base + (int64_t)first * ld, bytes);
-      if (PAIRED) ru = make_rsrc(base + (int64_t)(p.N + first) * ld, bytes);
+      rs[0] = make_rsrc(base + (int64_t)first * ld, bytes);
+      if (PAIRED) rs[1] = make_rsrc(base + (int64_t)(p.N + first) * ld, bytes);
     }
   }
-  // Load j of this wave's N of the slice, into its stage (lds + dst).
+  // MN-major: the reduction rows of the step's slices.  Of W they are the
+  // hidden units of one half of the gradient pair.
+  __device__ __forceinline__ void slices(const LinearParams& p) {
+    const int ld = (int)(IS_A ? p.lda : p.ldb);  // at most 4 MiB
+#pragma unroll
+    for (int g = 0; g < C::KG; ++g) {
+      int row = (kb + g) * 64, left = p.K - row;
+      if (!IS_A && !C::TA && p.F > 0) {
+        const bool up = row >= p.half;
+        left = up ? p.F + p.half - row : p.F - row;
+        row = up ? row - p.half + p.F : row;
+      }
+      const bool none = empty || left <= 0;
+      const int bytes = none ? 0 : (min(left, 64) - 1) * ld + cols * 2;
+      rs[g] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(from + (none ? 0 : (int64_t)row * ld)), (short)0,
+                                                bytes, 0x00020000);
+    }
+  }
+  // Load j of this wave's N of the step, into its stage (lds + dst).
   __device__ __forceinline__ void issue(const LinearParams& p, uint8_t* stage, int j, int wave, int lane) const {
     const int64_t ld = IS_A ? p.lda : p.ldb;
-    const int q = wave * N + j;
-    __amdgpu_buffer_rsrc_t r = rs;
+    constexpr int PIECES = COLS / 8;  // 1 KiB pieces of a slice
+    const int g = C::KG == 1 ? 0 : (wave * N + j) / PIECES, q = wave * N + j - g * PIECES;
+    __amdgpu_buffer_rsrc_t r = rs[0];
     int v, k = 0;
     if constexpr (MN) {  // whole stage rows of COLS columns
+      if (C::KG > 1 && g == 1) r = rs[C::KG - 1];
       constexpr int CH = COLS / 8;  // chunks per row
       const int row = q * (64 / CH) + lane / CH;
       const int c = (lane % CH) ^ mn_swz<CH>(row);
-      v = c * 8 < cols ? row * (int)ld + c * 16 : kOobOffset;
+      v = c * 8 < cols && (ROWS == COLS || c * 8 < ROWS) ? row * (int)ld + c * 16 : kOobOffset;
     } else {  // 8 stage rows of 128 bytes
       int row = q * 8;
       if constexpr (PAIRED) {  // stage rows: 16 gate rows, 16 up rows of the same hidden units, ...
         row = (q >> 2) * 16 + (q & 1) * 8;
-        if ((q >> 1) & 1) r = ru;
+        if ((q >> 1) & 1) r = rs[1];
       }
       const int r8 = lane >> 3, c = ((lane & 7) ^ lin_swz(r8)) * 16;
-      v = k_clip((row + r8) * (int)ld + c, kb * 128 + c, p.K * C::ES);
-      // the scalar offset counts against the range's end, which an empty
-      // range has at 0: it must not pass it
-      k = empty ? 0 : kb * 128;
+      const int slice = kb + g;
+      v = ROWS == COLS || q * 8 < ROWS ? k_clip((row + r8) * (int)ld + c, slice * 128 + c, p.K * C::ES) : kOobOffset;
+      // the scalar offset counts against the range's end and must not pass
+      // it: 0 where nothing is read
+      k = empty || (C::KG > 1 && slice >= p.nk) ? 0 : slice * 128;
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(stage + q * 1024), 16, v, k,
-                                             0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        r, (__attribute__((address_space(3))) void*)(stage + g * C::SLICE + q * 1024), 16, v, k, 0, 0);
   }
   __device__ __forceinline__ void advance(const LinearParams& p, int grid) {
     constexpr int FIRST = IS_A ? 0 : C::A_BYTES;
     dst = dst == FIRST + (C::STAGES - 1) * C::STAGE ? FIRST : dst + C::STAGE;
-    if (++kb == p.nk) {
-      kb = 0;
+    kb += C::KG;
+    if (kb >= t.kb1) {
       if (t.w >= 0) t = linear_work<C>(p, t.w + grid);
+      kb = t.kb0;
       range(p);
     } else if (MN) {
-      range(p);
+      slices(p);
     }
   }
 };
@@ -215,11 +250,11 @@ struct LinearAcc {
   }
 };
 
-// Four consecutive fp32 (zeros at and past column n_end), one load if aligned.
+// Four consecutive fp32 (zeros at and past column n_end).
 __device__ __forceinline__ f32x4 load_f32x4(const float* src, int n, int n_end) {
   f32x4 x = {0.f, 0.f, 0.f, 0.f};
-  if (n + 4 <= n_end && ((uintptr_t)(src + n) & 15) == 0) {
-    x = *(const f32x4*)(src + n);
+  if (n + 4 <= n_end) {
+    x = *(const f32x4_at4*)(src + n);
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -228,20 +263,21 @@ __device__ __forceinline__ f32x4 load_f32x4(const float* src, int n, int n_end) 
   return x;
 }
 
-// Columns [n, n + 8) of an output row from this lane and its neighbour: the
-// lanes of quarters kq and kq ^ 1 trade halves of two 16-column blocks, so
-// each stores 16 bytes.  n0 is the first block's first column.
-__device__ __forceinline__ void store_pair(uint16_t* row, int n0, int n_end, bool ok, bool vec, int lane, uint32_t a0,
+// Columns of two neighbouring 16-column blocks of an output row (first column
+// n0), four of each per lane: a0, a1 and b0, b1.  The lanes of quarters kq and
+// kq ^ 1 trade halves, so that an even lane holds eight columns of the first
+// block and an odd lane eight of the second: 16-byte stores.
+template <bool FULL>
+__device__ __forceinline__ void store_pair(uint16_t* row, int n0, int n_end, bool ok, int lane, uint32_t a0,
                                            uint32_t a1, uint32_t b0, uint32_t b1) {
   const int kq = lane >> 4;
-  const bool odd = kq & 1;
-  const int r0 = __shfl_xor((int)(odd ? a0 : b0), 16), r1 = __shfl_xor((int)(odd ? a1 : b1), 16);
-  const i32x4 w = odd ? i32x4{r0, r1, (int)b0, (int)b1} : i32x4{(int)a0, (int)a1, r0, r1};
-  const int n = n0 + (odd ? 16 + 4 * (kq - 1) : 4 * kq);
-  if (!ok || n >= n_end) return;
-  if (vec && n + 8 <= n_end) {
-    *(i32x4*)(row + n) = w;
-  } else {
+  const auto x = __builtin_amdgcn_permlane16_swap(a0, b0, false, false);
+  const auto y = __builtin_amdgcn_permlane16_swap(a1, b1, false, false);
+  const i32x4 w = {(int)x[0], (int)y[0], (int)x[1], (int)y[1]};
+  const int n = n0 + (kq & 1 ? 16 + 4 * (kq - 1) : 4 * kq);
+  if (FULL || (ok && n + 8 <= n_end)) {
+    *(i32x4_at2*)(row + n) = w;
+  } else if (ok) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       if (n + e < n_end) row[n + e] = (uint16_t)((uint32_t)w[e >> 1] >> ((e & 1) * 16));
@@ -249,11 +285,11 @@ __device__ __forceinline__ void store_pair(uint16_t* row, int n0, int n_end, boo
 }
 
 // Columns [n, n + 4) of an output row.
+template <bool FULL>
 __device__ __forceinline__ void store_quad(uint16_t* row, int n, int n_end, bool ok, uint32_t a0, uint32_t a1) {
-  if (!ok || n >= n_end) return;
-  if (n + 4 <= n_end && ((uintptr_t)(row + n) & 7) == 0) {
-    *(uint2*)(row + n) = make_uint2(a0, a1);
-  } else {
+  if (FULL || (ok && n + 4 <= n_end)) {
+    *(uint2_at2*)(row + n) = make_uint2(a0, a1);
+  } else if (ok) {
     const uint32_t w[2] = {a0, a1};
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -262,16 +298,18 @@ __device__ __forceinline__ void store_quad(uint16_t* row, int n, int n_end, bool
 }
 
 // The finished tile, straight from the accumulators.  Lane (l16, kq) holds
-// row l16 and columns [4 kq, +4) of every 16 x 16 block.
-template <class C>
-__device__ __forceinline__ void store_linear(const LinearParams& p, const LinearWork& t, const LinearAcc<C>& acc,
+// row l16 and columns [4 kq, +4) of every 16 x 16 block.  FULL: the whole tile
+// lies inside the output, so nothing is tested
+// (gated 4096 x 12288 x 1536: 250 us with the tests, 214 without).
+template <class C, int ACT, bool FULL>
+__device__ __forceinline__ void store_blocks(const LinearParams& p, const LinearWork& t, const LinearAcc<C>& acc,
                                              int wm, int wn, int lane) {
   const int l16 = lane & 15, kq = lane >> 4;
+  constexpr bool GRAD = C::E == kEpiGatedGrad;
   constexpr int STEP = C::GATED ? 2 : 1;       // accumulator blocks per output block
   constexpr int NB = C::SN / STEP;             // output blocks of the wave
   const int nw = t.n0 + wn * NB * 16;          // the wave's first output column
-  const int n_end = C::E == kEpiGatedGrad ? p.half : p.N;
-  const bool vec = (p.ldd & 7) == 0 && ((uintptr_t)p.D & 15) == 0 && (C::E != kEpiGatedGrad || (p.half & 7) == 0);
+  const int n_end = GRAD ? p.half : p.N;
   f32x4 sb[C::INT8 ? C::SN : 1];
   if constexpr (C::INT8) {
 #pragma unroll
@@ -281,19 +319,36 @@ __device__ __forceinline__ void store_linear(const LinearParams& p, const Linear
       if (C::GATED) sb[j * STEP + 1] = load_f32x4(p.sb + p.N, n, p.N);
     }
   }
+  if constexpr (C::E == kEpiPartial) {
+    float* part = p.P + (int64_t)(t.kb0 / p.split_nk) * p.M * p.N;
+#pragma unroll
+    for (int i = 0; i < C::SM; ++i) {
+      const int m = t.m0 + wm * C::WM + i * 16 + l16;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        const int n = nw + j * 16 + 4 * kq;  // N is a multiple of 4
+        if (FULL || (m < p.M && n < p.N)) *(f32x4*)(part + (int64_t)m * p.N + n) = acc.v[i][j];
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < C::SM; ++i) {
     const int m = t.m0 + wm * C::WM + i * 16 + l16;
-    bool ok = m < p.M;
+    bool ok = FULL || m < p.M;
     int64_t drow = m;
     if (C::TA && p.F > 0 && ok) {  // dW: rows of the gradient pair
       drow = pair_row(p, m);
-      ok = drow >= 0;
+      ok = FULL || drow >= 0;
     }
     uint16_t* row = p.D + drow * p.ldd;
     float sa = 0.f;
     if (C::INT8 && ok) sa = p.sa[m];
-    uint32_t lo[NB], hi[NB], lo2[C::E == kEpiGatedGrad ? NB : 1], hi2[C::E == kEpiGatedGrad ? NB : 1];
+    // the wave's 16 rows of P (full tiles: all of them inside)
+    __amdgpu_buffer_rsrc_t prs;
+    if constexpr (C::E == kEpiGatedKeep && FULL)
+      prs = make_rsrc(p.P + (int64_t)(t.m0 + wm * C::WM + i * 16) * p.ldp + nw, 0x7fffffff);
+    uint32_t lo[NB], hi[NB], lo2[GRAD ? NB : 1], hi2[GRAD ? NB : 1];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
       const int n = nw + j * 16 + 4 * kq;
@@ -307,29 +362,29 @@ __device__ __forceinline__ void store_linear(const LinearParams& p, const Linear
           if (C::GATED) b[r] = b[r] * sa * sb[j * STEP + STEP - 1][r];
         }
       }
-      if constexpr (C::E == kEpiGated) {
-        if (p.P && ok) {
+      if constexpr (C::E == kEpiGatedKeep) {
+        if constexpr (FULL) {
+          const int at = l16 * (int)p.ldp * 4 + kq * 16;
+          const i32x4 g = {__float_as_int(a[0]), __float_as_int(a[1]), __float_as_int(a[2]), __float_as_int(a[3])};
+          const i32x4 u = {__float_as_int(b[0]), __float_as_int(b[1]), __float_as_int(b[2]), __float_as_int(b[3])};
+          __builtin_amdgcn_raw_buffer_store_b128(g, prs, at, j * 64, 0);
+          __builtin_amdgcn_raw_buffer_store_b128(u, prs, at, j * 64 + p.N * 4, 0);
+        } else if (ok) {
           float* prow = p.P + (int64_t)m * p.ldp;
-          const bool v4 = n + 4 <= p.N && (p.N & 3) == 0 && ((uintptr_t)(prow + n) & 15) == 0;
-          if (v4) {
-            *(f32x4*)(prow + n) = f32x4{a[0], a[1], a[2], a[3]};
-            *(f32x4*)(prow + p.N + n) = f32x4{b[0], b[1], b[2], b[3]};
-          } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (n + r < p.N) {
-                prow[n + r] = a[r];
-                prow[p.N + n + r] = b[r];
-              }
-          }
+          for (int r = 0; r < 4; ++r)
+            if (n + r < p.N) {
+              prow[n + r] = a[r];
+              prow[p.N + n + r] = b[r];
+            }
         }
       }
-      if constexpr (C::E == kEpiGatedGrad) {
+      if constexpr (GRAD) {
         uint32_t h[2] = {0, 0};
         if (ok) {
           const uint16_t* hrow = p.dH + (int64_t)m * p.lddh;
-          if (n + 4 <= p.N && ((uintptr_t)(hrow + n) & 7) == 0) {
-            const uint2 u = *(const uint2*)(hrow + n);
+          if (FULL || n + 4 <= p.N) {
+            const uint2 u = *(const uint2_at2*)(hrow + n);
             h[0] = u.x;
             h[1] = u.y;
           } else {
@@ -342,8 +397,8 @@ __device__ __forceinline__ void store_linear(const LinearParams& p, const Linear
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float dh = to_f32((uint16_t)(h[r >> 1] >> (16 * (r & 1))));
-          gated_grad(dh, a[r], b[r], p.act, dg[r], du[r]);
-          if (n + r >= p.N) dg[r] = du[r] = 0.f;
+          gated_grad<ACT>(dh, a[r], b[r], dg[r], du[r]);
+          if (!FULL && n + r >= p.N) dg[r] = du[r] = 0.f;
         }
         lo2[j] = pack_bf16x2(du[0], du[1]);
         hi2[j] = pack_bf16x2(du[2], du[3]);
@@ -351,22 +406,55 @@ __device__ __forceinline__ void store_linear(const LinearParams& p, const Linear
         for (int r = 0; r < 4; ++r) a[r] = dg[r];
       } else if constexpr (C::GATED) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = gated_value(a[r], b[r], p.act);
+        for (int r = 0; r < 4; ++r) a[r] = gated_value<ACT>(a[r], b[r]);
       }
       lo[j] = pack_bf16x2(a[0], a[1]);
       hi[j] = pack_bf16x2(a[2], a[3]);
+      // one block at a time: interleaved, the blocks' temporaries do not fit
+      // beside the accumulators and the next tile's fragments
+      if (C::GATED) __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int j = 0; j + 1 < NB; j += 2) {
-      store_pair(row, nw + j * 16, n_end, ok, vec, lane, lo[j], hi[j], lo[j + 1], hi[j + 1]);
-      if constexpr (C::E == kEpiGatedGrad)
-        store_pair(row + p.half, nw + j * 16, n_end, ok, vec, lane, lo2[j], hi2[j], lo2[j + 1], hi2[j + 1]);
+      store_pair<FULL>(row, nw + j * 16, n_end, ok, lane, lo[j], hi[j], lo[j + 1], hi[j + 1]);
+      if constexpr (GRAD)
+        store_pair<FULL>(row + p.half, nw + j * 16, n_end, ok, lane, lo2[j], hi2[j], lo2[j + 1], hi2[j + 1]);
     }
     if constexpr (NB % 2 == 1) {  // the last block alone: 8 bytes a lane
-      store_quad(row, nw + (NB - 1) * 16 + 4 * kq, n_end, ok, lo[NB - 1], hi[NB - 1]);
-      if constexpr (C::E == kEpiGatedGrad)
-        store_quad(row + p.half, nw + (NB - 1) * 16 + 4 * kq, n_end, ok, lo2[NB - 1], hi2[NB - 1]);
+      store_quad<FULL>(row, nw + (NB - 1) * 16 + 4 * kq, n_end, ok, lo[NB - 1], hi[NB - 1]);
+      if constexpr (GRAD)
+        store_quad<FULL>(row + p.half, nw + (NB - 1) * 16 + 4 * kq, n_end, ok, lo2[NB - 1], hi2[NB - 1]);
     }
+  }
+}
+
+// Stores a finished tile.
+template <class C>
+__device__ __forceinline__ void store_linear(const LinearParams& p, const LinearWork& t, const LinearAcc<C>& acc,
+                                             int wm, int wn, int lane) {
+  bool full = t.n0 + C::OUT_N <= p.N;
+  if (C::TA && p.F > 0)
+    full = full && (t.m0 >= p.half ? t.m0 - p.half : t.m0) + C::BM <= p.F;
+  else
+    full = full && t.m0 + C::BM <= p.M;
+  if (C::E == kEpiGatedKeep) full = full && p.ldp <= 1 << 24;  // 32-bit offsets within 16 rows of P
+  if constexpr (C::GATED) {
+    if (p.act == kActSilu) {
+      if (full)
+        store_blocks<C, kActSilu, true>(p, t, acc, wm, wn, lane);
+      else
+        store_blocks<C, kActSilu, false>(p, t, acc, wm, wn, lane);
+    } else {
+      if (full)
+        store_blocks<C, kActGeluTanh, true>(p, t, acc, wm, wn, lane);
+      else
+        store_blocks<C, kActGeluTanh, false>(p, t, acc, wm, wn, lane);
+    }
+  } else {
+    if (full)
+      store_blocks<C, 0, true>(p, t, acc, wm, wn, lane);
+    else
+      store_blocks<C, 0, false>(p, t, acc, wm, wn, lane);
   }
 }
 
@@ -392,7 +480,7 @@ template <class C, int H, bool LOAD>
 __device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>& acc, const i32x4 (&a)[C::SM],
                                             const i32x4 (&b)[C::SN], i32x4 (&na)[C::SM], i32x4 (&nb)[C::SN],
                                             const FragReader<C::BM, C::TA, C::SM>& ra,
-                                            const FragReader<C::BN, C::TB, C::SN>& rb, const uint8_t* __restrict st_a,
+                                            const FragReader<C::BROWS, C::TB, C::SN>& rb, const uint8_t* __restrict st_a,
                                             const uint8_t* __restrict st_b, const Loader<C, true>& la,
                                             const Loader<C, false>& lb, uint8_t* __restrict ld_a,
                                             uint8_t* __restrict ld_b, int wave, int lane) {
@@ -433,9 +521,10 @@ __global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_ke
   __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS_BYTES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / C::WAVES_N, wn = wave % C::WAVES_N;
+  const int group = C::KG == 1 ? 0 : wave / C::GW, gwave = wave - group * C::GW;
+  const int wm = gwave / C::WAVES_N, wn = gwave % C::WAVES_N;
   const int grid = gridDim.x;
-  const int nk = p.nk;
+  const int slice = group * C::SLICE;  // the group's slice in a stage
 
   LinearWork cur = linear_work<C>(p, xcd_local_id(blockIdx.x, grid));
   if (cur.w < 0) return;
@@ -443,7 +532,7 @@ __global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_ke
   Loader<C, false> lb(p, cur);
 
   const FragReader<C::BM, C::TA, C::SM> ra(wm * C::WM, lane);
-  const FragReader<C::BN, C::TB, C::SN> rb(wn * C::WN, lane);
+  const FragReader<C::BROWS, C::TB, C::SN> rb(wn * C::WN, lane);
   i32x4 a0[C::SM], b0[C::SN], a1[C::SM], b1[C::SN];
   LinearAcc<C> acc;
   acc.zero();
@@ -459,22 +548,44 @@ __global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_ke
   }
   linear_sync<(C::STAGES - 1) * (C::LA + C::LB)>();
 #pragma unroll
-  for (int i = 0; i < C::SM; ++i) ra.read(lds, 0, lane, i, a0);
+  for (int i = 0; i < C::SM; ++i) ra.read(lds + slice, 0, lane, i, a0);
 #pragma unroll
-  for (int i = 0; i < C::SN; ++i) rb.read(lds + C::A_BYTES, 0, lane, i, b0);
-  int s = 0;  // stage of the current slice
+  for (int i = 0; i < C::SN; ++i) rb.read(lds + slice + C::A_BYTES, 0, lane, i, b0);
+  int s = slice;  // the group's slice of the current step
   while (cur.w >= 0) {
-    for (int kb = 0; kb < nk; ++kb) {
+    for (int kb = cur.kb0; kb < cur.kb1; kb += C::KG) {
       linear_half<C, 1, false>(p, acc, a0, b0, a1, b1, ra, rb, lds + s, lds + C::A_BYTES + s, la, lb, nullptr, nullptr,
                                wave, lane);
       linear_sync<(C::STAGES - 2) * (C::LA + C::LB)>();
-      s = s == (C::STAGES - 1) * C::STAGE ? 0 : s + C::STAGE;
+      s = s == slice + (C::STAGES - 1) * C::STAGE ? slice : s + C::STAGE;
       linear_half<C, 0, true>(p, acc, a1, b1, a0, b0, ra, rb, lds + s, lds + C::A_BYTES + s, la, lb, lds + la.dst,
                               lds + lb.dst, wave, lane);
       lb.advance(p, grid);
       la.advance(p, grid);
     }
-    store_linear<C>(p, cur, acc, wm, wn, lane);
+    if constexpr (C::KG > 1) {
+      // group 1's sums go through LDS; it writes them again only after the
+      // barriers of another tile
+      static_assert(C::KG == 2, "two groups");
+      typedef typename LinearAcc<C>::V V;
+      V* sums = (V*)(lds + C::STAGES * C::STAGE) + gwave * C::SM * C::SN * 64 + lane;
+      if (group == 1) {
+#pragma unroll
+        for (int i = 0; i < C::SM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::SN; ++j) sums[(i * C::SN + j) * 64] = acc.v[i][j];
+      }
+      lds_barrier();
+      if (group == 0) {
+#pragma unroll
+        for (int i = 0; i < C::SM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::SN; ++j) acc.v[i][j] += sums[(i * C::SN + j) * 64];
+        store_linear<C>(p, cur, acc, wm, wn, lane);
+      }
+    } else {
+      store_linear<C>(p, cur, acc, wm, wn, lane);
+    }
     acc.zero();
     cur = linear_work<C>(p, cur.w + grid);
   }

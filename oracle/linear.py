@@ -25,7 +25,8 @@ GELU_A = 0.044715
 def int8_cast(x: np.ndarray):
     """Codes and scales of each row, in the fp32 steps the definition fixes."""
     x = np.asarray(x, np.float32)
-    s = (np.maximum(np.abs(x).max(axis=1, initial=0.0), np.float32(1e-4)) / np.float32(127)).astype(np.float32)
+    step = np.float32(1) / np.float32(127)
+    s = np.maximum(np.abs(x).max(axis=1, initial=0.0), np.float32(1e-4)) * step
     return np.rint(x / s[:, None]).astype(np.int8), s
 
 

@@ -152,6 +152,8 @@ GRAD_SHAPES = [
     (1, 1, 8), (1, 40, 16), (2, 64, 264), (7, 33, 40), (16, 130, 136), (33, 63, 256), (64, 256, 512), (65, 100, 72),
     (128, 65, 1032), (129, 192, 128), (200, 257, 264), (300, 128, 520), (333, 96, 1528), (513, 300, 200),
     (1000, 64, 64), (700, 330, 392),
+    # few outputs of dX and a long sum: split over workgroups
+    (2, 2000, 64), (70, 3000, 136), (251, 1500, 264), (150, 1300, 1016),
 ]
 
 
@@ -170,7 +172,7 @@ def test_backward_matches_float64(gpu_lib, M, F, K, act, kept):
         gpu_lib.gated_ffn_bf16(Xd, Wd, torch.empty(M, F, dtype=torch.bfloat16, device="cuda"), P=P, activation=act)
     dX, dW = Output(M, K, pad), Output(2 * F, K, pad)
     # a workspace full of NaN: nothing of it may be read before it is written
-    ws = torch.full((max(gpu_lib.gated_ffn_backward_workspace_bytes(M, F), 1),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(gpu_lib.gated_ffn_backward_workspace_bytes(M, F, K), 1),), 255, dtype=torch.uint8, device="cuda")
     gpu_lib.gated_ffn_bf16_backward(dHd, Xd, Wd, dX.t, dW.t, P=P, activation=act, workspace=ws)
     dX.check_untouched()
     dW.check_untouched()
@@ -265,7 +267,7 @@ def test_step_on_another_stream_and_in_a_graph(gpu_lib):
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     outs = tuple(torch.empty_like(t) for t in want)
-    ws = torch.empty(gpu_lib.gated_ffn_backward_workspace_bytes(M, F), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gpu_lib.gated_ffn_backward_workspace_bytes(M, F, K), dtype=torch.uint8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step(ws=ws, outs=outs)
@@ -341,10 +343,15 @@ def test_int8_forward_refusals(lib, kw, status, needle):
 
 
 def test_workspace_query(lib):
-    assert lib.fg_gated_ffn_backward_workspace_bytes(-1, 4) == -1
-    assert lib.fg_gated_ffn_backward_workspace_bytes(0, 4) == 0
-    assert lib.fg_gated_ffn_backward_workspace_bytes(3, 1) >= 3 * 2 * 2
-    assert lib.fg_gated_ffn_backward_workspace_bytes(1 << 30, 1 << 20) > 1 << 50
+    assert lib.fg_gated_ffn_backward_workspace_bytes(-1, 4, 8) == -1
+    assert lib.fg_gated_ffn_backward_workspace_bytes(4, 4, -8) == -1
+    assert lib.fg_gated_ffn_backward_workspace_bytes(0, 4, 8) == 0
+    assert lib.fg_gated_ffn_backward_workspace_bytes(3, 1, 8) >= 3 * 2 * 2
+    assert lib.fg_gated_ffn_backward_workspace_bytes(1 << 30, 1 << 20, 1 << 20) > 1 << 50
+    # at most 32 MiB of partials, and none where two do not fit
+    pair = 2 * 64 * 2
+    assert lib.fg_gated_ffn_backward_workspace_bytes(4096, 64, 8192) == 4096 * pair
+    assert 0 < lib.fg_gated_ffn_backward_workspace_bytes(512, 64, 4096) - 512 * pair <= 32 << 20
 
 
 def test_wrappers_reject_cpu_tensors_and_unknown_activations():

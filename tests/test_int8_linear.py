@@ -30,7 +30,7 @@ def test_cast_definition_against_brute_force():
     q, s = ref.int8_cast(x)
     for m in range(5):
         top = max(max(abs(float(v)) for v in x[m]), float(np.float32(1e-4)))
-        assert s[m] == np.float32(np.float32(top) / np.float32(127))
+        assert s[m] == np.float32(np.float32(top) * np.float32(1 / 127))
         for k in range(32):
             assert q[m, k] == int(np.rint(np.float32(x[m, k] / s[m])))
     assert np.abs(q.astype(int)).max() <= 127
