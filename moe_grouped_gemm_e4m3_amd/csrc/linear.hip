@@ -57,16 +57,34 @@ double tile_count(const LinearParams& p, int64_t cols, bool gated, int bm, int b
 }
 
 // One tile per CU and round: `idle` a slice with few CUs at work, `busy` with
-// all of them (clock and cache contention), `store` for the epilogue.
+// all of them (clock and cache contention, which sets in towards the end),
+// `store` for the epilogue.
 double tile_us(double tiles, int cus, int nk, double idle, double busy, double store) {
   const double load = tiles < cus ? tiles / cus : 1.0;
-  return 3.0 + ceil(tiles / cus) * (nk * (idle + (busy - idle) * load) + store);
+  return 3.4 + ceil(tiles / cus) * (nk * (idle + (busy - idle) * load * load) + store);
 }
 
-// Two workgroups per CU: a round that leaves one workgroup per CU is cheaper.
-double tile2_us(double tiles, int cus, int nk, double one, double two) {
+// 64 x 64, eight waves in two groups: 0.185 us a slice (256 x 4096 x 7168 int8
+// 14.7 us, 26 on 128 x 128; 400 x 7168 x 2048 20 us against 12), 0.32 where
+// operands are MN-major.
+double small_us(double tiles, int cus, int nk, bool mn) {
+  const double slice = mn ? 0.32 : 0.185;
+  return tile_us(tiles, cus, nk, slice, slice, 1.2);
+}
+
+// 128 x 128, eight waves, four stages: 0.35 us alone, 0.52 with every CU at
+// work (1000 x 4096 x 7168 int8 34 us, 71 on 256 x 256), 0.5 and 0.62 where
+// operands are MN-major.
+double mid_us(double tiles, int cus, int nk, bool mn) {
+  return mn ? tile_us(tiles, cus, nk, 0.5, 0.62, 2.0) : tile_us(tiles, cus, nk, 0.35, 0.52, 2.0);
+}
+
+// 128 x 128, two workgroups of four waves per CU: 0.66 us alone, 1.0 for both
+// (4096 x 4096 x 7168 int8 112 us, 92 on 256 x 256); a round that leaves one
+// workgroup per CU is cheaper.
+double mid2_us(double tiles, int cus, int nk) {
   const double full = floor(tiles / (2 * cus)), rest = tiles - full * 2 * cus;
-  return 3.0 + full * (nk * two + 1.5) + (rest > 0 ? nk * (rest > cus ? two : one) + 1.5 : 0);
+  return 3.4 + full * (nk * 1.0 + 1.5) + (rest > 0 ? nk * (rest > cus ? 1.0 : 0.66) + 1.5 : 0);
 }
 
 template <class C>
@@ -78,12 +96,28 @@ fg_status launch_fewrow(const LinearParams& p, void* stream, const char* what) {
   return launched(what);
 }
 
-// A few-row workgroup fetches its rows' slices at about 80 GB/s; a launch's
-// rounds each add about 2 us of latency.
-double fewrow_us(const LinearParams& p, bool gated, int cus, int mf, int cf) {
-  const double parts = (double)((p.M + 16 * mf - 1) / (16 * mf)), out_n = gated ? 8 * cf : 16 * cf;
-  const double groups = parts * ceil(p.N / out_n), bytes = (double)p.nk * 128 * (std::min(p.M, 16 * mf) + 16 * cf);
-  return 1.0 + ceil(groups / cus) * (2.0 + bytes / 80e3);
+// Few-row shapes: 16 mf rows, 16 cf weight rows, waves.  A wave's step of one
+// slice takes `idle` to `busy` us by how many CUs are at work; workgroups that
+// share a CU take `shared` of their time one after the other.  Fitted to 1200
+// measurements (1 to 640 rows, 300 to 12288 columns, K of 512 to 14336 bytes,
+// int8 and gated bf16): the choice is within 2 % of the fastest shape on
+// average and 25 % at worst.
+struct FewRowShape {
+  int mf, cf, waves;
+  double base, idle, busy, shared;
+};
+constexpr FewRowShape kFewRowShapes[] = {
+    {1, 1, 4, 1.2, 0.20, 0.32, 0.75}, {1, 1, 8, 1.2, 0.22, 0.66, 0.70}, {1, 2, 4, 1.2, 0.18, 0.54, 0.70},
+    {2, 1, 4, 1.5, 0.18, 0.34, 0.85}, {2, 2, 4, 1.5, 0.22, 0.54, 0.85}, {4, 1, 4, 1.8, 0.26, 0.50, 0.85},
+    {4, 2, 4, 1.8, 0.46, 0.70, 1.00}, {4, 4, 4, 1.8, 0.95, 1.20, 1.30},
+};
+constexpr int kFewRowMost = 640;  // rows up to which these shapes are considered
+
+double fewrow_us(const LinearParams& p, bool gated, int cus, const FewRowShape& f) {
+  const double groups = (double)((p.M + 16 * f.mf - 1) / (16 * f.mf)) * ceil((double)p.N / (gated ? 8 * f.cf : 16 * f.cf));
+  const double load = groups < cus ? groups / cus : 1.0, turns = ceil(groups / cus);
+  const double one = 0.9 + (p.nk + f.waves - 1) / f.waves * (f.idle + (f.busy - f.idle) * load);
+  return f.base + (turns > 1 ? turns * f.shared : 1.0) * one;
 }
 
 // Splits of the reduction over workgroups (dX alone: its reduction is the
@@ -105,8 +139,9 @@ struct SplitPlan {
   int splits, nk;  // slices of a split (even)
 };
 
-SplitPlan plan_split(const LinearParams& p, int cus, int bm, int bn, double idle, double busy) {
-  const double tiles = tile_count(p, p.N, false, bm, bn);
+template <class F>
+SplitPlan plan_split(const LinearParams& p, int cus, int bm, F cost) {
+  const double tiles = tile_count(p, p.N, false, bm, bm);
   const int64_t one = (int64_t)p.M * p.N * 4;
   const int most = (int)std::min<int64_t>(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one), (int64_t)(cus / tiles));
   SplitPlan s{1e30, 1, p.nk};
@@ -114,7 +149,7 @@ SplitPlan plan_split(const LinearParams& p, int cus, int bm, int bn, double idle
   s.nk = (int)round_up((p.nk + most - 1) / most, 2);
   s.splits = (p.nk + s.nk - 1) / s.nk;
   // the partials are written and read at about 4 TB/s; the second launch is 4 us
-  s.us = tile_us(tiles * s.splits, cus, s.nk, idle, busy, 1.5) + 4.0 + 2.0 * s.splits * one / 4e6;
+  s.us = cost(tiles * s.splits, cus, s.nk, true) + 4.0 + 2.0 * s.splits * one / 4e6;
   return s;
 }
 
@@ -128,46 +163,36 @@ fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
   // 256 rows by 256, 224, 192 or 160: 1.2, 1.1, 1.0 and 0.92 us a slice with
   // few CUs at work, 1.45, 1.36, 1.15 and 1.02 with all, which the chip's power
   // limits (int8 4096 x 7168 x 16384: 380 us with 256 columns, 364 with 224;
-  // 4096 x 2112 x 7168: 80 with 256, 63 with 160).  128 x 128, two workgroups
-  // of four waves: 0.66 alone, 1.0 for both (112 us on 4096 x 4096 x 7168, 92
-  // on 256 x 256); one of eight waves with four stages: 0.48 and 0.58 (34 us
-  // on 1000 x 4096 x 7168, 71 on 256 x 256).  64 x 64 with eight waves in two
-  // groups: 0.22 (16 us on 256 x 4096 x 7168, 27 on 128 x 128), 0.34 where
-  // operands are MN-major.
+  // 4096 x 2112 x 7168: 80 with 256, 63 with 160).
   auto count = [&](int bm, int bn) { return tile_count(p, cols, gated, bm, bn); };
   const double w256 = tile_us(count(256, 256), cus, p.nk, 1.2, 1.45, 4.0);
   const double w224 = gated ? 1e30 : tile_us(count(256, 224), cus, p.nk, 1.1, 1.36, 4.0);
   const double w192 = gated ? tile_us(count(256, 192), cus, p.nk, 1.0, 1.15, 4.0) : 1e30;
   const double w160 = gated ? 1e30 : tile_us(count(256, 160), cus, p.nk, 0.92, 1.02, 3.5);
-  const double mid2 = tile2_us(count(128, 128), cus, p.nk, 0.66, 1.0);
-  const double mid = tile_us(count(128, 128), cus, p.nk, 0.48, 0.58, 1.5);
-  const double small_slice = TA || TB ? 0.34 : 0.22;
-  const double small = tile_us(count(64, 64), cus, p.nk, small_slice, small_slice, 1.5);
+  const double mid2 = mid2_us(count(128, 128), cus, p.nk);
+  const double mid = mid_us(count(128, 128), cus, p.nk, TA || TB);
+  const double small = small_us(count(64, 64), cus, p.nk, TA || TB);
   const double tile = std::min({w256, w224, w192, w160, mid2, mid, small});
   if constexpr (!TA && !TB && E != kEpiGatedGrad) {
-    if (p.M <= 256) {
-      static const int shapes[][2] = {{1, 1}, {1, 2}, {2, 1}, {2, 2}, {4, 1}, {4, 2}, {4, 4}};
+    if (p.M <= kFewRowMost) {
       int best = -1;
       double least = tile;
-      for (int i = 0; i < 7; ++i) {
-        const double t = fewrow_us(p, gated, cus, shapes[i][0], shapes[i][1]);
+      for (int i = 0; i < (int)(sizeof kFewRowShapes / sizeof *kFewRowShapes); ++i) {
+        const double t = fewrow_us(p, gated, cus, kFewRowShapes[i]);
         if (t < least) {
           least = t;
           best = i;
         }
       }
       switch (best) {
-        case 0:
-          // long chains of slices are shared out over eight waves (1 x 2112 x
-          // 7168 5.1 us against 6.1, 1 x 2048 x 1024 3.1 against 2.8)
-          if (p.nk >= 32) return launch_fewrow<FewRow<E, 1, 1, 8, 2>>(p, stream, what);
-          return launch_fewrow<FewRow<E, 1, 1, 4, 2>>(p, stream, what);
-        case 1: return launch_fewrow<FewRow<E, 1, 2, 4, 2>>(p, stream, what);
-        case 2: return launch_fewrow<FewRow<E, 2, 1, 4, 3>>(p, stream, what);
-        case 3: return launch_fewrow<FewRow<E, 2, 2, 4, 2>>(p, stream, what);
-        case 4: return launch_fewrow<FewRow<E, 4, 1, 4, 2>>(p, stream, what);
-        case 5: return launch_fewrow<FewRow<E, 4, 2, 4, 2>>(p, stream, what);
-        case 6: return launch_fewrow<FewRow<E, 4, 4, 4, 2>>(p, stream, what);
+        case 0: return launch_fewrow<FewRow<E, 1, 1, 4, 2>>(p, stream, what);
+        case 1: return launch_fewrow<FewRow<E, 1, 1, 8, 2>>(p, stream, what);
+        case 2: return launch_fewrow<FewRow<E, 1, 2, 4, 2>>(p, stream, what);
+        case 3: return launch_fewrow<FewRow<E, 2, 1, 4, 3>>(p, stream, what);
+        case 4: return launch_fewrow<FewRow<E, 2, 2, 4, 2>>(p, stream, what);
+        case 5: return launch_fewrow<FewRow<E, 4, 1, 4, 2>>(p, stream, what);
+        case 6: return launch_fewrow<FewRow<E, 4, 2, 4, 2>>(p, stream, what);
+        case 7: return launch_fewrow<FewRow<E, 4, 4, 4, 2>>(p, stream, what);
         default: break;
       }
     }
@@ -175,7 +200,7 @@ fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
   if constexpr (E == kEpiBf16 && TB && !TA) {
     // 251 x 1016 with 178 slices: 60 us on 64 64 x 64 tiles, a quarter of the
     // device; split four ways 25 us with the addition.
-    const SplitPlan a = plan_split(p, cus, 64, 64, 0.34, 0.34), b = plan_split(p, cus, 128, 128, 0.5, 0.6);
+    const SplitPlan a = plan_split(p, cus, 64, small_us), b = plan_split(p, cus, 128, mid_us);
     const SplitPlan& s = a.us <= b.us ? a : b;
     if (p.P && s.us < tile) {
       p.split_nk = s.nk;
