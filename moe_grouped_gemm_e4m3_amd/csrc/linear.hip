@@ -37,14 +37,21 @@ fg_status launched(const char* what) {
 // the same, both are 128 bytes and 2048 MFMA cycles on the 256 x 256 tile),
 // and the cheapest runs.  The estimates only rank candidates.
 
+// Lays p's output out in C's tiles (`splits` times over).
 template <class C>
-fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, const char* what, int splits = 1) {
+fg_status set_tiles(LinearParams& p, int64_t cols, const char* what, int splits = 1) {
   const int64_t tm = ((int64_t)p.M + C::BM - 1) / C::BM, tn = (cols + C::OUT_N - 1) / C::OUT_N;
   if (tm * tn * splits >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
   p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
   p.num_tiles = (int)(tm * tn) * splits;
   p.group_m = 8;
+  return FG_OK;
+}
+
+template <class C>
+fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, const char* what, int splits = 1) {
+  FG_TRY(set_tiles<C>(p, cols, what, splits));
   const int grid = std::min(cus * C::OCC, p.num_tiles);
   hipLaunchKernelGGL((linear_tile_kernel<C>), dim3((unsigned)grid), dim3(C::THREADS), 0, (hipStream_t)stream, p);
   return launched(what);
@@ -153,30 +160,80 @@ SplitPlan plan_split(const LinearParams& p, int cus, int bm, F cost) {
   return s;
 }
 
+template <int E>
+int slice_count(const LinearParams& p) {
+  return (int)std::max<int64_t>(1, ((int64_t)p.K * (epi_int8(E) ? 1 : 2) + 127) / 128);
+}
+
+// The cheapest tile for p (its slices set) and its time.
+enum TileKind { kW256, kW224, kW192, kW160, kMid2, kMid, kSmall };
+struct TilePlan {
+  TileKind kind;
+  double us;
+};
+
+TilePlan plan_tile(const LinearParams& p, int64_t cols, bool gated, bool mn, int cus) {
+  auto count = [&](int bm, int bn) { return tile_count(p, cols, gated, bm, bn); };
+  TilePlan best{kW256, 1e30};
+  auto offer = [&](TileKind kind, double us) {
+    if (us < best.us) best = TilePlan{kind, us};
+  };
+  // 256 rows by 256, 224, 192 or 160: 1.2, 1.1, 1.0 and 0.92 us a slice with
+  // few CUs at work, 1.45, 1.36, 1.15 and 1.02 with all, which the chip's power
+  // limits (int8 4096 x 7168 x 16384: 380 us with 256 columns, 364 with 224;
+  // 4096 x 2112 x 7168: 80 with 256, 63 with 160).
+  offer(kW256, tile_us(count(256, 256), cus, p.nk, 1.2, 1.45, 4.0));
+  if (gated) {
+    offer(kW192, tile_us(count(256, 192), cus, p.nk, 1.0, 1.15, 4.0));
+  } else {
+    offer(kW224, tile_us(count(256, 224), cus, p.nk, 1.1, 1.36, 4.0));
+    offer(kW160, tile_us(count(256, 160), cus, p.nk, 0.92, 1.02, 3.5));
+  }
+  offer(kMid2, mid2_us(count(128, 128), cus, p.nk));
+  offer(kMid, mid_us(count(128, 128), cus, p.nk, mn));
+  offer(kSmall, small_us(count(64, 64), cus, p.nk, mn));
+  return best;
+}
+
+template <int E, bool TA, bool TB>
+using MidTile = LinearTile<E, 128, 128, 4, 2, 1, 4, TA, TB>;
+template <int E, bool TA, bool TB>
+using SmallTile = LinearTile<E, 64, 64, 2, 2, 2, 4, TA, TB>;
+
 template <int E, bool TA = false, bool TB = false>
+fg_status launch_planned(LinearParams& p, TileKind kind, int64_t cols, int cus, void* stream, const char* what) {
+  switch (kind) {
+    case kW224:
+      if constexpr (!epi_gated(E)) return launch_tile<LinearTile<E, 256, 224, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+      break;
+    case kW192:
+      if constexpr (epi_gated(E)) return launch_tile<LinearTile<E, 256, 192, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+      break;
+    case kW160:
+      if constexpr (!epi_gated(E)) return launch_tile<LinearTile<E, 256, 160, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+      break;
+    case kMid2: return launch_tile<LinearTile<E, 128, 128, 2, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+    case kMid: return launch_tile<MidTile<E, TA, TB>>(p, cus, cols, stream, what);
+    case kSmall: return launch_tile<SmallTile<E, TA, TB>>(p, cus, cols, stream, what);
+    default: break;
+  }
+  return launch_tile<LinearTile<E, 256, 256, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+}
+
+// One product: the operands of the forward passes and of the recomputed
+// gradient pair, both K-major.
+template <int E>
 fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
   int cus = 0;
   FG_TRY(usable_cus(&cus));
   constexpr bool gated = epi_gated(E);
   const int64_t cols = E == kEpiGatedGrad ? p.half : p.N;
-  p.nk = (int)std::max<int64_t>(1, ((int64_t)p.K * (epi_int8(E) ? 1 : 2) + 127) / 128);
-  // 256 rows by 256, 224, 192 or 160: 1.2, 1.1, 1.0 and 0.92 us a slice with
-  // few CUs at work, 1.45, 1.36, 1.15 and 1.02 with all, which the chip's power
-  // limits (int8 4096 x 7168 x 16384: 380 us with 256 columns, 364 with 224;
-  // 4096 x 2112 x 7168: 80 with 256, 63 with 160).
-  auto count = [&](int bm, int bn) { return tile_count(p, cols, gated, bm, bn); };
-  const double w256 = tile_us(count(256, 256), cus, p.nk, 1.2, 1.45, 4.0);
-  const double w224 = gated ? 1e30 : tile_us(count(256, 224), cus, p.nk, 1.1, 1.36, 4.0);
-  const double w192 = gated ? tile_us(count(256, 192), cus, p.nk, 1.0, 1.15, 4.0) : 1e30;
-  const double w160 = gated ? 1e30 : tile_us(count(256, 160), cus, p.nk, 0.92, 1.02, 3.5);
-  const double mid2 = mid2_us(count(128, 128), cus, p.nk);
-  const double mid = mid_us(count(128, 128), cus, p.nk, TA || TB);
-  const double small = small_us(count(64, 64), cus, p.nk, TA || TB);
-  const double tile = std::min({w256, w224, w192, w160, mid2, mid, small});
-  if constexpr (!TA && !TB && E != kEpiGatedGrad) {
+  p.nk = slice_count<E>(p);
+  const TilePlan tile = plan_tile(p, cols, gated, false, cus);
+  if constexpr (E != kEpiGatedGrad) {
     if (p.M <= kFewRowMost) {
       int best = -1;
-      double least = tile;
+      double least = tile.us;
       for (int i = 0; i < (int)(sizeof kFewRowShapes / sizeof *kFewRowShapes); ++i) {
         const double t = fewrow_us(p, gated, cus, kFewRowShapes[i]);
         if (t < least) {
@@ -197,33 +254,118 @@ fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
       }
     }
   }
-  if constexpr (E == kEpiBf16 && TB && !TA) {
+  return launch_planned<E>(p, tile.kind, cols, cus, stream, what);
+}
+
+// ---------------------------------------------------------------------------
+// dX = pair . W and dW = pair^T . X, either or both.  Each has its own plan;
+// where neither fills the device, both go into one launch, with 128 x 128 or
+// 64 x 64 tiles each.
+
+struct GradPlan {
+  TileKind kind;
+  int splits;     // of dX's sum
+  double us;      // in a launch of its own
+  double tiles;   // workgroups in a shared launch, and the time of one
+  double tile;
+};
+
+// Adds dX's partials.
+fg_status launch_add(const LinearParams& p, int splits, void* stream, const char* what) {
+  const int64_t blocks = ((int64_t)p.M * (p.N / 4) + 255) / 256;
+  hipLaunchKernelGGL(add_partials_kernel, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16)), dim3(256), 0,
+                     (hipStream_t)stream, p, splits);
+  return launched(what);
+}
+
+template <class X, class W>
+fg_status launch_both(LinearParams& x, int splits, LinearParams& w, void* stream, const char* what) {
+  FG_TRY((set_tiles<X>(x, x.N, what, splits)));
+  FG_TRY((set_tiles<W>(w, w.N, what)));
+  hipLaunchKernelGGL((linear_grads_kernel<X, W>), dim3((unsigned)(x.num_tiles + w.num_tiles)), dim3(X::THREADS), 0,
+                     (hipStream_t)stream, x, w, x.num_tiles);
+  return launched(what);
+}
+
+template <int EX>
+fg_status launch_both(LinearParams& x, TileKind kx, int splits, LinearParams& w, TileKind kw, void* stream,
+                      const char* what) {
+  using MX = MidTile<EX, false, true>;
+  using SX = SmallTile<EX, false, true>;
+  using MW = MidTile<kEpiBf16, true, true>;
+  using SW = SmallTile<kEpiBf16, true, true>;
+  if (kx == kMid)
+    return kw == kMid ? launch_both<MX, MW>(x, splits, w, stream, what) : launch_both<MX, SW>(x, splits, w, stream, what);
+  return kw == kMid ? launch_both<SX, MW>(x, splits, w, stream, what) : launch_both<SX, SW>(x, splits, w, stream, what);
+}
+
+fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const char* what) {
+  int cus = 0;
+  FG_TRY(usable_cus(&cus));
+  GradPlan px{kW256, 1, 0, 0, 0}, pw{kW256, 1, 0, 0, 0};
+  double x_us = 0, w_us = 0;
+  if (x) {
+    x->nk = slice_count<kEpiBf16>(*x);
+    x->split_nk = x->nk;
+    const TilePlan t = plan_tile(*x, x->N, false, true, cus);
+    px.kind = t.kind;
+    px.us = t.us;
     // 251 x 1016 with 178 slices: 60 us on 64 64 x 64 tiles, a quarter of the
     // device; split four ways 25 us with the addition.
-    const SplitPlan a = plan_split(p, cus, 64, small_us), b = plan_split(p, cus, 128, mid_us);
+    const SplitPlan a = plan_split(*x, cus, 64, small_us), b = plan_split(*x, cus, 128, mid_us);
     const SplitPlan& s = a.us <= b.us ? a : b;
-    if (p.P && s.us < tile) {
-      p.split_nk = s.nk;
-      if (a.us <= b.us)
-        FG_TRY((launch_tile<LinearTile<kEpiPartial, 64, 64, 2, 2, 2, 4, TA, TB>>(p, cus, cols, stream, what, s.splits)));
-      else
-        FG_TRY((launch_tile<LinearTile<kEpiPartial, 128, 128, 4, 2, 1, 4, TA, TB>>(p, cus, cols, stream, what, s.splits)));
-      const int64_t blocks = ((int64_t)p.M * (p.N / 4) + 255) / 256;
-      hipLaunchKernelGGL(add_partials_kernel, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16)), dim3(256), 0,
-                         (hipStream_t)stream, p, s.splits);
-      return launched(what);
+    if (x->P && s.us < px.us) {
+      px = GradPlan{a.us <= b.us ? kSmall : kMid, s.splits, s.us, 0, 0};
+      x->split_nk = s.nk;
+    }
+    x_us = px.us;
+  }
+  if (w) {
+    w->nk = slice_count<kEpiBf16>(*w);
+    const TilePlan t = plan_tile(*w, w->N, false, true, cus);
+    pw.kind = t.kind;
+    pw.us = t.us;
+    w_us = pw.us;
+  }
+  if (x && w) {
+    // One launch: the workgroups of both, one to a CU, dX's first.  The device
+    // is busy for their total, and for the longest one at least.
+    double least = 0.95 * (x_us + w_us);
+    TileKind kx = kW256, kw = kW256;
+    for (const TileKind cx : {kMid, kSmall})
+      for (const TileKind cw : {kMid, kSmall}) {
+        if (px.splits > 1 && cx != px.kind) continue;
+        const int bx = cx == kMid ? 128 : 64, bw = cw == kMid ? 128 : 64;
+        const double nx = tile_count(*x, x->N, false, bx, bx) * px.splits, nw = tile_count(*w, w->N, false, bw, bw);
+        const double tx = x->split_nk * (cx == kMid ? 0.62 : 0.36) + (cx == kMid ? 2.5 : 1.5);
+        const double tw = w->nk * (cw == kMid ? 0.75 : 0.42) + (cw == kMid ? 2.5 : 1.5);  // both operands MN-major
+        const double us = 3.4 + std::max(std::max(tx, tw), (nx * tx + nw * tw) / cus + 0.5 * std::min(tx, tw)) +
+                          (px.splits > 1 ? 4.0 : 0.0);
+        if (us < least && nx + nw < (1 << 22)) {
+          least = us;
+          kx = cx;
+          kw = cw;
+        }
+      }
+    if (kx != kW256) {
+      if (px.splits == 1) return launch_both<kEpiBf16>(*x, kx, 1, *w, kw, stream, what);
+      FG_TRY(launch_both<kEpiPartial>(*x, kx, px.splits, *w, kw, stream, what));
+      return launch_add(*x, px.splits, stream, what);
     }
   }
-  if (tile == w256) return launch_tile<LinearTile<E, 256, 256, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
-  if constexpr (gated) {
-    if (tile == w192) return launch_tile<LinearTile<E, 256, 192, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
-  } else {
-    if (tile == w224) return launch_tile<LinearTile<E, 256, 224, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
-    if (tile == w160) return launch_tile<LinearTile<E, 256, 160, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+  if (x) {
+    if (px.splits > 1) {
+      if (px.kind == kSmall)
+        FG_TRY((launch_tile<SmallTile<kEpiPartial, false, true>>(*x, cus, x->N, stream, what, px.splits)));
+      else
+        FG_TRY((launch_tile<MidTile<kEpiPartial, false, true>>(*x, cus, x->N, stream, what, px.splits)));
+      FG_TRY(launch_add(*x, px.splits, stream, what));
+    } else {
+      FG_TRY((launch_planned<kEpiBf16, false, true>(*x, px.kind, x->N, cus, stream, what)));
+    }
   }
-  if (tile == mid2) return launch_tile<LinearTile<E, 128, 128, 2, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
-  if (tile == mid) return launch_tile<LinearTile<E, 128, 128, 4, 2, 1, 4, TA, TB>>(p, cus, cols, stream, what);
-  return launch_tile<LinearTile<E, 64, 64, 2, 2, 2, 4, TA, TB>>(p, cus, cols, stream, what);
+  if (w) FG_TRY((launch_planned<kEpiBf16, true, true>(*w, pw.kind, w->N, cus, stream, what)));
+  return FG_OK;
 }
 
 // Sizes every entry point shares; *empty when there is no output element.
@@ -427,20 +569,18 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
     }
   }
   // With M or F of zero the reductions below are empty and write zeros.
-  if (dX && M > 0) {
-    LinearParams g = p;
-    g.A = (const uint8_t*)workspace; g.lda = 2 * pair_ld; g.B = (const uint8_t*)W; g.ldb = 2 * ldw;
-    g.D = dX; g.ldd = lddx; g.M = M; g.N = K; g.K = F > 0 ? (int)pair_ld : 0;
-    if (F > 0 && partial_bytes(M, K) > 0) g.P = (float*)((uint8_t*)workspace + pair_bytes(M, F));
-    FG_TRY((launch_linear<kEpiBf16, false, true>(g, stream, what)));
+  LinearParams x = p, w = p;
+  const bool want_x = dX && M > 0, want_w = dW && F > 0;
+  if (want_x) {
+    x.A = (const uint8_t*)workspace; x.lda = 2 * pair_ld; x.B = (const uint8_t*)W; x.ldb = 2 * ldw;
+    x.D = dX; x.ldd = lddx; x.M = M; x.N = K; x.K = F > 0 ? (int)pair_ld : 0;
+    if (F > 0 && partial_bytes(M, K) > 0) x.P = (float*)((uint8_t*)workspace + pair_bytes(M, F));
   }
-  if (dW && F > 0) {
-    LinearParams g = p;
-    g.A = (const uint8_t*)workspace; g.lda = 2 * pair_ld; g.B = (const uint8_t*)X; g.ldb = 2 * ldx;
-    g.D = dW; g.ldd = lddw; g.M = (int)pair_ld; g.N = K; g.K = M;
-    FG_TRY((launch_linear<kEpiBf16, true, true>(g, stream, what)));
+  if (want_w) {
+    w.A = (const uint8_t*)workspace; w.lda = 2 * pair_ld; w.B = (const uint8_t*)X; w.ldb = 2 * ldx;
+    w.D = dW; w.ldd = lddw; w.M = (int)pair_ld; w.N = K; w.K = M;
   }
-  return FG_OK;
+  return launch_grads(want_x ? &x : nullptr, want_w ? &w : nullptr, stream, what);
 }
 
 int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F, int K) {

@@ -516,17 +516,17 @@ __device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>&
 // stage and the next slice has landed.  The loads run STAGES slices ahead
 // (into the workgroup's next tile too) and are issued in the half after the
 // barrier that frees their stage.
+//
+// Workgroup `block` of `grid`, with C::LDS_BYTES at lds.
 template <class C>
-__global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_kernel(LinearParams p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS_BYTES];
+__device__ __forceinline__ void linear_tiles(const LinearParams& p, uint8_t* lds, int block, int grid) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int group = C::KG == 1 ? 0 : wave / C::GW, gwave = wave - group * C::GW;
   const int wm = gwave / C::WAVES_N, wn = gwave % C::WAVES_N;
-  const int grid = gridDim.x;
   const int slice = group * C::SLICE;  // the group's slice in a stage
 
-  LinearWork cur = linear_work<C>(p, xcd_local_id(blockIdx.x, grid));
+  LinearWork cur = linear_work<C>(p, xcd_local_id(block, grid));
   if (cur.w < 0) return;
   Loader<C, true> la(p, cur);
   Loader<C, false> lb(p, cur);
@@ -591,6 +591,25 @@ __global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_ke
   }
   // no load may still be writing LDS when the workgroup ends
   __builtin_amdgcn_s_waitcnt(0);
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS, C::OCC * C::NW / 4) void linear_tile_kernel(LinearParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS_BYTES];
+  linear_tiles<C>(p, lds, blockIdx.x, gridDim.x);
+}
+
+// dX and dW in one launch: the first `blocks_x` workgroups take dX's tiles,
+// the others dW's.
+template <class X, class W>
+__global__ __launch_bounds__(X::THREADS, 2) void linear_grads_kernel(LinearParams px, LinearParams pw, int blocks_x) {
+  static_assert(X::THREADS == W::THREADS && X::NW == 8, "one workgroup size, two waves a SIMD");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[X::LDS_BYTES > W::LDS_BYTES ? X::LDS_BYTES : W::LDS_BYTES];
+  const int b = blockIdx.x;
+  if (b < blocks_x)
+    linear_tiles<X>(px, lds, b, blocks_x);
+  else
+    linear_tiles<W>(pw, lds, b - blocks_x, gridDim.x - blocks_x);
 }
 
 }  // namespace fg
