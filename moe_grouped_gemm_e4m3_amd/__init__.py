@@ -670,9 +670,15 @@ def _row_scales(t: torch.Tensor, name: str, rows: int, dev: int) -> int:
     return t.data_ptr()
 
 
+# torch.cuda.current_stream() builds a Stream object, 2.5 us; this is its handle.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(stream, dev: int) -> int:
     """The HIP stream of a call (None: torch's current one)."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    if stream is None and _current_raw_stream is not None:
+        return _current_raw_stream(dev)
+    return _stream(stream)
 
 
 def _activation(name: str) -> int:

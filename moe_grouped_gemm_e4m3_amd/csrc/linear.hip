@@ -4,6 +4,9 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
 
 #include "host_common.hpp"
 #include "linear_fewrow.hpp"
@@ -172,7 +175,41 @@ struct TilePlan {
   double us;
 };
 
+// The environment variable FG_LINEAR_PLAN overrides the choice (tuning and
+// tests): a tile ("w256", "w224", "w192", "w160", "mid2", "mid", "small"), a
+// few-row shape ("few0" .. "few7"), or for the gradients "split-mid",
+// "split-small" (dX's sum) or "share-X-W" (X and W: mid or small).  A plan
+// that the call does not have leaves it its own.
+const char* forced_plan() {
+  const char* f = getenv("FG_LINEAR_PLAN");
+  return f ? f : "";
+}
+
+bool forced_tile(bool gated, TileKind* kind) {
+  static const struct {
+    const char* name;
+    TileKind kind;
+  } names[] = {{"w256", kW256}, {"w224", kW224}, {"w192", kW192}, {"w160", kW160},
+               {"mid2", kMid2}, {"mid", kMid},   {"small", kSmall}};
+  const char* f = forced_plan();
+  if (!*f) return false;
+  for (const auto& n : names)
+    if (strcmp(f, n.name) == 0 && (gated ? n.kind != kW224 && n.kind != kW160 : n.kind != kW192)) {
+      *kind = n.kind;
+      return true;
+    }
+  return false;
+}
+
+bool shares(const char* forced, TileKind x, TileKind w) {
+  char name[32];
+  snprintf(name, sizeof name, "share-%s-%s", x == kMid ? "mid" : "small", w == kMid ? "mid" : "small");
+  return strcmp(forced, name) == 0;
+}
+
 TilePlan plan_tile(const LinearParams& p, int64_t cols, bool gated, bool mn, int cus) {
+  TileKind forced;
+  if (forced_tile(gated, &forced)) return TilePlan{forced, 0.0};
   auto count = [&](int bm, int bn) { return tile_count(p, cols, gated, bm, bn); };
   TilePlan best{kW256, 1e30};
   auto offer = [&](TileKind kind, double us) {
@@ -241,6 +278,8 @@ fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
           best = i;
         }
       }
+      const char* f = forced_plan();
+      if (strncmp(f, "few", 3) == 0 && f[3] >= '0' && f[3] <= '7' && !f[4]) best = f[3] - '0';
       switch (best) {
         case 0: return launch_fewrow<FewRow<E, 1, 1, 4, 2>>(p, stream, what);
         case 1: return launch_fewrow<FewRow<E, 1, 1, 8, 2>>(p, stream, what);
@@ -264,10 +303,8 @@ fg_status launch_linear(LinearParams& p, void* stream, const char* what) {
 
 struct GradPlan {
   TileKind kind;
-  int splits;     // of dX's sum
-  double us;      // in a launch of its own
-  double tiles;   // workgroups in a shared launch, and the time of one
-  double tile;
+  int splits;  // of dX's sum
+  double us;   // in a launch of its own
 };
 
 // Adds dX's partials.
@@ -302,7 +339,7 @@ fg_status launch_both(LinearParams& x, TileKind kx, int splits, LinearParams& w,
 fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const char* what) {
   int cus = 0;
   FG_TRY(usable_cus(&cus));
-  GradPlan px{kW256, 1, 0, 0, 0}, pw{kW256, 1, 0, 0, 0};
+  GradPlan px{kW256, 1, 0}, pw{kW256, 1, 0};
   double x_us = 0, w_us = 0;
   if (x) {
     x->nk = slice_count<kEpiBf16>(*x);
@@ -313,9 +350,12 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
     // 251 x 1016 with 178 slices: 60 us on 64 64 x 64 tiles, a quarter of the
     // device; split four ways 25 us with the addition.
     const SplitPlan a = plan_split(*x, cus, 64, small_us), b = plan_split(*x, cus, 128, mid_us);
-    const SplitPlan& s = a.us <= b.us ? a : b;
-    if (x->P && s.us < px.us) {
-      px = GradPlan{a.us <= b.us ? kSmall : kMid, s.splits, s.us, 0, 0};
+    const char* f = forced_plan();
+    const bool force_small = strcmp(f, "split-small") == 0, force_mid = strcmp(f, "split-mid") == 0;
+    const bool small_tiles = force_small || (!force_mid && a.us <= b.us);
+    const SplitPlan& s = small_tiles ? a : b;
+    if (x->P && s.splits > 1 && (s.us < px.us || force_small || force_mid)) {
+      px = GradPlan{small_tiles ? kSmall : kMid, s.splits, s.us};
       x->split_nk = s.nk;
     }
     x_us = px.us;
@@ -332,6 +372,7 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
     // is busy for their total, and for the longest one at least.
     double least = 0.95 * (x_us + w_us);
     TileKind kx = kW256, kw = kW256;
+    const char* forced = forced_plan();
     for (const TileKind cx : {kMid, kSmall})
       for (const TileKind cw : {kMid, kSmall}) {
         if (px.splits > 1 && cx != px.kind) continue;
@@ -341,7 +382,8 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
         const double tw = w->nk * (cw == kMid ? 0.75 : 0.42) + (cw == kMid ? 2.5 : 1.5);  // both operands MN-major
         const double us = 3.4 + std::max(std::max(tx, tw), (nx * tx + nw * tw) / cus + 0.5 * std::min(tx, tw)) +
                           (px.splits > 1 ? 4.0 : 0.0);
-        if (us < least && nx + nw < (1 << 22)) {
+        if (nx + nw >= (1 << 22)) continue;
+        if (*forced ? shares(forced, cx, cw) : us < least) {
           least = us;
           kx = cx;
           kw = cw;
