@@ -473,7 +473,7 @@ fg_status int8_cast_per_row_bf16(const uint16_t* x, int64_t ldx, int8_t* q, floa
  * M, N >= 0 arbitrary, K % 16 == 0, K <= 131056 (the sum of more products may
  * leave int32; FG_EUNSUPPORTED).  K == 0 writes D = sa * sb * 0.  Rows of
  * at most 4 MiB.  The product is scaled as (sum * sa[m]) * sb[n] in fp32 and
- * rounded once.  Allocates nothing.
+ * rounded once.  D may not overlap an input.  Allocates nothing.
  */
 fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
                        uint16_t* D, int64_t ldd, int M, int N, int K, void* stream);
@@ -491,7 +491,8 @@ typedef enum { FG_ACT_SILU = 0, FG_ACT_GELU_TANH = 1 } fg_activation;
  *   H   device [M, F] bf16, row stride ldh elements (ldh >= F); written
  *   P   NULL, or device fp32 [M, 2F] (row stride ldp >= 2F): receives [g u] for the backward pass
  * M, F >= 0 arbitrary, K % 8 == 0 (K == 0: g = u = 0), rows of at most 4 MiB.
- * g and u are accumulated in fp32 and not rounded before the activation.
+ * g and u are accumulated in fp32 and not rounded before the activation.  H
+ * and P may not overlap each other or an input.  Allocates nothing.
  */
 fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, uint16_t* H, int64_t ldh,
                          float* P, int64_t ldp, int M, int F, int K, int activation, void* stream);
@@ -524,7 +525,8 @@ int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F, int K);
  *     g = sx * sw[0:F] * (X . W[0:F]^T),  u likewise with rows F..2F-1,  H = bf16( act(g) * u ).
  *   X, sx, W, sw  as A, sa, B, sb of gemm_int8_nt, W and sw of 2F rows
  *   H             device [M, F] bf16, row stride ldh (ldh >= F); written
- * M, F >= 0 arbitrary; K as in gemm_int8_nt.
+ * M, F >= 0 arbitrary; K as in gemm_int8_nt.  H may not overlap an input.
+ * Allocates nothing.
  */
 fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const int8_t* W, int64_t ldw,
                          const float* sw, uint16_t* H, int64_t ldh, int M, int F, int K, int activation,
@@ -536,7 +538,8 @@ int fg_get_mk_alignment_for_contiguous_layout(void);
 /* Cap on the compute units the GEMM kernels spread their persistent workgroups
  * over (the digest's set_num_sms); 0 (the default) means all of them.
  * Results do not depend on the cap (every tile is computed whole by one
- * workgroup).  Process-wide, not thread-safe against concurrent launches. */
+ * workgroup), but for the bf16 gated block and its gradients, whose plan,
+ * and so the order of their fp32 sums, follows it.  Process-wide, not thread-safe against concurrent launches. */
 void fg_set_num_cus(int n);
 int fg_get_num_cus(void);
 

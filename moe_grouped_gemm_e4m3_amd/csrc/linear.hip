@@ -140,7 +140,7 @@ constexpr int64_t kMaxPartialBytes = (int64_t)32 << 20;
 // two fit.
 int64_t partial_bytes(int64_t M, int64_t N) {
   const int64_t one = M * N * 4;
-  if (2 * one > kMaxPartialBytes) return 0;
+  if (one > kMaxPartialBytes / 2) return 0;
   return round_up(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one) * one, 256);
 }
 
@@ -155,7 +155,7 @@ SplitPlan plan_split(const LinearParams& p, int cus, int bm, F cost) {
   const int64_t one = (int64_t)p.M * p.N * 4;
   const int most = (int)std::min<int64_t>(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one), (int64_t)(cus / tiles));
   SplitPlan s{1e30, 1, p.nk};
-  if (2 * one > kMaxPartialBytes || most < 2) return s;
+  if (one > kMaxPartialBytes / 2 || most < 2) return s;
   s.nk = (int)round_up((p.nk + most - 1) / most, 2);
   s.splits = (p.nk + s.nk - 1) / s.nk;
   // the partials are written and read at about 4 TB/s; the second launch is 4 us
