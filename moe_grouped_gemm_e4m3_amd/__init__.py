@@ -12,6 +12,10 @@ Layouts (Kb = ceil(K/128), Nb = ceil(N/128)):
   sa  fp32 [Kb, M] view of a [Kb, ld_sa] buffer (activation scales, K-group-major)
   B   e4m3 [N, K]                      sb  fp32 [Nb, Kb]
   D   bf16 [M, N]
+
+8-bit-integer products (int8, one fp32 scale per row of each operand) and the
+gated feed-forward block (bf16 or int8; W [2F, K], gate rows then up rows) take
+row-major matrices.
 """
 
 from __future__ import annotations

@@ -30,6 +30,9 @@ section; the texts are machine-extracted and partly machine-translated):
   bullets and in 7minutos.es, "Detalles y beneficios tecnicos".
 * the M-grouped contiguous and masked forms (``oracle.gemm``): "Dense ve
   Grouped GEMM" of the same digest.
+* the 8-bit-integer cast and product and the gated feed-forward block with its
+  gradients (``oracle.linear``): float64 definitions of their formulas, with
+  the error bounds that the kernels' roundings allow.
 * acceptance metrics (``oracle.metrics``).
 
 Every function is pinned by tests in ``tests/test_oracle.py`` against
@@ -37,6 +40,6 @@ something other than itself (torch's own float8/bfloat16 conversions, exact
 rational brute force, closed forms and invariants).
 """
 
-from . import e4m3, quant, gemm, metrics  # noqa: F401
+from . import e4m3, quant, gemm, linear, metrics  # noqa: F401
 
-__all__ = ["e4m3", "quant", "gemm", "metrics"]
+__all__ = ["e4m3", "quant", "gemm", "linear", "metrics"]
