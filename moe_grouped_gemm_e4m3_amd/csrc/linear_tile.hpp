@@ -87,53 +87,52 @@ __device__ __forceinline__ int lin_swz(int row) {
   return row & 7;
 }
 
-// The loads of one operand, slice after slice and tile after tile, into the
-// LDS stages: 1 KiB each, straight into LDS, shared out over the waves.  Past
-// the workgroup's last tile they load zeros and touch no memory: every slice
-// issues the same number of loads, which the main loop's waits count on.
+// The loads of one operand's slices into the LDS stages: 1 KiB each, straight
+// into LDS, shared out over the waves.
 template <class C, bool IS_A>
 struct Loader {
   static constexpr bool MN = IS_A ? C::TA : C::TB;
   static constexpr bool PAIRED = !IS_A && C::GATED;  // gate and up rows
   static constexpr int N = IS_A ? C::LA : C::LB;     // loads per wave
   static constexpr int ROWS = IS_A ? C::BM : C::BN, COLS = IS_A ? C::BM : C::BROWS;
-  LinearWork t;
-  int kb;     // first slice of the step in tile t
-  int dst;    // LDS offset of its stage
-  // the ranges read (K-major: the tile's rows, gated: gate and up rows;
-  // MN-major: each slice's reduction rows)
-  __amdgpu_buffer_rsrc_t rs[MN ? C::KG : PAIRED ? 2 : 1];
+  // the ranges read (K-major: the tile's rows; MN-major: each slice's
+  // reduction rows)
+  __amdgpu_buffer_rsrc_t rs[MN ? C::KG : 1];
+  const uint8_t *gate, *up;  // gated: the tile's gate and up rows
+  int bytes;
   int cols;   // rows (MN-major: columns) of the operand from the tile's first on
   bool empty; // nothing to read: every offset is out of range
   const uint8_t* from;  // MN-major: the operand at the tile's first column
+  const uint8_t* at;    // MN-major: the first slice's first row
 
-  __device__ __forceinline__ Loader(const LinearParams& p, const LinearWork& first) : t(first), kb(first.kb0) {
-    dst = IS_A ? 0 : C::A_BYTES;
-    range(p);
-  }
-  // Ranges of the step at slice kb of tile t.
-  __device__ __forceinline__ void range(const LinearParams& p) {
+  static __device__ __forceinline__ int64_t ld(const LinearParams& p) { return IS_A ? p.lda : p.ldb; }
+
+  // The ranges of tile t.
+  __device__ __forceinline__ void tile(const LinearParams& p, const LinearWork& t) {
     const uint8_t* base = IS_A ? p.A : p.B;
-    const int64_t ld = IS_A ? p.lda : p.ldb;
     const int first = IS_A ? t.m0 : t.n0;
     cols = (IS_A ? p.M : p.N) - first;
     // no tile, or one of a gradient pair's padding columns alone
     empty = t.w < 0 || cols <= 0;
     if constexpr (MN) {
       from = empty ? base : base + (int64_t)first * 2;
-      slices(p);
     } else {
-      const int64_t bytes = empty ? 0 : (int64_t)(cols - 1) * ld + p.K * C::ES;
-      rs[0] = make_rsrc(base + (int64_t)first * ld, bytes);
-      if (PAIRED) rs[1] = make_rsrc(base + (int64_t)(p.N + first) * ld, bytes);
+      bytes = empty ? 0 : (int)min((int64_t)(cols - 1) * ld(p) + p.K * C::ES, (int64_t)0x7fffffff);
+      gate = base + (int64_t)first * ld(p);
+      if (PAIRED)
+        up = base + (int64_t)(p.N + first) * ld(p);
+      else
+        rs[0] = rows(gate, bytes);
     }
   }
-  // MN-major: the reduction rows of the step's slices.  Of W they are the
-  // hidden units of one half of the gradient pair.
-  __device__ __forceinline__ void slices(const LinearParams& p) {
-    const int ld = (int)(IS_A ? p.lda : p.ldb);  // at most 4 MiB
+  // MN-major: the rows of the step at slice kb; of W they are the hidden units
+  // of one half of the gradient pair.  Returns how many steps from this one on
+  // are whole slices of rows that follow each other.
+  __device__ __forceinline__ int slices(const LinearParams& p, int kb) {
+    int whole = 0;
+    const int pitch = (int)ld(p);  // at most 4 MiB
 #pragma unroll
-    for (int g = 0; g < C::KG; ++g) {
+    for (int g = C::KG - 1; g >= 0; --g) {
       int row = (kb + g) * 64, left = p.K - row;
       if (!IS_A && !C::TA && p.F > 0) {
         const bool up = row >= p.half;
@@ -141,33 +140,46 @@ struct Loader {
         row = up ? row - p.half + p.F : row;
       }
       const bool none = empty || left <= 0;
-      const int bytes = none ? 0 : (min(left, 64) - 1) * ld + cols * 2;
-      rs[g] = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(from + (none ? 0 : (int64_t)row * ld)), (short)0,
-                                                bytes, 0x00020000);
+      at = from + (none ? 0 : (int64_t)row * pitch);
+      rs[g] = rows(at, none ? 0 : (min(left, 64) - 1) * pitch + cols * 2);
+      whole = left / (64 * C::KG);
+    }
+    return empty ? 1 : whole;
+  }
+  static __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const uint8_t* first, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(first), (short)0, bytes, 0x00020000);
+  }
+  // MN-major: the next step's slices, where they are whole and follow.
+  __device__ __forceinline__ void next(const LinearParams& p) {
+    if constexpr (MN) {
+      at += ld(p) * (64 * C::KG);
+#pragma unroll
+      for (int g = 0; g < C::KG; ++g) rs[g] = rows(at + ld(p) * (64 * g), (int)ld(p) * 63 + cols * 2);
     }
   }
-  // Load j of this wave's N of the step, into its stage (lds + dst).
-  __device__ __forceinline__ void issue(const LinearParams& p, uint8_t* stage, int j, int wave, int lane) const {
-    const int64_t ld = IS_A ? p.lda : p.ldb;
+  // Load j of this wave's N of the step at slice kb, into its stage.
+  __device__ __forceinline__ void issue(const LinearParams& p, uint8_t* stage, int kb, int j, int wave, int lane) const {
     constexpr int PIECES = COLS / 8;  // 1 KiB pieces of a slice
     const int g = C::KG == 1 ? 0 : (wave * N + j) / PIECES, q = wave * N + j - g * PIECES;
-    __amdgpu_buffer_rsrc_t r = rs[0];
+    __amdgpu_buffer_rsrc_t r;
     int v, k = 0;
     if constexpr (MN) {  // whole stage rows of COLS columns
-      if (C::KG > 1 && g == 1) r = rs[C::KG - 1];
+      r = C::KG > 1 && g == 1 ? rs[C::KG - 1] : rs[0];
       constexpr int CH = COLS / 8;  // chunks per row
       const int row = q * (64 / CH) + lane / CH;
       const int c = (lane % CH) ^ mn_swz<CH>(row);
-      v = c * 8 < cols && (ROWS == COLS || c * 8 < ROWS) ? row * (int)ld + c * 16 : kOobOffset;
+      v = c * 8 < cols && (ROWS == COLS || c * 8 < ROWS) ? row * (int)ld(p) + c * 16 : kOobOffset;
     } else {  // 8 stage rows of 128 bytes
       int row = q * 8;
       if constexpr (PAIRED) {  // stage rows: 16 gate rows, 16 up rows of the same hidden units, ...
         row = (q >> 2) * 16 + (q & 1) * 8;
-        if ((q >> 1) & 1) r = rs[1];
+        r = rows((q >> 1) & 1 ? up : gate, bytes);
+      } else {
+        r = rs[0];
       }
       const int r8 = lane >> 3, c = ((lane & 7) ^ lin_swz(r8)) * 16;
       const int slice = kb + g;
-      v = ROWS == COLS || q * 8 < ROWS ? k_clip((row + r8) * (int)ld + c, slice * 128 + c, p.K * C::ES) : kOobOffset;
+      v = ROWS == COLS || q * 8 < ROWS ? k_clip((row + r8) * (int)ld(p) + c, slice * 128 + c, p.K * C::ES) : kOobOffset;
       // the scalar offset counts against the range's end and must not pass
       // it: 0 where nothing is read
       k = empty || (C::KG > 1 && slice >= p.nk) ? 0 : slice * 128;
@@ -175,15 +187,44 @@ struct Loader {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         r, (__attribute__((address_space(3))) void*)(stage + g * C::SLICE + q * 1024), 16, v, k, 0, 0);
   }
+};
+
+// Both operands' loads, step after step and tile after tile.  Past the
+// workgroup's last tile they load zeros and touch no memory: every step issues
+// the same number of loads, which the main loop's waits count on.
+template <class C>
+struct Loads {
+  LinearWork t;
+  int kb;   // first slice of the step in tile t
+  int dst;  // LDS offset of its stage
+  int run;  // steps until the ranges have to be worked out anew
+  Loader<C, true> a;
+  Loader<C, false> b;
+
+  __device__ __forceinline__ Loads(const LinearParams& p, const LinearWork& first) : t(first), kb(first.kb0), dst(0) {
+    a.tile(p, t);
+    b.tile(p, t);
+    slices(p);
+  }
+  __device__ __forceinline__ void slices(const LinearParams& p) {
+    run = C::KG == 1 ? t.kb1 - kb : (t.kb1 - kb + C::KG - 1) / C::KG;
+    if (C::TA) run = min(run, a.slices(p, kb));
+    if (C::TB) run = min(run, b.slices(p, kb));
+    run = max(run, 1);
+  }
   __device__ __forceinline__ void advance(const LinearParams& p, int grid) {
-    constexpr int FIRST = IS_A ? 0 : C::A_BYTES;
-    dst = dst == FIRST + (C::STAGES - 1) * C::STAGE ? FIRST : dst + C::STAGE;
+    dst = dst == (C::STAGES - 1) * C::STAGE ? 0 : dst + C::STAGE;
     kb += C::KG;
-    if (kb >= t.kb1) {
-      if (t.w >= 0) t = linear_work<C>(p, t.w + grid);
-      kb = t.kb0;
-      range(p);
-    } else if (MN) {
+    a.next(p);
+    b.next(p);
+    // out of line: the main loop's straight path has no other branch
+    if (__builtin_expect(--run == 0, 0)) {
+      if (kb >= t.kb1) {
+        if (t.w >= 0) t = linear_work<C>(p, t.w + grid);
+        kb = t.kb0;
+        a.tile(p, t);
+        b.tile(p, t);
+      }
       slices(p);
     }
   }
@@ -481,9 +522,8 @@ __device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>&
                                             const i32x4 (&b)[C::SN], i32x4 (&na)[C::SM], i32x4 (&nb)[C::SN],
                                             const FragReader<C::BM, C::TA, C::SM>& ra,
                                             const FragReader<C::BROWS, C::TB, C::SN>& rb, const uint8_t* __restrict st_a,
-                                            const uint8_t* __restrict st_b, const Loader<C, true>& la,
-                                            const Loader<C, false>& lb, uint8_t* __restrict ld_a,
-                                            uint8_t* __restrict ld_b, int wave, int lane) {
+                                            const uint8_t* __restrict st_b, const Loads<C>& ld,
+                                            uint8_t* __restrict ld_a, uint8_t* __restrict ld_b, int wave, int lane) {
   constexpr int READS = (C::SM + C::SN + C::SN - 1) / C::SN;
   constexpr int LOADS = LOAD ? C::LA + C::LB : 0;
 #pragma unroll
@@ -499,9 +539,9 @@ __device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>&
     for (int r = 0; r < LOADS; ++r) {
       if (r * C::SN / LOADS != j) continue;
       if (r < C::LB)
-        lb.issue(p, ld_b, r, wave, lane);
+        ld.b.issue(p, ld_b, ld.kb, r, wave, lane);
       else
-        la.issue(p, ld_a, r - C::LB, wave, lane);
+        ld.a.issue(p, ld_a, ld.kb, r - C::LB, wave, lane);
     }
     __builtin_amdgcn_sched_barrier(0);
     acc.mma(a, b, j);
@@ -528,8 +568,7 @@ __device__ __forceinline__ void linear_tiles(const LinearParams& p, uint8_t* lds
 
   LinearWork cur = linear_work<C>(p, xcd_local_id(block, grid));
   if (cur.w < 0) return;
-  Loader<C, true> la(p, cur);
-  Loader<C, false> lb(p, cur);
+  Loads<C> ld(p, cur);
 
   const FragReader<C::BM, C::TA, C::SM> ra(wm * C::WM, lane);
   const FragReader<C::BROWS, C::TB, C::SN> rb(wn * C::WN, lane);
@@ -537,14 +576,13 @@ __device__ __forceinline__ void linear_tiles(const LinearParams& p, uint8_t* lds
   LinearAcc<C> acc;
   acc.zero();
 
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < C::STAGES; ++i) {
 #pragma unroll
-    for (int j = 0; j < C::LA; ++j) la.issue(p, lds + la.dst, j, wave, lane);
-    la.advance(p, grid);
+    for (int j = 0; j < C::LA; ++j) ld.a.issue(p, lds + ld.dst, ld.kb, j, wave, lane);
 #pragma unroll
-    for (int j = 0; j < C::LB; ++j) lb.issue(p, lds + lb.dst, j, wave, lane);
-    lb.advance(p, grid);
+    for (int j = 0; j < C::LB; ++j) ld.b.issue(p, lds + C::A_BYTES + ld.dst, ld.kb, j, wave, lane);
+    ld.advance(p, grid);
   }
   linear_sync<(C::STAGES - 1) * (C::LA + C::LB)>();
 #pragma unroll
@@ -554,14 +592,13 @@ __device__ __forceinline__ void linear_tiles(const LinearParams& p, uint8_t* lds
   int s = slice;  // the group's slice of the current step
   while (cur.w >= 0) {
     for (int kb = cur.kb0; kb < cur.kb1; kb += C::KG) {
-      linear_half<C, 1, false>(p, acc, a0, b0, a1, b1, ra, rb, lds + s, lds + C::A_BYTES + s, la, lb, nullptr, nullptr,
-                               wave, lane);
+      linear_half<C, 1, false>(p, acc, a0, b0, a1, b1, ra, rb, lds + s, lds + C::A_BYTES + s, ld, nullptr, nullptr, wave,
+                               lane);
       linear_sync<(C::STAGES - 2) * (C::LA + C::LB)>();
       s = s == slice + (C::STAGES - 1) * C::STAGE ? slice : s + C::STAGE;
-      linear_half<C, 0, true>(p, acc, a1, b1, a0, b0, ra, rb, lds + s, lds + C::A_BYTES + s, la, lb, lds + la.dst,
-                              lds + lb.dst, wave, lane);
-      lb.advance(p, grid);
-      la.advance(p, grid);
+      linear_half<C, 0, true>(p, acc, a1, b1, a0, b0, ra, rb, lds + s, lds + C::A_BYTES + s, ld, lds + ld.dst,
+                              lds + C::A_BYTES + ld.dst, wave, lane);
+      ld.advance(p, grid);
     }
     if constexpr (C::KG > 1) {
       // group 1's sums go through LDS; it writes them again only after the
