@@ -507,8 +507,8 @@ fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
  *   dX  device [M, K] bf16, row stride lddx, or NULL (not wanted)
  *   dW  device [2F, K] bf16, row stride lddw, or NULL (not wanted)
  *   workspace  device, 256-byte aligned, fg_gated_ffn_backward_workspace_bytes(M, F, K) bytes; holds
- *       [dg du] in bf16 and, where dX is small, fp32 partials of its sum over 2F; needs no
- *       initialisation; in use until the call's work has finished
+ *       [dg du] in bf16 and, where dX or the pair is small, fp32 partials of their sums (at most
+ *       32 MiB); needs no initialisation; in use until the call's work has finished
  * dX and dW accumulate in fp32 over the bf16 pair [dg du].  M == 0 writes
  * dW = 0, F == 0 writes dX = 0.  F <= 2^20.  Outputs may not overlap inputs.
  */

@@ -75,18 +75,17 @@ double tile_us(double tiles, int cus, int nk, double idle, double busy, double s
 }
 
 // 64 x 64, eight waves in two groups: 0.185 us a slice (256 x 4096 x 7168 int8
-// 14.7 us, 26 on 128 x 128; 400 x 7168 x 2048 20 us against 12), 0.32 where
-// operands are MN-major.
+// 14.7 us, 26 on 128 x 128; 400 x 7168 x 2048 20 us against 12), 0.28 to 0.33
+// where operands are MN-major.
 double small_us(double tiles, int cus, int nk, bool mn) {
-  const double slice = mn ? 0.32 : 0.185;
-  return tile_us(tiles, cus, nk, slice, slice, 1.2);
+  return mn ? tile_us(tiles, cus, nk, 0.28, 0.33, 1.2) : tile_us(tiles, cus, nk, 0.185, 0.185, 1.2);
 }
 
 // 128 x 128, eight waves, four stages: 0.35 us alone, 0.52 with every CU at
-// work (1000 x 4096 x 7168 int8 34 us, 71 on 256 x 256), 0.5 and 0.62 where
+// work (1000 x 4096 x 7168 int8 34 us, 71 on 256 x 256), 0.46 and 0.57 where
 // operands are MN-major.
 double mid_us(double tiles, int cus, int nk, bool mn) {
-  return mn ? tile_us(tiles, cus, nk, 0.5, 0.62, 2.0) : tile_us(tiles, cus, nk, 0.35, 0.52, 2.0);
+  return mn ? tile_us(tiles, cus, nk, 0.46, 0.57, 2.0) : tile_us(tiles, cus, nk, 0.35, 0.52, 2.0);
 }
 
 // 128 x 128, two workgroups of four waves per CU: 0.66 us alone, 1.0 for both
@@ -130,9 +129,10 @@ double fewrow_us(const LinearParams& p, bool gated, int cus, const FewRowShape& 
   return f.base + (turns > 1 ? turns * f.shared : 1.0) * one;
 }
 
-// Splits of the reduction over workgroups (dX alone: its reduction is the
-// long axis 2 F).  The fp32 partials of at most kMaxSplits splits and
-// kMaxPartialBytes go to the workspace and a second launch adds them.
+// Splits of the reduction over workgroups, in the backward pass: of dX's sum
+// over 2F, and of the recomputed pre-activations' over K.  The fp32 partials
+// of at most kMaxSplits splits and kMaxPartialBytes go to the workspace and
+// the next launch adds them.
 constexpr int kMaxSplits = 16;
 constexpr int64_t kMaxPartialBytes = (int64_t)32 << 20;
 
@@ -144,23 +144,30 @@ int64_t partial_bytes(int64_t M, int64_t N) {
   return round_up(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one) * one, 256);
 }
 
+// Splits of p's reduction on bm x bm tiles, with partials of `one` bytes.
 struct SplitPlan {
   double us;
   int splits, nk;  // slices of a split (even)
 };
 
 template <class F>
-SplitPlan plan_split(const LinearParams& p, int cus, int bm, F cost) {
-  const double tiles = tile_count(p, p.N, false, bm, bm);
-  const int64_t one = (int64_t)p.M * p.N * 4;
-  const int most = (int)std::min<int64_t>(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one), (int64_t)(cus / tiles));
+SplitPlan plan_split(const LinearParams& p, int64_t cols, bool gated, bool mn, int64_t one, int cus, int bm, F cost) {
+  const double tiles = tile_count(p, cols, gated, bm, bm);
   SplitPlan s{1e30, 1, p.nk};
-  if (one > kMaxPartialBytes / 2 || most < 2) return s;
+  if (one > kMaxPartialBytes / 2 || tiles > cus / 2) return s;
+  const int most = (int)std::min<int64_t>(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one), (int64_t)(cus / tiles));
   s.nk = (int)round_up((p.nk + most - 1) / most, 2);
   s.splits = (p.nk + s.nk - 1) / s.nk;
-  // the partials are written and read at about 4 TB/s; the second launch is 4 us
-  s.us = cost(tiles * s.splits, cus, s.nk, true) + 4.0 + 2.0 * s.splits * one / 4e6;
+  // the partials are written and read at about 4 TB/s; the second launch is 3 us
+  s.us = cost(tiles * s.splits, cus, s.nk, mn) + 3.0 + 2.0 * s.splits * one / 4e6;
   return s;
+}
+
+// Bytes of the pre-activations' partials: none where 64 x 64 tiles (32 hidden
+// units) already take more than a third of 256 CUs.
+constexpr int kMaxPairTiles = 85;
+int64_t pair_partial_bytes(int64_t M, int64_t cols) {
+  return (M + 63) / 64 * (cols / 64) > kMaxPairTiles ? 0 : partial_bytes(M, cols);
 }
 
 template <int E>
@@ -178,8 +185,9 @@ struct TilePlan {
 // The environment variable FG_LINEAR_PLAN overrides the choice (tuning and
 // tests): a tile ("w256", "w224", "w192", "w160", "mid2", "mid", "small"), a
 // few-row shape ("few0" .. "few7"), or for the gradients "split-mid",
-// "split-small" (dX's sum) or "share-X-W" (X and W: mid or small).  A plan
-// that the call does not have leaves it its own.
+// "split-small" (dX's sum), "pair-mid", "pair-small" (the recomputed
+// pre-activations' sums) or "share-X-W" (X and W: mid or small).  A plan that
+// the call does not have leaves it its own.
 const char* forced_plan() {
   const char* f = getenv("FG_LINEAR_PLAN");
   return f ? f : "";
@@ -349,7 +357,9 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
     px.us = t.us;
     // 251 x 1016 with 178 slices: 60 us on 64 64 x 64 tiles, a quarter of the
     // device; split four ways 25 us with the addition.
-    const SplitPlan a = plan_split(*x, cus, 64, small_us), b = plan_split(*x, cus, 128, mid_us);
+    const int64_t one = (int64_t)x->M * x->N * 4;
+    const SplitPlan a = plan_split(*x, x->N, false, true, one, cus, 64, small_us);
+    const SplitPlan b = plan_split(*x, x->N, false, true, one, cus, 128, mid_us);
     const char* f = forced_plan();
     const bool force_small = strcmp(f, "split-small") == 0, force_mid = strcmp(f, "split-mid") == 0;
     const bool small_tiles = force_small || (!force_mid && a.us <= b.us);
@@ -370,7 +380,7 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
   if (x && w) {
     // One launch: the workgroups of both, one to a CU, dX's first.  The device
     // is busy for their total, and for the longest one at least.
-    double least = 0.95 * (x_us + w_us);
+    double least = x_us + w_us;
     TileKind kx = kW256, kw = kW256;
     const char* forced = forced_plan();
     for (const TileKind cx : {kMid, kSmall})
@@ -378,8 +388,8 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
         if (px.splits > 1 && cx != px.kind) continue;
         const int bx = cx == kMid ? 128 : 64, bw = cw == kMid ? 128 : 64;
         const double nx = tile_count(*x, x->N, false, bx, bx) * px.splits, nw = tile_count(*w, w->N, false, bw, bw);
-        const double tx = x->split_nk * (cx == kMid ? 0.62 : 0.36) + (cx == kMid ? 2.5 : 1.5);
-        const double tw = w->nk * (cw == kMid ? 0.75 : 0.42) + (cw == kMid ? 2.5 : 1.5);  // both operands MN-major
+        const double tx = x->split_nk * (cx == kMid ? 0.56 : 0.36) + (cx == kMid ? 2.5 : 1.5);
+        const double tw = w->nk * (cw == kMid ? 0.66 : 0.42) + (cw == kMid ? 2.5 : 1.5);  // both operands MN-major
         const double us = 3.4 + std::max(std::max(tx, tw), (nx * tx + nw * tw) / cus + 0.5 * std::min(tx, tw)) +
                           (px.splits > 1 ? 4.0 : 0.0);
         if (nx + nw >= (1 << 22)) continue;
@@ -447,9 +457,54 @@ fg_status check_activation(int act) {
 
 int64_t pair_cols(int F) { return 2 * round_up(F, kPairAlign); }
 
-// The gradient pair, then dX's partials.
+// The gradient pair, then partials.
 int64_t pair_bytes(int M, int F) { return round_up((int64_t)M * pair_cols(F) * 2, 256); }
-int64_t backward_bytes(int M, int F, int K) { return pair_bytes(M, F) + partial_bytes(M, K); }
+int64_t backward_bytes(int M, int F, int K) {
+  return pair_bytes(M, F) + std::max(partial_bytes(M, K), pair_partial_bytes(M, pair_cols(F)));
+}
+
+// [dg du] from pre-activations in g.P: kept ones, or `parts` partial sums.
+template <bool PARTS>
+fg_status launch_gated_grad(const LinearParams& g, int parts, void* stream, const char* what) {
+  const int64_t blocks = ((int64_t)g.M * (g.half / (PARTS ? 4 : 8)) + 255) / 256;
+  const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 16));
+  if (g.act == kActSilu)
+    hipLaunchKernelGGL((gated_grad_kernel<kActSilu, PARTS>), grid, dim3(256), 0, (hipStream_t)stream, g, parts);
+  else
+    hipLaunchKernelGGL((gated_grad_kernel<kActGeluTanh, PARTS>), grid, dim3(256), 0, (hipStream_t)stream, g, parts);
+  return launched(what);
+}
+
+// [dg du] with the pre-activations recomputed: in the product's own epilogue,
+// or, where its tiles leave most of the device idle, from partial sums in
+// `partials` (with dW, 395 x 36 x 6232: 40 us without, 22 with; 595 x 175 x
+// 3320: 31 and 24).
+fg_status launch_recompute(LinearParams& g, float* partials, void* stream, const char* what) {
+  int cus = 0;
+  FG_TRY(usable_cus(&cus));
+  if (pair_partial_bytes(g.M, 2 * g.half) > 0) {
+    g.nk = slice_count<kEpiGatedPartial>(g);
+    const int64_t one = (int64_t)g.M * g.half * 8;
+    const SplitPlan a = plan_split(g, g.half, true, false, one, cus, 64, small_us);
+    const SplitPlan b = plan_split(g, g.half, true, false, one, cus, 128, mid_us);
+    const char* f = forced_plan();
+    const bool force_small = strcmp(f, "pair-small") == 0, force_mid = strcmp(f, "pair-mid") == 0;
+    const bool small_tiles = force_small || (!force_mid && a.us <= b.us);
+    const SplitPlan& s = small_tiles ? a : b;
+    const double whole = plan_tile(g, g.half, true, false, cus).us;
+    if (s.splits > 1 && ((!*f && s.us < whole) || force_small || force_mid)) {
+      g.P = partials;
+      g.ldp = 2 * g.half;
+      g.split_nk = s.nk;
+      if (small_tiles)
+        FG_TRY((launch_tile<SmallTile<kEpiGatedPartial, false, false>>(g, cus, g.half, stream, what, s.splits)));
+      else
+        FG_TRY((launch_tile<MidTile<kEpiGatedPartial, false, false>>(g, cus, g.half, stream, what, s.splits)));
+      return launch_gated_grad<true>(g, s.splits, stream, what);
+    }
+  }
+  return launch_linear<kEpiGatedGrad>(g, stream, what);
+}
 
 template <typename T>
 fg_status cast_rows(const T* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream, const char* what) {
@@ -598,17 +653,8 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
     g.dH = dH; g.lddh = lddh; g.P = const_cast<float*>(P); g.ldp = ldp;
     g.D = (uint16_t*)workspace; g.ldd = pair_ld;
     g.M = M; g.N = F; g.K = K;
-    if (P) {
-      const int64_t blocks = ((int64_t)M * (g.half / 8) + 255) / 256;
-      const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 16));
-      if (activation == FG_ACT_SILU)
-        hipLaunchKernelGGL((gated_grad_kernel<kActSilu>), grid, dim3(256), 0, (hipStream_t)stream, g);
-      else
-        hipLaunchKernelGGL((gated_grad_kernel<kActGeluTanh>), grid, dim3(256), 0, (hipStream_t)stream, g);
-      FG_TRY(launched(what));
-    } else {
-      FG_TRY((launch_linear<kEpiGatedGrad>(g, stream, what)));
-    }
+    FG_TRY(P ? launch_gated_grad<false>(g, 0, stream, what)
+             : launch_recompute(g, (float*)((uint8_t*)workspace + pair_bytes(M, F)), stream, what));
   }
   // With M or F of zero the reductions below are empty and write zeros.
   LinearParams x = p, w = p;

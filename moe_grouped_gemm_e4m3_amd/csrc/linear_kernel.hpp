@@ -38,8 +38,11 @@ enum LinearEpi {
   kEpiGatedInt8,  // the same with g, u = sa sb acc
   kEpiGatedGrad,  // D = bf16([dg du]) from g, u and dH
   kEpiGatedKeep,  // kEpiGated and P = [g u] in fp32
+  // P[split] = [g u], [M, 2 half] in fp32: one split of the reduction
+  kEpiGatedPartial,
 };
 constexpr bool epi_gated(int e) { return e >= kEpiGated; }
+constexpr bool epi_partial(int e) { return e == kEpiPartial || e == kEpiGatedPartial; }
 constexpr bool epi_int8(int e) { return e == kEpiInt8 || e == kEpiGatedInt8; }
 
 enum { kActSilu = 0, kActGeluTanh = 1 };
@@ -62,7 +65,7 @@ struct LinearParams {
   // As the reduction axis (dX) or the output rows (dW) index r stands for
   // hidden unit r < F of the first half and r - half of the second.
   int F, half;
-  // slices of the reduction (kEpiPartial: and of one split, an even number)
+  // slices of the reduction (partial sums: and of one split, an even number)
   // and output tiles of the persistent grid (linear_tile.hpp)
   int nk, split_nk;
   int tiles_m, tiles_n, num_tiles, group_m;
@@ -104,54 +107,81 @@ __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)(pack_bf16x2(v, 0.f) & 0xffff); }
 
-// [dg du] from the kept pre-activations P = [g u], eight columns a thread.
-// Bound by HBM: 10 bytes in and 4 out for each hidden unit and row.
-template <int ACT>
-__global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p) {
-  const int per_row = p.half / 8;
+// [dg du] from the pre-activations P = [g u]: the kept ones ([M, 2F]; eight
+// columns a thread, bound by HBM: 10 bytes in and 4 out for each hidden unit
+// and row), or PARTS of them, partial sums ([M, 2 half] each) that are added
+// in order; four columns a thread and eight partials in flight, since the
+// tensor is small and its loads' latency counts (112 x 119, 16 partials: 12 us
+// with eight columns and four).
+template <int ACT, bool PARTS>
+__global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p, int parts) {
+  constexpr int C = PARTS ? 4 : 8;
+  const int per_row = p.half / C;
   const int64_t total = (int64_t)p.M * per_row;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
     const int64_t m = i / per_row;
-    const int n = (int)(i - m * per_row) * 8;
+    const int n = (int)(i - m * per_row) * C;
     const float* gp = p.P + m * p.ldp + n;
-    const float* up = gp + p.N;
+    const float* up = gp + (PARTS ? p.half : p.N);
     const uint16_t* hp = p.dH + m * p.lddh + n;
-    float g[8], u[8], h[8];
-    if (n + 8 <= p.N) {
-      const f32x4 g0 = *(const f32x4_at4*)gp, g1 = *(const f32x4_at4*)(gp + 4);
-      const f32x4 u0 = *(const f32x4_at4*)up, u1 = *(const f32x4_at4*)(up + 4);
-      const uint4 hv = *(const uint4_at2*)hp;
-      const uint32_t hw[4] = {hv.x, hv.y, hv.z, hv.w};
+    float g[C], u[C];
+    uint32_t h[C / 2];
+    if (PARTS || n + C <= p.N) {
+      f32x4 gv[C / 4], uv[C / 4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        g[r] = g0[r];
-        g[4 + r] = g1[r];
-        u[r] = u0[r];
-        u[4 + r] = u1[r];
-        h[2 * r] = __uint_as_float(hw[r] << 16);
-        h[2 * r + 1] = __uint_as_float(hw[r] & 0xffff0000u);
+      for (int q = 0; q < C / 4; ++q) {
+        gv[q] = *(const f32x4_at4*)(gp + 4 * q);
+        uv[q] = *(const f32x4_at4*)(up + 4 * q);
+      }
+      if constexpr (PARTS) {
+        const int64_t one = p.M * p.ldp;
+#pragma unroll 8
+        for (int k = 1; k < parts; ++k) {
+          gv[0] += *(const f32x4*)(gp + k * one);
+          uv[0] += *(const f32x4*)(up + k * one);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < C; ++r) {
+        g[r] = gv[r / 4][r % 4];
+        u[r] = uv[r / 4][r % 4];
       }
     } else {
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const bool in = n + r < p.N;  // padding columns hold zeros
-        g[r] = in ? gp[r] : 0.f;
-        u[r] = in ? up[r] : 0.f;
-        h[r] = in ? to_f32(hp[r]) : 0.f;
+      for (int r = 0; r < C; ++r) {
+        g[r] = n + r < p.N ? gp[r] : 0.f;  // padding columns hold zeros
+        u[r] = n + r < p.N ? up[r] : 0.f;
       }
     }
-    uint32_t dg[4], du[4];
+    if (n + C <= p.N) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+      for (int q = 0; q < C / 4; ++q) {
+        const uint2 v = *(const uint2_at2*)(hp + 4 * q);
+        h[2 * q] = v.x;
+        h[2 * q + 1] = v.y;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < C / 2; ++q)
+        h[q] = (n + 2 * q < p.N ? (uint32_t)hp[2 * q] : 0u) | (n + 2 * q + 1 < p.N ? (uint32_t)hp[2 * q + 1] << 16 : 0u);
+    }
+    uint32_t dg[C / 2], du[C / 2];
+#pragma unroll
+    for (int q = 0; q < C / 2; ++q) {
       float a0, b0, a1, b1;
-      gated_grad<ACT>(h[2 * r], g[2 * r], u[2 * r], a0, b0);
-      gated_grad<ACT>(h[2 * r + 1], g[2 * r + 1], u[2 * r + 1], a1, b1);
-      dg[r] = pack_bf16x2(a0, a1);
-      du[r] = pack_bf16x2(b0, b1);
+      gated_grad<ACT>(__uint_as_float(h[q] << 16), g[2 * q], u[2 * q], a0, b0);
+      gated_grad<ACT>(__uint_as_float(h[q] & 0xffff0000u), g[2 * q + 1], u[2 * q + 1], a1, b1);
+      dg[q] = pack_bf16x2(a0, a1);
+      du[q] = pack_bf16x2(b0, b1);
     }
     uint16_t* dst = p.D + m * p.ldd + n;
-    *(uint4*)dst = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-    *(uint4*)(dst + p.half) = make_uint4(du[0], du[1], du[2], du[3]);
+    if constexpr (PARTS) {
+      *(uint2*)dst = make_uint2(dg[0], dg[1]);
+      *(uint2*)(dst + p.half) = make_uint2(du[0], du[1]);
+    } else {
+      *(uint4*)dst = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+      *(uint4*)(dst + p.half) = make_uint4(du[0], du[1], du[2], du[3]);
+    }
   }
 }
 
@@ -163,7 +193,7 @@ static __global__ __launch_bounds__(256) void add_partials_kernel(LinearParams p
   const f32x4* src = (const f32x4*)p.P;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
     f32x4 s = src[i];
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 1; k < splits; ++k) s += src[k * quads + i];
     const int64_t m = i / per_row;
     *(uint2_at2*)(p.D + m * p.ldd + (i - m * per_row) * 4) =

@@ -54,7 +54,7 @@ __device__ __forceinline__ LinearWork linear_work(const LinearParams& p, int w) 
   t.kb1 = p.nk;
   if (w < p.num_tiles) {
     t.w = w;
-    if (C::E == kEpiPartial) {  // every tile of one split, then the next split's
+    if (epi_partial(C::E)) {  // every tile of one split, then the next split's
       const int tiles = p.tiles_m * p.tiles_n, split = w / tiles;
       w -= split * tiles;
       t.kb0 = split * p.split_nk;
@@ -350,7 +350,7 @@ __device__ __forceinline__ void store_blocks(const LinearParams& p, const Linear
   constexpr int STEP = C::GATED ? 2 : 1;       // accumulator blocks per output block
   constexpr int NB = C::SN / STEP;             // output blocks of the wave
   const int nw = t.n0 + wn * NB * 16;          // the wave's first output column
-  const int n_end = GRAD ? p.half : p.N;
+  const int n_end = GRAD || C::E == kEpiGatedPartial ? p.half : p.N;
   f32x4 sb[C::INT8 ? C::SN : 1];
   if constexpr (C::INT8) {
 #pragma unroll
@@ -360,15 +360,20 @@ __device__ __forceinline__ void store_blocks(const LinearParams& p, const Linear
       if (C::GATED) sb[j * STEP + 1] = load_f32x4(p.sb + p.N, n, p.N);
     }
   }
-  if constexpr (C::E == kEpiPartial) {
-    float* part = p.P + (int64_t)(t.kb0 / p.split_nk) * p.M * p.N;
+  if constexpr (epi_partial(C::E)) {
+    const int cols = C::GATED ? 2 * p.half : p.N;
+    float* part = p.P + (int64_t)(t.kb0 / p.split_nk) * p.M * cols;
 #pragma unroll
     for (int i = 0; i < C::SM; ++i) {
       const int m = t.m0 + wm * C::WM + i * 16 + l16;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const int n = nw + j * 16 + 4 * kq;  // N is a multiple of 4
-        if (FULL || (m < p.M && n < p.N)) *(f32x4*)(part + (int64_t)m * p.N + n) = acc.v[i][j];
+        float* dst = part + (int64_t)m * cols + n;
+        if (FULL || (m < p.M && n < n_end)) {
+          *(f32x4*)dst = __builtin_bit_cast(f32x4, acc.v[i][j * STEP]);
+          if constexpr (C::GATED) *(f32x4*)(dst + p.half) = acc.v[i][j * STEP + 1];
+        }
       }
     }
     return;
@@ -479,7 +484,7 @@ __device__ __forceinline__ void store_linear(const LinearParams& p, const Linear
   else
     full = full && t.m0 + C::BM <= p.M;
   if (C::E == kEpiGatedKeep) full = full && p.ldp <= 1 << 24;  // 32-bit offsets within 16 rows of P
-  if constexpr (C::GATED) {
+  if constexpr (C::GATED && !epi_partial(C::E)) {
     if (p.act == kActSilu) {
       if (full)
         store_blocks<C, kActSilu, true>(p, t, acc, wm, wn, lane);

@@ -73,9 +73,10 @@ def test_gated_plans(gpu_lib, monkeypatch, plan, form, M, F, K):
     assert_within(out.f64(), ref.gated(g, u, act), ref.gated_bound(g, u, eg, eu, act), plan)
 
 
-@pytest.mark.parametrize("plan", ["w256", "w224", "w160", "mid2", "mid", "small", "split-mid", "split-small",
+@pytest.mark.parametrize("plan", ["w256", "w224", "w160", "mid2", "mid", "small", "split-mid", "split-small", "pair-mid", "pair-small",
                                   "share-mid-mid", "share-mid-small", "share-small-mid", "share-small-small"])
-@pytest.mark.parametrize("M,F,K", [(3, 11, 72), (130, 450, 136), (700, 100, 1304), (65, 700, 264)])
+@pytest.mark.parametrize("M,F,K", [(3, 11, 72), (130, 450, 136), (700, 100, 1304), (65, 700, 264),
+                                   (190, 70, 1928)])
 def test_gradient_plans(gpu_lib, monkeypatch, plan, M, F, K):
     announce(f"gradient plan {plan} {M}x{F}x{K}")
     forced(monkeypatch, plan)
