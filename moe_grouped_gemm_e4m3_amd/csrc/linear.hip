@@ -75,21 +75,21 @@ double tile_us(double tiles, int cus, int nk, double idle, double busy, double s
 }
 
 // 64 x 64, eight waves in two groups: 0.185 us a slice (256 x 4096 x 7168 int8
-// 14.7 us, 26 on 128 x 128; 400 x 7168 x 2048 20 us against 12), 0.28 to 0.33
+// 17 us, 28 on 128 x 128; 400 x 7168 x 2048 22 us against 13), 0.28 to 0.33
 // where operands are MN-major.
 double small_us(double tiles, int cus, int nk, bool mn) {
   return mn ? tile_us(tiles, cus, nk, 0.28, 0.33, 1.2) : tile_us(tiles, cus, nk, 0.185, 0.185, 1.2);
 }
 
 // 128 x 128, eight waves, four stages: 0.35 us alone, 0.52 with every CU at
-// work (1000 x 4096 x 7168 int8 34 us, 71 on 256 x 256), 0.46 and 0.57 where
+// work (1000 x 4096 x 7168 int8 33 us, 72 on 256 x 256), 0.46 and 0.57 where
 // operands are MN-major.
 double mid_us(double tiles, int cus, int nk, bool mn) {
   return mn ? tile_us(tiles, cus, nk, 0.46, 0.57, 2.0) : tile_us(tiles, cus, nk, 0.35, 0.52, 2.0);
 }
 
 // 128 x 128, two workgroups of four waves per CU: 0.66 us alone, 1.0 for both
-// (4096 x 4096 x 7168 int8 112 us, 92 on 256 x 256); a round that leaves one
+// (4096 x 4096 x 7168 int8 107 us, 92 on 256 x 256); a round that leaves one
 // workgroup per CU is cheaper.
 double mid2_us(double tiles, int cus, int nk) {
   const double full = floor(tiles / (2 * cus)), rest = tiles - full * 2 * cus;
@@ -225,8 +225,8 @@ TilePlan plan_tile(const LinearParams& p, int64_t cols, bool gated, bool mn, int
   };
   // 256 rows by 256, 224, 192 or 160: 1.2, 1.1, 1.0 and 0.92 us a slice with
   // few CUs at work, 1.45, 1.36, 1.15 and 1.02 with all, which the chip's power
-  // limits (int8 4096 x 7168 x 16384: 380 us with 256 columns, 364 with 224;
-  // 4096 x 2112 x 7168: 80 with 256, 63 with 160).
+  // limits (int8 4096 x 7168 x 16384: 372 us with 256 columns, 343 with 224;
+  // 4096 x 2112 x 7168: 78 with 256, 60 with 160).
   offer(kW256, tile_us(count(256, 256), cus, p.nk, 1.2, 1.45, 4.0));
   if (gated) {
     offer(kW192, tile_us(count(256, 192), cus, p.nk, 1.0, 1.15, 4.0));
@@ -355,8 +355,8 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
     const TilePlan t = plan_tile(*x, x->N, false, true, cus);
     px.kind = t.kind;
     px.us = t.us;
-    // 251 x 1016 with 178 slices: 60 us on 64 64 x 64 tiles, a quarter of the
-    // device; split four ways 25 us with the addition.
+    // 251 x 1016 with 178 slices: 52 us on 64 64 x 64 tiles, a quarter of the
+    // device; split 27 us with the addition.
     const int64_t one = (int64_t)x->M * x->N * 4;
     const SplitPlan a = plan_split(*x, x->N, false, true, one, cus, 64, small_us);
     const SplitPlan b = plan_split(*x, x->N, false, true, one, cus, 128, mid_us);

@@ -1,5 +1,14 @@
 // linear_tile.hpp -- the large-tile kernel of the 8-bit-integer and bf16
 // products (operations and epilogues: linear_kernel.hpp).
+//
+// A slice of a 256 x 256 tile is 2048 MFMA cycles for 64 KiB of loads; the
+// chip's power limits it (2.0 GHz): int8 4096 x 7168 x 16384 336 us, 2860
+// TOP/s; gated bf16 4096 x 2048 x 7168 150 us, 1600 TFLOP/s; dX and dW at
+// 4096 x 7168 x 4096 181 and 187 us, 1330 and 1290 TFLOP/s, their transposing
+// fragment reads twice as many.  Smaller tiles are bound by each CU's loads
+// and the barrier of a slice (128 x 128: 62 GB/s a CU).  K-major rows that do
+// not lie a multiple of 128 bytes apart cost 15 to 40 % more: a slice of such a
+// row takes parts of two cache lines.
 #pragma once
 
 #include "linear_kernel.hpp"
@@ -341,7 +350,8 @@ __device__ __forceinline__ void store_quad(uint16_t* row, int n, int n_end, bool
 // The finished tile, straight from the accumulators.  Lane (l16, kq) holds
 // row l16 and columns [4 kq, +4) of every 16 x 16 block.  FULL: the whole tile
 // lies inside the output, so nothing is tested
-// (gated 4096 x 12288 x 1536: 250 us with the tests, 214 without).
+// (gated with kept pre-activations, 4096 x 2048 x 7168: 177 us with the tests,
+// 158 without).
 template <class C, int ACT, bool FULL>
 __device__ __forceinline__ void store_blocks(const LinearParams& p, const LinearWork& t, const LinearAcc<C>& acc,
                                              int wm, int wn, int lane) {
@@ -519,9 +529,10 @@ __device__ __forceinline__ void linear_sync() {
 
 // One half of a slice: the MFMAs on fragments (a, b), and between them the
 // reads of the next half's fragments (na, nb) from stages st_a and st_b and
-// LOAD, the loads of a later slice into ld_a and ld_b, spread evenly: issued together they would fill the memory pipe's queue and hold up
-// the MFMAs behind them.  No two of the four stages overlap here, and the
-// compiler is told so: it would otherwise wait for the loads before it reads.
+// LOAD, the loads of a later slice into ld_a and ld_b, spread evenly: issued
+// together they would fill the memory pipe's queue and hold up the MFMAs
+// behind them.  No two of the four stages overlap here, and the compiler is
+// told so: it would otherwise wait for the loads before it reads.
 template <class C, int H, bool LOAD>
 __device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>& acc, const i32x4 (&a)[C::SM],
                                             const i32x4 (&b)[C::SN], i32x4 (&na)[C::SM], i32x4 (&nb)[C::SN],
