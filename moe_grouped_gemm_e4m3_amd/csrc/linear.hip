@@ -107,18 +107,18 @@ fg_status launch_fewrow(const LinearParams& p, void* stream, const char* what) {
 
 // Few-row shapes: 16 mf rows, 16 cf weight rows, waves.  A wave's step of one
 // slice takes `idle` to `busy` us by how many CUs are at work; workgroups that
-// share a CU take `shared` of their time one after the other.  Fitted to 1200
-// measurements (1 to 640 rows, 300 to 12288 columns, K of 512 to 14336 bytes,
-// int8 and gated bf16): the choice is within 2 % of the fastest shape on
-// average and 25 % at worst.
+// share a CU take `shared` of their time one after the other.  Fitted to 870
+// shapes (1 to 640 rows, 64 to 12000 columns, rows of 256 bytes to 15 KiB,
+// int8 and gated bf16): on 300 others the choice, tiles included, is 1 %
+// slower than the fastest on average, 45 % at worst.
 struct FewRowShape {
   int mf, cf, waves;
   double base, idle, busy, shared;
 };
 constexpr FewRowShape kFewRowShapes[] = {
-    {1, 1, 4, 1.2, 0.20, 0.32, 0.75}, {1, 1, 8, 1.2, 0.22, 0.66, 0.70}, {1, 2, 4, 1.2, 0.18, 0.54, 0.70},
-    {2, 1, 4, 1.5, 0.18, 0.34, 0.85}, {2, 2, 4, 1.5, 0.22, 0.54, 0.85}, {4, 1, 4, 1.8, 0.26, 0.50, 0.85},
-    {4, 2, 4, 1.8, 0.46, 0.70, 1.00}, {4, 4, 4, 1.8, 0.95, 1.20, 1.30},
+    {1, 1, 4, 1.20, 0.17, 0.32, 1.00}, {1, 1, 8, 1.47, 0.26, 0.55, 0.70}, {1, 2, 4, 1.15, 0.21, 0.49, 0.73},
+    {2, 1, 4, 1.57, 0.29, 0.36, 0.91}, {2, 2, 4, 1.50, 0.25, 0.54, 0.82}, {4, 1, 4, 2.00, 0.31, 0.47, 1.04},
+    {4, 2, 4, 1.80, 0.38, 0.80, 1.09}, {4, 4, 4, 1.75, 1.29, 1.29, 1.32},
 };
 constexpr int kFewRowMost = 640;  // rows up to which these shapes are considered
 
