@@ -38,7 +38,9 @@ fg_status launched(const char* what) {
 // Plans.  Each candidate's time is estimated from its tiles and slices with
 // costs measured on MI355X (256 CUs; microseconds; int8 and bf16 slices cost
 // the same, both are 128 bytes and 2048 MFMA cycles on the 256 x 256 tile),
-// and the cheapest runs.  The estimates only rank candidates.
+// and the cheapest runs.  The estimates only rank candidates: fitted to 700
+// random products and 150 gradients, on others the choice is 2 % (gradients 1 %)
+// slower than the fastest tile on average.
 
 // Lays p's output out in C's tiles (`splits` times over).
 template <class C>
@@ -74,26 +76,50 @@ double tile_us(double tiles, int cus, int nk, double idle, double busy, double s
   return 3.4 + ceil(tiles / cus) * (nk * (idle + (busy - idle) * load * load) + store);
 }
 
-// 64 x 64, eight waves in two groups: 0.185 us a slice (256 x 4096 x 7168 int8
-// 17 us, 28 on 128 x 128; 400 x 7168 x 2048 22 us against 13), 0.28 to 0.33
-// where operands are MN-major.
+// Two workgroups to a CU: `idle` to `one` a slice while every CU has at most
+// one, `two` for both.
+double pairs_us(double tiles, int cus, int nk, double idle, double one, double two, double store) {
+  const double full = floor(tiles / (2 * cus)), rest = tiles - full * 2 * cus, load = rest / cus;
+  double us = 3.4 + full * (nk * two + store);
+  if (rest > 0) us += nk * (rest > cus ? two : idle + (one - idle) * load * load) + store;
+  return us;
+}
+
+// The tiles below 256 rows, with their times a slice where both operands are
+// K-major and where one or both are MN-major (mn).
+//
+// 64 x 64, eight waves, for few tiles: in two groups (256 x 4096 x 7168 int8 17
+// us, 28 on 128 x 128); where operands are MN-major in one, so that every sum
+// of a gradient runs in the order of its slices and its bits depend on nothing
+// but the split.  There it serves splits and shared launches alone: two
+// workgroups of four waves are as fast with few tiles (dX 333 x 1528 x 2176 13
+// us both) and faster with many.
 double small_us(double tiles, int cus, int nk, bool mn) {
-  return mn ? tile_us(tiles, cus, nk, 0.28, 0.33, 1.2) : tile_us(tiles, cus, nk, 0.185, 0.185, 1.2);
+  return mn ? tile_us(tiles, cus, nk, 0.28, 0.35, 1.2) : tile_us(tiles, cus, nk, 0.177, 0.19, 1.5);
 }
 
-// 128 x 128, eight waves, four stages: 0.35 us alone, 0.52 with every CU at
-// work (1000 x 4096 x 7168 int8 33 us, 72 on 256 x 256), 0.46 and 0.57 where
-// operands are MN-major.
+// 64 x 64, two workgroups of four waves, where tiles outnumber the CUs (dW
+// 2176 x 1528 x 333 12 us, 13 on eight waves).
+double small2_us(double tiles, int cus, int nk, bool mn) {
+  return mn ? pairs_us(tiles, cus, nk, 0.22, 0.32, 0.68, 1.3) : pairs_us(tiles, cus, nk, 0.187, 0.19, 0.54, 1.25);
+}
+
+// 128 x 64, two workgroups of eight waves (512 x 4096 x 7168 int8 28 us, 31 on
+// 128 x 128 and on 64 x 64; gated bf16 333 x 1056 x 1528 11 us, 17 on 128 x 128).
+double half2_us(double tiles, int cus, int nk, bool mn) {
+  return mn ? pairs_us(tiles, cus, nk, 0.30, 0.39, 0.75, 1.7) : pairs_us(tiles, cus, nk, 0.23, 0.30, 0.66, 1.9);
+}
+
+// 128 x 128, eight waves, four stages (1000 x 4096 x 7168 int8 33 us, 72 on
+// 256 x 256).
 double mid_us(double tiles, int cus, int nk, bool mn) {
-  return mn ? tile_us(tiles, cus, nk, 0.46, 0.57, 2.0) : tile_us(tiles, cus, nk, 0.35, 0.52, 2.0);
+  return mn ? tile_us(tiles, cus, nk, 0.46, 0.53, 2.0) : tile_us(tiles, cus, nk, 0.44, 0.51, 2.4);
 }
 
-// 128 x 128, two workgroups of four waves per CU: 0.66 us alone, 1.0 for both
-// (4096 x 4096 x 7168 int8 107 us, 92 on 256 x 256); a round that leaves one
-// workgroup per CU is cheaper.
-double mid2_us(double tiles, int cus, int nk) {
-  const double full = floor(tiles / (2 * cus)), rest = tiles - full * 2 * cus;
-  return 3.4 + full * (nk * 1.0 + 1.5) + (rest > 0 ? nk * (rest > cus ? 1.0 : 0.66) + 1.5 : 0);
+// 128 x 128, two workgroups of four waves (dW 3072 x 2048 x 1500 28 us, 33 on
+// eight waves).
+double mid2_us(double tiles, int cus, int nk, bool mn) {
+  return mn ? pairs_us(tiles, cus, nk, 0.80, 0.80, 0.90, 1.5) : pairs_us(tiles, cus, nk, 0.70, 0.70, 0.90, 1.5);
 }
 
 template <class C>
@@ -158,8 +184,8 @@ SplitPlan plan_split(const LinearParams& p, int64_t cols, bool gated, bool mn, i
   const int most = (int)std::min<int64_t>(std::min<int64_t>(kMaxSplits, kMaxPartialBytes / one), (int64_t)(cus / tiles));
   s.nk = (int)round_up((p.nk + most - 1) / most, 2);
   s.splits = (p.nk + s.nk - 1) / s.nk;
-  // the partials are written and read at about 4 TB/s; the second launch is 3 us
-  s.us = cost(tiles * s.splits, cus, s.nk, mn) + 3.0 + 2.0 * s.splits * one / 4e6;
+  // the partials are written and read at about 4 TB/s; the second launch is 2.3 us
+  s.us = cost(tiles * s.splits, cus, s.nk, mn) + 2.3 + 2.0 * s.splits * one / 4e6;
   return s;
 }
 
@@ -176,15 +202,15 @@ int slice_count(const LinearParams& p) {
 }
 
 // The cheapest tile for p (its slices set) and its time.
-enum TileKind { kW256, kW224, kW192, kW160, kMid2, kMid, kSmall };
+enum TileKind { kW256, kW224, kW192, kW160, kMid2, kMid, kHalf2, kSmall2, kSmall };
 struct TilePlan {
   TileKind kind;
   double us;
 };
 
 // The environment variable FG_LINEAR_PLAN overrides the choice (tuning and
-// tests): a tile ("w256", "w224", "w192", "w160", "mid2", "mid", "small"), a
-// few-row shape ("few0" .. "few7"), or for the gradients "split-mid",
+// tests): a tile ("w256", "w224", "w192", "w160", "mid2", "mid", "half2",
+// "small2", "small"), a few-row shape ("few0" .. "few7"), or for the gradients "split-mid",
 // "split-small" (dX's sum), "pair-mid", "pair-small" (the recomputed
 // pre-activations' sums) or "share-X-W" (X and W: mid or small).  A plan that
 // the call does not have leaves it its own.
@@ -198,7 +224,7 @@ bool forced_tile(bool gated, TileKind* kind) {
     const char* name;
     TileKind kind;
   } names[] = {{"w256", kW256}, {"w224", kW224}, {"w192", kW192}, {"w160", kW160},
-               {"mid2", kMid2}, {"mid", kMid},   {"small", kSmall}};
+               {"mid2", kMid2}, {"mid", kMid},   {"half2", kHalf2}, {"small2", kSmall2}, {"small", kSmall}};
   const char* f = forced_plan();
   if (!*f) return false;
   for (const auto& n : names)
@@ -223,27 +249,29 @@ TilePlan plan_tile(const LinearParams& p, int64_t cols, bool gated, bool mn, int
   auto offer = [&](TileKind kind, double us) {
     if (us < best.us) best = TilePlan{kind, us};
   };
-  // 256 rows by 256, 224, 192 or 160: 1.2, 1.1, 1.0 and 0.92 us a slice with
-  // few CUs at work, 1.45, 1.36, 1.15 and 1.02 with all, which the chip's power
+  // 256 rows by 256, 224, 192 or 160: the time a slice grows with the CUs at
+  // work, since the chip's power
   // limits (int8 4096 x 7168 x 16384: 372 us with 256 columns, 343 with 224;
   // 4096 x 2112 x 7168: 78 with 256, 60 with 160).
-  offer(kW256, tile_us(count(256, 256), cus, p.nk, 1.2, 1.45, 4.0));
+  offer(kW256, tile_us(count(256, 256), cus, p.nk, 1.2, mn ? 1.3 : 1.45, 4.0));
   if (gated) {
-    offer(kW192, tile_us(count(256, 192), cus, p.nk, 1.0, 1.15, 4.0));
+    offer(kW192, tile_us(count(256, 192), cus, p.nk, 0.95, 1.03, 4.0));
   } else {
-    offer(kW224, tile_us(count(256, 224), cus, p.nk, 1.1, 1.36, 4.0));
-    offer(kW160, tile_us(count(256, 160), cus, p.nk, 0.92, 1.02, 3.5));
+    offer(kW224, tile_us(count(256, 224), cus, p.nk, 1.1, mn ? 1.22 : 1.36, 4.0));
+    offer(kW160, tile_us(count(256, 160), cus, p.nk, 0.92, mn ? 0.92 : 1.02, 3.5));
   }
-  offer(kMid2, mid2_us(count(128, 128), cus, p.nk));
+  offer(kMid2, mid2_us(count(128, 128), cus, p.nk, mn));
+  offer(kHalf2, half2_us(count(128, 64), cus, p.nk, mn));
+  offer(kSmall2, small2_us(count(64, 64), cus, p.nk, mn));
   offer(kMid, mid_us(count(128, 128), cus, p.nk, mn));
-  offer(kSmall, small_us(count(64, 64), cus, p.nk, mn));
+  if (!mn) offer(kSmall, small_us(count(64, 64), cus, p.nk, mn));
   return best;
 }
 
 template <int E, bool TA, bool TB>
 using MidTile = LinearTile<E, 128, 128, 4, 2, 1, 4, TA, TB>;
 template <int E, bool TA, bool TB>
-using SmallTile = LinearTile<E, 64, 64, 2, 2, 2, 4, TA, TB>;
+using SmallTile = LinearTile<E, 64, 64, TA || TB ? 4 : 2, 2, TA || TB ? 1 : 2, 4, TA, TB>;
 
 template <int E, bool TA = false, bool TB = false>
 fg_status launch_planned(LinearParams& p, TileKind kind, int64_t cols, int cus, void* stream, const char* what) {
@@ -258,6 +286,8 @@ fg_status launch_planned(LinearParams& p, TileKind kind, int64_t cols, int cus, 
       if constexpr (!epi_gated(E)) return launch_tile<LinearTile<E, 256, 160, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
       break;
     case kMid2: return launch_tile<LinearTile<E, 128, 128, 2, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
+    case kHalf2: return launch_tile<LinearTile<E, 128, 64, 4, 2, 1, 3, TA, TB>>(p, cus, cols, stream, what);
+    case kSmall2: return launch_tile<LinearTile<E, 64, 64, 2, 2, 1, 4, TA, TB>>(p, cus, cols, stream, what);
     case kMid: return launch_tile<MidTile<E, TA, TB>>(p, cus, cols, stream, what);
     case kSmall: return launch_tile<SmallTile<E, TA, TB>>(p, cus, cols, stream, what);
     default: break;
@@ -388,8 +418,8 @@ fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const cha
         if (px.splits > 1 && cx != px.kind) continue;
         const int bx = cx == kMid ? 128 : 64, bw = cw == kMid ? 128 : 64;
         const double nx = tile_count(*x, x->N, false, bx, bx) * px.splits, nw = tile_count(*w, w->N, false, bw, bw);
-        const double tx = x->split_nk * (cx == kMid ? 0.56 : 0.36) + (cx == kMid ? 2.5 : 1.5);
-        const double tw = w->nk * (cw == kMid ? 0.66 : 0.42) + (cw == kMid ? 2.5 : 1.5);  // both operands MN-major
+        const double tx = x->split_nk * (cx == kMid ? 0.57 : 0.45) + (cx == kMid ? 2.5 : 1.5);
+        const double tw = w->nk * (cw == kMid ? 0.63 : 0.37) + (cw == kMid ? 2.5 : 1.5);  // both operands MN-major
         const double us = 3.4 + std::max(std::max(tx, tw), (nx * tx + nw * tw) / cus + 0.5 * std::min(tx, tw)) +
                           (px.splits > 1 ? 4.0 : 0.0);
         if (nx + nw >= (1 << 22)) continue;

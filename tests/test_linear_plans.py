@@ -25,7 +25,7 @@ def forced(monkeypatch, plan):
     monkeypatch.setenv("FG_LINEAR_PLAN", plan)
 
 
-@pytest.mark.parametrize("plan", ["w256", "w224", "w160", "mid2", "mid", "small"] + FEW)
+@pytest.mark.parametrize("plan", ["w256", "w224", "w160", "mid2", "mid", "half2", "small2", "small"] + FEW)
 @pytest.mark.parametrize("M,N,K", SHAPES)
 def test_int8_plans(gpu_lib, monkeypatch, plan, M, N, K):
     if plan in FEW:
@@ -42,7 +42,7 @@ def test_int8_plans(gpu_lib, monkeypatch, plan, M, N, K):
     assert_within(out.f64(), want, bound, plan)
 
 
-@pytest.mark.parametrize("plan", ["w256", "w192", "mid2", "mid", "small"] + FEW)
+@pytest.mark.parametrize("plan", ["w256", "w192", "mid2", "mid", "half2", "small2", "small"] + FEW)
 @pytest.mark.parametrize("form", ["int8", "bf16", "kept"])
 @pytest.mark.parametrize("M,F,K", [(5, 19, 80), (129, 150, 400), (1100, 650, 144)])
 def test_gated_plans(gpu_lib, monkeypatch, plan, form, M, F, K):
@@ -73,7 +73,8 @@ def test_gated_plans(gpu_lib, monkeypatch, plan, form, M, F, K):
     assert_within(out.f64(), ref.gated(g, u, act), ref.gated_bound(g, u, eg, eu, act), plan)
 
 
-@pytest.mark.parametrize("plan", ["w256", "w224", "w160", "mid2", "mid", "small", "split-mid", "split-small", "pair-mid", "pair-small",
+@pytest.mark.parametrize("plan", ["w256", "w224", "w160", "mid2", "mid", "half2", "small2", "small", "split-mid",
+                                  "split-small", "pair-mid", "pair-small",
                                   "share-mid-mid", "share-mid-small", "share-small-mid", "share-small-small"])
 @pytest.mark.parametrize("M,F,K", [(3, 11, 72), (130, 450, 136), (700, 100, 1304), (65, 700, 264),
                                    (190, 70, 1928)])
@@ -101,7 +102,7 @@ def test_int8_bits_do_not_depend_on_the_plan(gpu_lib, monkeypatch):
     A, sa = (torch.from_numpy(t).cuda() for t in codes(M, K, 7))
     B, sb = (torch.from_numpy(t).cuda() for t in codes(N, K, 8))
     want = gpu_lib.gemm_int8_nt(A, sa, B, sb, torch.empty(M, N, dtype=torch.bfloat16, device="cuda"))
-    for plan in ["w256", "w224", "w160", "mid2", "mid", "small"] + FEW:
+    for plan in ["w256", "w224", "w160", "mid2", "mid", "half2", "small2", "small"] + FEW:
         forced(monkeypatch, plan)
         got = gpu_lib.gemm_int8_nt(A, sa, B, sb, torch.empty_like(want))
         assert torch.equal(got, want), plan
