@@ -210,10 +210,10 @@ struct TilePlan {
 
 // The environment variable FG_LINEAR_PLAN overrides the choice (tuning and
 // tests): a tile ("w256", "w224", "w192", "w160", "mid2", "mid", "half2",
-// "small2", "small"), a few-row shape ("few0" .. "few7"), or for the gradients "split-mid",
-// "split-small" (dX's sum), "pair-mid", "pair-small" (the recomputed
-// pre-activations' sums) or "share-X-W" (X and W: mid or small).  A plan that
-// the call does not have leaves it its own.
+// "small2", "small"), a few-row shape ("few0" .. "few7"), or for the gradients
+// "split-mid", "split-small" (dX's sum), "pair-mid", "pair-small" (the
+// recomputed pre-activations' sums) or "share-X-W" (X and W: mid or small).  A
+// plan that the call does not have leaves it its own.
 const char* forced_plan() {
   const char* f = getenv("FG_LINEAR_PLAN");
   return f ? f : "";
@@ -249,13 +249,13 @@ TilePlan plan_tile(const LinearParams& p, int64_t cols, bool gated, bool mn, int
   auto offer = [&](TileKind kind, double us) {
     if (us < best.us) best = TilePlan{kind, us};
   };
-  // 256 rows by 256, 224, 192 or 160: the time a slice grows with the CUs at
-  // work, since the chip's power
-  // limits (int8 4096 x 7168 x 16384: 372 us with 256 columns, 343 with 224;
-  // 4096 x 2112 x 7168: 78 with 256, 60 with 160).
+  // 256 rows by 256, 224, 192 or 160: the time of a slice grows with the CUs at
+  // work, since the chip's power limits these (int8 4096 x 7168 x 16384: 372 us
+  // with 256 columns, 343 with 224; 4096 x 2112 x 7168: 78 with 256, 60 with
+  // 160; gated bf16 4096 x 12288 x 1536: 238 with 256, 266 with 192).
   offer(kW256, tile_us(count(256, 256), cus, p.nk, 1.2, mn ? 1.3 : 1.45, 4.0));
   if (gated) {
-    offer(kW192, tile_us(count(256, 192), cus, p.nk, 0.95, 1.03, 4.0));
+    offer(kW192, tile_us(count(256, 192), cus, p.nk, 0.95, 1.15, 4.0));
   } else {
     offer(kW224, tile_us(count(256, 224), cus, p.nk, 1.1, mn ? 1.22 : 1.36, 4.0));
     offer(kW160, tile_us(count(256, 160), cus, p.nk, 0.92, mn ? 0.92 : 1.02, 3.5));
