@@ -446,6 +446,8 @@ fg_status fp8_cast_per_block_ue8m0_bf16(const uint16_t* w, int64_t ldw, uint8_t*
  * signed bytes with an fp32 scale per row (a token of the activations, an
  * output channel of the weights), or BF16.  All matrices are row-major with
  * their last dimension contiguous.
+ * Rows that lie a multiple of 128 bytes apart load fastest (others cost 13 to
+ * 40 % of a large product's time).
  * Only the backward pass needs a workspace.  Their plans depend only on the
  * arguments, the device and the CU cap, and sums have a fixed order, so
  * results are reproducible.
