@@ -106,3 +106,21 @@ def test_int8_bits_do_not_depend_on_the_plan(gpu_lib, monkeypatch):
         forced(monkeypatch, plan)
         got = gpu_lib.gemm_int8_nt(A, sa, B, sb, torch.empty_like(want))
         assert torch.equal(got, want), plan
+
+
+def test_gradient_bits_do_not_depend_on_the_tile(gpu_lib, monkeypatch):
+    """Each sum runs in the order of its slices; only a split changes it."""
+    M, F, K = 200, 150, 328
+    X, W, dH = (t.cuda() for t in block(M, F, K, 9))
+    P = torch.empty(M, 2 * F, device="cuda")
+    gpu_lib.gated_ffn_bf16(X, W, torch.empty_like(dH), P=P)
+    want = None
+    for plan in ["w256", "w224", "w160", "mid2", "mid", "half2", "small2", "small", "share-mid-mid", "share-mid-small",
+                 "share-small-mid", "share-small-small"]:
+        forced(monkeypatch, plan)
+        dX, dW = torch.empty_like(X), torch.empty_like(W)
+        gpu_lib.gated_ffn_bf16_backward(dH, X, W, dX, dW, P=P)
+        want = (dX, dW) if want is None else want
+        assert torch.equal(dW, want[1]), plan
+        if not plan.startswith("share"):  # a shared launch takes dX's own split
+            assert torch.equal(dX, want[0]), plan
