@@ -211,9 +211,9 @@ struct TilePlan {
 // The environment variable FG_LINEAR_PLAN overrides the choice (tuning and
 // tests): a tile ("w256", "w224", "w192", "w160", "mid2", "mid", "half2",
 // "small2", "small"), a few-row shape ("few0" .. "few7"), or for the gradients
-// "split-mid", "split-small" (dX's sum), "pair-mid", "pair-small" (the
-// recomputed pre-activations' sums) or "share-X-W" (X and W: mid or small).  A
-// plan that the call does not have leaves it its own.
+// "split-mid", "split-small" (dX's sum), "pair" (the recomputed
+// pre-activations' sums) or "share-X-W" (X and W: mid or small).  A plan that
+// the call does not have leaves it its own.
 const char* forced_plan() {
   const char* f = getenv("FG_LINEAR_PLAN");
   return f ? f : "";
@@ -289,7 +289,9 @@ fg_status launch_planned(LinearParams& p, TileKind kind, int64_t cols, int cus, 
     case kHalf2: return launch_tile<LinearTile<E, 128, 64, 4, 2, 1, 3, TA, TB>>(p, cus, cols, stream, what);
     case kSmall2: return launch_tile<LinearTile<E, 64, 64, 2, 2, 1, 4, TA, TB>>(p, cus, cols, stream, what);
     case kMid: return launch_tile<MidTile<E, TA, TB>>(p, cus, cols, stream, what);
-    case kSmall: return launch_tile<SmallTile<E, TA, TB>>(p, cus, cols, stream, what);
+    case kSmall:
+      if constexpr (!TA && !TB) return launch_tile<SmallTile<E, TA, TB>>(p, cus, cols, stream, what);
+      break;
     default: break;
   }
   return launch_tile<LinearTile<E, 256, 256, 4, 2, 1, 2, TA, TB>>(p, cus, cols, stream, what);
@@ -515,21 +517,13 @@ fg_status launch_recompute(LinearParams& g, float* partials, void* stream, const
   if (pair_partial_bytes(g.M, 2 * g.half) > 0) {
     g.nk = slice_count<kEpiGatedPartial>(g);
     const int64_t one = (int64_t)g.M * g.half * 8;
-    const SplitPlan a = plan_split(g, g.half, true, false, one, cus, 64, small_us);
-    const SplitPlan b = plan_split(g, g.half, true, false, one, cus, 128, mid_us);
+    const SplitPlan s = plan_split(g, g.half, true, false, one, cus, 64, small_us);
     const char* f = forced_plan();
-    const bool force_small = strcmp(f, "pair-small") == 0, force_mid = strcmp(f, "pair-mid") == 0;
-    const bool small_tiles = force_small || (!force_mid && a.us <= b.us);
-    const SplitPlan& s = small_tiles ? a : b;
-    const double whole = plan_tile(g, g.half, true, false, cus).us;
-    if (s.splits > 1 && ((!*f && s.us < whole) || force_small || force_mid)) {
+    if (s.splits > 1 && (*f ? strcmp(f, "pair") == 0 : s.us < plan_tile(g, g.half, true, false, cus).us)) {
       g.P = partials;
       g.ldp = 2 * g.half;
       g.split_nk = s.nk;
-      if (small_tiles)
-        FG_TRY((launch_tile<SmallTile<kEpiGatedPartial, false, false>>(g, cus, g.half, stream, what, s.splits)));
-      else
-        FG_TRY((launch_tile<MidTile<kEpiGatedPartial, false, false>>(g, cus, g.half, stream, what, s.splits)));
+      FG_TRY((launch_tile<SmallTile<kEpiGatedPartial, false, false>>(g, cus, g.half, stream, what, s.splits)));
       return launch_gated_grad<true>(g, s.splits, stream, what);
     }
   }

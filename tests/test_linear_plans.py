@@ -74,7 +74,7 @@ def test_gated_plans(gpu_lib, monkeypatch, plan, form, M, F, K):
 
 
 @pytest.mark.parametrize("plan", ["w256", "w224", "w160", "mid2", "mid", "half2", "small2", "small", "split-mid",
-                                  "split-small", "pair-mid", "pair-small",
+                                  "split-small", "pair",
                                   "share-mid-mid", "share-mid-small", "share-small-mid", "share-small-small"])
 @pytest.mark.parametrize("M,F,K", [(3, 11, 72), (130, 450, 136), (700, 100, 1304), (65, 700, 264),
                                    (190, 70, 1928)])
