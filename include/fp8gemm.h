@@ -460,7 +460,8 @@ fg_status fp8_cast_per_block_ue8m0_bf16(const uint16_t* w, int64_t ldw, uint8_t*
  *   x   device fp32 (or bf16) [M, K], row stride ldx elements (ldx >= K, 16-byte aligned rows)
  *   q   device [M, K], packed, 16-byte aligned
  *   s   device fp32 [M]
- * K % 16 == 0.  Input values must be finite.  K == 0 writes nothing.
+ * K % 16 == 0.  Input values must be finite.  K == 0 (the largest of no
+ * values is 0) writes s alone and reads neither x nor q.
  */
 fg_status int8_cast_per_row(const float* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream);
 fg_status int8_cast_per_row_bf16(const uint16_t* x, int64_t ldx, int8_t* q, float* s, int M, int K, void* stream);

@@ -723,7 +723,7 @@ def int8_cast_per_row(x, q=None, s=None, stream=None):
         with _on_stream(stream):
             q = torch.empty(M, K, dtype=torch.int8, device=x.device) if q is None else q
             s = torch.empty(M, dtype=torch.float32, device=x.device) if s is None else s
-    if _matrix(q, "q", torch.int8, M, K, dev) != K and M > 1:
+    if _matrix(q, "q", torch.int8, M, K, dev) != K and M > 1 and K > 0:
         raise ValueError("q must be contiguous")
     _call("int8_cast_per_row_bf16" if bf16 else "int8_cast_per_row", x.data_ptr(), ldx, q.data_ptr(),
           _row_scales(s, "s", M, dev), M, K, _raw_stream(stream, dev))

@@ -535,11 +535,13 @@ fg_status cast_rows(const T* x, int64_t ldx, int8_t* q, float* s, int M, int K, 
   clear_error();
   if (M < 0 || K < 0) return set_error(FG_EINVAL, "negative size M=%d K=%d", M, K);
   if (K % 16) return set_error(FG_EALIGN, "K=%d is not a multiple of 16", K);
-  if (M == 0 || K == 0) return FG_OK;
-  FG_TRY(require_ptr(x, 16, "x"));
-  FG_TRY(require_ptr(q, 16, "q"));
+  if (M == 0) return FG_OK;
   FG_TRY(require_ptr(s, 4, "s"));
-  FG_TRY(require_ld(ldx, K, 16 / (int)sizeof(T), "ldx"));
+  if (K > 0) {
+    FG_TRY(require_ptr(x, 16, "x"));
+    FG_TRY(require_ptr(q, 16, "q"));
+    FG_TRY(require_ld(ldx, K, 16 / (int)sizeof(T), "ldx"));
+  }
   const int pieces = K / (16 / (int)sizeof(T));
   const dim3 grid((unsigned)std::min(M, 1 << 20));
   // Two pieces a thread while they hold the row (4096 x 7168 bf16: 512 threads
