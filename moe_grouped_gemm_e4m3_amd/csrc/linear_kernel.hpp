@@ -254,7 +254,8 @@ __global__ __launch_bounds__(THREADS) void int8_cast_kernel(const T* __restrict_
   constexpr int V = 16 / sizeof(T), WAVES = THREADS / 64;
   __shared__ float red[WAVES];
   const int tid = threadIdx.x, pieces = K / V;
-  for (int m = blockIdx.x; m < M; m += gridDim.x) {
+  // unsigned: M may lie less than a grid below 2^31
+  for (unsigned m = blockIdx.x; m < (unsigned)M; m += gridDim.x) {
     const uint4* row = (const uint4*)(x + (int64_t)m * ldx);
     uint4 v[PIECES];
 #pragma unroll

@@ -38,3 +38,34 @@ def test_cast_of_empty_rows_needs_the_scales_alone():
         assert fn(None, 0, None, None, 4, 0, None) == 1
         assert "s is NULL" in lib.fg_last_error().decode()
         assert fn(None, 0, None, 0x10002, 4, 0, None) == 2
+
+
+@pytest.mark.gpu
+def test_cast_of_the_most_rows(gpu_lib):
+    """2^31 - 1 rows: the row count plus one turn of the grid passes 2^31."""
+    M, K = (1 << 31) - 1, 16
+    if torch.cuda.mem_get_info()[0] < 160 << 30:
+        pytest.skip("needs 104 GiB of device memory")
+    announce(f"int8 cast {M}x{K} bf16")
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    ends = [slice(0, 3), slice((1 << 30) - 1, (1 << 30) + 2), slice(M - (1 << 20) - 2, M - (1 << 20) + 2),
+            slice(M - 3, M)]
+    some = torch.randn(4, K, generator=torch.Generator().manual_seed(0)).bfloat16()
+    for e in ends:
+        x[e] = some[:e.stop - e.start].cuda()
+    q, s = gpu_lib.int8_cast_per_row(x)
+    for e in ends:
+        want_q, want_s = ref.int8_cast(some[:e.stop - e.start].float().numpy())
+        assert np.array_equal(s[e].cpu().numpy(), want_s), e
+        assert np.array_equal(q[e].cpu().numpy(), want_q), e
+    zero = ref.int8_cast(np.zeros((1, K), np.float32))[1][0]
+    rest = torch.ones(M, dtype=torch.bool, device="cuda")
+    for e in ends:
+        rest[e] = False
+    step = 1 << 23
+    for i in range(0, M, step):
+        j = slice(i, min(i + step, M))
+        assert bool(((s[j] == float(zero)) | ~rest[j]).all()), i
+        assert not (q[j].view(torch.int64).any(dim=1) & rest[j]).any(), i
+    del x, q, s, rest
+    torch.cuda.empty_cache()
