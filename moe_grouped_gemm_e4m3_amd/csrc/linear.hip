@@ -472,6 +472,16 @@ fg_status check_operand(const void* ptr, int64_t ld, int64_t cols, int item, con
   return FG_OK;
 }
 
+// Operands and the bytes between their rows.  Not called where K is 0: the
+// kernels then read nothing, and pointers and strides, which nobody checked,
+// must not go into their ranges.
+void set_operands(LinearParams& p, const void* A, int64_t lda, const void* B, int64_t ldb) {
+  p.A = (const uint8_t*)A;
+  p.lda = lda;
+  p.B = (const uint8_t*)B;
+  p.ldb = ldb;
+}
+
 fg_status check_workspace(const void* ws, int64_t bytes, int64_t need) {
   if (bytes < 0) return set_error(FG_EINVAL, "workspace_bytes=%lld is negative", (long long)bytes);
   if (!ws && bytes > 0) return set_error(FG_EINVAL, "workspace is NULL");
@@ -586,7 +596,8 @@ fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8
     FG_TRY(check_operand(B, ldb, K, 1, "B", "ldb"));
   }
   LinearParams p{};
-  p.A = (const uint8_t*)A; p.lda = lda; p.B = (const uint8_t*)B; p.ldb = ldb; p.sa = sa; p.sb = sb;
+  if (K > 0) set_operands(p, A, lda, B, ldb);
+  p.sa = sa; p.sb = sb;
   p.D = D; p.ldd = ldd; p.M = M; p.N = N; p.K = K;
   return launch_linear<kEpiInt8>(p, stream, "gemm_int8_nt");
 }
@@ -609,7 +620,8 @@ fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const in
     FG_TRY(check_operand(W, ldw, K, 1, "W", "ldw"));
   }
   LinearParams p{};
-  p.A = (const uint8_t*)X; p.lda = ldx; p.B = (const uint8_t*)W; p.ldb = ldw; p.sa = sx; p.sb = sw;
+  if (K > 0) set_operands(p, X, ldx, W, ldw);
+  p.sa = sx; p.sb = sw;
   p.D = H; p.ldd = ldh; p.M = M; p.N = F; p.K = K; p.act = activation;
   return launch_linear<kEpiGatedInt8>(p, stream, "gated_ffn_int8");
 }
@@ -632,7 +644,7 @@ fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
     FG_TRY(check_operand(W, ldw, K, 2, "W", "ldw"));
   }
   LinearParams p{};
-  p.A = (const uint8_t*)X; p.lda = 2 * ldx; p.B = (const uint8_t*)W; p.ldb = 2 * ldw;
+  if (K > 0) set_operands(p, X, 2 * ldx, W, 2 * ldw);
   p.D = H; p.ldd = ldh; p.P = P; p.ldp = ldp; p.M = M; p.N = F; p.K = K; p.act = activation;
   return P ? launch_linear<kEpiGatedKeep>(p, stream, "gated_ffn_bf16")
            : launch_linear<kEpiGated>(p, stream, "gated_ffn_bf16");

@@ -69,3 +69,27 @@ def test_cast_of_the_most_rows(gpu_lib):
         assert not (q[j].view(torch.int64).any(dim=1) & rest[j]).any(), i
     del x, q, s, rest
     torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ld", [-16, -(1 << 40), 1 << 60, 7])
+@pytest.mark.parametrize("M,N", [(5, 40), (700, 300)])
+def test_no_reduction_looks_at_no_operand(gpu_lib, M, N, ld):
+    """K = 0: outputs are zero whatever the operands' pointers and strides."""
+    announce(f"K=0 {M}x{N} ld={ld}")
+    lib = gpu_lib.load_library()
+    one = torch.ones(max(M, 2 * N), device="cuda")
+    D = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    P = torch.full((M, 2 * N), float("nan"), device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    calls = [
+        lambda: lib.gemm_int8_nt(None, ld, one.data_ptr(), None, ld, one.data_ptr(), D.data_ptr(), N, M, N, 0, s),
+        lambda: lib.gated_ffn_int8(None, ld, one.data_ptr(), None, ld, one.data_ptr(), D.data_ptr(), N, M, N, 0, 0, s),
+        lambda: lib.gated_ffn_bf16(None, ld, None, ld, D.data_ptr(), N, None, 0, M, N, 0, 1, s),
+        lambda: lib.gated_ffn_bf16(None, ld, None, ld, D.data_ptr(), N, P.data_ptr(), 2 * N, M, N, 0, 0, s),
+    ]
+    for call in calls:
+        D.fill_(float("nan"))
+        assert call() == 0, lib.fg_last_error()
+        assert (D == 0).all()
+    assert (P == 0).all()
