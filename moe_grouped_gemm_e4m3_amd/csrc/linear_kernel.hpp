@@ -94,13 +94,15 @@ __device__ __forceinline__ float gated_value(float g, float u) {
 
 // dg = dH u act'(g), du = dH act(g), act'(g) = s + g s (1 - s) y'(g).  Where
 // s (1 - s) has underflowed the last term is 0 (y' may have overflowed there).
+// dH is multiplied last: dH u and dH g may overflow where the gradient, with
+// act' or s near 0, does not.
 template <int ACT>
 __device__ __forceinline__ void gated_grad(float dh, float g, float u, float& dg, float& du) {
   const float s = act_gate<ACT>(g);
   const float t = s * (1.f - s);
   const float slope = ACT == kActSilu ? 1.f : kGelu2C * (1.f + 3.f * kGeluA * g * g);
-  dg = dh * u * (s + (t == 0.f ? 0.f : g * t * slope));
-  du = dh * g * s;
+  dg = dh * (u * (s + (t == 0.f ? 0.f : g * t * slope)));
+  du = dh * (g * s);
 }
 
 __device__ __forceinline__ float to_f32(float v) { return v; }

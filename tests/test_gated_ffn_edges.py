@@ -1,0 +1,46 @@
+"""Edge values and sizes of the gated feed-forward block."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import linear as ref
+from tests.helpers import announce
+from tests.linear_helpers import Output, assert_within, bf16, f64
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kept", [False, True], ids=["recomputed", "kept"])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_backward_of_closed_gates_under_large_gradients(gpu_lib, act, kept):
+    """dH g and dH u leave fp32's range, the gradients, with the gate closed,
+    do not: act and act' of a far negative value are 0.
+
+    Every sum has one term that is not 0, so closed gates give exact zeros."""
+    announce(f"closed gates {act} kept={kept}")
+    big = 2.0 ** 70
+    g = [-(2.0 ** 80), -(2.0 ** 64), 2.0, -(2.0 ** 100)]
+    u = [2.0 ** 80, 1.0, 2.0 ** 10, -(2.0 ** 90)]
+    M, F, K = 40, 4, 16
+    W = torch.zeros(2 * F, K)
+    W[:F, 0], W[F:, 1] = torch.tensor(g), torch.tensor(u)
+    X = torch.zeros(M, K)
+    X[7, :2] = 1.0
+    dH = torch.zeros(M, F)
+    dH[7] = torch.tensor([big, big, 1.0, big])
+    X, W, dH = bf16(X).cuda(), bf16(W).cuda(), bf16(dH).cuda()
+    P = None
+    if kept:
+        P = torch.empty(M, 2 * F, device="cuda")
+        gpu_lib.gated_ffn_bf16(X, W, torch.empty_like(dH), P=P, activation=act)
+    dX, dW = Output(M, K), Output(2 * F, K)
+    gpu_lib.gated_ffn_bf16_backward(dH, X, W, dX.t, dW.t, P=P, activation=act)
+    dg, du = ref.gated_grad(f64(dH)[7], np.array(g), np.array(u), act)
+    got = dW.f64()
+    assert np.isfinite(got).all() and np.isfinite(dX.f64()).all()
+    assert (got[[0, 1, 3, F, F + 1, F + 3]] == 0).all()  # closed gates: nothing flows
+    # the open gate: the pair and the output are rounded once each
+    want, near = np.array([dg[2], du[2]]), np.array([got[2, 0], got[F + 2, 0]])
+    assert_within(near, want, 2.0 ** -7 * np.abs(want), "open gate")
