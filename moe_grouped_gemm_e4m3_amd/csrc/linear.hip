@@ -53,7 +53,6 @@ fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, cons
 template <class C>
 fg_status launch_fewrow(const LinearParams& p, void* stream, const char* what) {
   const int64_t parts = ((int64_t)p.M + C::ROWS - 1) / C::ROWS, tiles = ((int64_t)p.N + C::OUT_N - 1) / C::OUT_N;
-  if (parts * tiles >= (1 << 23)) return set_error(FG_EUNSUPPORTED, "%s: too many output tiles", what);
   hipLaunchKernelGGL((fewrow_kernel<C>), dim3((unsigned)(parts * tiles)), dim3(C::THREADS), 0, (hipStream_t)stream, p,
                      (int)parts);
   return launched(what);

@@ -173,6 +173,9 @@ constexpr FewRowShape kFewRowShapes[] = {
 };
 constexpr int kFewRowShapeCount = sizeof kFewRowShapes / sizeof *kFewRowShapes;
 constexpr int kFewRowMost = 640;  // rows up to which these shapes are considered
+// Workgroups up to which they are: a grid of 512 threads each stays below 2^32
+// threads.  Wider outputs are the tiles', whose grid is persistent.
+constexpr int kFewRowMostGroups = (1 << 23) - 1;
 
 // Workgroups of few-row shape f.
 inline double fewrow_groups(const Product& p, const FewRowShape& f) {
@@ -186,6 +189,10 @@ inline double fewrow_us(const Product& p, int cus, const FewRowShape& f) {
   return f.base + (turns > 1 ? turns * f.shared : 1.0) * one;
 }
 
+inline bool forced_fewrow(const char* f, int shape) {
+  return strncmp(f, "few", 3) == 0 && f[3] == '0' + shape && !f[4];
+}
+
 // A forward product: few-row shape `few`, or, where that is negative, a tile.
 struct ForwardPlan {
   int few;
@@ -197,13 +204,14 @@ inline ForwardPlan plan_forward(const Product& p, int cus, const char* forced) {
   if (p.M > kFewRowMost) return plan;
   double least = tile.us;
   for (int i = 0; i < kFewRowShapeCount; ++i) {
+    if (fewrow_groups(p, kFewRowShapes[i]) > kFewRowMostGroups) continue;
     const double t = fewrow_us(p, cus, kFewRowShapes[i]);
+    if (forced_fewrow(forced, i)) return ForwardPlan{i, tile.kind};
     if (t < least) {
       least = t;
       plan.few = i;
     }
   }
-  if (strncmp(forced, "few", 3) == 0 && forced[3] >= '0' && forced[3] <= '7' && !forced[4]) plan.few = forced[3] - '0';
   return plan;
 }
 

@@ -46,6 +46,9 @@ static void forward(int64_t M, int64_t N, int64_t K, bool gated, int item, int c
   ++g_plans;
   CHECK(plan.few >= -1 && plan.few < kFewRowShapeCount, "few %d", plan.few);
   CHECK(plan.few < 0 || M <= kFewRowMost, "%lld rows", (long long)M);
+  // one workgroup a tile: at most 512 threads each, below 2^32 in all
+  CHECK(plan.few < 0 || fewrow_groups(p, kFewRowShapes[plan.few]) * 512 < 4294967296.0, "%lld x %lld: shape %d",
+        (long long)M, (long long)N, plan.few);
   CHECK(gated ? plan.tile != kW224 && plan.tile != kW160 : plan.tile != kW192, "tile %d", plan.tile);
 }
 
