@@ -106,18 +106,17 @@ inline double mid2_us(double tiles, int cus, int nk, bool mn) {
 // "split-mid", "split-small" (dX's sum), "pair" (the recomputed
 // pre-activations' sums) or "share-X-W" (X and W: mid or small).  A plan that
 // the call does not have leaves it its own.
-inline bool forced_tile(const char* f, bool gated, TileKind* kind) {
+inline bool forced_tile(const char* f, const Product& p, TileKind* kind) {
   static const struct {
     const char* name;
     TileKind kind;
   } names[] = {{"w256", kW256}, {"w224", kW224}, {"w192", kW192}, {"w160", kW160},
                {"mid2", kMid2}, {"mid", kMid},   {"half2", kHalf2}, {"small2", kSmall2}, {"small", kSmall}};
-  if (!*f) return false;
-  for (const auto& n : names)
-    if (strcmp(f, n.name) == 0 && (gated ? n.kind != kW224 && n.kind != kW160 : n.kind != kW192)) {
-      *kind = n.kind;
-      return true;
-    }
+  for (const auto& n : names) {
+    if (strcmp(f, n.name) != 0) continue;
+    *kind = n.kind;
+    return (p.gated ? n.kind != kW224 && n.kind != kW160 : n.kind != kW192) && !(p.mn && n.kind == kSmall);
+  }
   return false;
 }
 
@@ -130,7 +129,7 @@ inline bool shares(const char* forced, TileKind x, TileKind w) {
 // The cheapest tile for p and its time.
 inline TilePlan plan_tile(const Product& p, int cus, const char* forced) {
   TileKind kind;
-  if (forced_tile(forced, p.gated, &kind)) return TilePlan{kind, 0.0};
+  if (forced_tile(forced, p, &kind)) return TilePlan{kind, 0.0};
   auto count = [&](int bm, int bn) { return tile_count(p, bm, bn); };
   const bool mn = p.mn;
   TilePlan best{kW256, 1e30};
@@ -270,7 +269,7 @@ inline SplitPlan plan_recompute(const Product& g, int cus, const char* forced) {
   SplitPlan s{0.0, 1, g.nk};
   if (pair_partial_bytes(g.M, 2 * g.cols) == 0) return s;
   const SplitPlan split = plan_split(g, g.M * g.cols * 8, cus, 64, small_us);
-  const bool take = *forced ? strcmp(forced, "pair") == 0 : split.us < plan_tile(g, cus, forced).us;
+  const bool take = strcmp(forced, "pair") == 0 || split.us < plan_tile(g, cus, forced).us;  // (a forced tile's is 0)
   return split.splits > 1 && take ? split : s;
 }
 
@@ -284,12 +283,14 @@ struct GradsPlan {
 };
 inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, const char* forced) {
   GradsPlan plan{false, kW256, kW256, 1, 0};
+  bool separate = false;  // a forced plan of a launch for each
   double x_us = 0, w_us = 0;
   if (x) {
     plan.split_nk = x->nk;
     const TilePlan t = plan_tile(*x, cus, forced);
     plan.x = t.kind;
     x_us = t.us;
+    separate = t.us == 0;
     // 251 x 1016 with 178 slices: 52 us on 64 64 x 64 tiles, a quarter of the
     // device; split 27 us with the addition.
     const int64_t one = x->M * x->cols * 4;
@@ -303,6 +304,7 @@ inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, const c
       plan.splits = s.splits;
       plan.split_nk = s.nk;
       x_us = s.us;
+      separate = force_small || force_mid;
     }
   }
   if (w) {
@@ -310,11 +312,11 @@ inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, const c
     plan.w = t.kind;
     w_us = t.us;
   }
-  if (!x || !w) return plan;
+  if (!x || !w || separate) return plan;
   // One launch: the workgroups of both, one to a CU, dX's first.  The device
   // is busy for their total, and for the longest one at least.
-  double least = x_us + w_us;
   const GradsPlan own = plan;
+  double least = x_us + w_us;
   for (const TileKind cx : {kMid, kSmall})
     for (const TileKind cw : {kMid, kSmall}) {
       if (own.splits > 1 && cx != own.x) continue;
@@ -325,11 +327,11 @@ inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, const c
       const double us = 3.4 + std::max(std::max(tx, tw), (nx * tx + nw * tw) / cus + 0.5 * std::min(tx, tw)) +
                         (own.splits > 1 ? 4.0 : 0.0);
       if (nx + nw >= (1 << 22)) continue;
-      if (*forced ? shares(forced, cx, cw) : us < least) {
+      const GradsPlan both{true, cx, cw, own.splits, own.split_nk};
+      if (shares(forced, cx, cw)) return both;
+      if (us < least) {
         least = us;
-        plan.shared = true;
-        plan.x = cx;
-        plan.w = cw;
+        plan = both;
       }
     }
   return plan;

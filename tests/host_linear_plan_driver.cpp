@@ -27,6 +27,15 @@ static const char* const kForced[] = {"", "w256", "w224", "w192", "w160", "mid2"
                                       "share-mid-small", "share-small-mid", "share-small-small", "few8", "none", "split",
                                       "a name longer than any plan's, which fits no buffer made for one"};
 
+// A forced plan that a call does not have leaves it its own.
+static const char* const kNotGrads[] = {"small", "w192", "few0", "few7", "few8", "pair", "none", "split"};
+static const char* const kNotPair[] = {"w224", "w160", "few0", "few7", "few8", "split-mid", "share-mid-mid", "none", "split"};
+static const char* const kNotInt8[] = {"w192", "few8", "pair", "split-mid", "share-mid-mid", "none", "split"};
+
+static bool same(const GradsPlan& a, const GradsPlan& b) {
+  return a.shared == b.shared && a.x == b.x && a.w == b.w && a.splits == b.splits && a.split_nk == b.split_nk;
+}
+
 // What is true of every split of `nk` slices into partials of `one` bytes, in
 // a workspace of `room` bytes.
 static void check_split(int splits, int split_nk, int nk, int64_t one, int64_t room, const char* what, long long M,
@@ -50,6 +59,30 @@ static void forward(int64_t M, int64_t N, int64_t K, bool gated, int item, int c
   CHECK(plan.few < 0 || fewrow_groups(p, kFewRowShapes[plan.few]) * 512 < 4294967296.0, "%lld x %lld: shape %d",
         (long long)M, (long long)N, plan.few);
   CHECK(gated ? plan.tile != kW224 && plan.tile != kW160 : plan.tile != kW192, "tile %d", plan.tile);
+}
+
+static void own_plans(int64_t M, int64_t N, int64_t K, int cus) {
+  const Product a{M, N, slice_count(K, 1), false, false};
+  const ForwardPlan f = plan_forward(a, cus, "");
+  for (const char* forced : kNotInt8) {
+    const ForwardPlan g = plan_forward(a, cus, forced);
+    CHECK(f.few == g.few && f.tile == g.tile, "%s: %lld %lld %lld", forced, (long long)M, (long long)N, (long long)K);
+  }
+  if (K == 0 || N > 1 << 20) return;
+  const int64_t cols = pair_cols(N);
+  const Product g{M, cols / 2, slice_count(K, 2), true, false};
+  const SplitPlan s = plan_recompute(g, cus, "");
+  for (const char* forced : kNotPair) {
+    const SplitPlan t = plan_recompute(g, cus, forced);
+    CHECK(s.splits == t.splits && s.nk == t.nk && plan_tile(g, cus, "").kind == plan_tile(g, cus, forced).kind,
+          "%s: %lld %lld %lld", forced, (long long)M, (long long)N, (long long)K);
+  }
+  const Product x{M, K, slice_count(cols, 2), false, true}, w{cols, K, slice_count(M, 2), false, true};
+  for (int which = 1; which <= 3; ++which)
+    for (const char* forced : kNotGrads)
+      CHECK(same(plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, ""),
+                 plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, forced)),
+            "%s: %lld %lld %lld of %d", forced, (long long)M, (long long)N, (long long)K, which);
 }
 
 static void backward(int64_t M, int64_t F, int64_t K, int cus, const char* forced) {
@@ -95,6 +128,10 @@ int main() {
             forward(M, N, K, true, 2, cus, forced);
             if (K > 0 && N <= 1 << 20) backward(M, N, K, cus, forced);
           }
+  for (const int cus : cu_counts)
+    for (const int64_t M : rows)
+      for (const int64_t N : wide)
+        for (const int64_t K : depths) own_plans(M, N, K, cus);
   if (g_fail) {
     std::fprintf(stderr, "%ld check(s) failed\n", g_fail);
     return 1;
