@@ -908,6 +908,8 @@ fg_status usable_cus(int* cus) {
   return FG_OK;
 }
 
+bool print_launches() { return env_flag("FG_PRINT_CONFIGS"); }
+
 fg_status require_ptr(const void* p, uintptr_t align, const char* name) { return check_ptr(p, align, name); }
 
 fg_status require_ld(int64_t ld, int64_t row, int64_t mult, const char* name) {

@@ -16,6 +16,8 @@ void clear_error();
 fg_status set_error(fg_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 // Compute units of the current device, at most fg_set_num_cus()'s cap.
 fg_status usable_cus(int* cus);
+// The environment asks for a line on every launch (FG_PRINT_CONFIGS).
+bool print_launches();
 // FG_EINVAL / FG_EALIGN with the argument's name where a pointer or a row
 // stride does not fit.
 fg_status require_ptr(const void* p, uintptr_t align, const char* name);

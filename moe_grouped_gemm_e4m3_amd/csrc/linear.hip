@@ -4,6 +4,7 @@
 // is allocated.
 
 #include <algorithm>
+#include <cstdio>
 #include <cstdlib>
 
 #include "host_common.hpp"
@@ -42,10 +43,26 @@ fg_status set_tiles(LinearParams& p, int64_t cols, const char* what, int splits 
   return FG_OK;
 }
 
+// FG_PRINT_CONFIGS: a launch's product on C's tiles.
+template <class C>
+void print_tiles(const LinearParams& p, const char* what, const char* launch, int splits, int grid) {
+  if (print_launches())
+    fprintf(stderr, "[fp8gemm] %s %s M=%d N=%d K=%d tile=%dx%d threads=%d tiles=%d splits=%d grid=%d\n", what, launch, p.M,
+            p.N, p.K, C::BM, C::BN, C::THREADS, p.num_tiles, splits, grid);
+}
+
+// The launch of a product on C's tiles, as print_tiles() names it.
+template <class C>
+const char* launch_name() {
+  if (C::E == kEpiGatedGrad || C::E == kEpiGatedPartial) return "pair";
+  return C::TA ? "dW" : C::TB ? "dX" : "product";
+}
+
 template <class C>
 fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, const char* what, int splits = 1) {
   FG_TRY(set_tiles<C>(p, cols, what, splits));
   const int grid = std::min(cus * C::OCC, p.num_tiles);
+  print_tiles<C>(p, what, launch_name<C>(), splits, grid);
   hipLaunchKernelGGL((linear_tile_kernel<C>), dim3((unsigned)grid), dim3(C::THREADS), 0, (hipStream_t)stream, p);
   return launched(what);
 }
@@ -53,6 +70,9 @@ fg_status launch_tile(LinearParams& p, int cus, int64_t cols, void* stream, cons
 template <class C>
 fg_status launch_fewrow(const LinearParams& p, void* stream, const char* what) {
   const int64_t parts = ((int64_t)p.M + C::ROWS - 1) / C::ROWS, tiles = ((int64_t)p.N + C::OUT_N - 1) / C::OUT_N;
+  if (print_launches())
+    fprintf(stderr, "[fp8gemm] %s product M=%d N=%d K=%d few-row rows=%d cols=%d waves=%d grid=%lld\n", what, p.M, p.N, p.K,
+            C::ROWS, C::COLS, C::WAVES, (long long)(parts * tiles));
   hipLaunchKernelGGL((fewrow_kernel<C>), dim3((unsigned)(parts * tiles)), dim3(C::THREADS), 0, (hipStream_t)stream, p,
                      (int)parts);
   return launched(what);
@@ -134,6 +154,8 @@ template <class X, class W>
 fg_status launch_both(LinearParams& x, int splits, LinearParams& w, void* stream, const char* what) {
   FG_TRY((set_tiles<X>(x, x.N, what, splits)));
   FG_TRY((set_tiles<W>(w, w.N, what)));
+  print_tiles<X>(x, what, "shared dX", splits, x.num_tiles + w.num_tiles);
+  print_tiles<W>(w, what, "shared dW", 1, x.num_tiles + w.num_tiles);
   hipLaunchKernelGGL((linear_grads_kernel<X, W>), dim3((unsigned)(x.num_tiles + w.num_tiles)), dim3(X::THREADS), 0,
                      (hipStream_t)stream, x, w, x.num_tiles);
   return launched(what);
