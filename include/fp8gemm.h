@@ -539,7 +539,10 @@ fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const in
 int fg_get_mk_alignment_for_contiguous_layout(void);
 
 /* Cap on the compute units the GEMM kernels spread their persistent workgroups
- * over (the digest's set_num_sms); 0 (the default) means all of them.
+ * over (the digest's set_num_sms); 0 (the default) means all of them.  Kernels
+ * without persistent workgroups do not follow it: the few-row (decode) kernels,
+ * the casts and copies, and the gated backward pass's gradient pair (from kept
+ * pre-activations or partial sums) and addition of partial sums.
  * Results do not depend on the cap (every tile is computed whole by one
  * workgroup), but for the bf16 gated block and its gradients, whose plan,
  * and so the order of their fp32 sums, follows it.  Process-wide, not thread-safe against concurrent launches. */

@@ -902,9 +902,11 @@ fg_status set_error(fg_status st, const char* fmt, ...) {
   return st;
 }
 
-fg_status usable_cus(int* cus) {
+fg_status usable_cus(int* cus, bool* capped) {
   FG_TRY(device_cus(cus));
-  if (g_num_cus_cap > 0 && g_num_cus_cap < *cus) *cus = g_num_cus_cap;
+  const bool cap = g_num_cus_cap > 0 && g_num_cus_cap < *cus;
+  if (cap) *cus = g_num_cus_cap;
+  if (capped) *capped = cap;
   return FG_OK;
 }
 

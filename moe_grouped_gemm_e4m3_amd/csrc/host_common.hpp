@@ -14,8 +14,9 @@ namespace fg {
 void clear_error();
 // Sets the thread's error text and returns st.
 fg_status set_error(fg_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-// Compute units of the current device, at most fg_set_num_cus()'s cap.
-fg_status usable_cus(int* cus);
+// Compute units of the current device, at most fg_set_num_cus()'s cap; whether
+// the cap took any.
+fg_status usable_cus(int* cus, bool* capped = nullptr);
 // The environment asks for a line on every launch (FG_PRINT_CONFIGS).
 bool print_launches();
 // FG_EINVAL / FG_EALIGN with the argument's name where a pointer or a row

@@ -175,11 +175,12 @@ fg_status launch_both(LinearParams& x, TileKind kx, int splits, LinearParams& w,
 
 fg_status launch_grads(LinearParams* x, LinearParams* w, void* stream, const char* what) {
   int cus = 0;
-  FG_TRY(usable_cus(&cus));
+  bool capped = false;
+  FG_TRY(usable_cus(&cus, &capped));
   Product px{}, pw{};
   if (x) px = product<kEpiBf16>(*x, x->N, true);
   if (w) pw = product<kEpiBf16>(*w, w->N, true);
-  const GradsPlan plan = plan_grads(x ? &px : nullptr, w ? &pw : nullptr, cus, forced_plan());
+  const GradsPlan plan = plan_grads(x ? &px : nullptr, w ? &pw : nullptr, cus, capped, forced_plan());
   if (x) x->split_nk = plan.split_nk;
   if (plan.shared) {
     if (plan.splits == 1) return launch_both<kEpiBf16>(*x, plan.x, 1, *w, plan.w, stream, what);

@@ -275,13 +275,15 @@ inline SplitPlan plan_recompute(const Product& g, int cus, const char* forced) {
 
 // dX = pair . W and dW = pair^T . X.  Each has its own plan; where neither
 // fills the device, both go into one launch, with 128 x 128 or 64 x 64 tiles
-// each.
+// each.  That launch has a workgroup for every tile, which the device takes as
+// CUs become free, so it is not for a call that may use some of the CUs only
+// (`capped`): the persistent launches of their own keep to them.
 struct GradsPlan {
   bool shared;
   TileKind x, w;
   int splits, split_nk;  // of dX's sum: the splits and their slices
 };
-inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, const char* forced) {
+inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, bool capped, const char* forced) {
   GradsPlan plan{false, kW256, kW256, 1, 0};
   bool separate = false;  // a forced plan of a launch for each
   double x_us = 0, w_us = 0;
@@ -312,7 +314,7 @@ inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, const c
     plan.w = t.kind;
     w_us = t.us;
   }
-  if (!x || !w || separate) return plan;
+  if (!x || !w || separate || capped) return plan;
   // One launch: the workgroups of both, one to a CU, dX's first.  The device
   // is busy for their total, and for the longest one at least.
   const GradsPlan own = plan;

@@ -80,8 +80,8 @@ static void own_plans(int64_t M, int64_t N, int64_t K, int cus) {
   const Product x{M, K, slice_count(cols, 2), false, true}, w{cols, K, slice_count(M, 2), false, true};
   for (int which = 1; which <= 3; ++which)
     for (const char* forced : kNotGrads)
-      CHECK(same(plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, ""),
-                 plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, forced)),
+      CHECK(same(plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, false, ""),
+                 plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, false, forced)),
             "%s: %lld %lld %lld of %d", forced, (long long)M, (long long)N, (long long)K, which);
 }
 
@@ -91,8 +91,10 @@ static void backward(int64_t M, int64_t F, int64_t K, int cus, const char* force
   const SplitPlan s = plan_recompute(g, cus, forced);
   check_split(s.splits, s.nk, g.nk, M * cols * 4, room, "pair", M, F, K, cus);
   const Product x{M, K, slice_count(cols, 2), false, true}, w{cols, K, slice_count(M, 2), false, true};
-  for (int which = 1; which <= 3; ++which) {
-    const GradsPlan plan = plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, forced);
+  for (int i = 0; i < 6; ++i) {  // dX, dW, both; the same on some of the CUs only
+    const int which = i % 3 + 1;
+    const bool capped = i >= 3;
+    const GradsPlan plan = plan_grads(which & 1 ? &x : nullptr, which & 2 ? &w : nullptr, cus, capped, forced);
     ++g_plans;
     if (which & 1) {
       check_split(plan.splits, plan.split_nk, x.nk, M * K * 4, room, "dX", M, F, K, cus);
@@ -100,7 +102,7 @@ static void backward(int64_t M, int64_t F, int64_t K, int cus, const char* force
       CHECK(plan.splits == 1 || plan.x == kMid || plan.x == kSmall, "tile %d", plan.x);
       CHECK(plan.x != kW192, "tile %d", plan.x);
     }
-    CHECK(!plan.shared || which == 3, "one gradient alone");
+    CHECK(!plan.shared || (which == 3 && !capped), "one gradient alone, or a cap");
     if (plan.shared) {
       CHECK((plan.x == kMid || plan.x == kSmall) && (plan.w == kMid || plan.w == kSmall), "%d %d", plan.x, plan.w);
       const int bx = plan.x == kMid ? 128 : 64, bw = plan.w == kMid ? 128 : 64;
