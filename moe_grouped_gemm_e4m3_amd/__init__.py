@@ -702,9 +702,9 @@ def _on_stream(stream):
     return torch.cuda.stream(stream)
 
 
-def _byte_workspace(workspace: torch.Tensor):
-    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous uint8 CUDA tensor")
+def _byte_workspace(workspace: torch.Tensor, dev: int):
+    if workspace.dtype != torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor on the current CUDA device")
     n = workspace.numel()
     return (workspace.data_ptr() if n else None), n
 
@@ -808,7 +808,7 @@ def gated_ffn_bf16_backward(dH, X, W, dX, dW, P=None, activation="silu", stream=
     if workspace is None:
         with _on_stream(stream):
             workspace = torch.empty(gated_ffn_backward_workspace_bytes(M, F, K), dtype=torch.uint8, device=dH.device)
-    ws, ws_bytes = _byte_workspace(workspace)
+    ws, ws_bytes = _byte_workspace(workspace, dev)
     _call("gated_ffn_bf16_backward", dH.data_ptr(), lddh, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(P), ldp,
           _ptr(dX), lddx, _ptr(dW), lddw, M, F, K, act, ws, ws_bytes, _raw_stream(stream, dev))
     return dX, dW

@@ -44,3 +44,31 @@ def test_backward_of_closed_gates_under_large_gradients(gpu_lib, act, kept):
     # the open gate: the pair and the output are rounded once each
     want, near = np.array([dg[2], du[2]]), np.array([got[2, 0], got[F + 2, 0]])
     assert_within(near, want, 2.0 ** -7 * np.abs(want), "open gate")
+
+
+def test_backward_refuses_a_workspace_of_another_device(monkeypatch):
+    """Its memory is written by kernels of the operands' device."""
+    import moe_grouped_gemm_e4m3_amd as fg
+
+    class Workspace:  # a tensor of another device, as far as the wrapper looks
+        dtype, is_cuda = torch.uint8, True
+
+        def __init__(self, device):
+            self.device = device
+
+        get_device = lambda self: self.device  # noqa: E731
+        is_contiguous = lambda self: True  # noqa: E731
+        numel = lambda self: 1 << 20  # noqa: E731
+        data_ptr = lambda self: 0x10000  # noqa: E731
+
+    calls = []
+    monkeypatch.setattr(fg, "_device", lambda: 0)
+    monkeypatch.setattr(fg, "_matrix", lambda t, name, dtype, rows, cols, dev: cols)
+    monkeypatch.setattr(fg, "_raw_stream", lambda stream, dev: 0)
+    monkeypatch.setattr(fg, "_call", lambda name, *args: calls.append((name, args)))
+    x, w, dh = (bf16(torch.zeros(s)) for s in ((4, 16), (12, 16), (4, 6)))
+    with pytest.raises(TypeError, match="workspace"):
+        fg.gated_ffn_bf16_backward(dh, x, w, x.clone(), w.clone(), workspace=Workspace(1))
+    assert not calls
+    fg.gated_ffn_bf16_backward(dh, x, w, x.clone(), w.clone(), workspace=Workspace(0))
+    assert [name for name, _ in calls] == ["gated_ffn_bf16_backward"] and 0x10000 in calls[0][1]
