@@ -41,7 +41,9 @@ class GatedFFN(torch.autograd.Function):
         ctx.activation = activation
         return H
 
+    # a gradient of the gradients raises: the kernels have none to give
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dH):
         X, W, P = ctx.saved_tensors
         dX = torch.empty_like(X) if ctx.needs_input_grad[0] else None
