@@ -473,9 +473,9 @@ fg_status int8_cast_per_row_bf16(const uint16_t* x, int64_t ldx, int8_t* q, floa
  *   B   device [N, K] int8, row stride ldb bytes (ldb >= K, ldb % 16 == 0, B 16-byte aligned)
  *   sb  device fp32 [N]
  *   D   device [M, N] bf16, row stride ldd elements (ldd >= N); only D[0:M, 0:N] is written
- * M, N >= 0 arbitrary, K % 16 == 0, K <= 131056 (the sum of more products may
- * leave int32; FG_EUNSUPPORTED).  K == 0 writes D = sa * sb * 0.  Rows of
- * at most 4 MiB.  The product is scaled as (sum * sa[m]) * sb[n] in fp32 and
+ * 0 <= M <= 2^30, 0 <= N <= 2^29, K % 16 == 0, K <= 131056 (the sum of more
+ * products may leave int32), rows of at most 4 MiB (FG_EUNSUPPORTED past these
+ * limits).  K == 0 writes D = sa * sb * 0.  The product is scaled as (sum * sa[m]) * sb[n] in fp32 and
  * rounded once.  D may not overlap an input.  Allocates nothing.
  */
 fg_status gemm_int8_nt(const int8_t* A, int64_t lda, const float* sa, const int8_t* B, int64_t ldb, const float* sb,
@@ -493,7 +493,8 @@ typedef enum { FG_ACT_SILU = 0, FG_ACT_GELU_TANH = 1 } fg_activation;
  *   W   device [2F, K] bf16, gate rows then up rows, row stride ldw elements (as ldx)
  *   H   device [M, F] bf16, row stride ldh elements (ldh >= F); written
  *   P   NULL, or device fp32 [M, 2F] (row stride ldp >= 2F): receives [g u] for the backward pass
- * M, F >= 0 arbitrary, K % 8 == 0 (K == 0: g = u = 0), rows of at most 4 MiB.
+ * 0 <= M <= 2^30, 0 <= F <= 2^29, K % 8 == 0 (K == 0: g = u = 0), rows of X
+ * and W of at most 4 MiB.
  * g and u are accumulated in fp32 and not rounded before the activation.  H
  * and P may not overlap each other or an input.  Allocates nothing.
  */
@@ -513,14 +514,18 @@ fg_status gated_ffn_bf16(const uint16_t* X, int64_t ldx, const uint16_t* W, int6
  *       [dg du] in bf16 and, where dX or the pair is small, fp32 partials of their sums (at most
  *       32 MiB); needs no initialisation; in use until the call's work has finished
  * dX and dW accumulate in fp32 over the bf16 pair [dg du].  M == 0 writes
- * dW = 0, F == 0 writes dX = 0.  F <= 2^20.  Outputs may not overlap inputs.
+ * dW = 0, F == 0 writes dX = 0.  M <= 2^30; F <= 2^20 (a row of [dg du] is at
+ * most 4 MiB; with M == 0, F <= 2^28); K and rows of X and W as in the forward
+ * call.  Outputs may not overlap inputs.
  */
 fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16_t* X, int64_t ldx,
                                   const uint16_t* W, int64_t ldw, const float* P, int64_t ldp, uint16_t* dX,
                                   int64_t lddx, uint16_t* dW, int64_t lddw, int M, int F, int K, int activation,
                                   void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of gated_ffn_bf16_backward; -1 for sizes it rejects. */
+/* Workspace bytes of gated_ffn_bf16_backward; -1 for negative sizes, M or K
+ * above 2^30 and F above 2^28.  The call's other limits (F <= 2^20 with M > 0,
+ * K % 8 == 0, rows of 4 MiB) are not looked at here. */
 int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F, int K);
 
 /*
@@ -528,7 +533,7 @@ int64_t fg_gated_ffn_backward_workspace_bytes(int M, int F, int K);
  *     g = sx * sw[0:F] * (X . W[0:F]^T),  u likewise with rows F..2F-1,  H = bf16( act(g) * u ).
  *   X, sx, W, sw  as A, sa, B, sb of gemm_int8_nt, W and sw of 2F rows
  *   H             device [M, F] bf16, row stride ldh (ldh >= F); written
- * M, F >= 0 arbitrary; K as in gemm_int8_nt.  H may not overlap an input.
+ * M, F, K as M, N, K in gemm_int8_nt.  H may not overlap an input.
  * Allocates nothing.
  */
 fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const int8_t* W, int64_t ldw,

@@ -20,6 +20,7 @@
 namespace fg {
 namespace {
 
+// rows of an output, and of the weights of a gated output
 constexpr int64_t kMaxRows = (int64_t)1 << 30;
 constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;  // buffer offsets inside a tile are 32-bit
 // |sum| <= 128 * 128 * K must stay below 2^31
@@ -211,7 +212,8 @@ fg_status check_sizes(int M, int N, int K, int mult, bool* empty) {
     *empty = true;
     return FG_OK;
   }
-  if (M > kMaxRows || N > kMaxRows / 2) return set_error(FG_EUNSUPPORTED, "more than 2^30 rows");
+  if (M > kMaxRows) return set_error(FG_EUNSUPPORTED, "M=%d: more than 2^30 rows", M);
+  if (N > kMaxRows / 2) return set_error(FG_EUNSUPPORTED, "%d output columns, more than 2^29", N);
   return FG_OK;
 }
 
@@ -398,7 +400,8 @@ fg_status gated_ffn_bf16_backward(const uint16_t* dH, int64_t lddh, const uint16
   FG_TRY(check_activation(activation));
   // no gradient element is asked for: dX is M x K, dW 2F x K
   if (K == 0 || ((!dX || M == 0) && (!dW || F == 0))) return FG_OK;
-  if (M > kMaxRows || F > kMaxRows / 4) return set_error(FG_EUNSUPPORTED, "more than 2^30 rows");
+  if (M > kMaxRows) return set_error(FG_EUNSUPPORTED, "M=%d: more than 2^30 rows", M);
+  if (F > kMaxRows / 4) return set_error(FG_EUNSUPPORTED, "F=%d: more than 2^28 hidden units", F);
   FG_TRY(check_workspace(workspace, workspace_bytes, M > 0 && F > 0 ? backward_bytes(M, F, K) : 0));
   if (dX && M > 0) {
     FG_TRY(require_ptr(dX, 2, "dX"));

@@ -93,3 +93,18 @@ def test_no_reduction_looks_at_no_operand(gpu_lib, M, N, ld):
         assert call() == 0, lib.fg_last_error()
         assert (D == 0).all()
     assert (P == 0).all()
+
+
+@pytest.mark.parametrize("M,N,needle", [((1 << 30) + 1, 64, "M=1073741825: more than 2^30"),
+                                        (64, (1 << 29) + 1, "536870913 output columns, more than 2^29")])
+def test_size_limits_are_named(M, N, needle):
+    import moe_grouped_gemm_e4m3_amd as fg
+
+    lib, q = fg.load_library(), 0x10000
+    for st in (lib.gemm_int8_nt(q, 16, q, q, 16, q, q, N, M, N, 16, None),
+               lib.gated_ffn_int8(q, 16, q, q, 16, q, q, N, M, N, 16, 0, None),
+               lib.gated_ffn_bf16(q, 16, q, 16, q, N, None, 0, M, N, 16, 0, None)):
+        assert st == 3 and needle in lib.fg_last_error().decode()
+    F = min(N, (1 << 28) + 1)
+    st = lib.gated_ffn_bf16_backward(q, F, q, 16, q, 16, None, 0, q, 16, q, 16, M, F, 16, 0, q, 1 << 62, None)
+    assert st == 3 and ("M=1073741825" if M > 64 else "F=268435457: more than 2^28") in lib.fg_last_error().decode()
