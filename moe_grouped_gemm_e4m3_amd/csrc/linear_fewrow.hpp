@@ -87,7 +87,7 @@ __device__ __forceinline__ void fewrow_store(const LinearParams& p, int m, int n
   }
   uint16_t* dst = p.D + (int64_t)m * p.ldd + n;
   if (n + 4 <= p.N) {
-    *(uint2_at2*)dst = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+    *(u32x2_at2*)dst = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r)

@@ -26,8 +26,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // stride): the compiler makes one access of them, which the hardware takes at
 // any address.
 typedef i32x4 i32x4_at2 __attribute__((aligned(2)));
-typedef uint2 uint2_at2 __attribute__((aligned(2)));
-typedef uint4 uint4_at2 __attribute__((aligned(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 
 enum LinearEpi {
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p, int par
     if (n + C <= p.N) {
 #pragma unroll
       for (int q = 0; q < C / 4; ++q) {
-        const uint2 v = *(const uint2_at2*)(hp + 4 * q);
+        const u32x2 v = *(const u32x2_at2*)(hp + 4 * q);
         h[2 * q] = v.x;
         h[2 * q + 1] = v.y;
       }
@@ -198,8 +198,7 @@ static __global__ __launch_bounds__(256) void add_partials_kernel(LinearParams p
 #pragma unroll 8
     for (int k = 1; k < splits; ++k) s += src[k * quads + i];
     const int64_t m = i / per_row;
-    *(uint2_at2*)(p.D + m * p.ldd + (i - m * per_row) * 4) =
-        make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    *(u32x2_at2*)(p.D + m * p.ldd + (i - m * per_row) * 4) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
   }
 }
 

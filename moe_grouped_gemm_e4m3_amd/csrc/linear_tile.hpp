@@ -338,7 +338,7 @@ __device__ __forceinline__ void store_pair(uint16_t* row, int n0, int n_end, boo
 template <bool FULL>
 __device__ __forceinline__ void store_quad(uint16_t* row, int n, int n_end, bool ok, uint32_t a0, uint32_t a1) {
   if (FULL || (ok && n + 4 <= n_end)) {
-    *(uint2_at2*)(row + n) = make_uint2(a0, a1);
+    *(u32x2_at2*)(row + n) = u32x2{a0, a1};
   } else if (ok) {
     const uint32_t w[2] = {a0, a1};
 #pragma unroll
@@ -440,7 +440,7 @@ __device__ __forceinline__ void store_blocks(const LinearParams& p, const Linear
         if (ok) {
           const uint16_t* hrow = p.dH + (int64_t)m * p.lddh;
           if (FULL || n + 4 <= p.N) {
-            const uint2 u = *(const uint2_at2*)(hrow + n);
+            const u32x2 u = *(const u32x2_at2*)(hrow + n);
             h[0] = u.x;
             h[1] = u.y;
           } else {
