@@ -541,7 +541,7 @@ __device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>&
                                             const uint8_t* __restrict st_b, const Loads<C>& ld,
                                             uint8_t* __restrict ld_a, uint8_t* __restrict ld_b, int wave, int lane) {
   constexpr int READS = (C::SM + C::SN + C::SN - 1) / C::SN;
-  constexpr int LOADS = LOAD ? C::LA + C::LB : 0;
+  constexpr int LOADS = C::LA + C::LB;
 #pragma unroll
   for (int j = 0; j < C::SN; ++j) {
 #pragma unroll
@@ -553,7 +553,7 @@ __device__ __forceinline__ void linear_half(const LinearParams& p, LinearAcc<C>&
     }
 #pragma unroll
     for (int r = 0; r < LOADS; ++r) {
-      if (r * C::SN / LOADS != j) continue;
+      if (!LOAD || r * C::SN / LOADS != j) continue;
       if (r < C::LB)
         ld.b.issue(p, ld_b, ld.kb, r, wave, lane);
       else

@@ -15,6 +15,6 @@ from tests.test_host_sanitizers import CSRC, HIPCC, INCLUDE
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="ROCm toolchain not found")
 def test_no_access_claims_more_alignment_than_it_has():
     r = subprocess.run([HIPCC, "--offload-arch=gfx950", "-std=c++17", "-fsyntax-only", "-Werror=align-mismatch",
-                        "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "linear.hip")],
+                        "-Werror=division-by-zero", "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "linear.hip")],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-3000:]
