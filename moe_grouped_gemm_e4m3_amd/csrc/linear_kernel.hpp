@@ -163,6 +163,13 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(LinearParams p, int par
         h[2 * q + 1] = v.y;
       }
     } else {
+      if constexpr (PARTS) {
+        // padding columns hold zeros; their sums need not, where an infinite
+        // input met the zeros that stand for their weights
+#pragma unroll
+        for (int r = 0; r < C; ++r)
+          if (n + r >= p.N) g[r] = u[r] = 0.f;
+      }
 #pragma unroll
       for (int q = 0; q < C / 2; ++q)
         h[q] = (n + 2 * q < p.N ? (uint32_t)hp[2 * q] : 0u) | (n + 2 * q + 1 < p.N ? (uint32_t)hp[2 * q + 1] << 16 : 0u);

@@ -46,6 +46,31 @@ def test_backward_of_closed_gates_under_large_gradients(gpu_lib, act, kept):
     assert_within(near, want, 2.0 ** -7 * np.abs(want), "open gate")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("plan", ["pair", "small", "w256", "kept"])
+@pytest.mark.parametrize("M,F,K", [(190, 70, 1928), (40, 3, 1032)])
+def test_backward_of_an_infinite_input(gpu_lib, monkeypatch, plan, M, F, K):
+    """All weights and gradients positive, one input infinite: its row of dX
+    is infinite, not NaN, however the pre-activations are summed, and the other
+    rows do not see it."""
+    announce(f"infinite input {M}x{F}x{K} {plan}")
+    monkeypatch.setenv("FG_LINEAR_PLAN", "" if plan == "kept" else plan)
+    gen = torch.Generator().manual_seed(1)
+    X, W, dH = (bf16(torch.rand(s, generator=gen) / K + 1.0 / K) for s in ((M, K), (2 * F, K), (M, F)))
+    X[7, 5] = float("inf")
+    P = None
+    if plan == "kept":
+        P = torch.empty(M, 2 * F, device="cuda")
+        gpu_lib.gated_ffn_bf16(X.cuda(), W.cuda(), bf16(torch.empty(M, F)).cuda(), P=P)
+    dX, dW = Output(M, K), Output(2 * F, K)
+    gpu_lib.gated_ffn_bf16_backward(dH.cuda(), X.cuda(), W.cuda(), dX.t, dW.t, P=P)
+    got = f64(dX.t)
+    assert np.isposinf(got[7]).all()
+    rows = np.arange(M) != 7
+    wx, _, bx, _ = ref.gated_backward(f64(dH)[rows], f64(X)[rows], f64(W), "silu")
+    assert_within(got[rows], wx, bx, "the other rows")
+
+
 def test_backward_refuses_a_workspace_of_another_device(monkeypatch):
     """Its memory is written by kernels of the operands' device."""
     import moe_grouped_gemm_e4m3_amd as fg
