@@ -446,11 +446,13 @@ fg_status fp8_cast_per_block_ue8m0_bf16(const uint16_t* w, int64_t ldw, uint8_t*
  * signed bytes with an fp32 scale per row (a token of the activations, an
  * output channel of the weights), or BF16.  All matrices are row-major with
  * their last dimension contiguous.
- * Rows that lie a multiple of 128 bytes apart load fastest (others cost 13 to
- * 40 % of a large product's time).
+ * Rows that lie a multiple of 128 bytes apart load fastest (others cost up to
+ * 30 % of a product's time).
  * Only the backward pass needs a workspace.  Their plans depend only on the
- * arguments, the device and the CU cap, and sums have a fixed order, so
- * results are reproducible.
+ * arguments, the device, the CU cap and the environment variable
+ * FG_LINEAR_PLAN (read in every call, for tuning and tests: it forces a plan,
+ * and with it the order of bf16 sums).  Sums have a fixed order in every plan,
+ * so results are reproducible.
  */
 
 /*

@@ -263,8 +263,8 @@ fg_status launch_gated_grad(const LinearParams& g, int parts, void* stream, cons
 
 // [dg du] with the pre-activations recomputed: in the product's own epilogue,
 // or, where its tiles leave most of the device idle, from partial sums in
-// `partials` (with dW, 395 x 36 x 6232: 40 us without, 22 with; 595 x 175 x
-// 3320: 31 and 24).
+// `partials` (with dW, 395 x 36 x 6232: 36 us without, 19 with; 595 x 175 x
+// 3320: 26 and 21).
 fg_status launch_recompute(LinearParams& g, float* partials, void* stream, const char* what) {
   int cus = 0;
   FG_TRY(usable_cus(&cus));
@@ -294,7 +294,8 @@ fg_status cast_rows(const T* x, int64_t ldx, int8_t* q, float* s, int M, int K, 
   const int pieces = K / (16 / (int)sizeof(T));
   const dim3 grid((unsigned)std::min(M, 1 << 20));
   // Two pieces a thread while they hold the row (4096 x 7168 bf16: 512 threads
-  // 15.0 us, 5.9 TB/s; 4096 x 1024: 256 threads 5.7 us), four of a longer one.
+  // 16 us, 5.5 TB/s; 4096 x 1024: 256 threads 6.1 us), four of a longer one
+  // (4096 x 7168 fp32: 22 us, 6.7 TB/s from the last-level cache).
   if (pieces <= 512)
     hipLaunchKernelGGL((int8_cast_kernel<T, 256, 2>), grid, dim3(256), 0, (hipStream_t)stream, x, ldx, q, s, M, K);
   else if (pieces <= 1024)

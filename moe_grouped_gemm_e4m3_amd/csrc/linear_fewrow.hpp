@@ -10,13 +10,14 @@
 // (parts), which run side by side and share the weights in L2.  Nothing is
 // split over workgroups: where tiles are few, smaller row parts occupy the
 // device without an exchange (64 x 512 x 8192: four 16-row parts of eight
-// waves 5.2 us, one 64-row part 8.2, its slices split over four workgroups
-// through memory 7.3).
+// waves 4.2 us, one 64-row part 7.2; its slices split over four workgroups
+// through memory took 1.4 times the former).
 //
-// Measured with the weights in the last-level cache: int8 1 x 7168 x 2048 3.5
-// us (4.2 TB/s), gated int8 16 x 2048 x 7168 6.4 us (4.6 TB/s), gated bf16
-// 1 x 2048 x 7168 9.8 us (6 TB/s).  int8 128 x 2112 x 7168, 10.2 us, is bound
-// by what each CU fetches: its activations' rows next to its weights'.
+// Measured in a HIP graph with the weights in the last-level cache: int8 1 x
+// 7168 x 2048 2.9 us (5.1 TB/s), gated int8 16 x 2048 x 7168 5.1 us (5.8 TB/s),
+// gated bf16 1 x 2048 x 7168 10.1 us (5.8 TB/s).  int8 128 x 2112 x 7168, 9.9
+// us, is bound by what each CU fetches: its activations' rows next to its
+// weights'.
 #pragma once
 
 #include "linear_tile.hpp"

@@ -3,9 +3,9 @@
 // device and no HIP, so the sanitizer tests run it over sizes and CU counts.
 //
 // Each candidate's time is estimated from its tiles and slices with costs
-// measured on MI355X (256 CUs; microseconds; int8 and bf16 slices cost the
-// same, both are 128 bytes and 2048 MFMA cycles on the 256 x 256 tile), and
-// the cheapest runs.  The estimates only rank candidates: fitted to 700 random
+// measured on MI355X (256 CUs; microseconds, a call in a HIP graph; int8 and
+// bf16 slices cost the same, both are 128 bytes and 2048 MFMA cycles on the 256
+// x 256 tile), and the cheapest runs.  The estimates only rank candidates: fitted to 700 random
 // products and 150 gradients, on others the choice is 2 % (gradients 1 %)
 // slower than the fastest tile on average.
 #pragma once
@@ -66,36 +66,36 @@ inline double pairs_us(double tiles, int cus, int nk, double idle, double one, d
 // The tiles below 256 rows, with their times a slice where both operands are
 // K-major and where one or both are MN-major (mn).
 //
-// 64 x 64, eight waves, for few tiles: in two groups (256 x 4096 x 7168 int8 17
-// us, 28 on 128 x 128); where operands are MN-major in one, so that every sum
+// 64 x 64, eight waves, for few tiles: in two groups (256 x 4096 x 7168 int8 15
+// us, 25 on 128 x 128); where operands are MN-major in one, so that every sum
 // of a gradient runs in the order of its slices and its bits depend on nothing
 // but the split.  There it serves splits and shared launches alone: two
-// workgroups of four waves are as fast with few tiles (dX 333 x 1528 x 2176 13
-// us both) and faster with many.
+// workgroups of four waves are as fast with few tiles and faster with many.
 inline double small_us(double tiles, int cus, int nk, bool mn) {
   return mn ? tile_us(tiles, cus, nk, 0.28, 0.35, 1.2) : tile_us(tiles, cus, nk, 0.177, 0.19, 1.5);
 }
 
-// 64 x 64, two workgroups of four waves, where tiles outnumber the CUs (dW
-// 2176 x 1528 x 333 12 us, 13 on eight waves).
+// 64 x 64, two workgroups of four waves, where tiles outnumber the CUs (320 x
+// 4096 x 1024 int8 6.1 us, 8.3 on eight waves; dX 600 x 1528 x 2048 with the
+// pair's pass 18.4 us, 20.7 on 128 x 64).
 inline double small2_us(double tiles, int cus, int nk, bool mn) {
   return mn ? pairs_us(tiles, cus, nk, 0.22, 0.32, 0.68, 1.3) : pairs_us(tiles, cus, nk, 0.187, 0.19, 0.54, 1.25);
 }
 
-// 128 x 64, two workgroups of eight waves (512 x 4096 x 7168 int8 28 us, 31 on
+// 128 x 64, two workgroups of eight waves (512 x 4096 x 7168 int8 22 us, 25 on
 // 128 x 128 and on 64 x 64; gated bf16 333 x 1056 x 1528 11 us, 17 on 128 x 128).
 inline double half2_us(double tiles, int cus, int nk, bool mn) {
   return mn ? pairs_us(tiles, cus, nk, 0.30, 0.39, 0.75, 1.7) : pairs_us(tiles, cus, nk, 0.23, 0.30, 0.66, 1.9);
 }
 
-// 128 x 128, eight waves, four stages (1000 x 4096 x 7168 int8 33 us, 72 on
-// 256 x 256).
+// 128 x 128, eight waves, four stages (1000 x 4096 x 7168 int8 32 us, 70 on
+// 256 x 256; rows half a line off, 36).
 inline double mid_us(double tiles, int cus, int nk, bool mn) {
   return mn ? tile_us(tiles, cus, nk, 0.46, 0.53, 2.0) : tile_us(tiles, cus, nk, 0.44, 0.51, 2.4);
 }
 
-// 128 x 128, two workgroups of four waves (dW 3072 x 2048 x 1500 28 us, 33 on
-// eight waves).
+// 128 x 128, two workgroups of four waves (dW 2816 x 2048 x 1500 with the pair's
+// pass 33 us, 40 on eight waves).
 inline double mid2_us(double tiles, int cus, int nk, bool mn) {
   return mn ? pairs_us(tiles, cus, nk, 0.80, 0.80, 0.90, 1.5) : pairs_us(tiles, cus, nk, 0.70, 0.70, 0.90, 1.5);
 }
@@ -137,9 +137,12 @@ inline TilePlan plan_tile(const Product& p, int cus, const char* forced) {
     if (us < best.us) best = TilePlan{kind, us};
   };
   // 256 rows by 256, 224, 192 or 160: the time of a slice grows with the CUs at
-  // work, since the chip's power limits these (int8 4096 x 7168 x 16384: 372 us
-  // with 256 columns, 343 with 224; 4096 x 2112 x 7168: 78 with 256, 60 with
-  // 160; gated bf16 4096 x 12288 x 1536: 238 with 256, 266 with 192).
+  // work, since the chip's power limits these (int8 4096 x 7168 x 16384: 374 us
+  // with 256 columns, 346 with 224; 4096 x 2112 x 7168: 71 with 256, 60 with
+  // 160; gated bf16 4096 x 12288 x 1536: 227 with 256, 242 with 192; 1500 x 6000
+  // x 3008: 122 and 107.  Between these two the choice is within 1 % of the
+  // better on 17 gated shapes, bf16 and int8, of 1000 to 8192 rows, 1536 to
+  // 14336 units and reductions of 1024 to 7168).
   offer(kW256, tile_us(count(256, 256), cus, p.nk, 1.2, mn ? 1.3 : 1.45, 4.0));
   if (p.gated) {
     offer(kW192, tile_us(count(256, 192), cus, p.nk, 0.95, 1.15, 4.0));
@@ -293,8 +296,8 @@ inline GradsPlan plan_grads(const Product* x, const Product* w, int cus, bool ca
     plan.x = t.kind;
     x_us = t.us;
     separate = t.us == 0;
-    // 251 x 1016 with 178 slices: 52 us on 64 64 x 64 tiles, a quarter of the
-    // device; split 27 us with the addition.
+    // 251 x 1016 with 178 slices, with the pair's pass: 55 us on 64 64 x 64
+    // tiles, a quarter of the device; split 25 us with the addition.
     const int64_t one = x->M * x->cols * 4;
     const SplitPlan a = plan_split(*x, one, cus, 64, small_us);
     const SplitPlan b = plan_split(*x, one, cus, 128, mid_us);

@@ -1,14 +1,20 @@
 // linear_tile.hpp -- the large-tile kernel of the 8-bit-integer and bf16
 // products (operations and epilogues: linear_kernel.hpp).
 //
+// Times in this file and in linear_plan.hpp are of one call among others in a
+// HIP graph, on operands that stay the same (other operands in every call and
+// kernel traces: up to 10 % more).
+//
 // A slice of a 256 x 256 tile is 2048 MFMA cycles for 64 KiB of loads; the
-// chip's power limits it (2.0 GHz): int8 4096 x 7168 x 16384 336 us, 2860
-// TOP/s; gated bf16 4096 x 2048 x 7168 150 us, 1600 TFLOP/s; dX and dW at
-// 4096 x 7168 x 4096 181 and 187 us, 1330 and 1290 TFLOP/s, their transposing
-// fragment reads twice as many.  Smaller tiles are bound by each CU's loads
-// and the barrier of a slice (128 x 128: 62 GB/s a CU).  K-major rows that do
-// not lie a multiple of 128 bytes apart cost 15 to 40 % more: a slice of such a
-// row takes parts of two cache lines.
+// chip's power limits the tiles of 256 rows (2.0 GHz): int8 4096 x 7168 x 16384
+// on 256 x 224 tiles 345 us, 2790 TOP/s; gated bf16 4096 x 2048 x 7168 on 256 x
+// 256 164 us, 1460 TFLOP/s; dX and dW at 4096 x 7168 x 4096 on 256 x 224 199
+// and 203 us in a trace, 1210 and 1190 TFLOP/s, their transposing fragment
+// reads twice as many.  Smaller tiles take two to three times their MFMAs' time
+// for a slice: its loads and LDS reads and the barrier (128 x 128: 62 GB/s of
+// loads a CU).  K-major rows that do not lie a multiple of 128 bytes apart cost
+// up to 30 % more (half a line off: 4 to 16 %): a slice of such a row takes
+// parts of two cache lines.
 #pragma once
 
 #include "linear_kernel.hpp"
@@ -350,8 +356,8 @@ __device__ __forceinline__ void store_quad(uint16_t* row, int n, int n_end, bool
 // The finished tile, straight from the accumulators.  Lane (l16, kq) holds
 // row l16 and columns [4 kq, +4) of every 16 x 16 block.  FULL: the whole tile
 // lies inside the output, so nothing is tested
-// (gated with kept pre-activations, 4096 x 2048 x 7168: 177 us with the tests,
-// 158 without).
+// (gated with kept pre-activations, 4096 x 2048 x 7168: 192 us with the tests,
+// 175 without).
 template <class C, int ACT, bool FULL>
 __device__ __forceinline__ void store_blocks(const LinearParams& p, const LinearWork& t, const LinearAcc<C>& acc,
                                              int wm, int wn, int lane) {
