@@ -5,11 +5,14 @@ CPU only."""
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 
 import pytest
 
-from tests.test_host_sanitizers import CSRC, HIPCC, INCLUDE
+from moe_grouped_gemm_e4m3_amd.build import CSRC, INCLUDE
+
+HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 
 
 @pytest.mark.skipif(not os.path.exists(HIPCC), reason="ROCm toolchain not found")
