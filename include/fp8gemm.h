@@ -542,6 +542,136 @@ fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const in
                          const float* sw, uint16_t* H, int64_t ldh, int M, int F, int K, int activation,
                          void* stream);
 
+/*
+ * 4-bit weights with a scale for each group of a row, and their product with a
+ * few rows of bf16 activations.
+ *
+ * Packing.  Columns 8 i .. 8 i + 7 of a row are one little-endian 32-bit word:
+ * column 8 i + j in bits 8 j .. 8 j + 3 and column 8 i + 4 + j in bits 8 j + 4 ..
+ * 8 j + 7 (j < 4).  A row is padded to whole chunks of 128 columns (64 bytes);
+ * columns 32 m + 8 q .. 32 m + 8 q + 7 of a chunk (m, q < 4) are its word 4 q + m.
+ * What padding words hold does not matter to the products.
+ *
+ * Groups.  `group` is 32, 64 or a multiple of 128; group g of a row is its
+ * columns g group .. (g + 1) group - 1, the last one may be partial.  K % 32 == 0.
+ * With Kg = ceil(K / group), Kp = ceil(K / 128):
+ *   q  device [N][64 Kp] bytes, packed, 16-byte aligned
+ *   s  device bf16 [N][Kg]
+ *   z  NULL (every zero point is 8), or device uint8 [N][Kg], 0 <= z <= 255
+ * stand for w[n,k] = s[n, k / group] * (q[n,k] - z[n, k / group]).
+ */
+
+/*
+ * Cast of weights to this form (x: fp32, or bf16 widened exactly), in fp32 steps:
+ *   z == NULL:  s = bf16(max(max |x|, 1e-20f) / 7),                q = clamp(rint(x / s) + 8, 0, 15)
+ *   else:       lo = min(min x, 0), hi = max(max x, 0),
+ *               s = bf16(max(hi - lo, 1e-20f) / 15), z = clamp(rint(-lo / s), 0, 15),
+ *               q = clamp(rint(x / s) + z, 0, 15)
+ * over each group.  w: device [N, K], row stride ldw elements (ldw >= K,
+ * 16-byte aligned rows).  Padding words are written as zeros.  Input values must
+ * be finite.  K <= 2^20.  N == 0 or K == 0 writes nothing.
+ */
+fg_status int4_cast_per_group(const float* w, int64_t ldw, uint8_t* q, uint16_t* s, uint8_t* z, int N, int K, int group,
+                              void* stream);
+fg_status int4_cast_per_group_bf16(const uint16_t* w, int64_t ldw, uint8_t* q, uint16_t* s, uint8_t* z, int N, int K,
+                                   int group, void* stream);
+
+/*
+ * D[m,n] = bf16( sum_k A[m,k] * sb[n, k / group] * (B[n,k] - zb[n, k / group]) )
+ *   A   device [M, K] bf16, row stride lda elements (lda >= K, lda % 8 == 0, 16-byte aligned, rows of at most 4 MiB)
+ *   B, sb, zb  4-bit weights [N, K] as above (zb may be NULL)
+ *   D   device [M, N] bf16, row stride ldd elements (ldd >= N); only D[0:M, 0:N] is written
+ * Made for M <= 64, where the weights are read once; more rows are taken 64 at a
+ * time.  M, N <= 2^30, K % 32 == 0, K <= 2^20.  K == 0 writes zeros.  Sums are in
+ * fp32, the zero point is taken out of a group's sum once, and the result is
+ * rounded once.  A row of A with an infinity or a NaN gives a row of D that holds
+ * infinities or NaN.  Sums have a fixed order, which depends on the sizes only.
+ * D may not overlap an input.  Allocates nothing.
+ */
+fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const uint16_t* sb, const uint8_t* zb,
+                       uint16_t* D, int64_t ldd, int M, int N, int K, int group, void* stream);
+
+/* Scores of the expert router: a softmax over the experts, or a sigmoid of each logit. */
+typedef enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 } fg_scoring;
+
+/*
+ * Expert router.  For each token, s = softmax(l) or sigmoid(l), and the k experts
+ * with the largest s + bias (without a bias and with one group: with the largest
+ * logits); equal ones in the order of their indices.  With groups > 1 the E /
+ * groups consecutive experts of a group stand together: a group's value is the
+ * sum of its two largest s + bias, and only experts of the top_groups groups
+ * with the largest values are candidates.
+ *   logits   device fp32 (or bf16) [T, E], row stride ld elements
+ *   bias     NULL, or device fp32 [E]
+ *   ids      device int32 [T, k]: the chosen experts, best first
+ *   weights  device fp32 [T, k]: scale * s of the chosen, with `normalize` over
+ *            the sum of the chosen s (0 where that is 0)
+ * An expert whose logit (or bias) is -infinity is no candidate; places that no
+ * candidate is left for hold id -1 and weight 0.  A NaN is chosen after all
+ * numbers and gives NaN weights: under softmax all of its row's.
+ * 1 <= k <= min(E, 64), E <= 1024, groups <= 64 divides E.  Scores and what they
+ * are compared by are computed in 64 bits, weights are rounded once.
+ */
+fg_status moe_route(const float* logits, int64_t ld, const float* bias, int32_t* ids, float* weights, int T, int E, int k,
+                    int scoring, int groups, int top_groups, int normalize, float scale, void* stream);
+fg_status moe_route_bf16(const uint16_t* logits, int64_t ld, const float* bias, int32_t* ids, float* weights, int T, int E,
+                         int k, int scoring, int groups, int top_groups, int normalize, float scale, void* stream);
+
+/*
+ * Its gradient: dlogits (device, the logits' type, [T, E], row stride ld_dl;
+ * every element is written) from dweights (device fp32 [T, k]), the logits and
+ * the forward call's ids, scoring, normalize and scale.  Places whose id is not
+ * in [0, E) have no gradient; the choice itself and the bias have none.  With an
+ * id in two places of a row both add up.
+ */
+fg_status moe_route_backward(const float* dweights, const float* logits, int64_t ld, const int32_t* ids, float* dlogits,
+                             int64_t ld_dl, int T, int E, int k, int scoring, int normalize, float scale, void* stream);
+fg_status moe_route_backward_bf16(const float* dweights, const uint16_t* logits, int64_t ld, const int32_t* ids,
+                                  uint16_t* dlogits, int64_t ld_dl, int T, int E, int k, int scoring, int normalize,
+                                  float scale, void* stream);
+
+/*
+ * A whole expert layer for a few tokens, in two kernels:
+ *     D[t] = bf16( sum_j weights[t,j] * W2[e] . h ),  e = ids[t,j],
+ *     h = act(g) * u,  g = W1[e][0:F] . X[t],  u = W1[e][F:2F] . X[t].
+ *   X    device [T, K] bf16, row stride ldx elements (ldx >= K, ldx % 8 == 0, 16-byte aligned, rows of at most 4 MiB)
+ *   W1   device [E, 2F, K] e4m3, packed, gate rows then up rows, 16-byte aligned
+ *   s1   device fp32 [E][ceil(2F/128)][ceil(K/128)]   (fp8_cast_per_block of each expert's W1)
+ *   W2   device [E, K, F] e4m3, packed, 16-byte aligned
+ *   s2   device fp32 [E][ceil(K/128)][ceil(F/128)]
+ *   ids  device int32 [T, k]; a place whose id is not in [0, E) is left out
+ *        (moe_route's -1, or an expert of another device), and its weight is not read
+ *   weights  device fp32 [T, k]
+ *   D    device [T, K] bf16, row stride ldd elements (ldd >= K); a token with no place left gets zeros
+ *   workspace  device, 256-byte aligned, fg_moe_ffn_workspace_bytes(T, k, F) bytes; needs no
+ *        initialisation; in use until the call's work has finished
+ * Activations are not quantised: products are of bf16 X (or of h, kept as the sum
+ * of two bf16) with the exact values of the codes, summed in fp32; D is rounded
+ * once.  A token that names an expert twice has the sum of both weights.  The
+ * weights of every named expert are read once for each 64 tokens; with many
+ * tokens for each expert the grouped GEMMs are faster.  Sums have a fixed order,
+ * which depends on the sizes and ids only.
+ * T <= 2^20, 1 <= k <= 32, 1 <= E <= 1024, K and F multiples of 16 up to 2^16.
+ * F == 0 writes zeros.  D may not overlap an input.  Allocates nothing.
+ */
+fg_status moe_ffn_fp8(const uint16_t* X, int64_t ldx, const uint8_t* W1, const float* s1, const uint8_t* W2,
+                      const float* s2, const int32_t* ids, const float* weights, uint16_t* D, int64_t ldd, int T, int k,
+                      int E, int F, int K, int activation, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The same on 4-bit weights (see int4_cast_per_group):
+ *   W1, s1, z1  E matrices of [2F, K], one after the other; W2, s2, z2  E of [K, F]
+ *   (z1, z2 may be NULL)
+ * K and F multiples of 32 up to 2^16.  Everything else as moe_ffn_fp8.
+ */
+fg_status moe_ffn_int4(const uint16_t* X, int64_t ldx, const uint8_t* W1, const uint16_t* s1, const uint8_t* z1,
+                       const uint8_t* W2, const uint16_t* s2, const uint8_t* z2, const int32_t* ids, const float* weights,
+                       uint16_t* D, int64_t ldd, int T, int k, int E, int F, int K, int group, int activation,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of moe_ffn_fp8 and moe_ffn_int4; -1 for sizes that they refuse. */
+int64_t fg_moe_ffn_workspace_bytes(int T, int k, int F);
+
 /* Row alignment of each expert segment in the contiguous layout: 128. */
 int fg_get_mk_alignment_for_contiguous_layout(void);
 

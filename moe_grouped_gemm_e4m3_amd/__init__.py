@@ -16,6 +16,10 @@ Layouts (Kb = ceil(K/128), Nb = ceil(N/128)):
 8-bit-integer products (int8, one fp32 scale per row of each operand) and the
 gated feed-forward block (bf16 or int8; W [2F, K], gate rows then up rows) take
 row-major matrices.
+
+4-bit weights (uint8, two codes a byte, a bf16 scale and optionally a zero
+point for each group of a row) are packed as include/fp8gemm.h describes;
+int4_cast_per_group makes them.
 """
 
 from __future__ import annotations
@@ -59,6 +63,13 @@ __all__ = [
     "gated_ffn_bf16_backward",
     "gated_ffn_backward_workspace_bytes",
     "gated_ffn_int8",
+    "int4_cast_per_group",
+    "gemm_int4_nt",
+    "moe_route",
+    "moe_route_backward",
+    "moe_ffn_fp8",
+    "moe_ffn_int4",
+    "moe_ffn_workspace_bytes",
     "get_mk_alignment_for_contiguous_layout",
     "set_num_cus",
     "get_num_cus",
@@ -73,6 +84,7 @@ FG_STATUS = {0: "FG_OK", 1: "FG_EINVAL", 2: "FG_EALIGN", 3: "FG_EUNSUPPORTED", 4
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SIGNATURES = {
     "gemm_fp8_nt": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I, _P]),
     "gemm_fp8_nt_ws": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I, _I, _I, _P, _I64, _P]),
@@ -108,6 +120,17 @@ _SIGNATURES = {
         _I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
     "fg_gated_ffn_backward_workspace_bytes": (_I64, [_I, _I, _I]),
     "gated_ffn_int8": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _P]),
+    "int4_cast_per_group": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _P]),
+    "int4_cast_per_group_bf16": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _P]),
+    "gemm_int4_nt": (_I, [_P, _I64, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P]),
+    "moe_route": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
+    "moe_route_bf16": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
+    "moe_route_backward": (_I, [_P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _F, _P]),
+    "moe_route_backward_bf16": (_I, [_P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _F, _P]),
+    "moe_ffn_fp8": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _P, _I64, _P]),
+    "moe_ffn_int4": (
+        _I, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _I, _I, _I, _P, _I64, _P]),
+    "fg_moe_ffn_workspace_bytes": (_I64, [_I, _I, _I]),
     "fg_get_mk_alignment_for_contiguous_layout": (_I, []),
     "fg_set_num_cus": (None, [_I]),
     "fg_get_num_cus": (_I, []),
@@ -812,6 +835,189 @@ def gated_ffn_bf16_backward(dH, X, W, dX, dW, P=None, activation="silu", stream=
     _call("gated_ffn_bf16_backward", dH.data_ptr(), lddh, X.data_ptr(), ldx, W.data_ptr(), ldw, _ptr(P), ldp,
           _ptr(dX), lddx, _ptr(dW), lddw, M, F, K, act, ws, ws_bytes, _raw_stream(stream, dev))
     return dX, dW
+
+
+def _packed(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """Address of a contiguous tensor of `dtype` and `shape` on device `dev`."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {str(dtype)[6:]} tensor on the current CUDA device, got {t.dtype} on {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _group_count(K: int, group: int) -> int:
+    if group not in (32, 64) and (group <= 0 or group % 128):
+        raise ValueError(f"group must be 32, 64 or a multiple of 128, got {group}")
+    return -(-K // group)
+
+
+def int4_cast_per_group(w, group=128, symmetric=False, q=None, s=None, z=None, stream=None):
+    """4-bit codes of fp32 or bf16 weights w [N, K] (K % 32 == 0) with a bf16 scale, and unless
+    `symmetric` a zero point, for each `group` columns (32, 64 or a multiple of 128) of a row:
+    w ~ s (q - z), z = 8 if symmetric.  -> (q uint8 [N, 64 ceil(K/128)], s bf16 [N, Kg],
+    z uint8 [N, Kg] or None), Kg = ceil(K/group)."""
+    if w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    N, K = w.shape
+    kg, width = _group_count(K, group), -(-K // 128) * 64
+    if symmetric and z is not None:
+        raise ValueError("a symmetric cast has no zero points")
+    dev = _device()
+    bf16 = w.dtype is torch.bfloat16
+    ldw = _matrix(w, "w", torch.bfloat16 if bf16 else torch.float32, N, K, dev)
+    with _on_stream(stream):
+        q = torch.empty(N, width, dtype=torch.uint8, device=w.device) if q is None else q
+        s = torch.empty(N, kg, dtype=torch.bfloat16, device=w.device) if s is None else s
+        if z is None and not symmetric:
+            z = torch.empty(N, kg, dtype=torch.uint8, device=w.device)
+    _call("int4_cast_per_group_bf16" if bf16 else "int4_cast_per_group", w.data_ptr(), ldw,
+          _packed(q, "q", torch.uint8, (N, width), dev), _packed(s, "s", torch.bfloat16, (N, kg), dev),
+          None if symmetric else _packed(z, "z", torch.uint8, (N, kg), dev), N, K, group, _raw_stream(stream, dev))
+    return q, s, None if symmetric else z
+
+
+def gemm_int4_nt(A, B, sb, D, zb=None, group=128, stream=None):
+    """D[M,N] = bf16(A . W^T), W[n,k] = sb[n, k/group] (B[n,k] - zb[n, k/group]), for bf16 A [M, K] and
+    4-bit weights as int4_cast_per_group makes them (zb None: zero points of 8).  For few rows: the
+    weights are read once for each 64."""
+    if A.dim() != 2 or D.dim() != 2:
+        raise ValueError("A and D must be matrices")
+    M, K = A.shape
+    N = D.shape[1]
+    kg = _group_count(K, group)
+    bf16, dev = torch.bfloat16, _device()
+    lda, ldd = _matrix(A, "A", bf16, M, K, dev), _matrix(D, "D", bf16, M, N, dev)
+    _call("gemm_int4_nt", A.data_ptr(), lda, _packed(B, "B", torch.uint8, (N, -(-K // 128) * 64), dev),
+          _packed(sb, "sb", bf16, (N, kg), dev), None if zb is None else _packed(zb, "zb", torch.uint8, (N, kg), dev),
+          D.data_ptr(), ldd, M, N, K, group, _raw_stream(stream, dev))
+    return D
+
+
+SCORINGS = {"softmax": 0, "sigmoid": 1}
+
+
+def _scoring(name: str) -> int:
+    kind = SCORINGS.get(name)
+    if kind is None:
+        raise ValueError(f"scoring must be one of {sorted(SCORINGS)}, got {name!r}")
+    return kind
+
+
+def _logits(t: torch.Tensor, dev: int):
+    if t.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    bf16 = t.dtype is torch.bfloat16
+    return bf16, _matrix(t, "logits", torch.bfloat16 if bf16 else torch.float32, t.shape[0], t.shape[1], dev)
+
+
+def moe_route(logits, k, ids=None, weights=None, bias=None, scoring="softmax", groups=1, top_groups=1, normalize=True,
+              scale=1.0, stream=None):
+    """The k experts of each token and their weights from fp32 or bf16 logits [T, E]: scores s =
+    softmax or sigmoid of the logits, the largest s + bias win (with groups > 1 only within the
+    top_groups groups whose two best add up to most), weights = scale * s, divided by the chosen
+    experts' sum if `normalize`.  Experts with a logit of -inf are never chosen; places without a
+    candidate hold id -1 and weight 0.  -> (ids int32 [T, k] best first, weights fp32 [T, k])."""
+    dev = _device()
+    bf16, ld = _logits(logits, dev)
+    T, E = logits.shape
+    if ids is None or weights is None:
+        with _on_stream(stream):
+            ids = torch.empty(T, k, dtype=torch.int32, device=logits.device) if ids is None else ids
+            weights = torch.empty(T, k, dtype=torch.float32, device=logits.device) if weights is None else weights
+    _call("moe_route_bf16" if bf16 else "moe_route", logits.data_ptr(), ld,
+          None if bias is None else _packed(bias, "bias", torch.float32, (E,), dev),
+          _packed(ids, "ids", torch.int32, (T, k), dev), _packed(weights, "weights", torch.float32, (T, k), dev), T, E, k,
+          _scoring(scoring), groups, top_groups, bool(normalize), scale, _raw_stream(stream, dev))
+    return ids, weights
+
+
+def moe_route_backward(dweights, logits, ids, dlogits=None, scoring="softmax", normalize=True, scale=1.0, stream=None):
+    """Gradient of moe_route's weights with respect to the logits: dlogits [T, E] (the logits' type)
+    from dweights fp32 [T, k], the logits and the forward call's ids, scoring, normalize and scale."""
+    dev = _device()
+    bf16, ld = _logits(logits, dev)
+    T, E = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    k = ids.shape[1]
+    if dlogits is None:
+        with _on_stream(stream):
+            dlogits = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+    ld_dl = _matrix(dlogits, "dlogits", logits.dtype, T, E, dev)
+    _call("moe_route_backward_bf16" if bf16 else "moe_route_backward",
+          _packed(dweights, "dweights", torch.float32, (T, k), dev), logits.data_ptr(), ld,
+          _packed(ids, "ids", torch.int32, (T, k), dev), dlogits.data_ptr(), ld_dl, T, E, k, _scoring(scoring),
+          bool(normalize), scale, _raw_stream(stream, dev))
+    return dlogits
+
+
+def moe_ffn_workspace_bytes(T: int, k: int, F: int) -> int:
+    """Device workspace bytes moe_ffn_fp8 and moe_ffn_int4 need."""
+    n = load_library().fg_moe_ffn_workspace_bytes(T, k, F)
+    if n < 0:
+        raise ValueError(f"sizes {(T, k, F)} not accepted")
+    return n
+
+
+def _layer(X, ids, weights, D, F, workspace, stream, dev):
+    """What both expert layers take besides their weights, checked."""
+    T, K = X.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T, k]")
+    k = ids.shape[1]
+    ldx, ldd = _matrix(X, "X", torch.bfloat16, T, K, dev), _matrix(D, "D", torch.bfloat16, T, K, dev)
+    idp, wp = _packed(ids, "ids", torch.int32, (T, k), dev), _packed(weights, "weights", torch.float32, (T, k), dev)
+    if workspace is None:
+        with _on_stream(stream):
+            workspace = torch.empty(moe_ffn_workspace_bytes(T, k, F), dtype=torch.uint8, device=X.device)
+    ws, ws_bytes = _byte_workspace(workspace, dev)
+    return T, K, k, ldx, ldd, idp, wp, ws, ws_bytes
+
+
+def moe_ffn_fp8(X, W1, s1, W2, s2, ids, weights, D, activation="silu", stream=None, workspace=None):
+    """A whole expert layer for a few tokens: D[t] = bf16(sum_j weights[t,j] W2[e] (act(g) u)), e =
+    ids[t,j], [g; u] = W1[e] X[t], for bf16 X [T, K], e4m3 W1 [E, 2F, K] (gate rows, then up rows) and
+    W2 [E, K, F] with factors of 128 x 128 blocks s1 [E, ceil(2F/128), Kb], s2 [E, Nb, ceil(F/128)],
+    and moe_route's ids and weights (ids outside [0, E) are left out).  The workspace
+    (moe_ffn_workspace_bytes) comes from torch's allocator if not given."""
+    if X.dim() != 2 or W1.dim() != 3 or W2.dim() != 3 or D.dim() != 2:
+        raise ValueError("X and D must be matrices, W1 [E, 2F, K] and W2 [E, K, F]")
+    E, F = W2.shape[0], W2.shape[2]
+    dev = _device()
+    T, K, k, ldx, ldd, idp, wp, ws, ws_bytes = _layer(X, ids, weights, D, F, workspace, stream, dev)
+    W1, W2 = _fp8(W1, "W1"), _fp8(W2, "W2")
+    kb, fb = -(-K // 128), -(-F // 128)
+    _call("moe_ffn_fp8", X.data_ptr(), ldx, _packed(W1, "W1", torch.uint8, (E, 2 * F, K), dev),
+          _packed(s1, "s1", torch.float32, (E, -(-2 * F // 128), kb), dev),
+          _packed(W2, "W2", torch.uint8, (E, K, F), dev), _packed(s2, "s2", torch.float32, (E, kb, fb), dev), idp, wp,
+          D.data_ptr(), ldd, T, k, E, F, K, _activation(activation), ws, ws_bytes, _raw_stream(stream, dev))
+    return D
+
+
+def moe_ffn_int4(X, W1, s1, W2, s2, ids, weights, D, z1=None, z2=None, group=128, activation="silu", stream=None,
+                 workspace=None):
+    """moe_ffn_fp8 on 4-bit weights: W1 uint8 [E, 2F, 64 ceil(K/128)], s1 bf16 (z1 uint8 or None)
+    [E, 2F, ceil(K/group)], W2 [E, K, 64 ceil(F/128)], s2 (z2) [E, K, ceil(F/group)], every expert's as
+    int4_cast_per_group makes them."""
+    if X.dim() != 2 or W1.dim() != 3 or W2.dim() != 3 or D.dim() != 2:
+        raise ValueError("X and D must be matrices, W1 [E, 2F, ...] and W2 [E, K, ...]")
+    if W1.shape[1] % 2:
+        raise ValueError("W1 must hold as many up rows as gate rows")
+    E, F = W1.shape[0], W1.shape[1] // 2
+    dev = _device()
+    T, K, k, ldx, ldd, idp, wp, ws, ws_bytes = _layer(X, ids, weights, D, F, workspace, stream, dev)
+    u8, bf16 = torch.uint8, torch.bfloat16
+    kg, fg_ = _group_count(K, group), _group_count(F, group)
+    _call("moe_ffn_int4", X.data_ptr(), ldx, _packed(W1, "W1", u8, (E, 2 * F, -(-K // 128) * 64), dev),
+          _packed(s1, "s1", bf16, (E, 2 * F, kg), dev),
+          None if z1 is None else _packed(z1, "z1", u8, (E, 2 * F, kg), dev),
+          _packed(W2, "W2", u8, (E, K, -(-F // 128) * 64), dev), _packed(s2, "s2", bf16, (E, K, fg_), dev),
+          None if z2 is None else _packed(z2, "z2", u8, (E, K, fg_), dev), idp, wp, D.data_ptr(), ldd, T, k, E, F, K, group,
+          _activation(activation), ws, ws_bytes, _raw_stream(stream, dev))
+    return D
 
 
 def get_mk_alignment_for_contiguous_layout() -> int:

@@ -39,6 +39,8 @@ SOURCES = [
     ("fp8gemm.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("ue8m0.hip", []),
     ("linear.hip", []),
+    ("int4.hip", []),
+    ("experts.hip", []),
 ]
 
 

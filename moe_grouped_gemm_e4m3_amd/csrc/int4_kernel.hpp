@@ -1,0 +1,179 @@
+// int4_kernel.hpp -- the cast to 4-bit codes and the product of a few bf16 rows
+// with them.
+//
+//   cast     symmetric:  s = bf16(max(amax, 1e-20) / 7),   z = 8
+//            zero point: s = bf16(max(hi - lo, 1e-20) / 15), z = rint(-lo / s)     lo <= 0 <= hi
+//            q = clamp(rint(x / s) + z, 0, 15)
+//   product  D[m, n] = bf16( sum_k A[m, k] s[n, k/g] (B[n, k] - z[n, k/g]) )
+#pragma once
+
+#include "weight_stream.hpp"
+
+namespace fg {
+
+constexpr int kInt4Chunk = 64;  // bytes of 128 codes
+
+// Byte offset in a row of the word that holds columns 8 word .. 8 word + 7.
+__device__ __forceinline__ int64_t int4_word_at(int word) {
+  const int in = word & 15;
+  return (int64_t)(word >> 4) * kInt4Chunk + ((in & 3) * 4 + (in >> 2)) * 4;
+}
+
+struct Int4CastParams {
+  const void* x;
+  int64_t ldx;  // elements
+  uint8_t* q;
+  uint16_t* s;
+  uint8_t* z;  // NULL: symmetric
+  int N, K, group;
+  int groups, words;  // of a row: scale groups; words with the padding ones
+  int64_t units;      // rows x unit groups
+  int per_row;        // unit groups of a row
+};
+
+template <typename T>
+__device__ __forceinline__ void int4_load8(const T* x, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const f32x4 a = *(const f32x4_at4*)x, b = *(const f32x4_at4*)(x + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  } else {
+    const i32x4 a = *(const i32x4_at2*)x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float((uint32_t)a[i] << 16);
+      v[2 * i + 1] = __uint_as_float((uint32_t)a[i] & 0xffff0000u);
+    }
+  }
+}
+
+// LANES lanes share a group and take its words in turn (groups of up to 128:
+// a word each, and the row is read once; longer ones are read twice, the second
+// time from cache).  Bound by HBM: 4 or 2 bytes in and half a byte out for each weight.
+template <typename T, int LANES>
+__global__ __launch_bounds__(256) void int4_cast_kernel(Int4CastParams p) {
+  constexpr int UNITS = 256 / LANES;
+  const int l = threadIdx.x % LANES;
+  const int group_words = p.group / 8, k_words = p.K / 8;
+  for (int64_t u0 = (int64_t)blockIdx.x * UNITS; u0 < p.units; u0 += (int64_t)gridDim.x * UNITS) {
+    // lanes past the last unit follow it, for the exchanges, and store nothing
+    const int64_t u = min(u0 + threadIdx.x / LANES, p.units - 1);
+    const bool live = u0 + threadIdx.x / LANES < p.units;
+    const int64_t n = u / p.per_row;
+    const int g = (int)(u - n * p.per_row);
+    const T* row = (const T*)p.x + n * p.ldx;
+    const int w0 = g * group_words, w1 = min(w0 + group_words, k_words);
+    float lo = 0.f, hi = 0.f, v[8];
+    for (int w = w0 + l; w < w1; w += LANES) {
+      int4_load8(row + 8 * w, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo = fminf(lo, v[i]);
+        hi = fmaxf(hi, v[i]);
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < LANES; d *= 2) {
+      lo = fminf(lo, __shfl_xor(lo, d));
+      hi = fmaxf(hi, __shfl_xor(hi, d));
+    }
+    const float span = p.z ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+    const uint16_t sb = bf16_bits(fmaxf(span, p.z ? 1e-20f / 15.f : 1e-20f / 7.f));
+    const float s = to_f32(sb);
+    const float z = p.z ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 8.f;
+    if (live && l == 0 && g < p.groups) {
+      p.s[n * p.groups + g] = sb;
+      if (p.z) p.z[n * p.groups + g] = (uint8_t)z;
+    }
+    // the last group's lanes write the row's padding words too
+    const int end = g == p.per_row - 1 ? p.words : w0 + group_words;
+    for (int w = w0 + l; w < end; w += LANES) {
+      uint32_t word = 0;
+      if (w < w1) {
+        if (group_words > LANES || g == p.per_row - 1) int4_load8(row + 8 * w, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t c = (uint32_t)fminf(fmaxf(rintf(v[i] / s) + z, 0.f), 15.f);
+          word |= c << (8 * (i & 3) + 4 * (i >> 2));
+        }
+      }
+      if (live) *(uint32_t*)(p.q + n * (int64_t)p.words * 4 + int4_word_at(w)) = word;
+    }
+  }
+}
+
+struct Int4Params {
+  const uint16_t* A;
+  int64_t lda;  // elements
+  const uint8_t* B;
+  const uint16_t* s;
+  const uint8_t* z;  // NULL: 8
+  uint16_t* D;
+  int64_t ldd;
+  int M, N, K, group, groups;
+  int row_bytes;  // of B
+  int parts;      // row parts
+  bool wide;
+};
+
+template <int GPC_, int MT_, int CF_, int WAVES_, int DEPTH_>
+struct Int4Tile {
+  using S = Stream<kInt4Group, GPC_, MT_, CF_, 1, 1, DEPTH_>;
+  static constexpr int WAVES = WAVES_, THREADS = 64 * WAVES, ROWS = 16 * MT_, COLS = 16 * CF_;
+  static constexpr int BLOCKS = MT_ * CF_;
+};
+
+// Grid: column tiles x row parts, parts fastest.  The waves share out a tile's
+// chunks of K; their partials are added in wave order.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void int4_product_kernel(Int4Params p) {
+  using S = typename C::S;
+  __shared__ f32x4 red[C::WAVES][C::BLOCKS][64];
+  const int lane = threadIdx.x & 63, l16 = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = blockIdx.x / p.parts;
+  const int m0 = (blockIdx.x - tile * p.parts) * C::ROWS, n0 = tile * C::COLS;
+  const int rows = min(C::ROWS, p.M - m0);
+
+  Sources<S> src;
+  src.K = p.K;
+  src.group = p.group;
+  src.has_z = p.z != nullptr;
+  src.wide = p.wide;
+  // rows past N are outside the ranges and read as zeros
+  src.q[0] = make_rsrc(p.B + (int64_t)n0 * p.row_bytes, (int64_t)(p.N - n0) * p.row_bytes);
+  src.s[0] = make_rsrc(p.s + (int64_t)n0 * p.groups, (int64_t)(p.N - n0) * p.groups * 2);
+  src.z[0] = make_rsrc(p.z ? p.z + (int64_t)n0 * p.groups : nullptr, p.z ? (int64_t)(p.N - n0) * p.groups : 0);
+  src.q_off = l16 * p.row_bytes; src.q_tile = 16 * p.row_bytes;
+  src.s_off = l16 * p.groups * 2; src.s_tile = 32 * p.groups;
+  src.z_off = l16 * p.groups; src.z_tile = 16 * p.groups;
+  src.x = make_rsrc(p.A + (int64_t)m0 * p.lda, ((int64_t)(rows - 1) * p.lda + p.K) * 2);
+#pragma unroll
+  for (int t = 0; t < S::MT; ++t) src.x_off[t] = min(16 * t + l16, rows - 1) * (int)(2 * p.lda);
+  src.x_part = 0;
+
+  f32x4 acc[S::MT][S::CF];
+#pragma unroll
+  for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+    for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  stream_chunks<S>(acc, src, wave, (p.K + 127) >> 7, C::WAVES);
+#pragma unroll
+  for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+    for (int c = 0; c < S::CF; ++c) red[wave][t * S::CF + c][lane] = acc[t][c];
+  __syncthreads();
+  for (int x = threadIdx.x; x < C::BLOCKS * 256; x += C::THREADS) {
+    const int col = x & (C::COLS - 1), row = x / C::COLS;
+    const int b = (row >> 4) * S::CF + (col >> 4), at = ((row & 15) >> 2) * 16 + (col & 15), i = row & 3;
+    float v = red[0][b][at][i];
+#pragma unroll
+    for (int w = 1; w < C::WAVES; ++w) v += red[w][b][at][i];
+    if (row < rows && n0 + col < p.N) p.D[(int64_t)(m0 + row) * p.ldd + n0 + col] = bf16_bits(v);
+  }
+}
+
+}  // namespace fg

@@ -33,6 +33,8 @@ section; the texts are machine-extracted and partly machine-translated):
 * the 8-bit-integer cast and product and the gated feed-forward block with its
   gradients (``oracle.linear``): float64 definitions of their formulas, with
   the error bounds that the kernels' roundings allow.
+* the expert router with its gradient, 4-bit weights and the expert layers for
+  a few tokens (``oracle.experts``): the same.
 * acceptance metrics (``oracle.metrics``).
 
 Every function is pinned by tests in ``tests/test_oracle.py`` against
@@ -40,6 +42,6 @@ something other than itself (torch's own float8/bfloat16 conversions, exact
 rational brute force, closed forms and invariants).
 """
 
-from . import e4m3, quant, gemm, linear, metrics  # noqa: F401
+from . import e4m3, quant, gemm, linear, experts, metrics  # noqa: F401
 
-__all__ = ["e4m3", "quant", "gemm", "linear", "metrics"]
+__all__ = ["e4m3", "quant", "gemm", "linear", "experts", "metrics"]
