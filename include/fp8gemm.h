@@ -589,7 +589,11 @@ fg_status int4_cast_per_group_bf16(const uint16_t* w, int64_t ldw, uint8_t* q, u
  * D may not overlap an input.  Allocates nothing.
  */
 fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const uint16_t* sb, const uint8_t* zb,
-                       uint16_t* D, int64_t ldd, int M, int N, int K, int group, void* stream);
+                       uint16_t* D, int64_t ldd, int M, int N, int K, int group, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gemm_int4_nt; -1 for sizes that it refuses. */
+int64_t fg_int4_workspace_bytes(int M, int N, int K);
 
 /* Scores of the expert router: a softmax over the experts, or a sigmoid of each logit. */
 typedef enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 } fg_scoring;
@@ -661,7 +665,7 @@ fg_status moe_ffn_fp8(const uint16_t* X, int64_t ldx, const uint8_t* W1, const f
 /*
  * The same on 4-bit weights (see int4_cast_per_group):
  *   W1, s1, z1  E matrices of [2F, K], one after the other; W2, s2, z2  E of [K, F]
- *   (z1, z2 may be NULL)
+ *   (z1 and z2 may both be NULL)
  * K and F multiples of 32 up to 2^16.  Everything else as moe_ffn_fp8.
  */
 fg_status moe_ffn_int4(const uint16_t* X, int64_t ldx, const uint8_t* W1, const uint16_t* s1, const uint8_t* z1,

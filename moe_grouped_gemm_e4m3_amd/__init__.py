@@ -65,6 +65,7 @@ __all__ = [
     "gated_ffn_int8",
     "int4_cast_per_group",
     "gemm_int4_nt",
+    "int4_workspace_bytes",
     "moe_route",
     "moe_route_backward",
     "moe_ffn_fp8",
@@ -122,7 +123,8 @@ _SIGNATURES = {
     "gated_ffn_int8": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _P]),
     "int4_cast_per_group": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _P]),
     "int4_cast_per_group_bf16": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _P]),
-    "gemm_int4_nt": (_I, [_P, _I64, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P]),
+    "gemm_int4_nt": (_I, [_P, _I64, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _P, _I64, _P]),
+    "fg_int4_workspace_bytes": (_I64, [_I, _I, _I]),
     "moe_route": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
     "moe_route_bf16": (_I, [_P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P]),
     "moe_route_backward": (_I, [_P, _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _I, _F, _P]),
@@ -879,7 +881,15 @@ def int4_cast_per_group(w, group=128, symmetric=False, q=None, s=None, z=None, s
     return q, s, None if symmetric else z
 
 
-def gemm_int4_nt(A, B, sb, D, zb=None, group=128, stream=None):
+def int4_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Device workspace bytes gemm_int4_nt needs (0 for most sizes)."""
+    n = load_library().fg_int4_workspace_bytes(M, N, K)
+    if n < 0:
+        raise ValueError(f"sizes {(M, N, K)} not accepted")
+    return n
+
+
+def gemm_int4_nt(A, B, sb, D, zb=None, group=128, stream=None, workspace=None):
     """D[M,N] = bf16(A . W^T), W[n,k] = sb[n, k/group] (B[n,k] - zb[n, k/group]), for bf16 A [M, K] and
     4-bit weights as int4_cast_per_group makes them (zb None: zero points of 8).  For few rows: the
     weights are read once for each 64."""
@@ -890,9 +900,18 @@ def gemm_int4_nt(A, B, sb, D, zb=None, group=128, stream=None):
     kg = _group_count(K, group)
     bf16, dev = torch.bfloat16, _device()
     lda, ldd = _matrix(A, "A", bf16, M, K, dev), _matrix(D, "D", bf16, M, N, dev)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _byte_workspace(workspace, dev)
+    elif M > 4:
+        ws_bytes = int4_workspace_bytes(M, N, K)
+        if ws_bytes:
+            with _on_stream(stream):
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
+            ws = workspace.data_ptr()
     _call("gemm_int4_nt", A.data_ptr(), lda, _packed(B, "B", torch.uint8, (N, -(-K // 128) * 64), dev),
           _packed(sb, "sb", bf16, (N, kg), dev), None if zb is None else _packed(zb, "zb", torch.uint8, (N, kg), dev),
-          D.data_ptr(), ldd, M, N, K, group, _raw_stream(stream, dev))
+          D.data_ptr(), ldd, M, N, K, group, ws, ws_bytes, _raw_stream(stream, dev))
     return D
 
 

@@ -1,0 +1,152 @@
+// decode_plan.hpp -- which kernels the 4-bit product and the few-token expert
+// layers run: host arithmetic on sizes only.
+//
+// Two organisations (weight_stream.hpp): waves of a workgroup that share out a
+// tile's reduction, each with its own columns of the activations ("split": many
+// small tiles, for few rows), and waves with weight rows of their own that share
+// the activations' columns ("wide": fewer bytes through LDS for each weight, for
+// more rows).  The figures beside the rules are in microseconds, in a HIP graph.
+//
+// FG_DECODE_PLAN names parts of a plan, separated by commas, for tuning and
+// tests; one that a call does not have leaves it its own.
+#pragma once
+
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+namespace fg {
+
+constexpr int kLayerTokens = 64;        // tokens a pass over the experts' weights serves
+constexpr int64_t kPartialBytes = 512 << 10;  // of a token's partial sums
+
+// Whether `name` is one of the comma-separated words of `forced`.
+inline bool names(const char* forced, const char* name) {
+  const size_t n = strlen(name);
+  for (const char* p = forced; (p = strstr(p, name)) != nullptr; p += n)
+    if ((p == forced || p[-1] == ',') && (p[n] == 0 || p[n] == ',')) return true;
+  return false;
+}
+
+inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// ---------------------------------------------------------------------------
+// gemm_int4_nt
+
+enum Int4Kind { kSplit2, kSplit2Deep, kSplit8, kSplit8Deep, kSplit16, kSplit16Deep, kWide16, kWide64, kInt4Kinds };
+constexpr const char* kInt4Names[kInt4Kinds] = {"split2", "split2deep", "split8", "split8deep", "split16", "split16deep",
+                                                "wide16", "wide64"};
+struct Int4Plan {
+  Int4Kind kind;
+  int k_parts;  // wide: parts of the reduction, joined by a second kernel
+};
+
+inline Int4Plan plan_int4(int M, int N, int K, const char* forced) {
+  const int chunks = ceil_div(K, 256);
+  const int64_t weights = (int64_t)N * K;
+  // The reduction of a 16-column tile over eight waves instead of four where the
+  // tiles are few or the reduction is long (1 x 2112 x 7168: 6.6 for 8.9; 1 x
+  // 7168 x 16384: 13.4 for 16.3; 1 x 24576 x 1536: 9.5 for 7.7).
+  const bool deep = chunks >= 16 && N <= 4096;
+  Int4Kind kind;
+  if (M <= 2)
+    kind = deep || chunks >= 32 ? kSplit2Deep : kSplit2;
+  else if (M <= 4)
+    kind = deep ? kSplit8Deep : kSplit8;
+  else if (M <= 16 && weights < (1 << 25))
+    // 16 x 4096 x 4096: 5.7, 9.5 wide; 16 x 24576 x 1536: 13 or more, 8.5 wide
+    kind = M <= 8 ? (deep ? kSplit8Deep : kSplit8) : deep && N < 4096 ? kSplit16Deep : kSplit16;
+  else if (weights < (1 << 23))
+    kind = kSplit16;  // 64 x 1000 x 1024: 3.7, 5.5 wide
+  else
+    // 64 x 16384 x 4096: 31 on 64 rows, 36 on 16; 64 x 4096 x 4096: 13 on 16
+    kind = M > 32 && weights >= (1 << 25) ? kWide64 : kWide16;
+  for (int k = 0; k < kInt4Kinds; ++k)
+    if (names(forced, kInt4Names[k])) kind = (Int4Kind)k;
+  Int4Plan p{kind, 1};
+  if (kind == kWide16 || kind == kWide64) {
+    // one round of workgroups on 256 CUs, two chunks each at least
+    const int64_t tiles = (int64_t)ceil_div(N, 128) * ceil_div(M, kind == kWide64 ? 64 : 16);
+    p.k_parts = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, chunks / 2, 16}));
+    for (int n = 1; n <= 8 && n <= std::max(1, chunks); ++n) {
+      const char word[] = {'k', 'p', 'a', 'r', 't', 's', (char)('0' + n), 0};
+      if (names(forced, word)) p.k_parts = n;
+    }
+  }
+  return p;
+}
+
+inline int64_t int4_partial_bytes(int M, int N, const Int4Plan& p) {
+  return p.k_parts > 1 ? (int64_t)p.k_parts * M * N * 4 : 0;
+}
+
+// ---------------------------------------------------------------------------
+// expert layers
+
+enum UpKind { kUpSplit4, kUpSplit4Two, kUpSplit16, kUpWide, kUpWideDeep, kUpWide8, kUpKinds };
+constexpr const char* kUpNames[kUpKinds] = {"up-split4", "up-split4-two", "up-split16", "up-wide", "up-wide-deep", "up-wide8"};
+enum DownKind { kDownSplit1, kDownSplit1Two, kDownSplit4, kDownSplit4Two, kDownWide16, kDownWide16Deep, kDownWide32, kDownKinds };
+constexpr const char* kDownNames[kDownKinds] = {"down-split1", "down-split1-two", "down-split4", "down-split4-two", "down-wide16",
+                                                "down-wide16-deep", "down-wide32"};
+struct LayerPlan {
+  UpKind up;
+  DownKind down;
+  int parts;  // wide down: parts of the experts' chunks, joined by a third kernel
+};
+inline bool wide_down(DownKind k) { return k >= kDownWide16; }
+
+inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const char* forced) {
+  T = std::min(T, kLayerTokens);
+  const int pairs = T * k, active = std::min(E, pairs);  // experts with tokens, at most
+  const int64_t wide4 = (int64_t)ceil_div(F, 64) * active, wide8 = (int64_t)ceil_div(F, 128) * active;
+  LayerPlan p{};
+  // up.  E4m3 weights (T=16, 16 of 16 experts of 2048 x 7168: wide 81, split 88;
+  // 8 of 2048 x 1024: wide 12.3, split 8.3; 32 of 2048 x 4096: wide 90, a deeper
+  // ring 82).  4-bit weights cost more arithmetic and LDS for each byte, so that
+  // sharing pays from four tokens on (T=4, 16 experts of 2048 x 7168: 49 for 56).
+  if (fp8)
+    p.up = T <= 4 ? kUpSplit4 : wide4 < 256 ? kUpSplit16 : K >= 4096 ? kUpWideDeep : kUpWide;
+  else if (T >= 4 && wide8 >= 384)
+    p.up = kUpWide8;
+  else if (T <= 4)
+    // two tiles of hidden units where workgroups abound (T=1, 8 experts of 2048 x 7168: 30.4 for 32.2)
+    p.up = (int64_t)ceil_div(F, 16) * active >= 1024 ? kUpSplit4Two : kUpSplit4;
+  else
+    p.up = wide4 >= 256 ? kUpWide : kUpSplit16;
+  for (int i = 0; i < kUpKinds; ++i)
+    if (names(forced, kUpNames[i]) && (fp8 ? i != kUpWide8 && i != kUpSplit4Two : i != kUpWideDeep)) p.up = (UpKind)i;
+  // down.  A third kernel costs about 3 us, so that small layers go without
+  // (T=8, 8 experts of 2048 x 1024: 9.7 for 13.0; 64 of 2048 x 704: 26.6 for 21.9).
+  const bool small = T <= 8 && pairs <= 2 * E && (int64_t)active * F * K <= (1 << 25);
+  const int tiles = ceil_div(K, 128);
+  if (T == 1)
+    p.down = fp8 && K > 4096 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
+  else if (T <= 4 || small)
+    p.down = !fp8 && K > 4096 ? kDownSplit4Two : kDownSplit4;  // T=2, 4-bit, 7168 x 2048: 38 for 43; 4096 x 2048: 24 for 15
+  else if (pairs > 8 * E)
+    p.down = kDownWide32;  // T=64, 32 tokens an expert: 122 for 149; 6 tokens: 43 for 40
+  else
+    p.down = fp8 && T > 16 ? kDownWide16Deep : kDownWide16;  // T=64, 8 tokens an expert: 66 for 83
+  for (int i = 0; i < kDownKinds; ++i)
+    if (names(forced, kDownNames[i]) && (fp8 ? i != kDownSplit4Two : i != kDownSplit1Two && i != kDownWide16Deep) &&
+        (i != kDownSplit1Two || T <= 16))  // its sums of more tokens do not fit LDS
+      p.down = (DownKind)i;
+  p.parts = 1;
+  if (wide_down(p.down)) {
+    // workgroups for one round: two on a CU where their LDS allows it
+    const int round = fp8 && p.down == kDownWide16 && T <= 32 ? 512 : 256;
+    const int64_t chunks = (int64_t)active * ceil_div(F, fp8 ? 128 : 256);
+    p.parts = (int)std::max<int64_t>(1, std::min<int64_t>({round / tiles, chunks, kPartialBytes / 4 / K}));
+    if (T == 1 || names(forced, "one-part")) p.parts = 1;
+  }
+  return p;
+}
+
+// Workspace: the hidden units of every pair, then partial sums.
+inline int64_t hidden_bytes(int T, int k, int F) { return ((int64_t)T * k * F * 4 + 255) / 256 * 256; }
+inline int64_t layer_bytes(int T, int k, int F) {
+  return hidden_bytes(T, k, F) + (T > 1 ? std::min(T, kLayerTokens) * kPartialBytes : 0);
+}
+
+}  // namespace fg

@@ -4,7 +4,9 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <cstdlib>
 
+#include "decode_plan.hpp"
 #include "experts_kernel.hpp"
 #include "host_common.hpp"
 #include "int4_host.hpp"
@@ -121,35 +123,124 @@ fg_status route_backward(const float* dw, const L* logits, int64_t ld, const int
 // ---------------------------------------------------------------------------
 // expert layers
 
-template <class C>
-fg_status launch_down(const ExpertParams& p, int passes, void* stream, const char* what) {
-  const int tiles = (p.K + C::COLS - 1) / C::COLS;
-  if (print_launches())
-    fprintf(stderr, "[fp8gemm] %s down T=%d K=%d F=%d rows=%d cols=%d waves=%d grid=%dx%d\n", what, p.T, p.K, p.F, C::ROWS,
-            C::COLS, C::WAVES, tiles, passes);
-  hipLaunchKernelGGL((experts_down_kernel<C>), dim3(tiles, passes), dim3(C::THREADS), C::lds_bytes(p.T),
-                     (hipStream_t)stream, p);
-  return launched(what);
+// More than 64 KiB of dynamic LDS has to be asked for.
+fg_status allow_lds(const void* kernel, int bytes, const char* what) {
+  if (bytes + (int)sizeof(Pairs) > 160 * 1024) return set_error(FG_EUNSUPPORTED, "%s: %d bytes of LDS", what, bytes);
+  const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return set_error(FG_EHIP, "%s: %d bytes of LDS: %s", what, bytes, hipGetErrorString(e));
+  return FG_OK;
 }
 
-template <int FMT, int GPC>
-fg_status launch_layer(const ExpertParams& p, void* stream, const char* what) {
-  const int passes = (p.T + kLayerTokens - 1) / kLayerTokens;
-  const int pairs = std::min(p.T, kLayerTokens) * p.k;
-  ExpertParams u = p;
-  u.by_pair = pairs < p.E;
-  if (p.F > 0) {
-    const dim3 grid(p.F / 16, u.by_pair ? pairs : p.E, passes);
+struct LayerLaunch {
+  const ExpertParams& p;
+  LayerPlan plan;
+  int passes;  // of 64 tokens
+  float* partial;
+  void* stream;
+  const char* what;
+
+  void print(const char* kernel, const char* kind, int parts) const {
     if (print_launches())
-      fprintf(stderr, "[fp8gemm] %s up T=%d F=%d K=%d grid=%dx%dx%d\n", what, p.T, p.F, p.K, grid.x, grid.y, grid.z);
-    hipLaunchKernelGGL((experts_up_kernel<FMT, GPC>), grid, dim3(64 * kUpWaves), 0, (hipStream_t)stream, u);
-    FG_TRY(launched(what));
+      fprintf(stderr, "[fp8gemm] %s %s T=%d k=%d E=%d F=%d K=%d %s parts=%d\n", what, kernel, p.T, p.k, p.E, p.F, p.K, kind,
+              parts);
   }
-  if (p.T <= 16) return launch_down<DownTile<FMT, GPC, 1, 1, 8, 2>>(p, passes, stream, what);
-  return launch_down<DownTile<FMT, GPC, 2, 1, 8, 1>>(p, passes, stream, what);
+
+  template <class C>
+  fg_status up() const {
+    const int pairs = std::min(p.T, kLayerTokens) * p.k;
+    ExpertParams u = p;
+    u.by_pair = pairs < p.E;
+    const dim3 grid(ceil_div(p.F, C::UNITS), u.by_pair ? pairs : p.E, passes);
+    print("up", kUpNames[plan.up], 1);
+    if constexpr (C::WIDE)
+      hipLaunchKernelGGL((experts_wide_up_kernel<C>), grid, dim3(C::THREADS), 0, (hipStream_t)stream, u);
+    else
+      hipLaunchKernelGGL((experts_up_kernel<C>), grid, dim3(C::THREADS), 0, (hipStream_t)stream, u);
+    return launched(what);
+  }
+
+  template <class C>
+  fg_status down() const {
+    const int lds = C::lds_bytes(std::min(p.T, kLayerTokens));
+    FG_TRY(allow_lds((const void*)experts_down_kernel<C>, lds, what));
+    print("down", kDownNames[plan.down], 1);
+    hipLaunchKernelGGL((experts_down_kernel<C>), dim3(ceil_div(p.K, C::COLS), passes), dim3(C::THREADS), lds,
+                       (hipStream_t)stream, p);
+    return launched(what);
+  }
+
+  // A pass of tokens at a time: they share the partial sums' place.
+  template <class C>
+  fg_status down_wide() const {
+    const int lds = C::lds_bytes(std::min(p.T, kLayerTokens));
+    FG_TRY(allow_lds((const void*)experts_wide_down_kernel<C>, lds, what));
+    for (int t0 = 0; t0 < p.T; t0 += kLayerTokens) {
+      const int T = std::min(kLayerTokens, p.T - t0);
+      print("down", kDownNames[plan.down], plan.parts);
+      hipLaunchKernelGGL((experts_wide_down_kernel<C>), dim3(ceil_div(p.K, C::COLS), plan.parts), dim3(C::THREADS), lds,
+                         (hipStream_t)stream, p, t0, partial);
+      FG_TRY(launched(what));
+      if (plan.parts == 1) continue;
+      hipLaunchKernelGGL(join_parts_kernel, dim3(ceil_div((int64_t)T * p.K, 1024)), dim3(256), 0, (hipStream_t)stream, partial,
+                         plan.parts, p.D + (int64_t)t0 * p.ldd, p.ldd, T, p.K);
+      FG_TRY(launched(what));
+    }
+    return FG_OK;
+  }
+};
+
+template <class Fmt>
+fg_status launch_layer(const ExpertParams& p, void* stream, const char* what) {
+  const char* forced = getenv("FG_DECODE_PLAN");
+  const LayerPlan plan = plan_layer(Fmt::FP8, p.T, p.k, p.E, p.F, p.K, forced ? forced : "");
+  const LayerLaunch l{p, plan, ceil_div(p.T, kLayerTokens), (float*)((uint8_t*)p.H + hidden_bytes(p.T, p.k, p.F)), stream, what};
+  if (p.F > 0) {
+    fg_status st = FG_OK;
+    switch (plan.up) {
+      case kUpSplit4: st = l.up<UpTile<Fmt, 1, 4, 2, 4>>(); break;
+      case kUpSplit4Two:
+        if constexpr (!Fmt::FP8) st = l.up<UpTile<Fmt, 2, 4, 2, 4>>();
+        break;
+      case kUpSplit16: st = l.up<UpTile<Fmt, 1, 4, 2, 16>>(); break;
+      case kUpWide: st = l.up<WideUp<Fmt, 1, 4, 2, Fmt::FP8 ? 32 : 16>>(); break;
+      case kUpWideDeep:
+        if constexpr (Fmt::FP8) st = l.up<WideUp<Fmt, 1, 4, 3, 32>>();
+        break;
+      case kUpWide8:
+        // scales of groups of 32 leave no room for 32 tokens
+        if constexpr (!Fmt::FP8) st = l.up<WideUp<Fmt, 1, 8, 2, Fmt::GPC == 4 ? 16 : 32>>();
+        break;
+      default: break;
+    }
+    FG_TRY(st);
+  }
+  switch (plan.down) {
+    case kDownSplit1: return l.down<DownTile<Fmt, 1, 8, 2, 1>>();
+    case kDownSplit1Two:
+      if constexpr (Fmt::FP8) return l.down<DownTile<Fmt, 2, 8, 3, 1>>();
+      break;
+    case kDownSplit4: return l.down<DownTile<Fmt, 1, 8, 2, 4>>();
+    case kDownSplit4Two:
+      if constexpr (!Fmt::FP8) return l.down<DownTile<Fmt, 2, 4, 3, 4>>();
+      break;
+    case kDownWide16: return l.down_wide<WideDown<Fmt, 2, 4, 2, 16>>();
+    case kDownWide16Deep:
+      if constexpr (Fmt::FP8) return l.down_wide<WideDown<Fmt, 2, 4, 3, 16>>();
+      break;
+    case kDownWide32: return l.down_wide<WideDown<Fmt, 2, 4, 2, 32>>();
+    default: break;
+  }
+  return FG_OK;
 }
 
-int64_t layer_bytes(int T, int k, int F) { return (int64_t)T * k * F * 4; }
+struct LaunchLayer {
+  const ExpertParams& p;
+  void* stream;
+  template <class Fmt>
+  fg_status run() const {
+    return launch_layer<Fmt>(p, stream, "moe_ffn_int4");
+  }
+};
 
 fg_status check_layer(const ExpertParams& p, int mult, const void* workspace, int64_t workspace_bytes, int scale_align,
                       bool* empty) {
@@ -237,7 +328,7 @@ fg_status moe_ffn_fp8(const uint16_t* X, int64_t ldx, const uint8_t* W1, const f
   if (empty) return FG_OK;
   p.row1 = K; p.row2 = F;
   p.groups1 = (K + 127) / 128; p.groups2 = (F + 127) / 128;
-  return launch_layer<kFp8Block, 1>(p, stream, "moe_ffn_fp8");
+  return launch_layer<Fp8Block>(p, stream, "moe_ffn_fp8");
 }
 
 fg_status moe_ffn_int4(const uint16_t* X, int64_t ldx, const uint8_t* W1, const uint16_t* s1, const uint8_t* z1,
@@ -251,16 +342,14 @@ fg_status moe_ffn_int4(const uint16_t* X, int64_t ldx, const uint8_t* W1, const 
   p.H = (uint16_t*)workspace;
   p.T = T; p.k = k; p.E = E; p.F = F; p.K = K; p.act = activation; p.group = group;
   FG_TRY(check_group(group));
+  if ((z1 != nullptr) != (z2 != nullptr)) return set_error(FG_EINVAL, "z1 and z2: one of them is NULL");
   bool empty;
   FG_TRY(check_layer(p, 32, workspace, workspace_bytes, 2, &empty));
   if (empty) return FG_OK;
   p.row1 = int4_row_bytes(K); p.row2 = int4_row_bytes(F);
   p.groups1 = int4_groups(K, group); p.groups2 = int4_groups(F, group);
-  p.wide1 = int4_wide(K, s1, z1); p.wide2 = int4_wide(F, s2, z2);
-  const char* what = "moe_ffn_int4";
-  if (group == 32) return launch_layer<kInt4Group, 4>(p, stream, what);
-  if (group == 64) return launch_layer<kInt4Group, 2>(p, stream, what);
-  return launch_layer<kInt4Group, 1>(p, stream, what);
+  // the zero points of both matrices, or of neither: a missing one is refused above
+  return with_int4_format(group, z1 != nullptr, LaunchLayer{p, stream});
 }
 
 }  // extern "C"

@@ -20,11 +20,12 @@
 // weights, at the first of the two places.
 #pragma once
 
+#include "decode_plan.hpp"
 #include "weight_stream.hpp"
 
 namespace fg {
 
-constexpr int kLayerTokens = 64;    // tokens a pass over the weights serves: a lane each
+static_assert(kLayerTokens == 64, "a lane for each token");
 constexpr int kMaxExperts = 1024;   // `down` keeps a set of tokens for each in LDS
 constexpr int kMaxChoices = 32;
 
@@ -43,7 +44,6 @@ struct ExpertParams {
   int group;
   int row1, row2;        // bytes of a weight row
   int groups1, groups2;  // scale groups (e4m3: block columns) of a row
-  bool wide1, wide2;
   bool by_pair;  // up: blockIdx.y is a pair (fewer pairs than experts), else an expert
 };
 
@@ -51,19 +51,19 @@ struct ExpertParams {
 template <class S>
 __device__ __forceinline__ void set_weights(Sources<S>& src, int r, const uint8_t* W, const void* s, const uint8_t* z,
                                             int e, int rows, int row0, int row_bytes, int groups) {
-  const int l16 = threadIdx.x & 15;
   const int64_t at = (int64_t)e * rows + row0;
   src.q[r] = make_rsrc(W + at * row_bytes, (int64_t)(rows - row0) * row_bytes);
-  src.q_off = l16 * row_bytes;
-  src.q_tile = 16 * row_bytes;
+  src.row_bytes = row_bytes;
+  src.groups = groups;
   if constexpr (S::FP8) {
-    src.fs[r] = (const float*)s + ((int64_t)e * ((rows + 127) >> 7) + (row0 >> 7)) * groups;
+    // a tile of 16 rows lies in one block row; rows past the matrix follow its last
+    const int blocks = (rows + 127) >> 7;
+#pragma unroll
+    for (int i = 0; i < S::PER; ++i)
+      src.fs[r * S::PER + i] = (const float*)s + ((int64_t)e * blocks + min((row0 + 16 * i) >> 7, blocks - 1)) * groups;
   } else {
     src.s[r] = make_rsrc((const uint16_t*)s + at * groups, (int64_t)(rows - row0) * groups * 2);
     src.z[r] = make_rsrc(z ? z + at * groups : nullptr, z ? (int64_t)(rows - row0) * groups : 0);
-    src.has_z = z != nullptr;
-    src.s_off = l16 * groups * 2; src.s_tile = 32 * groups;
-    src.z_off = l16 * groups; src.z_tile = 16 * groups;
   }
 }
 
@@ -75,73 +75,95 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[S::MT][S::CF]) {
     for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-constexpr int kUpWaves = 4;
+// h of token t's place j and hidden unit f, as the sum of two bf16.
+__device__ __forceinline__ void store_hidden(const ExpertParams& p, int t, int j, int f, float g, float u) {
+  const float h = p.act == kActSilu ? gated_value<kActSilu>(g, u) : gated_value<kActGeluTanh>(g, u);
+  const uint16_t top = bf16_bits(h);
+  // the rest of an infinity or a NaN would be a NaN
+  const float rest = (top & 0x7f80) == 0x7f80 ? 0.f : h - to_f32(top);
+  uint16_t* dst = p.H + ((int64_t)t * p.k + j) * 2 * p.F + f;
+  dst[0] = top;
+  dst[p.F] = bf16_bits(rest);
+}
 
-// One tile of 16 MT member tokens, from member `base` on, and 16 hidden units.
-template <int FMT, int GPC, int MT, int DEPTH>
+// KiB of X in a chunk that holds `rows` rows.
+template <class Fmt, int PARTS>
+constexpr int x_kib(int rows) {
+  const int kib = rows * PARTS * (Fmt::FP8 ? 256 : 512) / 1024;
+  return kib > 1 ? kib : 1;
+}
+
+// PER: tiles of 16 hidden units.  MOST: tokens of an expert in one go (4, 16 or 32).
+template <class Fmt_, int PER_, int WAVES_, int DEPTH_, int MOST_>
+struct UpTile {
+  using Fmt = Fmt_;
+  static constexpr bool WIDE = false;
+  static constexpr int PER = PER_, WAVES = WAVES_, MOST = MOST_;
+  static constexpr int RING = DEPTH_ * (2 * PER * 2048 + x_kib<Fmt, 1>(MOST) * 1024);
+  static constexpr int MT = MOST > 16 ? 2 : 1, THREADS = 64 * WAVES, UNITS = 16 * PER;
+  static constexpr int WAVE_LDS = RING + scale_lds<Fmt, 2 * PER>();
+  static constexpr int BLOCKS = 2 * PER * MT;  // 16 x 16 sums of a wave
+  static_assert(BLOCKS * 1024 <= WAVE_LDS, "LDS");
+};
+
+// Up to ROWS member tokens, from member `base` on, and C::UNITS hidden units.
+template <class C, int ROWS>
 __device__ __forceinline__ void up_tile(const ExpertParams& p, int e, int t0, int f0, int base, int members,
-                                        const int* list, f32x4 (*red)[4][64]) {
-  using S = Stream<FMT, GPC, MT, 2, 2, 1, DEPTH>;
-  const int lane = threadIdx.x & 63, l16 = lane & 15;
+                                        const int* list, uint8_t* lds) {
+  constexpr int MT = ROWS > 16 ? 2 : 1;
+  using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 1>(ROWS), 2 * C::PER, 2, 1, C::RING>;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Sources<S> src;
   src.K = p.K;
-  src.group = p.group;
-  src.wide = p.wide1;
+  set_group(src, p.group);
   set_weights(src, 0, p.W1, p.s1, p.z1, e, 2 * p.F, f0, p.row1, p.groups1);
   set_weights(src, 1, p.W1, p.s1, p.z1, e, 2 * p.F, p.F + f0, p.row1, p.groups1);
   const int T = min(kLayerTokens, p.T - t0);
   src.x = make_rsrc(p.X + (int64_t)t0 * p.ldx, ((int64_t)(T - 1) * p.ldx + p.K) * 2);
 #pragma unroll
-  for (int t = 0; t < MT; ++t) src.x_off[t] = (list[min(base + 16 * t + l16, members - 1)] & 63) * (int)(2 * p.ldx);
-  src.x_part = 0;
+  for (int i = 0; i < S::X_LOADS; ++i) src.x_off[i] = (list[min(base + x_row_of<S>(i), members - 1)] & 63) * (int)(2 * p.ldx);
 
-  f32x4 acc[MT][2];
+  f32x4 acc[MT][2 * C::PER];
   clear<S>(acc);
-  stream_chunks<S>(acc, src, wave, (p.K + 127) >> 7, kUpWaves);
+  uint8_t* mine = lds + wave * C::WAVE_LDS;
+  const int chunks = (p.K + S::COLS - 1) / S::COLS;
+  stream_chunks<S>(acc, src, mine, (uint32_t*)(mine + C::RING), chunks * wave / C::WAVES, chunks * (wave + 1) / C::WAVES,
+                   5 * blockIdx.x);
+  f32x4* sums = (f32x4*)mine;
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    red[wave][2 * t][lane] = acc[t][0];
-    red[wave][2 * t + 1][lane] = acc[t][1];
-  }
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int c = 0; c < 2 * C::PER; ++c) sums[(2 * C::PER * t + c) * 64 + lane] = acc[t][c];
   __syncthreads();
+  for (int x = threadIdx.x; x < MT * C::PER * 256; x += C::THREADS) {
+    const int col = x & 15, row = (x >> 4) & 15, b = x >> 8, t = b / C::PER, c = b - t * C::PER;
+    const int at = ((2 * C::PER * t + c) * 64 + (row >> 2) * 16 + col) * 4 + (row & 3);
+    float g = 0.f, u = 0.f;
 #pragma unroll
-  for (int x = threadIdx.x; x < MT * 256; x += 64 * kUpWaves) {
-    const int col = x & 15, row = (x >> 4) & 15, t = x >> 8;
-    const int at = (row >> 2) * 16 + col, i = row & 3;
-    float g = red[0][2 * t][at][i], u = red[0][2 * t + 1][at][i];
-#pragma unroll
-    for (int w = 1; w < kUpWaves; ++w) {
-      g += red[w][2 * t][at][i];
-      u += red[w][2 * t + 1][at][i];
+    for (int w = 0; w < C::WAVES; ++w) {
+      const float* part = (const float*)(lds + w * C::WAVE_LDS);
+      g += part[at];
+      u += part[at + C::PER * 256];
     }
-    const int m = base + 16 * t + row;
-    if (m < members) {
+    const int m = base + 16 * t + row, f = f0 + 16 * c + col;
+    if (m < members && f < p.F && 16 * t + row < ROWS) {
       const int pair = list[m];
-      const float h = p.act == kActSilu ? gated_value<kActSilu>(g, u) : gated_value<kActGeluTanh>(g, u);
-      const uint16_t top = bf16_bits(h);
-      // the rest of an infinity or a NaN would be a NaN
-      const float rest = (top & 0x7f80) == 0x7f80 ? 0.f : h - to_f32(top);
-      uint16_t* dst = p.H + ((int64_t)(t0 + (pair & 63)) * p.k + (pair >> 6)) * 2 * p.F + f0 + col;
-      dst[0] = top;
-      dst[p.F] = bf16_bits(rest);
+      store_hidden(p, t0 + (pair & 63), pair >> 6, f, g, u);
     }
   }
 }
 
-// Grid: tiles of 16 hidden units, pairs or experts, passes of 64 tokens.
-template <int FMT, int GPC>
-__global__ __launch_bounds__(64 * kUpWaves) void experts_up_kernel(ExpertParams p) {
-  __shared__ f32x4 red[kUpWaves][4][64];
-  __shared__ int list[kLayerTokens];
-  const int lane = threadIdx.x & 63;
-  const int t0 = blockIdx.z * kLayerTokens, T = min(kLayerTokens, p.T - t0);
+// The expert of a workgroup of `up`, and its tokens in `list` (t | place << 6,
+// the first place that names it).  -> how many; 0: nothing to do.
+__device__ __forceinline__ int expert_tokens(const ExpertParams& p, int t0, int& e, int* list) {
+  const int lane = threadIdx.x & 63, T = min(kLayerTokens, p.T - t0);
   const int32_t* ids = p.ids + (int64_t)t0 * p.k;
-  int e = blockIdx.y;
+  e = blockIdx.y;
   if (p.by_pair) {
-    if ((int)blockIdx.y >= T * p.k) return;
+    if ((int)blockIdx.y >= T * p.k) return 0;
     e = load_invariant(ids + blockIdx.y);
-    if ((unsigned)e >= (unsigned)p.E) return;
+    if ((unsigned)e >= (unsigned)p.E) return 0;
   }
   // the first of this lane's token's places that name e
   int place = -1;
@@ -149,127 +171,233 @@ __global__ __launch_bounds__(64 * kUpWaves) void experts_up_kernel(ExpertParams 
     for (int j = p.k - 1; j >= 0; --j)
       if (ids[lane * p.k + j] == e) place = j;
   const unsigned long long mask = __ballot(place >= 0);
-  if (mask == 0) return;
+  if (mask == 0) return 0;
   if (p.by_pair) {
     // the first pair of an expert stands for all of them
     const int first = __builtin_ctzll(mask);
-    if (first * p.k + __builtin_amdgcn_readlane(place, first) != (int)blockIdx.y) return;
+    if (first * p.k + __builtin_amdgcn_readlane(place, first) != (int)blockIdx.y) return 0;
   }
-  const int members = __builtin_popcountll(mask);
   if (threadIdx.x < 64 && place >= 0) list[__builtin_popcountll(mask & ((1ull << lane) - 1))] = lane | place << 6;
   __syncthreads();
-  const int f0 = blockIdx.x * 16;
-  for (int base = 0; base < members; base += 32) {
-    if (base) __syncthreads();  // red is read
-    if (members - base <= 16)
-      up_tile<FMT, GPC, 1, 2>(p, e, t0, f0, base, members, list, red);
+  return __builtin_popcountll(mask);
+}
+
+// Grid: tiles of C::UNITS hidden units, pairs or experts, passes of 64 tokens.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void experts_up_kernel(ExpertParams p) {
+  // one object: with two, the compiler waits for all loads into LDS before a read of it
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::WAVES * C::WAVE_LDS + kLayerTokens * 4];
+  int* list = (int*)(lds + C::WAVES * C::WAVE_LDS);
+  const int t0 = blockIdx.z * kLayerTokens, f0 = blockIdx.x * C::UNITS;
+  int e;
+  const int members = expert_tokens(p, t0, e, list);
+  for (int base = 0; base < members; base += C::MOST) {
+    if (base) __syncthreads();  // the sums are read
+    const int left = members - base;
+    if (C::MOST == 4 || left <= 4)
+      up_tile<C, 4>(p, e, t0, f0, base, members, list, lds);
+    else if (C::MOST == 16 || left <= 16)
+      up_tile<C, C::MOST < 16 ? C::MOST : 16>(p, e, t0, f0, base, members, list, lds);
     else
-      up_tile<FMT, GPC, 2, 2>(p, e, t0, f0, base, members, list, red);
+      up_tile<C, C::MOST>(p, e, t0, f0, base, members, list, lds);
   }
 }
 
-template <int FMT_, int GPC_, int MT_, int CF_, int WAVES_, int DEPTH_>
-struct DownTile {
-  using S = Stream<FMT_, GPC_, MT_, CF_, 1, 2, DEPTH_>;
-  static constexpr int WAVES = WAVES_, THREADS = 64 * WAVES, COLS = 16 * CF_, ROWS = 16 * MT_;
-  static int lds_bytes(int T) { return WAVES * (T < kLayerTokens ? T : kLayerTokens) * COLS * 4; }
+// ---- more tokens: the waves of a workgroup share the tokens' columns ----
+
+template <class Fmt_, int PER_, int WAVES_, int DEPTH_, int MOST_>
+struct WideUp {
+  using Fmt = Fmt_;
+  static constexpr bool WIDE = true;
+  static constexpr int PER = PER_, WAVES = WAVES_, THREADS = 64 * WAVES, UNITS = 16 * PER * WAVES, MOST = MOST_;
+  static constexpr int SCALES = Fmt::GPC == 4 ? 64 : 32;
+  static constexpr int RING = DEPTH_ * (WAVES * PER * 4096 + x_kib<Fmt, 1>(MOST) * 1024);
+  static constexpr int SCALE_LDS = scale_lds<Fmt, 2 * PER, SCALES>();  // of a wave
+  static constexpr int LDS = RING + WAVES * SCALE_LDS;
 };
+
+template <class C, int ROWS>
+__device__ __forceinline__ void wide_up_tile(const ExpertParams& p, int e, int t0, int f0, int base, int members,
+                                             const int* list, uint8_t* ring, uint8_t* scales) {
+  constexpr int MT = ROWS > 16 ? 2 : 1;
+  using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 1>(ROWS), 2 * C::PER, 2, 1, C::RING, C::WAVES, C::SCALES>;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  Sources<S> src;
+  src.K = p.K;
+  set_group(src, p.group);
+  const int f = f0 + 16 * C::PER * wave;  // past F: some rows that are there, for nothing
+  set_weights(src, 0, p.W1, p.s1, p.z1, e, 2 * p.F, min(f, p.F - 16), p.row1, p.groups1);
+  set_weights(src, 1, p.W1, p.s1, p.z1, e, 2 * p.F, p.F + min(f, p.F - 16), p.row1, p.groups1);
+  const int T = min(kLayerTokens, p.T - t0);
+  src.x = make_rsrc(p.X + (int64_t)t0 * p.ldx, ((int64_t)(T - 1) * p.ldx + p.K) * 2);
+#pragma unroll
+  for (int i = 0; i < S::X_LOADS; ++i) src.x_off[i] = (list[min(base + x_row_of<S>(i), members - 1)] & 63) * (int)(2 * p.ldx);
+  f32x4 acc[MT][2 * C::PER];
+  clear<S>(acc);
+  stream_chunks<S>(acc, src, ring, (uint32_t*)(scales + wave * C::SCALE_LDS), 0, (p.K + S::COLS - 1) / S::COLS,
+                   5 * blockIdx.x);
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int m = base + 16 * t + 4 * quarter + i;
+      if (m >= members || 16 * t + 4 * quarter + i >= ROWS) continue;
+      const int pair = list[m];
+#pragma unroll
+      for (int c = 0; c < C::PER; ++c)
+        if (f + 16 * c + l16 < p.F)
+          store_hidden(p, t0 + (pair & 63), pair >> 6, f + 16 * c + l16, acc[t][c][i], acc[t][C::PER + c][i]);
+    }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void experts_wide_up_kernel(ExpertParams p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[C::LDS + kLayerTokens * 4];
+  uint8_t* scales = ring + C::RING;
+  int* list = (int*)(ring + C::LDS);
+  const int t0 = blockIdx.z * kLayerTokens, f0 = blockIdx.x * C::UNITS;
+  int e;
+  const int members = expert_tokens(p, t0, e, list);
+  for (int base = 0; base < members; base += C::MOST) {
+    if (C::MOST == 16 || members - base <= 16)
+      wide_up_tile<C, 16>(p, e, t0, f0, base, members, list, ring, scales);
+    else
+      wide_up_tile<C, C::MOST>(p, e, t0, f0, base, members, list, ring, scales);
+  }
+}
+
+// MOST: tokens of an expert in one go (1, 4 or 16).
+template <class Fmt_, int CF_, int WAVES_, int DEPTH_, int MOST_>
+struct DownTile {
+  using Fmt = Fmt_;
+  static constexpr int CF = CF_, WAVES = WAVES_, MOST = MOST_;
+  static constexpr int RING = DEPTH_ * (CF * 2048 + x_kib<Fmt, 2>(MOST) * 1024);
+  static constexpr int THREADS = 64 * WAVES, COLS = 16 * CF;
+  static constexpr int WAVE_LDS = RING + scale_lds<Fmt, CF>();
+  static int lds_bytes(int T) { return WAVES * (WAVE_LDS + T * COLS * 4); }
+};
+
+// What `down` knows of the pairs: the experts with tokens, in order.
+struct Pairs {
+  unsigned long long tokens[kMaxExperts];  // that go to an expert
+  uint16_t item_expert[kMaxExperts], item_start[kMaxExperts + 1];
+  int items;
+};
+
+__device__ __forceinline__ void sort_pairs(Pairs& s, const ExpertParams& p, const int32_t* ids, int T) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int i = tid; i < p.E; i += blockDim.x) s.tokens[i] = 0;
+  __syncthreads();
+  for (int i = tid; i < T * p.k; i += blockDim.x) {
+    const int e = ids[i];
+    if ((unsigned)e < (unsigned)p.E) atomicOr(&s.tokens[e], 1ull << (i / p.k));
+  }
+  __syncthreads();
+  if (tid < 64) {
+    int n = 0, start = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+      const int e = e0 + lane;
+      const int members = e < p.E ? __builtin_popcountll(s.tokens[e]) : 0;
+      const unsigned long long any = __ballot(members > 0);
+      int before = members;  // inclusive sum over the lanes
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(before, d);
+        if (lane >= d) before += o;
+      }
+      if (members > 0) {
+        const int at = n + __builtin_popcountll(any & ((1ull << lane) - 1));
+        s.item_expert[at] = (uint16_t)e;
+        s.item_start[at] = (uint16_t)(start + before - members);
+      }
+      n += __builtin_popcountll(any);
+      start += __builtin_amdgcn_readlane(before, 63);
+    }
+    if (lane == 0) {
+      s.items = n;
+      s.item_start[n] = (uint16_t)start;
+    }
+  }
+  __syncthreads();
+}
+
+// The r-th token of a set: its first place that names expert e, and the weights
+// of all such places.
+struct Member {
+  int token, place;
+  float w;
+};
+__device__ __forceinline__ Member member(const ExpertParams& p, const int32_t* ids, const float* weights,
+                                         unsigned long long set, int e, int r) {
+  for (; r > 0; --r) set &= set - 1;
+  Member m{__builtin_ctzll(set), -1, 0.f};
+  for (int j = 0; j < p.k; ++j)
+    if (ids[m.token * p.k + j] == e) {
+      const float w = weights[m.token * p.k + j];
+      m.w = m.place < 0 ? w : m.w + w;
+      if (m.place < 0) m.place = j;
+    }
+  return m;
+}
 
 // Grid: tiles of COLS outputs, passes of 64 tokens.
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p) {
-  using S = typename C::S;
-  extern __shared__ float sums[];  // [WAVES][T][COLS]
-  __shared__ unsigned long long tokens[kMaxExperts];  // that go to an expert
-  // experts with their tiles of ROWS tokens, and how many
-  __shared__ uint16_t items[kMaxExperts * (kLayerTokens / C::ROWS)];
-  __shared__ int item_count;
-  __shared__ int pair_of[C::WAVES][C::ROWS], token_of[C::WAVES][C::ROWS];
-  __shared__ float weight_of[C::WAVES][C::ROWS];
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  __shared__ Pairs pairs;
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int t0 = blockIdx.y * kLayerTokens, T = min(kLayerTokens, p.T - t0);
   const int32_t* ids = p.ids + (int64_t)t0 * p.k;
   const float* weights = p.w + (int64_t)t0 * p.k;
   const int n0 = blockIdx.x * C::COLS;
-
-  for (int i = tid; i < p.E; i += C::THREADS) tokens[i] = 0;
+  float* sums = (float*)(lds + C::WAVES * C::WAVE_LDS);  // [WAVES][T][COLS]
   for (int i = tid; i < C::WAVES * T * C::COLS; i += C::THREADS) sums[i] = 0.f;
-  __syncthreads();
-  for (int i = tid; i < T * p.k; i += C::THREADS) {
-    const int e = ids[i];
-    if ((unsigned)e < (unsigned)p.E) atomicOr(&tokens[e], 1ull << (i / p.k));
-  }
-  __syncthreads();
-  if (wave == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int members = e < p.E ? __builtin_popcountll(tokens[e]) : 0;
-#pragma unroll
-      for (int sub = 0; sub < kLayerTokens / C::ROWS; ++sub) {
-        const unsigned long long any = __ballot(members > sub * C::ROWS);
-        if (members > sub * C::ROWS) items[n + __builtin_popcountll(any & ((1ull << lane) - 1))] = (uint16_t)(e | sub << 10);
-        n += __builtin_popcountll(any);
-      }
-    }
-    if (lane == 0) item_count = n;
-  }
-  __syncthreads();
+  sort_pairs(pairs, p, ids, T);
 
-  const int chunks = (p.F + 127) >> 7;
-  const int total = item_count * chunks;
+  using S = Stream<typename C::Fmt, 1, x_kib<typename C::Fmt, 2>(C::MOST), C::CF, 1, 2, C::RING>;
+  const int chunks = (p.F + S::COLS - 1) / S::COLS;
+  const int total = pairs.items * chunks;
   int at = (int)((int64_t)total * wave / C::WAVES);
   const int end = (int)((int64_t)total * (wave + 1) / C::WAVES);
   float* mine = sums + wave * T * C::COLS;
-  Sources<S> src;
-  src.K = p.F;
-  src.group = p.group;
-  src.wide = p.wide2;
-  src.x = make_rsrc(p.H + (int64_t)t0 * p.k * 2 * p.F, (int64_t)T * p.k * 4 * p.F);
-  src.x_part = 2 * p.F;
+  uint8_t* ring = lds + wave * C::WAVE_LDS;
   while (at < end) {
     const int item = __builtin_amdgcn_readfirstlane(at / chunks), c0 = at - item * chunks;
     const int c1 = min(chunks, c0 + end - at);
     at += c1 - c0;
-    const int what = __builtin_amdgcn_readfirstlane(items[item]);
-    const int e = what & 1023, base = (what >> 10) * C::ROWS;
-    const unsigned long long mask = tokens[e];
-    const int rows = min(C::ROWS, __builtin_popcountll(mask) - base);
-    const int rank = __builtin_popcountll(mask & ((1ull << lane) - 1)) - base;
-    if (((mask >> lane) & 1) && rank >= 0 && rank < C::ROWS) {
-      int place = -1;
-      float w = 0.f;
-      for (int j = 0; j < p.k; ++j)
-        if (ids[lane * p.k + j] == e) {
-          w = place < 0 ? weights[lane * p.k + j] : w + weights[lane * p.k + j];
-          if (place < 0) place = j;
-        }
-      pair_of[wave][rank] = lane * p.k + place;
-      token_of[wave][rank] = lane;
-      weight_of[wave][rank] = w;
-    }
-    // a wave's own LDS accesses are in order; the compiler keeps them so
-    __builtin_amdgcn_wave_barrier();
-    set_weights(src, 0, p.W2, p.s2, p.z2, e, p.K, n0, p.row2, p.groups2);
+    const int e = __builtin_amdgcn_readfirstlane(pairs.item_expert[item]);
+    const int start = __builtin_amdgcn_readfirstlane(pairs.item_start[item]);
+    const int members = __builtin_amdgcn_readfirstlane(pairs.item_start[item + 1]) - start;
+    for (int base = 0; base < members; base += C::MOST) {
+      const int rows = min(C::MOST, members - base);
+      const Member me = member(p, ids, weights, pairs.tokens[e], e, base + min(l16, rows - 1));
+      Sources<S> src;
+      src.K = p.F;
+      set_group(src, p.group);
+      src.x = make_rsrc(p.H + (int64_t)t0 * p.k * 2 * p.F, (int64_t)T * p.k * 4 * p.F);
+      set_weights(src, 0, p.W2, p.s2, p.z2, e, p.K, n0, p.row2, p.groups2);
 #pragma unroll
-    for (int t = 0; t < S::MT; ++t) src.x_off[t] = pair_of[wave][min(16 * t + l16, rows - 1)] * 4 * p.F;
-    f32x4 acc[S::MT][S::CF];
-    clear<S>(acc);
-    stream_chunks<S>(acc, src, c0, c1, 1);
-#pragma unroll
-    for (int t = 0; t < S::MT; ++t)
+      for (int i = 0; i < S::X_LOADS; ++i) {
+        const int r = min(x_row_of<S>(i), rows - 1);
+        src.x_off[i] = __shfl(me.token * p.k + me.place, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
+      }
+      f32x4 acc[S::MT][S::CF];
+      clear<S>(acc);
+      stream_chunks<S>(acc, src, ring, (uint32_t*)(ring + C::RING), c0, c1, 5 * blockIdx.x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 16 * t + 4 * quarter + i;
+        const int r = 4 * quarter + i;
+        const float wr = __shfl(me.w, r);
+        const int tr = __shfl(me.token, r);
         if (r < rows) {
-          const float w = weight_of[wave][r];
-          float* row = mine + token_of[wave][r] * C::COLS + l16;
+          float* row = mine + tr * C::COLS + l16;
 #pragma unroll
-          for (int c = 0; c < S::CF; ++c) row[16 * c] += w * acc[t][c][i];
+          for (int c = 0; c < S::CF; ++c) row[16 * c] += wr * acc[0][c][i];
         }
       }
-    __builtin_amdgcn_wave_barrier();
+    }
   }
   __syncthreads();
   for (int i = tid; i < T * C::COLS; i += C::THREADS) {
@@ -278,6 +406,101 @@ __global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p
 #pragma unroll
     for (int w = 1; w < C::WAVES; ++w) v += sums[w * T * C::COLS + i];
     if (n < p.K) p.D[(int64_t)(t0 + t) * p.ldd + n] = bf16_bits(v);
+  }
+}
+
+// Waves share an item's hidden units; a workgroup does a part of all items'
+// chunks for COLS outputs and, with more than one part, leaves its sums to
+// join_parts_kernel.
+template <class Fmt_, int CF_, int WAVES_, int DEPTH_, int MOST_>
+struct WideDown {
+  using Fmt = Fmt_;
+  static constexpr int CF = CF_, WAVES = WAVES_, THREADS = 64 * WAVES, COLS = 16 * CF * WAVES, MOST = MOST_;
+  static constexpr int RING = DEPTH_ * (WAVES * CF * 2048 + x_kib<Fmt, 2>(MOST) * 1024);
+  static constexpr int SCALE_LDS = scale_lds<Fmt, CF>();
+  static int lds_bytes(int T) { return RING + WAVES * SCALE_LDS + T * COLS * 4; }
+};
+
+template <class C, int ROWS>
+__device__ __forceinline__ void wide_down_item(const ExpertParams& p, const int32_t* ids, const float* weights, int t0, int T,
+                                               unsigned long long set, int e, int base, int members, int n0, int c0, int c1,
+                                               uint8_t* ring, uint8_t* scales, float* sums) {
+  constexpr int MT = ROWS > 16 ? 2 : 1;
+  using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 2>(ROWS), C::CF, 1, 2, C::RING, C::WAVES>;
+  const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rows = min(ROWS, members - base);
+  const Member me = member(p, ids, weights, set, e, base + min(lane & (16 * MT - 1), rows - 1));
+  Sources<S> src;
+  src.K = p.F;
+  set_group(src, p.group);
+  src.x = make_rsrc(p.H + (int64_t)t0 * p.k * 2 * p.F, (int64_t)T * p.k * 4 * p.F);
+  set_weights(src, 0, p.W2, p.s2, p.z2, e, p.K, min(n0 + 16 * C::CF * wave, p.K - 16), p.row2,
+              p.groups2);  // past K: some rows that are there, for nothing
+#pragma unroll
+  for (int i = 0; i < S::X_LOADS; ++i) {
+    const int r = min(x_row_of<S>(i), rows - 1);
+    src.x_off[i] = __shfl(me.token * p.k + me.place, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
+  }
+  f32x4 acc[MT][C::CF];
+  clear<S>(acc);
+  stream_chunks<S>(acc, src, ring, (uint32_t*)(scales + wave * C::SCALE_LDS), c0, c1, 5 * blockIdx.x);
+  float* mine = sums + 16 * C::CF * wave + l16;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 16 * t + 4 * quarter + i;
+      const float w = __shfl(me.w, r);
+      const int token = __shfl(me.token, r);
+      if (r < rows) {
+#pragma unroll
+        for (int c = 0; c < C::CF; ++c) mine[token * C::COLS + 16 * c] += w * acc[t][c][i];
+      }
+    }
+}
+
+// Grid: tiles of COLS outputs, parts.  One pass of tokens from t0 on.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void experts_wide_down_kernel(ExpertParams p, int t0, float* partial) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  __shared__ Pairs pairs;
+  const int tid = threadIdx.x;
+  const int T = min(kLayerTokens, p.T - t0);
+  const int32_t* ids = p.ids + (int64_t)t0 * p.k;
+  const float* weights = p.w + (int64_t)t0 * p.k;
+  const int n0 = blockIdx.x * C::COLS;
+  uint8_t* scales = lds + C::RING;
+  float* sums = (float*)(scales + C::WAVES * C::SCALE_LDS);  // [T][COLS]
+  for (int i = tid; i < T * C::COLS; i += C::THREADS) sums[i] = 0.f;
+  sort_pairs(pairs, p, ids, T);
+  constexpr int COLS = C::Fmt::FP8 ? 128 : 256;
+  const int chunks = (p.F + COLS - 1) / COLS;
+  const int total = pairs.items * chunks;
+  int at = (int)((int64_t)total * blockIdx.y / gridDim.y);
+  const int end = (int)((int64_t)total * (blockIdx.y + 1) / gridDim.y);
+  while (at < end) {
+    const int item = __builtin_amdgcn_readfirstlane(at / chunks), c0 = at - item * chunks;
+    const int c1 = min(chunks, c0 + end - at);
+    at += c1 - c0;
+    const int e = __builtin_amdgcn_readfirstlane(pairs.item_expert[item]);
+    const unsigned long long set = pairs.tokens[e];
+    const int members = __builtin_amdgcn_readfirstlane(__builtin_popcountll(set));
+    for (int base = 0; base < members; base += C::MOST) {
+      if (C::MOST == 16 || members - base <= 16)
+        wide_down_item<C, 16>(p, ids, weights, t0, T, set, e, base, members, n0, c0, c1, lds, scales, sums);
+      else
+        wide_down_item<C, C::MOST>(p, ids, weights, t0, T, set, e, base, members, n0, c0, c1, lds, scales, sums);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < T * C::COLS; i += C::THREADS) {
+    const int t = i / C::COLS, n = n0 + (i & (C::COLS - 1));
+    if (n >= p.K) continue;
+    if (gridDim.y == 1)
+      p.D[(int64_t)(t0 + t) * p.ldd + n] = bf16_bits(sums[i]);
+    else
+      partial[((int64_t)blockIdx.y * T + t) * p.K + n] = sums[i];
   }
 }
 

@@ -4,7 +4,9 @@
 
 #include <algorithm>
 #include <cstdio>
+#include <cstdlib>
 
+#include "decode_plan.hpp"
 #include "host_common.hpp"
 #include "int4_host.hpp"
 #include "int4_kernel.hpp"
@@ -66,24 +68,60 @@ fg_status cast(const T* x, int64_t ldx, uint8_t* q, uint16_t* s, uint8_t* z, int
   return launched(what);
 }
 
-template <class C>
-fg_status launch_product(Int4Params& p, void* stream) {
-  const int64_t tiles = ((int64_t)p.N + C::COLS - 1) / C::COLS;
-  p.parts = (p.M + C::ROWS - 1) / C::ROWS;
-  if (tiles * p.parts >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "gemm_int4_nt: too many output tiles");
-  if (print_launches())
-    fprintf(stderr, "[fp8gemm] gemm_int4_nt M=%d N=%d K=%d group=%d rows=%d cols=%d waves=%d grid=%lld\n", p.M, p.N, p.K,
-            p.group, C::ROWS, C::COLS, C::WAVES, (long long)(tiles * p.parts));
-  hipLaunchKernelGGL((int4_product_kernel<C>), dim3((unsigned)(tiles * p.parts)), dim3(C::THREADS), 0,
-                     (hipStream_t)stream, p);
-  return launched("gemm_int4_nt");
-}
+struct ProductLaunch {
+  Int4Params& p;
+  Int4Plan plan;
+  float* partial;
+  void* stream;
 
-template <int GPC>
-fg_status launch_gpc(Int4Params& p, void* stream) {
-  if (p.M <= 16) return launch_product<Int4Tile<GPC, 1, 1, 4, 2>>(p, stream);
-  if (p.M <= 32) return launch_product<Int4Tile<GPC, 2, 2, 4, 2>>(p, stream);
-  return launch_product<Int4Tile<GPC, 4, 2, 4, 1>>(p, stream);
+  template <class C>
+  fg_status split() const {
+    const int64_t tiles = ceil_div(p.N, C::COLS);
+    p.parts = ceil_div(p.M, C::ROWS);
+    if (tiles * p.parts >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "gemm_int4_nt: too many output tiles");
+    print();
+    hipLaunchKernelGGL((int4_product_kernel<C>), dim3((unsigned)(tiles * p.parts)), dim3(C::THREADS), 0, (hipStream_t)stream, p);
+    return launched("gemm_int4_nt");
+  }
+
+  template <class C>
+  fg_status wide() const {
+    const dim3 grid(ceil_div(p.N, C::COLS), ceil_div(p.M, C::ROWS), plan.k_parts);
+    if (grid.y > 65535) return set_error(FG_EUNSUPPORTED, "gemm_int4_nt: M=%d: too many row tiles", p.M);
+    print();
+    hipLaunchKernelGGL((int4_wide_kernel<C>), grid, dim3(C::THREADS), 0, (hipStream_t)stream, p, partial);
+    FG_TRY(launched("gemm_int4_nt"));
+    if (plan.k_parts == 1) return FG_OK;
+    const int64_t blocks = ((int64_t)p.M * p.N + 1023) / 1024;
+    hipLaunchKernelGGL(join_parts_kernel, dim3((unsigned)std::min<int64_t>(blocks, 1 << 16)), dim3(256), 0, (hipStream_t)stream,
+                       partial, plan.k_parts, p.D, p.ldd, p.M, p.N);
+    return launched("gemm_int4_nt");
+  }
+
+  void print() const {
+    if (print_launches())
+      fprintf(stderr, "[fp8gemm] gemm_int4_nt M=%d N=%d K=%d group=%d %s parts=%d\n", p.M, p.N, p.K, p.group,
+              kInt4Names[plan.kind], plan.k_parts);
+  }
+
+  template <class Fmt>
+  fg_status run() const {
+    switch (plan.kind) {
+      case kSplit2: return split<Int4Tile<Fmt, 2, 1, 4, 2>>();
+      case kSplit2Deep: return split<Int4Tile<Fmt, 2, 1, 8, 2>>();
+      case kSplit8: return split<Int4Tile<Fmt, 8, 1, 4, 2>>();
+      case kSplit8Deep: return split<Int4Tile<Fmt, 8, 1, 8, 2>>();
+      case kSplit16: return split<Int4Tile<Fmt, 16, 1, 4, 2>>();
+      case kSplit16Deep: return split<Int4Tile<Fmt, 16, 1, 6, 2>>();
+      case kWide16: return wide<Int4Wide<Fmt, 16, 1, 8, 2>>();
+      default: return wide<Int4Wide<Fmt, 64, 1, 8, 2>>();
+    }
+  }
+};
+
+Int4Plan planned(int M, int N, int K) {
+  const char* forced = getenv("FG_DECODE_PLAN");
+  return plan_int4(M, N, K, forced ? forced : "");
 }
 
 }  // namespace
@@ -104,7 +142,8 @@ fg_status int4_cast_per_group_bf16(const uint16_t* w, int64_t ldw, uint8_t* q, u
 }
 
 fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const uint16_t* sb, const uint8_t* zb,
-                       uint16_t* D, int64_t ldd, int M, int N, int K, int group, void* stream) {
+                       uint16_t* D, int64_t ldd, int M, int N, int K, int group, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
   clear_error();
   if (M < 0 || N < 0 || K < 0) return set_error(FG_EINVAL, "negative size M=%d N=%d K=%d", M, N, K);
   if (K % 32) return set_error(FG_EALIGN, "K=%d is not a multiple of 32", K);
@@ -112,6 +151,14 @@ fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const u
   if (M == 0 || N == 0) return FG_OK;
   if (M > kMaxRows || N > kMaxRows) return set_error(FG_EUNSUPPORTED, "M=%d N=%d: more than 2^30", M, N);
   if (K > kMaxK) return set_error(FG_EUNSUPPORTED, "K=%d above 2^20", K);
+  const Int4Plan plan = planned(M, N, K);
+  const int64_t need = int4_partial_bytes(M, N, plan);
+  if (workspace_bytes < 0) return set_error(FG_EINVAL, "workspace_bytes=%lld is negative", (long long)workspace_bytes);
+  if (!workspace && workspace_bytes > 0) return set_error(FG_EINVAL, "workspace is NULL");
+  if (workspace && ((uintptr_t)workspace & 255)) return set_error(FG_EALIGN, "workspace is not 256-byte aligned");
+  if (workspace_bytes < need)
+    return set_error(FG_EINVAL, "workspace_bytes=%lld is smaller than the %lld needed", (long long)workspace_bytes,
+                     (long long)need);
   FG_TRY(require_ptr(D, 2, "D"));
   FG_TRY(require_ld(ldd, N, 1, "ldd"));
   Int4Params p{};
@@ -125,11 +172,13 @@ fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const u
     p.A = A; p.lda = lda; p.B = B; p.s = sb; p.z = zb;
     p.groups = int4_groups(K, group);
     p.row_bytes = int4_row_bytes(K);
-    p.wide = int4_wide(K, sb, zb);
   }
-  if (group == 32) return launch_gpc<4>(p, stream);
-  if (group == 64) return launch_gpc<2>(p, stream);
-  return launch_gpc<1>(p, stream);
+  return with_int4_format(group, zb != nullptr, ProductLaunch{p, plan, (float*)workspace, stream});
+}
+
+int64_t fg_int4_workspace_bytes(int M, int N, int K) {
+  if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxK) return -1;
+  return M > 0 && N > 0 ? int4_partial_bytes(M, N, planned(M, N, K)) : 0;
 }
 
 }  // extern "C"

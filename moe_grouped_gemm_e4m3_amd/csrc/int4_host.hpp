@@ -3,6 +3,7 @@
 #pragma once
 
 #include "host_common.hpp"
+#include "weight_stream.hpp"
 
 namespace fg {
 
@@ -13,10 +14,12 @@ inline int int4_groups(int K, int group) { return (K + group - 1) / group; }
 // Rows are padded to whole chunks of 128 codes.
 inline int int4_row_bytes(int K) { return (K + 127) / 128 * 64; }
 
-// The scales (zero points) of a chunk's groups are one aligned load: every row
-// starts a whole number of chunks into arrays that are aligned to it.
-inline bool int4_wide(int K, const void* s, const void* z) {
-  return K % 128 == 0 && ((uintptr_t)s & 7) == 0 && ((uintptr_t)z & 3) == 0;
+// f.run<Format>() for the format of a call.
+template <class F>
+fg_status with_int4_format(int group, bool zeros, const F& f) {
+  if (group == 32) return zeros ? f.template run<Int4Group<4, true>>() : f.template run<Int4Group<4, false>>();
+  if (group == 64) return zeros ? f.template run<Int4Group<2, true>>() : f.template run<Int4Group<2, false>>();
+  return zeros ? f.template run<Int4Group<1, true>>() : f.template run<Int4Group<1, false>>();
 }
 
 }  // namespace fg

@@ -116,64 +116,125 @@ struct Int4Params {
   int M, N, K, group, groups;
   int row_bytes;  // of B
   int parts;      // row parts
-  bool wide;
 };
 
-template <int GPC_, int MT_, int CF_, int WAVES_, int DEPTH_>
-struct Int4Tile {
-  using S = Stream<kInt4Group, GPC_, MT_, CF_, 1, 1, DEPTH_>;
-  static constexpr int WAVES = WAVES_, THREADS = 64 * WAVES, ROWS = 16 * MT_, COLS = 16 * CF_;
-  static constexpr int BLOCKS = MT_ * CF_;
-};
-
-// Grid: column tiles x row parts, parts fastest.  The waves share out a tile's
-// chunks of K; their partials are added in wave order.
-template <class C>
-__global__ __launch_bounds__(C::THREADS) void int4_product_kernel(Int4Params p) {
-  using S = typename C::S;
-  __shared__ f32x4 red[C::WAVES][C::BLOCKS][64];
-  const int lane = threadIdx.x & 63, l16 = lane & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x / p.parts;
-  const int m0 = (blockIdx.x - tile * p.parts) * C::ROWS, n0 = tile * C::COLS;
-  const int rows = min(C::ROWS, p.M - m0);
-
-  Sources<S> src;
+// The weights and activations of a tile: rows [m0, m0 + rows) of A, weight rows
+// from n0 on.
+template <class S>
+__device__ __forceinline__ void set_tile(Sources<S>& src, const Int4Params& p, int m0, int rows, int n0) {
   src.K = p.K;
-  src.group = p.group;
-  src.has_z = p.z != nullptr;
-  src.wide = p.wide;
+  set_group(src, p.group);
   // rows past N are outside the ranges and read as zeros
   src.q[0] = make_rsrc(p.B + (int64_t)n0 * p.row_bytes, (int64_t)(p.N - n0) * p.row_bytes);
   src.s[0] = make_rsrc(p.s + (int64_t)n0 * p.groups, (int64_t)(p.N - n0) * p.groups * 2);
   src.z[0] = make_rsrc(p.z ? p.z + (int64_t)n0 * p.groups : nullptr, p.z ? (int64_t)(p.N - n0) * p.groups : 0);
-  src.q_off = l16 * p.row_bytes; src.q_tile = 16 * p.row_bytes;
-  src.s_off = l16 * p.groups * 2; src.s_tile = 32 * p.groups;
-  src.z_off = l16 * p.groups; src.z_tile = 16 * p.groups;
+  src.row_bytes = p.row_bytes;
+  src.groups = p.groups;
   src.x = make_rsrc(p.A + (int64_t)m0 * p.lda, ((int64_t)(rows - 1) * p.lda + p.K) * 2);
 #pragma unroll
-  for (int t = 0; t < S::MT; ++t) src.x_off[t] = min(16 * t + l16, rows - 1) * (int)(2 * p.lda);
-  src.x_part = 0;
+  for (int i = 0; i < S::X_LOADS; ++i) src.x_off[i] = min(x_row_of<S>(i), rows - 1) * (int)(2 * p.lda);
+}
+
+// A tile of ROWS rows and 16 CF columns; the waves share out its chunks of K.
+template <class Fmt, int ROWS_, int CF_, int WAVES_, int DEPTH_>
+struct Int4Tile {
+  static constexpr int MT = (ROWS_ + 15) / 16, CF = CF_, WAVES = WAVES_;
+  static constexpr int NX = ROWS_ > 2 ? ROWS_ / 2 : 1;
+  static constexpr int RING = DEPTH_ * (CF * 2048 + NX * 1024);
+  using S = Stream<Fmt, MT, NX, CF, 1, 1, RING>;
+  static constexpr int THREADS = 64 * WAVES, ROWS = ROWS_, COLS = 16 * CF;
+  static constexpr int BLOCKS = MT * CF;
+  static constexpr int WAVE_LDS = RING + scale_lds<Fmt, CF>();
+  static_assert(BLOCKS * 1024 <= WAVE_LDS, "LDS");
+};
+
+// Grid: column tiles x row parts, parts fastest.  The waves' partials are added
+// in wave order.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void int4_product_kernel(Int4Params p) {
+  using S = typename C::S;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::WAVES * C::WAVE_LDS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tile = blockIdx.x / p.parts;
+  const int m0 = (blockIdx.x - tile * p.parts) * C::ROWS, n0 = tile * C::COLS;
+  const int rows = min(C::ROWS, p.M - m0);
+  Sources<S> src;
+  set_tile(src, p, m0, rows, n0);
 
   f32x4 acc[S::MT][S::CF];
 #pragma unroll
   for (int t = 0; t < S::MT; ++t)
 #pragma unroll
     for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  stream_chunks<S>(acc, src, wave, (p.K + 127) >> 7, C::WAVES);
+  uint8_t* mine = lds + wave * C::WAVE_LDS;
+  const int chunks = (p.K + S::COLS - 1) / S::COLS;
+  stream_chunks<S>(acc, src, mine, (uint32_t*)(mine + C::RING), chunks * wave / C::WAVES, chunks * (wave + 1) / C::WAVES,
+                   5 * tile);
+  f32x4* sums = (f32x4*)mine;
 #pragma unroll
   for (int t = 0; t < S::MT; ++t)
 #pragma unroll
-    for (int c = 0; c < S::CF; ++c) red[wave][t * S::CF + c][lane] = acc[t][c];
+    for (int c = 0; c < S::CF; ++c) sums[(t * S::CF + c) * 64 + lane] = acc[t][c];
   __syncthreads();
   for (int x = threadIdx.x; x < C::BLOCKS * 256; x += C::THREADS) {
     const int col = x & (C::COLS - 1), row = x / C::COLS;
-    const int b = (row >> 4) * S::CF + (col >> 4), at = ((row & 15) >> 2) * 16 + (col & 15), i = row & 3;
-    float v = red[0][b][at][i];
+    const int at = (((row >> 4) * S::CF + (col >> 4)) * 64 + ((row & 15) >> 2) * 16 + (col & 15)) * 4 + (row & 3);
+    float v = 0.f;
 #pragma unroll
-    for (int w = 1; w < C::WAVES; ++w) v += red[w][b][at][i];
+    for (int w = 0; w < C::WAVES; ++w) v += ((const float*)(lds + w * C::WAVE_LDS))[at];
     if (row < rows && n0 + col < p.N) p.D[(int64_t)(m0 + row) * p.ldd + n0 + col] = bf16_bits(v);
   }
+}
+
+// A tile of ROWS rows and 16 CF WAVES columns and a part of K; the waves share
+// the activations' columns.
+template <class Fmt_, int ROWS_, int CF_, int WAVES_, int DEPTH_>
+struct Int4Wide {
+  using Fmt = Fmt_;
+  static constexpr int MT = ROWS_ / 16, CF = CF_, WAVES = WAVES_, ROWS = ROWS_;
+  static constexpr int RING = DEPTH_ * (WAVES * CF * 2048 + ROWS * 512);
+  using S = Stream<Fmt, MT, ROWS / 2, CF, 1, 1, RING, WAVES>;
+  static constexpr int THREADS = 64 * WAVES, COLS = 16 * CF * WAVES;
+  static constexpr int LDS = RING + WAVES * scale_lds<Fmt, CF>();
+};
+
+// Grid: column tiles, row parts, parts of K.
+template <class C>
+__global__ __launch_bounds__(C::THREADS) void int4_wide_kernel(Int4Params p, float* partial) {
+  using S = typename C::S;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[C::LDS];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m0 = blockIdx.y * C::ROWS, n0 = blockIdx.x * C::COLS + 16 * C::CF * wave;
+  const int rows = min(C::ROWS, p.M - m0);
+  Sources<S> src;
+  set_tile(src, p, m0, rows, min(n0, p.N - 1));  // past N: some rows that are there, for nothing
+  f32x4 acc[S::MT][S::CF];
+#pragma unroll
+  for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+    for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int chunks = (p.K + S::COLS - 1) / S::COLS;
+  const int first = (int)((int64_t)chunks * blockIdx.z / gridDim.z), end = (int)((int64_t)chunks * (blockIdx.z + 1) / gridDim.z);
+  stream_chunks<S>(acc, src, lds, (uint32_t*)(lds + C::RING + wave * scale_lds<typename C::Fmt, C::CF>()), first, end,
+                   5 * blockIdx.x);
+#pragma unroll
+  for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * t + 4 * quarter + i;
+      if (row >= rows) continue;
+#pragma unroll
+      for (int c = 0; c < S::CF; ++c) {
+        const int n = n0 + 16 * c + l16;
+        if (n >= p.N) continue;
+        if (gridDim.z == 1)
+          p.D[(int64_t)(m0 + row) * p.ldd + n] = bf16_bits(acc[t][c][i]);
+        else
+          partial[((int64_t)blockIdx.z * p.M + m0 + row) * p.N + n] = acc[t][c][i];
+      }
+    }
 }
 
 }  // namespace fg

@@ -13,231 +13,391 @@
 // both formats.  The zero point leaves the sum because it is constant in a
 // group: the sum of X comes from the matrix cores too, as a product with ones.
 //
-// Weights go from global memory to registers in 16-byte loads, without LDS: a
-// wave's 16 weight rows are the columns of a 16x16x32 MFMA, whose order of k is
-// free as long as X's follows it.  A wave takes chunks of 128 columns and keeps
-// DEPTH of them in flight.
+// A wave streams chunks of 128 bytes of its weight rows (128 e4m3 or 256 4-bit
+// columns) through an LDS ring that it alone uses, DEPTH - 1 of them in flight,
+// with the same columns of X next to them.  Weights loaded into registers in the
+// matrix cores' layout (16 rows by 16 bytes) cost an access of the vector cache
+// for every lane, 64 for 1 KiB, and that rate, about one a clock, bounded the
+// 4-bit layers at 2.3 TB/s; whole rows of 128 bytes cost a quarter of them.
 #pragma once
 
-#include "linear_kernel.hpp"
+#include "linear_fewrow.hpp"
 
 namespace fg {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-enum WeightFormat { kFp8Block, kInt4Group };
-
-// GPC: scale groups in a chunk (4-bit: 4, 2 or 1 for groups of 32, 64 and any
-// multiple of 128).  MT: row tiles of 16.  CF: weight tiles of 16 rows.  REGIONS:
-// the weight tiles lie in so many places of the matrix (2: gate and up rows).
-// PARTS: X is the sum of so many bf16 matrices.
-template <int FMT_, int GPC_, int MT_, int CF_, int REGIONS_, int PARTS_, int DEPTH_>
-struct Stream {
-  static constexpr int FMT = FMT_, GPC = GPC_, MT = MT_, CF = CF_, REGIONS = REGIONS_, PARTS = PARTS_, DEPTH = DEPTH_;
-  static constexpr bool FP8 = FMT == kFp8Block;
-  static constexpr int WL = FP8 ? 2 : 1;      // 16-byte loads of a weight row's chunk and lane
-  static constexpr int PER = CF / REGIONS;    // weight tiles of a region
-  static_assert(CF % REGIONS == 0, "tiles");
+// Formats.  GPC: scale groups in 128 columns (4, 2 or 1 for groups of 32, 64 and
+// any multiple of 128).  Z: with zero points (else 8).
+struct Fp8Block {
+  static constexpr bool FP8 = true, Z = false;
+  static constexpr int GPC = 1;
+};
+template <int GPC_, bool Z_>
+struct Int4Group {
+  static constexpr bool FP8 = false, Z = Z_;
+  static constexpr int GPC = GPC_;
 };
 
-// Where a wave's weights and activations are.  Offsets are a lane's, in bytes.
+// MT: row tiles of 16.  NX: KiB of X in a chunk (so X_ROWS rows are there).  CF:
+// weight tiles of 16 rows, in REGIONS places of the matrix (2: gate and up
+// rows).  PARTS: X is the sum of so many bf16 matrices.  RING: bytes of the ring.
+// SHARE: waves that work on the same columns, with one copy of X, a ring and a
+// barrier for each chunk; 1: a wave on its own.  SCALES: 4-bit groups of each
+// weight row whose scales wait in LDS.
+template <class Fmt_, int MT_, int NX_, int CF_, int REGIONS_, int PARTS_, int RING_, int SHARE_ = 1, int SCALES_ = 32>
+struct Stream {
+  using Fmt = Fmt_;
+  static constexpr int MT = MT_, NX = NX_, CF = CF_, REGIONS = REGIONS_, PARTS = PARTS_;
+  static constexpr bool FP8 = Fmt::FP8, Z = Fmt::Z;
+  static constexpr int GPC = Fmt::GPC;
+  static constexpr int PER = CF / REGIONS;           // weight tiles of a region
+  static constexpr int HALVES = FP8 ? 1 : 2;         // pieces of 128 columns in a chunk
+  static constexpr int COLS = 128 * HALVES;          // columns of a chunk
+  static constexpr int X_PART = 2 * COLS;            // bytes of one row and part of X
+  static constexpr int X_ROW = X_PART * PARTS;
+  static constexpr int X_ROWS = NX * 1024 / X_ROW;
+  static constexpr int SHARE = SHARE_;
+  static constexpr int SLOT = SHARE * CF * 2048 + NX * 1024;  // X, then every wave's weights
+  static constexpr int X_LOADS = NX > SHARE ? NX / SHARE : 1;  // of a wave
+  static constexpr int LOADS = CF * 2 + X_LOADS;
+  static constexpr int FIT = RING_ / SLOT, MOST = 63 / LOADS + 1;
+  static constexpr int DEPTH = FIT < MOST ? FIT : MOST;
+  static constexpr int SCALES = SCALES_;
+  static constexpr int SCALE_LD = SCALES + 1;        // words; odd, so that rows lie in different banks
+  static_assert(CF % REGIONS == 0 && DEPTH >= 2 && X_ROWS <= 16 * MT, "stream");
+};
+// LDS bytes of a wave's scales.
+template <class Fmt, int CF, int SCALES = 32>
+constexpr int scale_lds() {
+  return Fmt::FP8 ? 0 : 16 * CF * (SCALES + 1) * 4;
+}
+
+// Where a wave's weights and activations are.
 template <class S>
 struct Sources {
   __amdgpu_buffer_rsrc_t q[S::REGIONS], s[S::REGIONS], z[S::REGIONS];
-  int q_off, s_off, z_off;    // this lane's row of a region's first tile
-  int q_tile, s_tile, z_tile;  // from one tile of a region to the next
-  const float* fs[S::REGIONS];  // e4m3: the block row's factors
+  const float* fs[S::CF];  // e4m3: the factors of every tile's block row
+  int row_bytes, groups;   // of a weight row
   __amdgpu_buffer_rsrc_t x;
-  int x_off[S::MT];  // this lane's row of every row tile
-  int x_part;        // from one part of X to the next
-  int K, group;
-  bool has_z, wide;  // wide: the scales of a chunk are one aligned load
+  int x_off[S::X_LOADS];   // this lane's row and part of X in every load, bytes
+  int K;
+  int group_chunks, group_shift;  // GPC 1: multiples of 128 in a group, and their logarithm (-1: no power of two)
 };
 
 template <class S>
-struct Chunk {
-  i32x4 w[S::CF][S::WL];
-  i32x4 x[S::PARTS][S::MT][4];
-  float fs[S::REGIONS];
-  uint32_t s[S::CF][S::GPC], z[S::CF][S::GPC];
-};
-
-// Column of X (from the chunk's first) of a lane's piece m of 8, as the weights' loads have it.
-template <bool FP8>
-__device__ __forceinline__ int piece_col(int m, int quarter) {
-  return FP8 ? (m >> 1) * 64 + quarter * 16 + (m & 1) * 8 : m * 32 + quarter * 8;
+__device__ __forceinline__ void set_group(Sources<S>& src, int group) {
+  src.group_chunks = group >> 7;
+  src.group_shift = (src.group_chunks & (src.group_chunks - 1)) ? -1 : 31 - __builtin_clz(src.group_chunks | 1);
+}
+// Scale group of the 128 columns `half` and part g of them.
+template <class S>
+__device__ __forceinline__ int group_of(const Sources<S>& src, int half, int g) {
+  return S::GPC > 1 ? half * S::GPC + g : src.group_shift >= 0 ? half >> src.group_shift : half / src.group_chunks;
 }
 
-template <class S, bool TAIL>
-__device__ __forceinline__ void load_chunk(Chunk<S>& c, const Sources<S>& src, int chunk) {
-  const int quarter = (threadIdx.x & 63) >> 4;
+// A lane's place in load i of X: lanes are pieces of 16 bytes of rows, parts
+// after each other; a piece's place in its 8 is exchanged by the row, which
+// spreads the matrix cores' reads over the banks.
+// Load i of a wave is KiB x_kib_of(i) of X: the waves share them out (where
+// there are fewer KiB than waves, some load the same).
+template <class S>
+__device__ __forceinline__ int x_kib_of(int i) {
+  if (S::SHARE == 1) return i;
+  return (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * S::X_LOADS + i) & (S::NX - 1);
+}
+template <class S>
+__device__ __forceinline__ int x_row_of(int i) {
+  return (x_kib_of<S>(i) * 1024 + (threadIdx.x & 63) * 16) / S::X_ROW;
+}
+template <class S>
+__device__ __forceinline__ int x_part_of() {
+  return ((threadIdx.x & 63) * 16 % S::X_ROW) / S::X_PART;
+}
+
+// This wave's weights in a slot.
+template <class S>
+__device__ __forceinline__ int weights_at() {
+  return S::NX * 1024 + (S::SHARE == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * S::CF * 2048);
+}
+
+// Loads chunk c into a slot.  Past column K, and where it is not wanted, zeros,
+// without touching memory (but counted as loads).  The scalar offset counts against the
+// range's end and must not pass it: every range holds a row at least.
+template <class S>
+__device__ __forceinline__ void load_chunk(const Sources<S>& src, uint8_t* slot, int c, bool want) {
+  typedef __attribute__((address_space(3))) void* Lds;
+  const int lane = threadIdx.x & 63;
+  const int r8 = lane >> 3, byte = ((lane & 7) ^ r8) * 16;
+  const bool in = byte < (want ? (S::FP8 ? src.K : src.row_bytes) - c * 128 : 0);
+  uint8_t* mine = slot + weights_at<S>();
 #pragma unroll
-  for (int r = 0; r < S::REGIONS; ++r) {
-    if constexpr (S::FP8) c.fs[r] = *(const __attribute__((address_space(4))) float*)(src.fs[r] + chunk);
+  for (int t = 0; t < S::CF; ++t)
 #pragma unroll
-    for (int i = 0; i < S::PER; ++i) {
-      const int cf = r * S::PER + i;
-#pragma unroll
-      for (int j = 0; j < S::WL; ++j) {
-        int v = src.q_off + i * src.q_tile + (S::FP8 ? j * 64 + quarter * 16 : quarter * 16);
-        if (S::FP8 && TAIL && chunk * 128 + j * 64 + quarter * 16 >= src.K) v = kOobOffset;
-        c.w[cf][j] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(src.q[r], v, chunk * (S::FP8 ? 128 : 64), 0));
-      }
-      if constexpr (!S::FP8) {
-        const int g = S::GPC == 1 ? chunk * 128 / src.group : chunk * S::GPC;
-        const int sv = src.s_off + i * src.s_tile, zv = src.z_off + i * src.z_tile;
-        if (S::GPC > 1 && src.wide) {
-          if constexpr (S::GPC == 4) {
-            const u32x2 t = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(src.s[r], sv, 2 * g, 0));
-            c.s[cf][0] = t.x << 16; c.s[cf][1] = t.x & 0xffff0000u;
-            c.s[cf][2] = t.y << 16; c.s[cf][3] = t.y & 0xffff0000u;
-          } else if constexpr (S::GPC == 2) {
-            const uint32_t t = __builtin_amdgcn_raw_buffer_load_b32(src.s[r], sv, 2 * g, 0);
-            c.s[cf][0] = t << 16; c.s[cf][1] = t & 0xffff0000u;
-          }
-          if (src.has_z) {
-            uint32_t t = 0;
-            if constexpr (S::GPC == 4) t = __builtin_amdgcn_raw_buffer_load_b32(src.z[r], zv, g, 0);
-            if constexpr (S::GPC == 2) t = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.z[r], zv, g, 0);
-#pragma unroll
-            for (int h = 0; h < S::GPC; ++h) c.z[cf][h] = (t >> (8 * h)) & 255u;
-          }
-        } else {
-#pragma unroll
-          for (int h = 0; h < S::GPC; ++h) {
-            if (TAIL && h > 0 && chunk * 128 + h * (128 / S::GPC) >= src.K) continue;
-            c.s[cf][h] = (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s[r], sv, 2 * (g + h), 0) << 16;
-            if (src.has_z) c.z[cf][h] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z[r], zv, g + h, 0);
-          }
-        }
-        if (!src.has_z) {
-#pragma unroll
-          for (int h = 0; h < S::GPC; ++h) c.z[cf][h] = 8;
-        }
-      }
+    for (int h = 0; h < 2; ++h) {
+      const int v = ((t % S::PER) * 16 + h * 8 + r8) * src.row_bytes + byte;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src.q[t / S::PER], (Lds)(mine + t * 2048 + h * 1024), 16,
+                                               in ? v : kOobOffset, c * 128, 0, 0);
     }
+  const int cols_left = want ? src.K - c * S::COLS : 0;
+#pragma unroll
+  for (int i = 0; i < S::X_LOADS; ++i) {
+    const int at = (lane * 16) & (S::X_PART - 1);  // in the row and part, before the exchange
+    const int col = (at ^ ((x_row_of<S>(i) & 7) << 4)) >> 1;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src.x, (Lds)(slot + x_kib_of<S>(i) * 1024), 16,
+                                             col < cols_left ? src.x_off[i] + 2 * col : kOobOffset,
+                                             c * (2 * S::COLS), 0, 0);
   }
+}
+
+// Scales and zero points of groups g0 .. g_last (at most SCALES) of the wave's
+// rows into LDS, one word each: bf16 scale above, zero point below.  Groups of
+// the last chunk that the row does not have get scales of zero: what stands
+// behind a row's last scale may be anything, and 0 NaN is not 0.
+template <class S>
+__device__ __forceinline__ void load_scales(const Sources<S>& src, uint32_t* scales, int g0, int g_last) {
+  const int lane = threadIdx.x & 63, r8 = lane >> 3;
+  const int n = min(S::SCALES, g_last + 1 - g0);
+#pragma unroll 1
+  for (int j0 = 0; j0 < min(n + 2 * S::GPC - 1, S::SCALES); j0 += 16) {
+    uint32_t w[S::CF][2][2];
 #pragma unroll
-  for (int p = 0; p < S::PARTS; ++p)
+    for (int t = 0; t < S::CF; ++t)
 #pragma unroll
-    for (int t = 0; t < S::MT; ++t)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int col = piece_col<S::FP8>(m, quarter);
-        int v = src.x_off[t] + p * src.x_part + 2 * col;
-        if (TAIL && chunk * 128 + col >= src.K) v = kOobOffset;
-        c.x[p][t][m] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(src.x, v, chunk * 256, 0));
-      }
+        for (int y = 0; y < 2; ++y) {
+          const int g = j0 + 8 * y + (lane & 7), row = (t % S::PER) * 16 + h * 8 + r8;
+          const int at = g < n ? row * src.groups + g0 + g : 0x3fffffff;  // out of every range
+          const uint32_t s = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s[t / S::PER], 2 * at, 0, 0);
+          const uint32_t z = S::Z ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z[t / S::PER], at, 0, 0) : 8u;
+          w[t][h][y] = s << 16 | z;
+        }
+#pragma unroll
+    for (int t = 0; t < S::CF; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) scales[(t * 16 + h * 8 + r8) * S::SCALE_LD + j0 + 8 * y + (lane & 7)] = w[t][h][y];
+  }
 }
 
 // Eight weights as bf16: e4m3 bytes, or the eight codes of a 4-bit word.
-__device__ __forceinline__ bf16x8 widen_fp8(int lo, int hi) {
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
+__device__ __forceinline__ bf16x8 widen_bytes(int lo, int hi, float scale) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
   return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 __device__ __forceinline__ bf16x8 widen_int4(int w) {
-  const int lo = w & 0x0f0f0f0f, hi = (int)((uint32_t)w >> 4) & 0x0f0f0f0f;
-  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false);
-  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true);
-  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false);
-  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true);
-  return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+  return widen_bytes(w & 0x0f0f0f0f, (int)((uint32_t)w >> 4) & 0x0f0f0f0f, 512.f);
 }
 
-template <class S, bool TAIL>
-__device__ __forceinline__ void add_chunk(f32x4 (&acc)[S::MT][S::CF], const Chunk<S>& c, const Sources<S>& src, int chunk) {
+__device__ __forceinline__ f32x4 mfma_bf16(i32x4 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), b, c, 0, 0, 0);
+}
+
+// A lane's 8 columns of X for matrix product m of 128 columns `half` of a slot,
+// in the order of its weights: e4m3, 16 bytes of each 64, 8 at a time; 4 bits,
+// word m of piece `quarter`.  Pieces are exchanged inside groups of 8, so an
+// address is one of a few lane constants and an immediate.
+template <class S>
+__device__ __forceinline__ i32x4 x_piece(const uint8_t* slot, int t, int part, int half, int m) {
+  const int lane = threadIdx.x & 63, quarter = lane >> 4;
+  // rows past the slot's are never looked at again
+  const int row = (16 * t + (lane & 15)) & (S::X_ROWS - 1);
+  const int in8 = S::FP8 ? 2 * quarter + (m & 1) : (m & 1) * 4 + quarter;
+  const int eight = S::FP8 ? m >> 1 : half * 2 + (m >> 1);
+  return *(const i32x4*)(slot + (row * S::X_ROW + ((in8 ^ (row & 7)) << 4)) + part * S::X_PART + eight * 128);
+}
+// 16 bytes of a lane's weight row in tile t: piece 4 j + quarter of 8.
+template <class S>
+__device__ __forceinline__ i32x4 w_piece(const uint8_t* slot, int t, int j) {
+  const int lane = threadIdx.x & 63, l16 = lane & 15;
+  return *(const i32x4*)(slot + weights_at<S>() + (l16 * 128 + (((4 * j + (lane >> 4)) ^ (l16 & 7)) << 4)) + t * 2048);
+}
+
+// acc += the slot's products.
+template <class S>
+__device__ __forceinline__ void add_chunk(f32x4 (&acc)[S::MT][S::CF], const Sources<S>& src, const uint8_t* slot,
+                                          const float (&fs)[S::CF], const uint32_t* scales, int chunk, int g0) {
   if constexpr (S::FP8) {
+    i32x4 x[S::PARTS][S::MT][4];
+#pragma unroll
+    for (int p = 0; p < S::PARTS; ++p)
+#pragma unroll
+      for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[p][t][m] = x_piece<S>(slot, t, p, 0, m);
 #pragma unroll
     for (int cf = 0; cf < S::CF; ++cf) {
       f32x4 P[S::MT];
 #pragma unroll
       for (int t = 0; t < S::MT; ++t) P[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const bf16x8 b = widen_fp8(c.w[cf][m >> 1][2 * (m & 1)], c.w[cf][m >> 1][2 * (m & 1) + 1]);
+      for (int j = 0; j < 2; ++j) {
+        const i32x4 w = w_piece<S>(slot, cf, j);
 #pragma unroll
-        for (int t = 0; t < S::MT; ++t)
+        for (int h = 0; h < 2; ++h) {
+          const bf16x8 b = widen_bytes(w[2 * h], w[2 * h + 1], 1.f);
 #pragma unroll
-          for (int p = 0; p < S::PARTS; ++p)
-            P[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, c.x[p][t][m]), b, P[t], 0, 0, 0);
+          for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+            for (int p = 0; p < S::PARTS; ++p) P[t] = mfma_bf16(x[p][t][2 * j + h], b, P[t]);
+        }
       }
-      const float s = c.fs[cf / S::PER];
 #pragma unroll
       for (int t = 0; t < S::MT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][cf][i] = __builtin_fmaf(s, P[t][i], acc[t][cf][i]);
+        for (int i = 0; i < 4; ++i) acc[t][cf][i] = __builtin_fmaf(fs[cf], P[t][i], acc[t][cf][i]);
     }
   } else {
     constexpr int MPG = 4 / S::GPC;
     const __bf16 one = (__bf16)1.f;
     const bf16x8 ones = bf16x8{one, one, one, one, one, one, one, one};
+    const int l16 = threadIdx.x & 15;
 #pragma unroll
-    for (int g = 0; g < S::GPC; ++g) {
-      if (TAIL && g > 0 && chunk * 128 + g * (128 / S::GPC) >= src.K) continue;  // groups past the row's last
-      f32x4 sum[S::MT];
+    for (int half = 0; half < 2; ++half) {
+      i32x4 x[S::PARTS][S::MT][4], w[S::CF];
 #pragma unroll
-      for (int t = 0; t < S::MT; ++t) {
-        sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int cf = 0; cf < S::CF; ++cf) w[cf] = w_piece<S>(slot, cf, half);
 #pragma unroll
-        for (int m = g * MPG; m < (g + 1) * MPG; ++m)
-#pragma unroll
-          for (int p = 0; p < S::PARTS; ++p)
-            sum[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, c.x[p][t][m]), ones, sum[t], 0, 0, 0);
-      }
-#pragma unroll
-      for (int cf = 0; cf < S::CF; ++cf) {
-        f32x4 P[S::MT];
-#pragma unroll
-        for (int t = 0; t < S::MT; ++t) P[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int m = g * MPG; m < (g + 1) * MPG; ++m) {
-          const bf16x8 b = widen_int4(c.w[cf][0][m]);
-#pragma unroll
-          for (int t = 0; t < S::MT; ++t)
-#pragma unroll
-            for (int p = 0; p < S::PARTS; ++p)
-              P[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, c.x[p][t][m]), b, P[t], 0, 0, 0);
-        }
-        const float s = __uint_as_float(c.s[cf][g]), z = (float)c.z[cf][g];
+      for (int p = 0; p < S::PARTS; ++p)
 #pragma unroll
         for (int t = 0; t < S::MT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[t][cf][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[t][i], P[t][i]), acc[t][cf][i]);
+          for (int m = 0; m < 4; ++m) x[p][t][m] = x_piece<S>(slot, t, p, half, m);
+#pragma unroll
+      for (int g = 0; g < S::GPC; ++g) {
+        const int at = group_of(src, chunk * 2 + half, g) - g0;
+        f32x4 sum[S::MT];
+#pragma unroll
+        for (int t = 0; t < S::MT; ++t) {
+          sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int m = g * MPG; m < (g + 1) * MPG; ++m)
+#pragma unroll
+            for (int p = 0; p < S::PARTS; ++p) sum[t] = mfma_bf16(x[p][t][m], ones, sum[t]);
+        }
+#pragma unroll
+        for (int cf = 0; cf < S::CF; ++cf) {
+          const uint32_t sz = scales[(cf * 16 + l16) * S::SCALE_LD + at];
+          f32x4 P[S::MT];
+#pragma unroll
+          for (int t = 0; t < S::MT; ++t) P[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int m = g * MPG; m < (g + 1) * MPG; ++m) {
+            const bf16x8 b = widen_int4(w[cf][m]);
+#pragma unroll
+            for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+              for (int p = 0; p < S::PARTS; ++p) P[t] = mfma_bf16(x[p][t][m], b, P[t]);
+          }
+          const float s = __uint_as_float(sz & 0xffff0000u), z = S::Z ? (float)(uint8_t)sz : 8.f;
+#pragma unroll
+          for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[t][cf][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[t][i], P[t][i]), acc[t][cf][i]);
+        }
       }
     }
   }
 }
 
-// acc += the products of chunks first, first + step, ... below `end`; the
-// chunk that holds column K's group end, if partial, is chunk K / 128.
+// acc += the products of chunks [first, end), from the `turn`-th on and around.
+// ring: this wave's LDS, or the sharing waves' (which all call with the same
+// chunks).  No load is outstanding when it returns.
+//
+// The turn is the tile's, so that tiles which run side by side read different
+// columns: rows a power of two of bytes apart have the same columns in the same
+// memory channels.
 template <class S>
-__device__ __forceinline__ void stream_chunks(f32x4 (&acc)[S::MT][S::CF], const Sources<S>& src, int first, int end,
-                                              int step) {
-  const int whole = min(end, src.K >> 7);  // chunks without a tail
-  const int n = first < whole ? (whole - first + step - 1) / step : 0;
-  Chunk<S> c[S::DEPTH];
+__device__ __forceinline__ void stream_chunks(f32x4 (&acc)[S::MT][S::CF], const Sources<S>& src, uint8_t* ring,
+                                              uint32_t* scales, int first, int end, unsigned turn) {
+  if (first >= end) return;
+  int ahead = first + (int)(turn % (unsigned)(end - first));  // the next chunk to load
+  int c = ahead;
+  auto next_of = [&](int x) { return x + 1 == end ? first : x + 1; };
+  const int n = end - first;
 #pragma unroll
-  for (int d = 0; d < S::DEPTH; ++d)
-    if (d < n) load_chunk<S, false>(c[d], src, first + d * step);
-  int i = 0;
-  for (; i + S::DEPTH <= n; i += S::DEPTH) {
-#pragma unroll
-    for (int d = 0; d < S::DEPTH; ++d) {
-      add_chunk<S, false>(acc, c[d], src, first + (i + d) * step);
-      if (i + d + S::DEPTH < n) load_chunk<S, false>(c[d], src, first + (i + d + S::DEPTH) * step);
-    }
+  for (int d = 0; d < S::DEPTH - 1; ++d) {
+    load_chunk<S>(src, ring + d * S::SLOT, ahead, d < n);
+    ahead = next_of(ahead);
   }
+  typedef const __attribute__((address_space(4))) float* Scalar;
+  int slot = 0, g0 = 0, g_end = 0;
+  const int last_half = (src.K - 1) >> 7, halves = S::HALVES;
+  const int g_first = group_of(src, halves * first, 0);
+  const int g_last = group_of(src, min(halves * end - 1, last_half), S::GPC - 1);
+  float next[S::CF];
+  if constexpr (S::FP8) {
 #pragma unroll
-  for (int d = 0; d < S::DEPTH; ++d)
-    if (i + d < n) add_chunk<S, false>(acc, c[d], src, first + (i + d) * step);
-  const int last = src.K >> 7;  // the partial chunk
-  if ((src.K & 127) && last < end && last >= first && (last - first) % step == 0) {
-    load_chunk<S, true>(c[0], src, last);
-    add_chunk<S, true>(acc, c[0], src, last);
+    for (int t = 0; t < S::CF; ++t) next[t] = *(Scalar)(src.fs[t] + c);
+  }
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    float fs[S::CF];
+    if constexpr (S::FP8) {
+#pragma unroll
+      for (int t = 0; t < S::CF; ++t) {
+        fs[t] = next[t];
+        next[t] = *(Scalar)(src.fs[t] + next_of(c));
+      }
+    } else {
+      const int lo = group_of(src, 2 * c, 0), hi = group_of(src, min(2 * c + 1, last_half), S::GPC - 1);
+      if (lo < g0 || hi >= g_end) {
+        // scales of the groups from here on, or of all: the ring fills meanwhile
+        g0 = g_last - g_first < S::SCALES ? g_first : lo;
+        g_end = g0 + S::SCALES;
+        load_scales<S>(src, scales, g0, min(g_last, src.groups - 1));
+      }
+    }
+    const int into = slot == 0 ? S::DEPTH - 1 : slot - 1;  // the slot read in the last turn
+    if constexpr (S::SHARE > 1) {
+      // every wave's loads of this chunk are done, and its reads of the last
+      wait_loads<(S::DEPTH - 2) * S::LOADS>();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    load_chunk<S>(src, ring + into * S::SLOT, ahead, i + S::DEPTH - 1 < n);
+    ahead = next_of(ahead);
+    if constexpr (S::SHARE == 1) wait_loads<(S::DEPTH - 1) * S::LOADS>();
+    add_chunk<S>(acc, src, ring + slot * S::SLOT, fs, scales, c, g0);
+    // the slot is loaded again in the next turn: its reads are done
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_sched_barrier(0);
+    slot = slot == S::DEPTH - 1 ? 0 : slot + 1;
+    c = next_of(c);
+  }
+  wait_loads<0>();
+  if constexpr (S::SHARE > 1) {
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// D = bf16(sums of parts, added in their order); partial: [parts][M][N].
+static __global__ __launch_bounds__(256) void join_parts_kernel(const float* partial, int parts, uint16_t* D, int64_t ldd,
+                                                                int M, int N) {
+  const int64_t all = (int64_t)M * N, step = (int64_t)gridDim.x * 1024;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all; i += step) {
+    const int64_t m = i / N;
+    const int n = (int)(i - m * N);
+    if (n + 4 <= N) {
+      f32x4 v = *(const f32x4_at4*)(partial + i);
+#pragma unroll 8
+      for (int s = 1; s < parts; ++s) v += *(const f32x4_at4*)(partial + s * all + i);
+      *(u32x2_at2*)(D + m * ldd + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    } else {
+      for (int64_t j = i; j < i + 4 && j < all; ++j) {
+        float v = partial[j];
+        for (int s = 1; s < parts; ++s) v += partial[s * all + j];
+        D[j / N * ldd + j % N] = bf16_bits(v);
+      }
+    }
   }
 }
 

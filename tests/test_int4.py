@@ -113,6 +113,45 @@ def test_product_of_whole_layers(gpu_lib, M, N, K, group):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("plan", ["split2", "split2deep", "split8", "split8deep", "split16", "split16deep", "wide16", "wide64",
+                                  "wide16,kparts3", "wide64,kparts5", "wide16,kparts8"])
+def test_every_plan(gpu_lib, monkeypatch, capfd, plan, group, zeros):
+    monkeypatch.setenv("FG_DECODE_PLAN", plan)
+    monkeypatch.setenv("FG_PRINT_CONFIGS", "1")
+    for M, N, K in ((1, 40, 96), (7, 130, 2208), (37, 131, 4128), (70, 33, 1056)):
+        check_product(gpu_lib, M, N, K, group, zeros, seed=M, pad=M % 2)
+    assert capfd.readouterr().err.count(" " + plan.split(",")[0] + " ") == 4
+
+
+@pytest.mark.gpu
+def test_workspace(gpu_lib):
+    """A product whose reduction is split: with a workspace, with one that holds NaN, with torch's, on another stream;
+    one that is too small or misaligned is refused."""
+    announce("int4 workspace")
+    M, N, K = 30, 512, 24576
+    need = gpu_lib.int4_workspace_bytes(M, N, K)
+    assert need >= 2 * M * N * 4 and gpu_lib.int4_workspace_bytes(1, N, K) == 0
+    q, s, z = weights(N, K, 128, True, 1)
+    B, sb, zb = to_gpu(q, s, z, True)
+    A = bf16(torch.randn(M, K, generator=torch.Generator().manual_seed(3))).cuda()
+    D = [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    gpu_lib.gemm_int4_nt(A, B, sb, D[0], zb=zb)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    gpu_lib.gemm_int4_nt(A, B, sb, D[1], zb=zb, workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    gpu_lib.gemm_int4_nt(A, B, sb, D[2], zb=zb, stream=side)
+    side.synchronize()
+    assert_within(f64(D[0]), *ref.gemm_int4(f64(A), q, s, z, 128), "split reduction")
+    assert torch.equal(D[0].view(torch.int16), D[1].view(torch.int16)) and torch.equal(D[0].view(torch.int16), D[2].view(torch.int16))
+    for bad in (ws[:need - 256], ws[16:]):
+        with pytest.raises(gpu_lib.FP8GemmError):
+            gpu_lib.gemm_int4_nt(A, B, sb, D[0], zb=zb, workspace=bad)
+
+
+@pytest.mark.gpu
 def test_empty_and_no_reduction(gpu_lib):
     announce("int4 empty")
     bf = dict(dtype=torch.bfloat16, device="cuda")
@@ -169,8 +208,9 @@ def test_offsets_past_32_bits(gpu_lib, N, K):
     assert (D[:, :-48] == 0).all()
 
 
-def product_call(lib, A=0x10000, lda=512, B=0x10000, s=0x10000, z=None, D=0x10000, ldd=64, M=4, N=64, K=512, group=128):
-    return lib.gemm_int4_nt(A, lda, B, s, z, D, ldd, M, N, K, group, None)
+def product_call(lib, A=0x10000, lda=512, B=0x10000, s=0x10000, z=None, D=0x10000, ldd=64, M=4, N=64, K=512, group=128, ws=None,
+                 nbytes=0):
+    return lib.gemm_int4_nt(A, lda, B, s, z, D, ldd, M, N, K, group, ws, nbytes, None)
 
 
 @pytest.mark.parametrize("kw,status,needle", [
@@ -180,6 +220,8 @@ def product_call(lib, A=0x10000, lda=512, B=0x10000, s=0x10000, z=None, D=0x1000
     (dict(A=0x10008), 2, "A is not"), (dict(B=0x10008), 2, "B is not"), (dict(s=0x10001), 2, "sb"), (dict(D=0x10001), 2, "D"),
     (dict(lda=511), 1, "lda=511"), (dict(lda=516), 2, "lda=516"), (dict(ldd=63), 1, "ldd=63"),
     (dict(lda=(1 << 21) + 8), 3, "4 MiB"), (dict(K=(1 << 20) + 32, lda=1 << 21), 3, "K="), (dict(M=(1 << 30) + 1), 3, "2^30"),
+    (dict(nbytes=-1), 1, "negative"), (dict(nbytes=64), 1, "workspace is NULL"), (dict(ws=0x10010, nbytes=64), 2, "256-byte"),
+    (dict(M=32, N=512, ldd=512, K=24576, lda=24576), 1, "smaller than the"),
     (dict(M=0, A=None, B=None, s=None, D=None), 0, ""), (dict(N=0, A=None, B=None, s=None, D=None), 0, "")])
 def test_product_refusals(kw, status, needle):
     import moe_grouped_gemm_e4m3_amd as fg

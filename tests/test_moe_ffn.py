@@ -105,6 +105,29 @@ def test_layer(gpu_lib, fmt, T, E, k, F, K):
           offset=T % 2)
 
 
+UPS = ["up-split4", "up-split4-two", "up-split16", "up-wide", "up-wide-deep", "up-wide8"]
+DOWNS = ["down-split1", "down-split1-two", "down-split4", "down-split4-two", "down-wide16", "down-wide16-deep", "down-wide32"]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FORMATS, ids=str)
+@pytest.mark.parametrize("plan", UPS + DOWNS + ["down-wide16,one-part", "down-wide32,one-part"])
+def test_every_plan(gpu_lib, monkeypatch, capfd, fmt, plan):
+    """Each kernel of either half, at sizes that end inside its tiles, with experts of one token and of more than one tile."""
+    monkeypatch.setenv("FG_DECODE_PLAN", plan)
+    monkeypatch.setenv("FG_PRINT_CONFIGS", "1")
+    sizes = [(1, 3, 2, 160, 288), (13, 3, 2, 1056, 416), (64, 2, 1, 352, 160), (70, 4, 3, 96, 544)]
+    if plan == "down-split1-two":
+        sizes = sizes[:2]
+    for T, E, k, F, K in sizes:
+        check(gpu_lib, Layer(fmt, E, F, K, seed=T), T, k, pad=T % 2)
+    ran = capfd.readouterr().err
+    has = {"up-split4-two": fmt != "fp8", "up-wide8": fmt != "fp8", "down-split4-two": fmt != "fp8", "up-wide-deep": fmt == "fp8",
+           "down-split1-two": fmt == "fp8", "down-wide16-deep": fmt == "fp8"}
+    if has.get(plan.split(",")[0], True):
+        assert ran.count(plan.split(",")[0] + " ") >= len(sizes)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,E,k,F,K", [(1, 2, 1, 16, 16), (3, 4, 2, 48, 80), (20, 3, 2, 176, 144), (64, 2, 2, 208, 336)])
 def test_fp8_columns_of_16(gpu_lib, T, E, k, F, K):
@@ -297,7 +320,7 @@ def test_decode_step_in_a_graph(gpu_lib, fmt):
 
 
 def call(lib, fmt="fp8", X=0x10000, ldx=64, W1=0x10000, s1=0x10000, W2=0x10000, s2=0x10000, ids=0x10000, w=0x10000, D=0x10000,
-         ldd=64, T=4, k=2, E=4, F=64, K=64, act=0, ws=0x10000, nbytes=1 << 20, group=128):
+         ldd=64, T=4, k=2, E=4, F=64, K=64, act=0, ws=0x10000, nbytes=1 << 22, group=128):
     if fmt == "fp8":
         return lib.moe_ffn_fp8(X, ldx, W1, s1, W2, s2, ids, w, D, ldd, T, k, E, F, K, act, ws, nbytes, None)
     return lib.moe_ffn_int4(X, ldx, W1, s1, None, W2, s2, None, ids, w, D, ldd, T, k, E, F, K, group, act, ws, nbytes, None)
@@ -312,7 +335,7 @@ def call(lib, fmt="fp8", X=0x10000, ldx=64, W1=0x10000, s1=0x10000, W2=0x10000, 
     (dict(X=0x10008), 2, "X is not"), (dict(W1=0x10008), 2, "W1 is not"), (dict(W2=0x10004), 2, "W2 is not"),
     (dict(s1=0x10001), 2, "s1"), (dict(ids=0x10002), 2, "ids"), (dict(w=0x10002), 2, "weights"), (dict(D=0x10001), 2, "D is not"),
     (dict(ldx=56), 1, "ldx=56"), (dict(ldx=68), 2, "ldx=68"), (dict(ldd=63), 1, "ldd=63"), (dict(ldx=(1 << 21) + 8), 3, "4 MiB"),
-    (dict(ws=None), 1, "workspace is NULL"), (dict(ws=0x10010), 2, "workspace"), (dict(nbytes=2047), 1, "smaller than the 2048"),
+    (dict(ws=None), 1, "workspace is NULL"), (dict(ws=0x10010), 2, "workspace"), (dict(nbytes=2099199), 1, "smaller than the 2099200"),
     (dict(nbytes=-1), 1, "negative"), (dict(E=1025), 3, "E=1025"), (dict(k=33), 3, "k=33"), (dict(T=(1 << 20) + 1), 3, "T=1048577"),
     (dict(K=65568, ldx=65568, ldd=65568), 3, "K=65568"), (dict(F=65568), 3, "F=65568"),
     (dict(T=0, X=None, W1=None, W2=None, D=None, ids=None, w=None, ws=None, nbytes=0), 0, "")])
@@ -331,8 +354,10 @@ def test_group_refusals_and_workspace_query():
     for group in (0, 16, 48, 192, -32):
         assert call(lib, "int4", group=group) == 1 and "group" in lib.fg_last_error().decode()
     assert call(lib, "int4", K=48) == 2
-    assert fg.moe_ffn_workspace_bytes(3, 2, 64) == 3 * 2 * 64 * 4
-    assert fg.moe_ffn_workspace_bytes(1 << 20, 32, 1 << 16) == 1 << 43
+    # hidden units (two bf16 each, rounded to 256 bytes), and half a MiB of partial sums for each of up to 64 tokens
+    assert fg.moe_ffn_workspace_bytes(1, 3, 16) == 256
+    assert fg.moe_ffn_workspace_bytes(3, 2, 64) == 3 * 2 * 64 * 4 + (3 << 19)
+    assert fg.moe_ffn_workspace_bytes(1 << 20, 32, 1 << 16) == (1 << 43) + (64 << 19)
     for bad in ((-1, 2, 64), (1, -1, 64), (1, 2, -64), ((1 << 20) + 1, 1, 64), (1, 33, 64), (1, 1, (1 << 16) + 16)):
         with pytest.raises(ValueError):
             fg.moe_ffn_workspace_bytes(*bad)
