@@ -12,8 +12,8 @@
 // A wave takes a token, a lane the experts lane, lane + 64, ...  Scores, what
 // decides between experts, and sums are in 64 bits: the choice is then that of
 // the formula wherever two experts differ by more than 1e-15, and the work is
-// still small (a token's scores are read once; the kernels are bound by the
-// latency of k rounds of finding the largest).
+// still small (a token's scores are read once).  Bound by latency: two loads, an
+// exponential, and k rounds of finding the largest.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -40,15 +40,66 @@ struct RouteParams {
 // In the place of a NaN where experts are compared: below every score, above "no candidate".
 constexpr double kLast = -1e300;
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-  return v;
+// Reductions over the wave's lanes by data-parallel moves: lanes of a row, then
+// rows, into lane 63 (an exchange through LDS costs five times as much).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t lane_move(uint32_t v, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false);
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lane_move(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = lane_move<CTRL, ROWS>((uint32_t)b, 0u), hi = lane_move<CTRL, ROWS>((uint32_t)(b >> 32), 0u);
+  return __builtin_bit_cast(double, lo | hi << 32);
+}
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+__device__ __forceinline__ double from_lane(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t lo = from_lane((uint32_t)b, lane), hi = from_lane((uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, lo | hi << 32);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += lane_move<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
+  v += lane_move<0x112, 0xf>(v);
+  v += lane_move<0x114, 0xf>(v);
+  v += lane_move<0x118, 0xf>(v);
+  v += lane_move<0x142, 0xa>(v);  // the last lane of rows 0 and 2 to the next row
+  v += lane_move<0x143, 0xc>(v);  // lane 31 to rows 2 and 3
+  return from_lane(v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, lane_move<0x111, 0xf>(v, 0u));
+  v = max(v, lane_move<0x112, 0xf>(v, 0u));
+  v = max(v, lane_move<0x114, 0xf>(v, 0u));
+  v = max(v, lane_move<0x118, 0xf>(v, 0u));
+  v = max(v, lane_move<0x142, 0xa>(v, 0u));
+  v = max(v, lane_move<0x143, 0xc>(v, 0u));
+  return from_lane(v, 63);
+}
+
+// The value of lane ^ D's group of D lanes, in which all lanes hold the same.
+template <int D>
+__device__ __forceinline__ double other_group(double v) {
+  if (D == 1) return lane_move<0xb1, 0xf>(v);   // quad_perm 1 0 3 2
+  if (D == 2) return lane_move<0x4e, 0xf>(v);   // quad_perm 2 3 0 1
+  if (D == 4) return lane_move<0x141, 0xf>(v);  // mirrored halves of a row
+  if (D == 8) return lane_move<0x140, 0xf>(v);  // mirrored row
+  return __shfl_xor(v, D);
+}
+
+// Integers that order as the numbers do, above 0; a NaN stands in the place of
+// -infinity, below all numbers.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return v != v ? 0x007fffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t order_of(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return b >> 63 ? ~b : b | (uint64_t)1 << 63;
+}
+__device__ __forceinline__ float wave_max_logit(float v) {
+  const uint32_t b = wave_max(order_of(v));
+  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
 }
 __device__ __forceinline__ double sigmoid64(double l) { return 1.0 / (1.0 + exp(-l)); }
 
@@ -60,7 +111,14 @@ __device__ __forceinline__ void merge_two(double& a, double& b, double c, double
   b = b < low ? low : b;
 }
 
-// SLOTS: experts of a lane.  SCORED: a bias or groups, so that scores decide; else the logits do.
+template <int D>
+__device__ __forceinline__ void merge_groups(double& a, double& b) {
+  const double c = other_group<D>(a), d = other_group<D>(b);
+  merge_two(a, b, c, d);
+}
+
+// SLOTS: experts of a lane.  SCORED: a bias or groups, so that scores decide
+// (in 64 bits); else the logits do.
 template <typename L, int SLOTS, bool SCORED>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p) {
   __shared__ double by_expert[SCORED ? kRouteWaves : 1][SCORED ? 64 * SLOTS : 1];
@@ -69,104 +127,137 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteParams p) 
   const double none = -__builtin_inf();
   if (t >= p.T) return;
   const L* row = (const L*)p.logits + t * p.ld;
-  float l[SLOTS];
+  float l[SLOTS], bias[SLOTS];
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) {
     const int e = lane + 64 * s;
     l[s] = e < p.E ? to_f32(row[e]) : -__builtin_inff();
+    bias[s] = SCORED && p.bias && e < p.E ? p.bias[e] : 0.f;
   }
-  // softmax: the largest logit and the sum over all experts
+  // softmax: the largest logit and the sum over all experts, which cancels where
+  // the chosen scores are divided by their sum (but for a NaN)
   float top = 0.f;
-  double sum = 1.0;
+  double scale = 1.0;
   if (!p.sigmoid) {
     top = l[0];
+    bool nan = l[0] != l[0];
 #pragma unroll
-    for (int s = 1; s < SLOTS; ++s) top = fmaxf(top, l[s]);
-    top = wave_max(top);
+    for (int s = 1; s < SLOTS; ++s) {
+      top = fmaxf(top, l[s]);
+      nan |= l[s] != l[s];
+    }
+    top = wave_max_logit(top);
     if (top == -__builtin_inff()) top = 0.f;
-    sum = 0.0;
+    if (__any(nan)) {
+      scale = __builtin_nan("");
+    } else if (SCORED || !p.normalize) {
+      double sum = 0.0;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s)
-      if (lane + 64 * s < p.E) sum += exp((double)l[s] - (double)top);
-    sum = wave_sum(sum);
+      for (int s = 0; s < SLOTS; ++s)
+        if (lane + 64 * s < p.E) sum += exp((double)l[s] - (double)top);
+      sum = wave_sum(sum);
+      scale = sum == 0.0 ? 0.0 : 1.0 / sum;
+    }
   }
-  auto score = [&](float x) {
-    return p.sigmoid ? sigmoid64(x) : sum == 0.0 ? 0.0 : exp((double)x - (double)top) / sum;
-  };
-  double by[SLOTS];
-#pragma unroll
-  for (int s = 0; s < SLOTS; ++s) {
-    const int e = lane + 64 * s;
-    double v = l[s];
-    if (SCORED && l[s] != -__builtin_inff()) {
-      v = score(l[s]);
-      if (p.bias) v += p.bias[e];
-    }
-    by[s] = v != v ? kLast : v;
-  }
-  if (SCORED && p.groups > 1) {
-    // groups' sums of their two best: each group has a power of two of lanes
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s) by_expert[wave][lane + 64 * s] = by[s];
-    __builtin_amdgcn_wave_barrier();
-    int per = 64;
-    while (per * p.groups > 64) per >>= 1;
-    const int size = p.E / p.groups, g = lane / per, l0 = lane - g * per;
-    double a = none, b = none;
-    if (g < p.groups)
-      for (int i = l0; i < size; i += per) merge_two(a, b, by_expert[wave][g * size + i], none);
-    for (int d = 1; d < per; d *= 2) {
-      const double c = __shfl_xor(a, d), e = __shfl_xor(b, d);
-      merge_two(a, b, c, e);
-    }
-    const double total = a == none ? none : a + (b == none ? 0.0 : b);
-    int rank = 0;
-    for (int o = 0; o < p.groups; ++o) {
-      const double other = __shfl(total, o * per);
-      rank += other > total || (other == total && o < g);
-    }
-    const unsigned long long kept = __ballot(g < p.groups && rank < p.top);
+  auto score = [&](float x) { return p.sigmoid ? sigmoid64(x) : exp((double)x - (double)top) * scale; };
+  // what experts are compared by: 32 bits, and where these are equal 32 more;
+  // 0: no candidate (every candidate's upper bits are above 0)
+  uint32_t key[SLOTS], low[SCORED ? SLOTS : 1];
+  double sc[SCORED ? SLOTS : 1];
+  if constexpr (SCORED) {
+    double by[SLOTS];
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const int e = lane + 64 * s;
-      if (e < p.E && !((kept >> (e / size * per)) & 1)) by[s] = none;
+      sc[s] = 0.0;
+      by[s] = none;
+      if (l[s] != -__builtin_inff()) {
+        sc[s] = score(l[s]);
+        by[s] = p.bias ? sc[s] + bias[s] : sc[s];
+      }
+      if (by[s] != by[s]) by[s] = kLast;
     }
+    if (p.groups > 1) {
+      // groups' sums of their two best: each group has a power of two of lanes
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) by_expert[wave][lane + 64 * s] = by[s];
+      __builtin_amdgcn_wave_barrier();
+      int per = 64;
+      while (per * p.groups > 64) per >>= 1;
+      const int size = p.E / p.groups, g = lane / per, l0 = lane - g * per;
+      double a = none, b = none;
+      if (g < p.groups)
+        for (int i = l0; i < size; i += per) merge_two(a, b, by_expert[wave][g * size + i], none);
+      if (per > 1) merge_groups<1>(a, b);
+      if (per > 2) merge_groups<2>(a, b);
+      if (per > 4) merge_groups<4>(a, b);
+      if (per > 8) merge_groups<8>(a, b);
+      if (per > 16) merge_groups<16>(a, b);
+      if (per > 32) merge_groups<32>(a, b);
+      const double total = a == none ? none : a + (b == none ? 0.0 : b);
+      int rank = 0;
+      for (int o = 0; o < p.groups; ++o) {
+        const double other = from_lane(total, o * per);
+        rank += other > total || (other == total && o < g);
+      }
+      const unsigned long long kept = __ballot(g < p.groups && rank < p.top);
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        const int e = lane + 64 * s;
+        if (e < p.E && !((kept >> (e / size * per)) & 1)) by[s] = none;
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const uint64_t o = by[s] == none ? 0 : order_of(by[s]);
+      key[s] = (uint32_t)(o >> 32);
+      low[s] = (uint32_t)o;
+      by_expert[wave][lane + 64 * s] = sc[s];
+    }
+    __builtin_amdgcn_wave_barrier();
+  } else {
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) key[s] = l[s] == -__builtin_inff() ? 0 : order_of(l[s]);
   }
   // k rounds of finding the largest; equal ones go to the lowest expert
   int chosen = -1;
-  float logit = 0.f;
   for (int j = 0; j < p.k; ++j) {
-    double best = by[0];
-    int at = lane;
-    float x = l[0];
+    uint32_t best = key[0];
 #pragma unroll
-    for (int s = 1; s < SLOTS; ++s)
-      if (by[s] > best) {
-        best = by[s];
-        at = lane + 64 * s;
-        x = l[s];
-      }
+    for (int s = 1; s < SLOTS; ++s) best = max(best, key[s]);
+    best = wave_max(best);
+    if (best == 0) break;  // no candidate is left
+    // the lanes and slots that hold it: usually one
+    unsigned long long held[SLOTS];
+    int count = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const double v = __shfl_xor(best, d);
-      const int o = __shfl_xor(at, d);
-      const bool take = v > best || (v == best && o < at);
-      best = take ? v : best;
-      at = take ? o : at;
+    for (int s = 0; s < SLOTS; ++s) {
+      held[s] = __ballot(key[s] == best);
+      count += __builtin_popcountll(held[s]);
     }
-    if (best == none) break;  // no candidate is left
-    const float won = __shfl(x, at & 63);
-    if (lane == j) {
-      chosen = at;
-      logit = won;
-    }
-    if (lane == (at & 63)) {
+    if (SCORED && count > 1) {
+      uint32_t lo = 0;
 #pragma unroll
-      for (int s = 0; s < SLOTS; ++s)
-        if (s == at >> 6) by[s] = none;
+      for (int s = 0; s < SLOTS; ++s) lo = key[s] == best ? max(lo, low[s]) : lo;
+      lo = wave_max(lo);
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) held[s] = __ballot(key[s] == best && low[s] == lo);
     }
+    int e = 0;
+#pragma unroll
+    for (int s = SLOTS - 1; s >= 0; --s)
+      if (held[s]) e = 64 * s + __builtin_ctzll(held[s]);
+    if (lane == j) chosen = e;
+    const int mine = e - lane;  // 64 s for the lane and slot that hold it
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) key[s] = mine == 64 * s ? 0 : key[s];
   }
-  double share = chosen >= 0 ? score(logit) : 0.0;
+  double share = 0.0;
+  if (chosen >= 0) {
+    if constexpr (SCORED)
+      share = by_expert[wave][chosen];
+    else
+      share = score(to_f32(row[chosen]));
+  }
   if (p.normalize) {
     const double all = wave_sum(share);
     share = all == 0.0 ? 0.0 : share / all;
@@ -202,29 +293,36 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteG
   const bool there = (unsigned)id < (unsigned)p.E;
   const double g = there ? (double)p.dw[t * p.k + lane] * p.scale : 0.0;
   const float x = there ? to_f32(row[id]) : 0.f;
-  float l[SLOTS];
+  // softmax: the largest logit and the sum over all experts; normalised, the sum
+  // cancels (but for a NaN)
+  double e[SLOTS];
   float top = 0.f;
-  double sum = 1.0;
+  double scale = 1.0;
   const bool dense = !p.sigmoid && !p.normalize;
   if (!p.sigmoid) {
+    float l[SLOTS];
+    bool nan = false;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const int e = lane + 64 * s;
-      l[s] = e < p.E ? to_f32(row[e]) : -__builtin_inff();
+      l[s] = lane + 64 * s < p.E ? to_f32(row[lane + 64 * s]) : -__builtin_inff();
       top = s == 0 ? l[0] : fmaxf(top, l[s]);
+      nan |= l[s] != l[s];
     }
-    top = wave_max(top);
+    top = wave_max_logit(top);
     if (top == -__builtin_inff()) top = 0.f;
-    sum = 0.0;
+    if (__any(nan)) scale = __builtin_nan("");
+    if (dense) {
+      double sum = 0.0;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s)
-      if (lane + 64 * s < p.E) sum += exp((double)l[s] - (double)top);
-    sum = wave_sum(sum);
+      for (int s = 0; s < SLOTS; ++s) {
+        e[s] = lane + 64 * s < p.E ? exp((double)l[s] - (double)top) : 0.0;
+        sum += e[s];
+      }
+      sum = wave_sum(sum);
+      scale = sum == 0.0 ? 0.0 : 1.0 / sum;
+    }
   }
-  auto score = [&](float v) {
-    return p.sigmoid ? sigmoid64(v) : sum == 0.0 ? 0.0 : exp((double)v - (double)top) / sum;
-  };
-  const double s_j = there ? score(x) : 0.0;
+  const double s_j = !there ? 0.0 : p.sigmoid ? sigmoid64(x) : exp((double)x - (double)top) * scale;
   double q = s_j;
   if (p.normalize) {
     const double all = wave_sum(s_j);
@@ -237,13 +335,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteG
   L* out = (L*)p.dl + t * p.ld_dl;
   double dl[SLOTS];
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) dl[s] = dense && lane + 64 * s < p.E ? -score(l[s]) * mean : 0.0;
+  for (int s = 0; s < SLOTS; ++s) dl[s] = dense ? -(e[s] * scale) * mean : 0.0;
   for (int j = 0; j < p.k; ++j) {
-    const int e = __shfl(id, j);
-    const double v = __shfl(d, j);
+    const int to = (int)from_lane((uint32_t)id, j) - lane;
+    const double v = from_lane(d, j);
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s)
-      if (e == lane + 64 * s) dl[s] += v;
+      if (to == 64 * s) dl[s] += v;
   }
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s)
