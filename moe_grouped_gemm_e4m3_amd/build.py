@@ -31,16 +31,17 @@ HIPCC_FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
-# Sources and their own options.  The fp32-factor kernels keep MFMA results in
-# VGPRs (the promotion FMAs read them directly); the power-of-two-factor
+# Sources and their own options.  The fp32-factor kernels and the streams of
+# few-token weights keep MFMA results in VGPRs (the FMAs that scale them read
+# them directly); the power-of-two-factor
 # kernel accumulates in the matrix core and is built without that option, so
 # its accumulators go to the accumulation registers.
 SOURCES = [
     ("fp8gemm.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
     ("ue8m0.hip", []),
     ("linear.hip", []),
-    ("int4.hip", []),
-    ("experts.hip", []),
+    ("int4.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
+    ("experts.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"]),
 ]
 
 

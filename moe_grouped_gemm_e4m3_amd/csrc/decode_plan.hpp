@@ -94,6 +94,8 @@ struct LayerPlan {
   DownKind down;
   int parts;  // wide down: parts of the experts' chunks, joined by a third kernel
 };
+// LDS bytes of what `down` knows of a pass's pairs (experts_kernel.hpp).
+inline int pairs_bytes(int E, int T, int k) { return E * 12 + T * k * 6 + 4; }
 inline bool wide_down(DownKind k) { return k >= kDownWide16; }
 
 inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const char* forced) {
@@ -124,7 +126,7 @@ inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const c
     p.down = fp8 && K > 4096 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
   else if (T <= 4 || small)
     p.down = !fp8 && K > 4096 ? kDownSplit4Two : kDownSplit4;  // T=2, 4-bit, 7168 x 2048: 38 for 43; 4096 x 2048: 24 for 15
-  else if (pairs > 8 * E)
+  else if (pairs > 8 * E && (fp8 || pairs_bytes(E, T, k) <= 12 << 10))  // (4 bits: the rest of LDS is taken)
     p.down = kDownWide32;  // T=64, 32 tokens an expert: 122 for 149; 6 tokens: 43 for 40
   else
     p.down = fp8 && T > 16 ? kDownWide16Deep : kDownWide16;  // T=64, 8 tokens an expert: 66 for 83

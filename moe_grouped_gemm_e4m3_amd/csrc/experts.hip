@@ -125,7 +125,7 @@ fg_status route_backward(const float* dw, const L* logits, int64_t ld, const int
 
 // More than 64 KiB of dynamic LDS has to be asked for.
 fg_status allow_lds(const void* kernel, int bytes, const char* what) {
-  if (bytes + (int)sizeof(Pairs) > 160 * 1024) return set_error(FG_EUNSUPPORTED, "%s: %d bytes of LDS", what, bytes);
+  if (bytes > 160 * 1024) return set_error(FG_EUNSUPPORTED, "%s: %d bytes of LDS", what, bytes);
   const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return set_error(FG_EHIP, "%s: %d bytes of LDS: %s", what, bytes, hipGetErrorString(e));
   return FG_OK;
@@ -161,7 +161,7 @@ struct LayerLaunch {
 
   template <class C>
   fg_status down() const {
-    const int lds = C::lds_bytes(std::min(p.T, kLayerTokens));
+    const int T = std::min(p.T, kLayerTokens), lds = C::lds_bytes(T) + pairs_bytes(p.E, T, p.k);
     FG_TRY(allow_lds((const void*)experts_down_kernel<C>, lds, what));
     print("down", kDownNames[plan.down], 1);
     hipLaunchKernelGGL((experts_down_kernel<C>), dim3(ceil_div(p.K, C::COLS), passes), dim3(C::THREADS), lds,
@@ -172,7 +172,7 @@ struct LayerLaunch {
   // A pass of tokens at a time: they share the partial sums' place.
   template <class C>
   fg_status down_wide() const {
-    const int lds = C::lds_bytes(std::min(p.T, kLayerTokens));
+    const int most = std::min(p.T, kLayerTokens), lds = C::lds_bytes(most) + pairs_bytes(p.E, most, p.k);
     FG_TRY(allow_lds((const void*)experts_wide_down_kernel<C>, lds, what));
     for (int t0 = 0; t0 < p.T; t0 += kLayerTokens) {
       const int T = std::min(kLayerTokens, p.T - t0);

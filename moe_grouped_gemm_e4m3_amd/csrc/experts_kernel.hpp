@@ -165,11 +165,17 @@ __device__ __forceinline__ int expert_tokens(const ExpertParams& p, int t0, int&
     e = load_invariant(ids + blockIdx.y);
     if ((unsigned)e >= (unsigned)p.E) return 0;
   }
-  // the first of this lane's token's places that name e
+  // the first of this lane's token's places that name e; ids come eight at a time
   int place = -1;
   if (lane < T)
-    for (int j = p.k - 1; j >= 0; --j)
-      if (ids[lane * p.k + j] == e) place = j;
+    for (int j0 = (p.k - 1) & ~7; j0 >= 0; j0 -= 8) {
+      int id[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) id[j] = ids[lane * p.k + min(j0 + j, p.k - 1)];
+#pragma unroll
+      for (int j = 7; j >= 0; --j)
+        if (id[j] == e) place = min(j0 + j, p.k - 1);
+    }
   const unsigned long long mask = __ballot(place >= 0);
   if (mask == 0) return 0;
   if (p.by_pair) {
@@ -278,28 +284,52 @@ struct DownTile {
   static int lds_bytes(int T) { return WAVES * (WAVE_LDS + T * COLS * 4); }
 };
 
-// What `down` knows of the pairs: the experts with tokens, in order.
+// What `down` knows of the pairs, in dynamic LDS: the experts with tokens, and
+// for each its tokens in order, with the first place that names it and the
+// weights of all such places.
 struct Pairs {
-  unsigned long long tokens[kMaxExperts];  // that go to an expert
-  uint16_t item_expert[kMaxExperts], item_start[kMaxExperts + 1];
-  int items;
+  unsigned long long* tokens;  // [E] that go to an expert
+  float* weight;               // [T k]
+  int* items;                  // [1] experts with tokens
+  uint16_t *expert;            // [min(E, T k)] of an item
+  uint16_t *start;             // [E] of its tokens in `weight` and `pair`
+  uint16_t *pair;              // [T k]: t k + j
 };
+__device__ __forceinline__ Pairs pairs_at(uint8_t* lds, int E, int n) {
+  Pairs s;
+  s.tokens = (unsigned long long*)lds;
+  s.weight = (float*)(s.tokens + E);
+  s.items = (int*)(s.weight + n);
+  s.expert = (uint16_t*)(s.items + 1);
+  s.start = s.expert + E;
+  s.pair = s.start + E;
+  return s;
+}
 
-__device__ __forceinline__ void sort_pairs(Pairs& s, const ExpertParams& p, const int32_t* ids, int T) {
-  const int tid = threadIdx.x, lane = tid & 63;
+__device__ __forceinline__ void sort_pairs(const Pairs& s, const ExpertParams& p, int t0, int T) {
+  const int tid = threadIdx.x, lane = tid & 63, n = T * p.k;
+  const int32_t* ids = p.ids + (int64_t)t0 * p.k;
+  const float* weights = p.w + (int64_t)t0 * p.k;
   for (int i = tid; i < p.E; i += blockDim.x) s.tokens[i] = 0;
+  if (tid == 0) *s.items = 0;
   __syncthreads();
-  for (int i = tid; i < T * p.k; i += blockDim.x) {
+  bool twice = false;
+  for (int i = tid; i < n; i += blockDim.x) {
     const int e = ids[i];
-    if ((unsigned)e < (unsigned)p.E) atomicOr(&s.tokens[e], 1ull << (i / p.k));
+    const unsigned long long bit = 1ull << (i / p.k);
+    if ((unsigned)e < (unsigned)p.E) twice |= (atomicOr(&s.tokens[e], bit) & bit) != 0;
   }
+  if (twice) *s.items = 1;  // some token names an expert twice
+  __syncthreads();
+  twice = *s.items != 0;
   __syncthreads();
   if (tid < 64) {
-    int n = 0, start = 0;
+    int count = 0, start = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       const int e = e0 + lane;
       const int members = e < p.E ? __builtin_popcountll(s.tokens[e]) : 0;
       const unsigned long long any = __ballot(members > 0);
+      if (any == 0) continue;
       int before = members;  // inclusive sum over the lanes
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) {
@@ -307,72 +337,77 @@ __device__ __forceinline__ void sort_pairs(Pairs& s, const ExpertParams& p, cons
         if (lane >= d) before += o;
       }
       if (members > 0) {
-        const int at = n + __builtin_popcountll(any & ((1ull << lane) - 1));
-        s.item_expert[at] = (uint16_t)e;
-        s.item_start[at] = (uint16_t)(start + before - members);
+        s.expert[count + __builtin_popcountll(any & ((1ull << lane) - 1))] = (uint16_t)e;
+        s.start[e] = (uint16_t)(start + before - members);
       }
-      n += __builtin_popcountll(any);
+      count += __builtin_popcountll(any);
       start += __builtin_amdgcn_readlane(before, 63);
     }
-    if (lane == 0) {
-      s.items = n;
-      s.item_start[n] = (uint16_t)start;
+    if (lane == 0) *s.items = count;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += blockDim.x) {
+    const int e = ids[i], t = i / p.k;
+    if ((unsigned)e >= (unsigned)p.E) continue;
+    float w = weights[i];
+    if (twice) {
+      bool first = true;
+      for (int j = t * p.k; j < i; ++j) first &= ids[j] != e;
+      if (!first) continue;
+      for (int j = i + 1; j < (t + 1) * p.k; ++j)
+        if (ids[j] == e) w += weights[j];
     }
+    const int at = s.start[e] + __builtin_popcountll(s.tokens[e] & ((1ull << t) - 1));
+    s.pair[at] = (uint16_t)i;
+    s.weight[at] = w;
   }
   __syncthreads();
 }
 
-// The r-th token of a set: its first place that names expert e, and the weights
-// of all such places.
+// Token r of an item.
 struct Member {
-  int token, place;
+  int token, pair;
   float w;
 };
-__device__ __forceinline__ Member member(const ExpertParams& p, const int32_t* ids, const float* weights,
-                                         unsigned long long set, int e, int r) {
-  for (; r > 0; --r) set &= set - 1;
-  Member m{__builtin_ctzll(set), -1, 0.f};
-  for (int j = 0; j < p.k; ++j)
-    if (ids[m.token * p.k + j] == e) {
-      const float w = weights[m.token * p.k + j];
-      m.w = m.place < 0 ? w : m.w + w;
-      if (m.place < 0) m.place = j;
-    }
-  return m;
+__device__ __forceinline__ Member member(const ExpertParams& p, const Pairs& s, int e, int r) {
+  const int at = s.start[e] + r;
+  return Member{s.pair[at] / p.k, s.pair[at], s.weight[at]};
 }
 
 // Grid: tiles of COLS outputs, passes of 64 tokens.
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  __shared__ Pairs pairs;
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int t0 = blockIdx.y * kLayerTokens, T = min(kLayerTokens, p.T - t0);
-  const int32_t* ids = p.ids + (int64_t)t0 * p.k;
-  const float* weights = p.w + (int64_t)t0 * p.k;
   const int n0 = blockIdx.x * C::COLS;
   float* sums = (float*)(lds + C::WAVES * C::WAVE_LDS);  // [WAVES][T][COLS]
+  const Pairs pairs = pairs_at((uint8_t*)(sums + C::WAVES * T * C::COLS), p.E, T * p.k);
   for (int i = tid; i < C::WAVES * T * C::COLS; i += C::THREADS) sums[i] = 0.f;
-  sort_pairs(pairs, p, ids, T);
+  sort_pairs(pairs, p, t0, T);
 
   using S = Stream<typename C::Fmt, 1, x_kib<typename C::Fmt, 2>(C::MOST), C::CF, 1, 2, C::RING>;
   const int chunks = (p.F + S::COLS - 1) / S::COLS;
-  const int total = pairs.items * chunks;
-  int at = (int)((int64_t)total * wave / C::WAVES);
-  const int end = (int)((int64_t)total * (wave + 1) / C::WAVES);
+  const int items = __builtin_amdgcn_readfirstlane(*pairs.items), total = items * chunks;
+  int at = (int)((int64_t)total * wave / C::WAVES), end = (int)((int64_t)total * (wave + 1) / C::WAVES);
+  if (items <= C::WAVES) {
+    // every wave inside an item: a second one would cost another wait for its first weights
+    const int each = items > 0 ? C::WAVES / items : 1, item = wave / each, part = wave - item * each;
+    at = item < items ? item * chunks + chunks * part / each : 0;
+    end = item < items ? item * chunks + chunks * (part + 1) / each : 0;
+  }
   float* mine = sums + wave * T * C::COLS;
   uint8_t* ring = lds + wave * C::WAVE_LDS;
   while (at < end) {
     const int item = __builtin_amdgcn_readfirstlane(at / chunks), c0 = at - item * chunks;
     const int c1 = min(chunks, c0 + end - at);
     at += c1 - c0;
-    const int e = __builtin_amdgcn_readfirstlane(pairs.item_expert[item]);
-    const int start = __builtin_amdgcn_readfirstlane(pairs.item_start[item]);
-    const int members = __builtin_amdgcn_readfirstlane(pairs.item_start[item + 1]) - start;
+    const int e = __builtin_amdgcn_readfirstlane(pairs.expert[item]);
+    const int members = __builtin_amdgcn_readfirstlane(__builtin_popcountll(pairs.tokens[e]));
     for (int base = 0; base < members; base += C::MOST) {
       const int rows = min(C::MOST, members - base);
-      const Member me = member(p, ids, weights, pairs.tokens[e], e, base + min(l16, rows - 1));
+      const Member me = member(p, pairs, e, base + min(l16, rows - 1));
       Sources<S> src;
       src.K = p.F;
       set_group(src, p.group);
@@ -381,7 +416,7 @@ __global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p
 #pragma unroll
       for (int i = 0; i < S::X_LOADS; ++i) {
         const int r = min(x_row_of<S>(i), rows - 1);
-        src.x_off[i] = __shfl(me.token * p.k + me.place, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
+        src.x_off[i] = __shfl(me.pair, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
       }
       f32x4 acc[S::MT][S::CF];
       clear<S>(acc);
@@ -422,15 +457,14 @@ struct WideDown {
 };
 
 template <class C, int ROWS>
-__device__ __forceinline__ void wide_down_item(const ExpertParams& p, const int32_t* ids, const float* weights, int t0, int T,
-                                               unsigned long long set, int e, int base, int members, int n0, int c0, int c1,
+__device__ __forceinline__ void wide_down_item(const ExpertParams& p, const Pairs& pairs, int t0, int T, int e, int base, int members, int n0, int c0, int c1,
                                                uint8_t* ring, uint8_t* scales, float* sums) {
   constexpr int MT = ROWS > 16 ? 2 : 1;
   using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 2>(ROWS), C::CF, 1, 2, C::RING, C::WAVES>;
   const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rows = min(ROWS, members - base);
-  const Member me = member(p, ids, weights, set, e, base + min(lane & (16 * MT - 1), rows - 1));
+  const Member me = member(p, pairs, e, base + min(lane & (16 * MT - 1), rows - 1));
   Sources<S> src;
   src.K = p.F;
   set_group(src, p.group);
@@ -440,7 +474,7 @@ __device__ __forceinline__ void wide_down_item(const ExpertParams& p, const int3
 #pragma unroll
   for (int i = 0; i < S::X_LOADS; ++i) {
     const int r = min(x_row_of<S>(i), rows - 1);
-    src.x_off[i] = __shfl(me.token * p.k + me.place, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
+    src.x_off[i] = __shfl(me.pair, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
   }
   f32x4 acc[MT][C::CF];
   clear<S>(acc);
@@ -464,33 +498,30 @@ __device__ __forceinline__ void wide_down_item(const ExpertParams& p, const int3
 template <class C>
 __global__ __launch_bounds__(C::THREADS) void experts_wide_down_kernel(ExpertParams p, int t0, float* partial) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-  __shared__ Pairs pairs;
   const int tid = threadIdx.x;
   const int T = min(kLayerTokens, p.T - t0);
-  const int32_t* ids = p.ids + (int64_t)t0 * p.k;
-  const float* weights = p.w + (int64_t)t0 * p.k;
   const int n0 = blockIdx.x * C::COLS;
   uint8_t* scales = lds + C::RING;
   float* sums = (float*)(scales + C::WAVES * C::SCALE_LDS);  // [T][COLS]
+  const Pairs pairs = pairs_at((uint8_t*)(sums + T * C::COLS), p.E, T * p.k);
   for (int i = tid; i < T * C::COLS; i += C::THREADS) sums[i] = 0.f;
-  sort_pairs(pairs, p, ids, T);
+  sort_pairs(pairs, p, t0, T);
   constexpr int COLS = C::Fmt::FP8 ? 128 : 256;
   const int chunks = (p.F + COLS - 1) / COLS;
-  const int total = pairs.items * chunks;
+  const int total = __builtin_amdgcn_readfirstlane(*pairs.items) * chunks;
   int at = (int)((int64_t)total * blockIdx.y / gridDim.y);
   const int end = (int)((int64_t)total * (blockIdx.y + 1) / gridDim.y);
   while (at < end) {
     const int item = __builtin_amdgcn_readfirstlane(at / chunks), c0 = at - item * chunks;
     const int c1 = min(chunks, c0 + end - at);
     at += c1 - c0;
-    const int e = __builtin_amdgcn_readfirstlane(pairs.item_expert[item]);
-    const unsigned long long set = pairs.tokens[e];
-    const int members = __builtin_amdgcn_readfirstlane(__builtin_popcountll(set));
+    const int e = __builtin_amdgcn_readfirstlane(pairs.expert[item]);
+    const int members = __builtin_amdgcn_readfirstlane(__builtin_popcountll(pairs.tokens[e]));
     for (int base = 0; base < members; base += C::MOST) {
       if (C::MOST == 16 || members - base <= 16)
-        wide_down_item<C, 16>(p, ids, weights, t0, T, set, e, base, members, n0, c0, c1, lds, scales, sums);
+        wide_down_item<C, 16>(p, pairs, t0, T, e, base, members, n0, c0, c1, lds, scales, sums);
       else
-        wide_down_item<C, C::MOST>(p, ids, weights, t0, T, set, e, base, members, n0, c0, c1, lds, scales, sums);
+        wide_down_item<C, C::MOST>(p, pairs, t0, T, e, base, members, n0, c0, c1, lds, scales, sums);
     }
   }
   __syncthreads();

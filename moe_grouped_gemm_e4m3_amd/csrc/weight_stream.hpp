@@ -150,37 +150,40 @@ __device__ __forceinline__ void load_chunk(const Sources<S>& src, uint8_t* slot,
   }
 }
 
-// Scales and zero points of groups g0 .. g_last (at most SCALES) of the wave's
-// rows into LDS, one word each: bf16 scale above, zero point below.  Groups of
-// the last chunk that the row does not have get scales of zero: what stands
-// behind a row's last scale may be anything, and 0 NaN is not 0.
+// Scales and zero points of 16 groups from g on of the wave's rows, on their way
+// to LDS: one word each, bf16 scale above, zero point below.  Groups from g_end
+// on (of the last chunk, that the row does not have) get scales of zero: what
+// stands behind a row's last scale may be anything, and 0 NaN is not 0.
 template <class S>
-__device__ __forceinline__ void load_scales(const Sources<S>& src, uint32_t* scales, int g0, int g_last) {
-  const int lane = threadIdx.x & 63, r8 = lane >> 3;
-  const int n = min(S::SCALES, g_last + 1 - g0);
-#pragma unroll 1
-  for (int j0 = 0; j0 < min(n + 2 * S::GPC - 1, S::SCALES); j0 += 16) {
-    uint32_t w[S::CF][2][2];
+struct ScaleLoads {
+  uint32_t s[S::CF][2][2], z[S::CF][2][2];
+
+  __device__ __forceinline__ void load(const Sources<S>& src, int g, int g_end) {
+    const int lane = threadIdx.x & 63, r8 = lane >> 3;
 #pragma unroll
     for (int t = 0; t < S::CF; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int g = j0 + 8 * y + (lane & 7), row = (t % S::PER) * 16 + h * 8 + r8;
-          const int at = g < n ? row * src.groups + g0 + g : 0x3fffffff;  // out of every range
-          const uint32_t s = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s[t / S::PER], 2 * at, 0, 0);
-          const uint32_t z = S::Z ? (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z[t / S::PER], at, 0, 0) : 8u;
-          w[t][h][y] = s << 16 | z;
+          const int x = g + 8 * y + (lane & 7), row = (t % S::PER) * 16 + h * 8 + r8;
+          const int at = x < g_end ? row * src.groups + x : 0x3fffffff;  // out of every range
+          s[t][h][y] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s[t / S::PER], 2 * at, 0, 0);
+          if (S::Z) z[t][h][y] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z[t / S::PER], at, 0, 0);
         }
+  }
+  // scales: of a row's group g
+  __device__ __forceinline__ void store(uint32_t* scales) const {
+    const int lane = threadIdx.x & 63, r8 = lane >> 3;
 #pragma unroll
     for (int t = 0; t < S::CF; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) scales[(t * 16 + h * 8 + r8) * S::SCALE_LD + j0 + 8 * y + (lane & 7)] = w[t][h][y];
+        for (int y = 0; y < 2; ++y)
+          scales[(t * 16 + h * 8 + r8) * S::SCALE_LD + 8 * y + (lane & 7)] = s[t][h][y] << 16 | (S::Z ? z[t][h][y] : 8u);
   }
-}
+};
 
 // Eight weights as bf16: e4m3 bytes, or the eight codes of a 4-bit word.
 __device__ __forceinline__ bf16x8 widen_bytes(int lo, int hi, float scale) {
@@ -218,88 +221,97 @@ __device__ __forceinline__ i32x4 w_piece(const uint8_t* slot, int t, int j) {
   return *(const i32x4*)(slot + weights_at<S>() + (l16 * 128 + (((4 * j + (lane >> 4)) ^ (l16 & 7)) << 4)) + t * 2048);
 }
 
-// acc += the slot's products.
+// acc += the slot's products.  Products that follow each other are of different
+// tiles, and a group's sums are scaled while the matrix cores work on the next
+// group's: with a wave or two on a SIMD, what waits for a result is not hidden
+// by other waves.
 template <class S>
 __device__ __forceinline__ void add_chunk(f32x4 (&acc)[S::MT][S::CF], const Sources<S>& src, const uint8_t* slot,
                                           const float (&fs)[S::CF], const uint32_t* scales, int chunk, int g0) {
+  const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
   if constexpr (S::FP8) {
-    i32x4 x[S::PARTS][S::MT][4];
+    f32x4 P[S::MT][S::CF];
 #pragma unroll
-    for (int p = 0; p < S::PARTS; ++p)
+    for (int t = 0; t < S::MT; ++t)
 #pragma unroll
-      for (int t = 0; t < S::MT; ++t)
+      for (int cf = 0; cf < S::CF; ++cf) P[t][cf] = zero;
 #pragma unroll
-        for (int m = 0; m < 4; ++m) x[p][t][m] = x_piece<S>(slot, t, p, 0, m);
+    for (int j = 0; j < 2; ++j) {
+      i32x4 w[S::CF];
 #pragma unroll
-    for (int cf = 0; cf < S::CF; ++cf) {
-      f32x4 P[S::MT];
+      for (int cf = 0; cf < S::CF; ++cf) w[cf] = w_piece<S>(slot, cf, j);
 #pragma unroll
-      for (int t = 0; t < S::MT; ++t) P[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int h = 0; h < 2; ++h) {
+        bf16x8 b[S::CF];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const i32x4 w = w_piece<S>(slot, cf, j);
+        for (int cf = 0; cf < S::CF; ++cf) b[cf] = widen_bytes(w[cf][2 * h], w[cf][2 * h + 1], 1.f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bf16x8 b = widen_bytes(w[2 * h], w[2 * h + 1], 1.f);
+        for (int p = 0; p < S::PARTS; ++p)
 #pragma unroll
-          for (int t = 0; t < S::MT; ++t)
+          for (int t = 0; t < S::MT; ++t) {
+            const i32x4 x = x_piece<S>(slot, t, p, 0, 2 * j + h);
 #pragma unroll
-            for (int p = 0; p < S::PARTS; ++p) P[t] = mfma_bf16(x[p][t][2 * j + h], b, P[t]);
-        }
+            for (int cf = 0; cf < S::CF; ++cf) P[t][cf] = mfma_bf16(x, b[cf], P[t][cf]);
+          }
       }
-#pragma unroll
-      for (int t = 0; t < S::MT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][cf][i] = __builtin_fmaf(fs[cf], P[t][i], acc[t][cf][i]);
     }
+#pragma unroll
+    for (int t = 0; t < S::MT; ++t)
+#pragma unroll
+      for (int cf = 0; cf < S::CF; ++cf)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][cf][i] = __builtin_fmaf(fs[cf], P[t][cf][i], acc[t][cf][i]);
   } else {
-    constexpr int MPG = 4 / S::GPC;
+    constexpr int MPG = 4 / S::GPC, GROUPS = 2 * S::GPC;
     const __bf16 one = (__bf16)1.f;
     const bf16x8 ones = bf16x8{one, one, one, one, one, one, one, one};
     const int l16 = threadIdx.x & 15;
+    f32x4 sum[2][S::MT], P[2][S::MT][S::CF];
+    uint32_t sz[2][S::CF];
+    i32x4 w[S::CF];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      i32x4 x[S::PARTS][S::MT][4], w[S::CF];
+    for (int g = 0; g <= GROUPS; ++g) {
+      const int now = g & 1, last = 1 - now;
+      if (g < GROUPS) {
+        const int half = g / S::GPC, in = g % S::GPC;
+        if (in == 0) {
 #pragma unroll
-      for (int cf = 0; cf < S::CF; ++cf) w[cf] = w_piece<S>(slot, cf, half);
-#pragma unroll
-      for (int p = 0; p < S::PARTS; ++p)
-#pragma unroll
-        for (int t = 0; t < S::MT; ++t)
-#pragma unroll
-          for (int m = 0; m < 4; ++m) x[p][t][m] = x_piece<S>(slot, t, p, half, m);
-#pragma unroll
-      for (int g = 0; g < S::GPC; ++g) {
-        const int at = group_of(src, chunk * 2 + half, g) - g0;
-        f32x4 sum[S::MT];
-#pragma unroll
-        for (int t = 0; t < S::MT; ++t) {
-          sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int m = g * MPG; m < (g + 1) * MPG; ++m)
-#pragma unroll
-            for (int p = 0; p < S::PARTS; ++p) sum[t] = mfma_bf16(x[p][t][m], ones, sum[t]);
+          for (int cf = 0; cf < S::CF; ++cf) w[cf] = w_piece<S>(slot, cf, half);
         }
+        const int at = group_of(src, chunk * 2 + half, in) - g0;
 #pragma unroll
         for (int cf = 0; cf < S::CF; ++cf) {
-          const uint32_t sz = scales[(cf * 16 + l16) * S::SCALE_LD + at];
-          f32x4 P[S::MT];
+          sz[now][cf] = scales[(cf * 16 + l16) * S::SCALE_LD + at];
 #pragma unroll
-          for (int t = 0; t < S::MT; ++t) P[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int t = 0; t < S::MT; ++t) P[now][t][cf] = zero;
+        }
 #pragma unroll
-          for (int m = g * MPG; m < (g + 1) * MPG; ++m) {
-            const bf16x8 b = widen_int4(w[cf][m]);
+        for (int t = 0; t < S::MT; ++t) sum[now][t] = zero;
 #pragma unroll
-            for (int t = 0; t < S::MT; ++t)
+        for (int m = in * MPG; m < (in + 1) * MPG; ++m) {
+          bf16x8 b[S::CF];
 #pragma unroll
-              for (int p = 0; p < S::PARTS; ++p) P[t] = mfma_bf16(x[p][t][m], b, P[t]);
-          }
-          const float s = __uint_as_float(sz & 0xffff0000u), z = S::Z ? (float)(uint8_t)sz : 8.f;
+          for (int cf = 0; cf < S::CF; ++cf) b[cf] = widen_int4(w[cf][m]);
+#pragma unroll
+          for (int p = 0; p < S::PARTS; ++p)
+#pragma unroll
+            for (int t = 0; t < S::MT; ++t) {
+              const i32x4 x = x_piece<S>(slot, t, p, half, m);
+              sum[now][t] = mfma_bf16(x, ones, sum[now][t]);
+#pragma unroll
+              for (int cf = 0; cf < S::CF; ++cf) P[now][t][cf] = mfma_bf16(x, b[cf], P[now][t][cf]);
+            }
+        }
+      }
+      if (g > 0) {
+#pragma unroll
+        for (int cf = 0; cf < S::CF; ++cf) {
+          const float s = __uint_as_float(sz[last][cf] & 0xffff0000u), z = S::Z ? (float)(uint8_t)sz[last][cf] : 8.f;
 #pragma unroll
           for (int t = 0; t < S::MT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              acc[t][cf][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[t][i], P[t][i]), acc[t][cf][i]);
+              acc[t][cf][i] = __builtin_fmaf(s, __builtin_fmaf(-z, sum[last][t][i], P[last][t][cf][i]), acc[t][cf][i]);
         }
       }
     }
@@ -321,16 +333,34 @@ __device__ __forceinline__ void stream_chunks(f32x4 (&acc)[S::MT][S::CF], const 
   int c = ahead;
   auto next_of = [&](int x) { return x + 1 == end ? first : x + 1; };
   const int n = end - first;
+  // 4 bits: scales of groups [g0, g0 + SCALES) wait in LDS.  The first 16 are on
+  // their way before the ring's loads, which waits for them would include.
+  int g0 = 0, g_all = 0, g_last = 0;
+  if constexpr (!S::FP8) {
+    g_last = group_of(src, 2 * end - 1, S::GPC - 1);  // of the last chunk, whether the row has it or not
+    const int g_first = group_of(src, 2 * first, 0);
+    g0 = g_last - g_first < S::SCALES ? g_first : group_of(src, 2 * c, 0);
+    g_all = min(src.groups, g_last + 1);
+  }
+  typename std::conditional<S::FP8, int, ScaleLoads<S>>::type loads;
+  if constexpr (!S::FP8) loads.load(src, g0, g_all);
 #pragma unroll
   for (int d = 0; d < S::DEPTH - 1; ++d) {
     load_chunk<S>(src, ring + d * S::SLOT, ahead, d < n);
     ahead = next_of(ahead);
   }
   typedef const __attribute__((address_space(4))) float* Scalar;
-  int slot = 0, g0 = 0, g_end = 0;
-  const int last_half = (src.K - 1) >> 7, halves = S::HALVES;
-  const int g_first = group_of(src, halves * first, 0);
-  const int g_last = group_of(src, min(halves * end - 1, last_half), S::GPC - 1);
+  int slot = 0;
+  auto load_scales = [&](bool first_are_here) {
+    if constexpr (!S::FP8) {
+      const int all = min(S::SCALES, g_last + 1 - g0);
+      for (int g = 0; g < all; g += 16) {
+        if (g > 0 || !first_are_here) loads.load(src, g0 + g, g_all);
+        loads.store(scales + g);
+      }
+    }
+  };
+  load_scales(true);
   float next[S::CF];
   if constexpr (S::FP8) {
 #pragma unroll
@@ -346,12 +376,11 @@ __device__ __forceinline__ void stream_chunks(f32x4 (&acc)[S::MT][S::CF], const 
         next[t] = *(Scalar)(src.fs[t] + next_of(c));
       }
     } else {
-      const int lo = group_of(src, 2 * c, 0), hi = group_of(src, min(2 * c + 1, last_half), S::GPC - 1);
-      if (lo < g0 || hi >= g_end) {
-        // scales of the groups from here on, or of all: the ring fills meanwhile
-        g0 = g_last - g_first < S::SCALES ? g_first : lo;
-        g_end = g0 + S::SCALES;
-        load_scales<S>(src, scales, g0, min(g_last, src.groups - 1));
+      const int lo = group_of(src, 2 * c, 0);
+      if (lo < g0 || group_of(src, 2 * c + 1, S::GPC - 1) >= g0 + S::SCALES) {
+        // the next groups' scales: the ring fills meanwhile
+        g0 = lo;
+        load_scales(false);
       }
     }
     const int into = slot == 0 ? S::DEPTH - 1 : slot - 1;  // the slot read in the last turn
