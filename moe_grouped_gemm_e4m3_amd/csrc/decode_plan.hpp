@@ -34,9 +34,9 @@ inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // ---------------------------------------------------------------------------
 // gemm_int4_nt
 
-enum Int4Kind { kSplit2, kSplit2Deep, kSplit8, kSplit8Deep, kSplit16, kSplit16Deep, kWide16, kWide64, kInt4Kinds };
+enum Int4Kind { kSplit2, kSplit2Deep, kSplit8, kSplit8Deep, kSplit16, kSplit16Deep, kWide16, kWide32, kWide64, kInt4Kinds };
 constexpr const char* kInt4Names[kInt4Kinds] = {"split2", "split2deep", "split8", "split8deep", "split16", "split16deep",
-                                                "wide16", "wide64"};
+                                                "wide16", "wide32", "wide64"};
 struct Int4Plan {
   Int4Kind kind;
   int k_parts;  // wide: parts of the reduction, joined by a second kernel
@@ -59,15 +59,17 @@ inline Int4Plan plan_int4(int M, int N, int K, const char* forced) {
     kind = M <= 8 ? (deep ? kSplit8Deep : kSplit8) : deep && N < 4096 ? kSplit16Deep : kSplit16;
   else if (weights < (1 << 23))
     kind = kSplit16;  // 64 x 1000 x 1024: 3.7, 5.5 wide
+  else if (weights < (1 << 25))
+    kind = M <= 32 ? kWide16 : kWide32;  // 32 x 2112 x 7168: 12.9 on 16 rows, 14.3 on 32; 64 rows: 17.2 and 16.0
   else
-    // 64 x 16384 x 4096: 31 on 64 rows, 36 on 16; 64 x 4096 x 4096: 13 on 16
-    kind = M > 32 && weights >= (1 << 25) ? kWide64 : kWide16;
+    // 32 x 7168 x 16384: 28 on 16 rows, 26 on 32; 64 rows: 48, 45, and 39 on 64
+    kind = M <= 16 ? kWide16 : M <= 32 ? kWide32 : kWide64;
   for (int k = 0; k < kInt4Kinds; ++k)
     if (names(forced, kInt4Names[k])) kind = (Int4Kind)k;
   Int4Plan p{kind, 1};
-  if (kind == kWide16 || kind == kWide64) {
+  if (kind >= kWide16) {
     // one round of workgroups on 256 CUs, two chunks each at least
-    const int64_t tiles = (int64_t)ceil_div(N, 128) * ceil_div(M, kind == kWide64 ? 64 : 16);
+    const int64_t tiles = (int64_t)ceil_div(N, 128) * ceil_div(M, kind == kWide64 ? 64 : kind == kWide32 ? 32 : 16);
     p.k_parts = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, chunks / 2, 16}));
     for (int n = 1; n <= 8 && n <= std::max(1, chunks); ++n) {
       const char word[] = {'k', 'p', 'a', 'r', 't', 's', (char)('0' + n), 0};
@@ -84,8 +86,8 @@ inline int64_t int4_partial_bytes(int M, int N, const Int4Plan& p) {
 // ---------------------------------------------------------------------------
 // expert layers
 
-enum UpKind { kUpSplit4, kUpSplit4Two, kUpSplit16, kUpWide, kUpWideDeep, kUpWide8, kUpKinds };
-constexpr const char* kUpNames[kUpKinds] = {"up-split4", "up-split4-two", "up-split16", "up-wide", "up-wide-deep", "up-wide8"};
+enum UpKind { kUpSplit2, kUpSplit4, kUpSplit16, kUpWide, kUpWideDeep, kUpWide8, kUpKinds };
+constexpr const char* kUpNames[kUpKinds] = {"up-split2", "up-split4", "up-split16", "up-wide", "up-wide-deep", "up-wide8"};
 enum DownKind { kDownSplit1, kDownSplit1Two, kDownSplit4, kDownSplit4Two, kDownWide16, kDownWide16Deep, kDownWide32, kDownKinds };
 constexpr const char* kDownNames[kDownKinds] = {"down-split1", "down-split1-two", "down-split4", "down-split4-two", "down-wide16",
                                                 "down-wide16-deep", "down-wide32"};
@@ -112,18 +114,18 @@ inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const c
   else if (T >= 4 && wide8 >= 384)
     p.up = kUpWide8;
   else if (T <= 4)
-    // two tiles of hidden units where workgroups abound (T=1, 8 experts of 2048 x 7168: 30.4 for 32.2)
-    p.up = (int64_t)ceil_div(F, 16) * active >= 1024 ? kUpSplit4Two : kUpSplit4;
+    // room for two tokens only leaves more workgroups on a CU (T=2, 16 experts of 2048 x 7168: 75 for 79)
+    p.up = T <= 2 ? kUpSplit2 : kUpSplit4;
   else
     p.up = wide4 >= 256 ? kUpWide : kUpSplit16;
   for (int i = 0; i < kUpKinds; ++i)
-    if (names(forced, kUpNames[i]) && (fp8 ? i != kUpWide8 && i != kUpSplit4Two : i != kUpWideDeep)) p.up = (UpKind)i;
+    if (names(forced, kUpNames[i]) && (fp8 ? i != kUpWide8 && i != kUpSplit2 : i != kUpWideDeep)) p.up = (UpKind)i;
   // down.  A third kernel costs about 3 us, so that small layers go without
   // (T=8, 8 experts of 2048 x 1024: 9.7 for 13.0; 64 of 2048 x 704: 26.6 for 21.9).
   const bool small = T <= 8 && pairs <= 2 * E && (int64_t)active * F * K <= (1 << 25);
   const int tiles = ceil_div(K, 128);
   if (T == 1)
-    p.down = fp8 && K > 4096 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
+    p.down = K > 4096 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
   else if (T <= 4 || small)
     p.down = !fp8 && K > 4096 ? kDownSplit4Two : kDownSplit4;  // T=2, 4-bit, 7168 x 2048: 38 for 43; 4096 x 2048: 24 for 15
   else if (pairs > 8 * E && (fp8 || pairs_bytes(E, T, k) <= 12 << 10))  // (4 bits: the rest of LDS is taken)
@@ -131,7 +133,7 @@ inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const c
   else
     p.down = fp8 && T > 16 ? kDownWide16Deep : kDownWide16;  // T=64, 8 tokens an expert: 66 for 83
   for (int i = 0; i < kDownKinds; ++i)
-    if (names(forced, kDownNames[i]) && (fp8 ? i != kDownSplit4Two : i != kDownSplit1Two && i != kDownWide16Deep) &&
+    if (names(forced, kDownNames[i]) && (fp8 ? i != kDownSplit4Two : i != kDownWide16Deep) &&
         (i != kDownSplit1Two || T <= 16))  // its sums of more tokens do not fit LDS
       p.down = (DownKind)i;
   p.parts = 1;

@@ -197,10 +197,10 @@ fg_status launch_layer(const ExpertParams& p, void* stream, const char* what) {
   if (p.F > 0) {
     fg_status st = FG_OK;
     switch (plan.up) {
-      case kUpSplit4: st = l.up<UpTile<Fmt, 1, 4, 2, 4>>(); break;
-      case kUpSplit4Two:
-        if constexpr (!Fmt::FP8) st = l.up<UpTile<Fmt, 2, 4, 2, 4>>();
+      case kUpSplit2:
+        if constexpr (!Fmt::FP8) st = l.up<UpTile<Fmt, 1, 4, 2, 2>>();
         break;
+      case kUpSplit4: st = l.up<UpTile<Fmt, 1, 4, 2, 4>>(); break;
       case kUpSplit16: st = l.up<UpTile<Fmt, 1, 4, 2, 16>>(); break;
       case kUpWide: st = l.up<WideUp<Fmt, 1, 4, 2, Fmt::FP8 ? 32 : 16>>(); break;
       case kUpWideDeep:
@@ -216,9 +216,7 @@ fg_status launch_layer(const ExpertParams& p, void* stream, const char* what) {
   }
   switch (plan.down) {
     case kDownSplit1: return l.down<DownTile<Fmt, 1, 8, 2, 1>>();
-    case kDownSplit1Two:
-      if constexpr (Fmt::FP8) return l.down<DownTile<Fmt, 2, 8, 3, 1>>();
-      break;
+    case kDownSplit1Two: return l.down<DownTile<Fmt, 2, 8, Fmt::FP8 ? 3 : 2, 1>>();
     case kDownSplit4: return l.down<DownTile<Fmt, 1, 8, 2, 4>>();
     case kDownSplit4Two:
       if constexpr (!Fmt::FP8) return l.down<DownTile<Fmt, 2, 4, 3, 4>>();

@@ -93,7 +93,7 @@ constexpr int x_kib(int rows) {
   return kib > 1 ? kib : 1;
 }
 
-// PER: tiles of 16 hidden units.  MOST: tokens of an expert in one go (4, 16 or 32).
+// PER: tiles of 16 hidden units.  MOST: tokens of an expert in one go (2, 4 or 16).
 template <class Fmt_, int PER_, int WAVES_, int DEPTH_, int MOST_>
 struct UpTile {
   using Fmt = Fmt_;
@@ -200,10 +200,8 @@ __global__ __launch_bounds__(C::THREADS) void experts_up_kernel(ExpertParams p) 
   for (int base = 0; base < members; base += C::MOST) {
     if (base) __syncthreads();  // the sums are read
     const int left = members - base;
-    if (C::MOST == 4 || left <= 4)
-      up_tile<C, 4>(p, e, t0, f0, base, members, list, lds);
-    else if (C::MOST == 16 || left <= 16)
-      up_tile<C, C::MOST < 16 ? C::MOST : 16>(p, e, t0, f0, base, members, list, lds);
+    if (C::MOST <= 4 || left <= 4)
+      up_tile<C, C::MOST < 4 ? C::MOST : 4>(p, e, t0, f0, base, members, list, lds);
     else
       up_tile<C, C::MOST>(p, e, t0, f0, base, members, list, lds);
   }
@@ -453,7 +451,8 @@ struct WideDown {
   static constexpr int CF = CF_, WAVES = WAVES_, THREADS = 64 * WAVES, COLS = 16 * CF * WAVES, MOST = MOST_;
   static constexpr int RING = DEPTH_ * (WAVES * CF * 2048 + x_kib<Fmt, 2>(MOST) * 1024);
   static constexpr int SCALE_LDS = scale_lds<Fmt, CF>();
-  static int lds_bytes(int T) { return RING + WAVES * SCALE_LDS + T * COLS * 4; }
+  static constexpr int TOKENS_AT = RING + WAVES * SCALE_LDS;
+  static int lds_bytes(int T) { return TOKENS_AT + T * COLS * 4; }
 };
 
 template <class C, int ROWS>
@@ -502,7 +501,7 @@ __global__ __launch_bounds__(C::THREADS) void experts_wide_down_kernel(ExpertPar
   const int T = min(kLayerTokens, p.T - t0);
   const int n0 = blockIdx.x * C::COLS;
   uint8_t* scales = lds + C::RING;
-  float* sums = (float*)(scales + C::WAVES * C::SCALE_LDS);  // [T][COLS]
+  float* sums = (float*)(lds + C::TOKENS_AT);  // [T][COLS]
   const Pairs pairs = pairs_at((uint8_t*)(sums + T * C::COLS), p.E, T * p.k);
   for (int i = tid; i < T * C::COLS; i += C::THREADS) sums[i] = 0.f;
   sort_pairs(pairs, p, t0, T);

@@ -114,6 +114,7 @@ struct ProductLaunch {
       case kSplit16: return split<Int4Tile<Fmt, 16, 1, 4, 2>>();
       case kSplit16Deep: return split<Int4Tile<Fmt, 16, 1, 6, 2>>();
       case kWide16: return wide<Int4Wide<Fmt, 16, 1, 8, 2>>();
+      case kWide32: return wide<Int4Wide<Fmt, 32, 1, 8, 2>>();
       default: return wide<Int4Wide<Fmt, 64, 1, 8, 2>>();
     }
   }

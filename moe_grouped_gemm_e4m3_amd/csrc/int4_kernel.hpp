@@ -196,7 +196,7 @@ struct Int4Wide {
   static constexpr int RING = DEPTH_ * (WAVES * CF * 2048 + ROWS * 512);
   using S = Stream<Fmt, MT, ROWS / 2, CF, 1, 1, RING, WAVES>;
   static constexpr int THREADS = 64 * WAVES, COLS = 16 * CF * WAVES;
-  static constexpr int LDS = RING + WAVES * scale_lds<Fmt, CF>();
+  static constexpr int SCALE_LDS = scale_lds<Fmt, CF>(), LDS = RING + WAVES * SCALE_LDS;
 };
 
 // Grid: column tiles, row parts, parts of K.
@@ -217,8 +217,7 @@ __global__ __launch_bounds__(C::THREADS) void int4_wide_kernel(Int4Params p, flo
     for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int chunks = (p.K + S::COLS - 1) / S::COLS;
   const int first = (int)((int64_t)chunks * blockIdx.z / gridDim.z), end = (int)((int64_t)chunks * (blockIdx.z + 1) / gridDim.z);
-  stream_chunks<S>(acc, src, lds, (uint32_t*)(lds + C::RING + wave * scale_lds<typename C::Fmt, C::CF>()), first, end,
-                   5 * blockIdx.x);
+  stream_chunks<S>(acc, src, lds, (uint32_t*)(lds + C::RING + wave * C::SCALE_LDS), first, end, 5 * blockIdx.x);
 #pragma unroll
   for (int t = 0; t < S::MT; ++t)
 #pragma unroll

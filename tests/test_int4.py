@@ -115,8 +115,8 @@ def test_product_of_whole_layers(gpu_lib, M, N, K, group):
 @pytest.mark.gpu
 @pytest.mark.parametrize("zeros", [True, False])
 @pytest.mark.parametrize("group", [32, 64, 128, 256])
-@pytest.mark.parametrize("plan", ["split2", "split2deep", "split8", "split8deep", "split16", "split16deep", "wide16", "wide64",
-                                  "wide16,kparts3", "wide64,kparts5", "wide16,kparts8"])
+@pytest.mark.parametrize("plan", ["split2", "split2deep", "split8", "split8deep", "split16", "split16deep", "wide16", "wide32", "wide64",
+                                  "wide16,kparts3", "wide32,kparts2", "wide64,kparts5", "wide16,kparts8"])
 def test_every_plan(gpu_lib, monkeypatch, capfd, plan, group, zeros):
     monkeypatch.setenv("FG_DECODE_PLAN", plan)
     monkeypatch.setenv("FG_PRINT_CONFIGS", "1")

@@ -105,7 +105,7 @@ def test_layer(gpu_lib, fmt, T, E, k, F, K):
           offset=T % 2)
 
 
-UPS = ["up-split4", "up-split4-two", "up-split16", "up-wide", "up-wide-deep", "up-wide8"]
+UPS = ["up-split2", "up-split4", "up-split16", "up-wide", "up-wide-deep", "up-wide8"]
 DOWNS = ["down-split1", "down-split1-two", "down-split4", "down-split4-two", "down-wide16", "down-wide16-deep", "down-wide32"]
 
 
@@ -122,8 +122,8 @@ def test_every_plan(gpu_lib, monkeypatch, capfd, fmt, plan):
     for T, E, k, F, K in sizes:
         check(gpu_lib, Layer(fmt, E, F, K, seed=T), T, k, pad=T % 2)
     ran = capfd.readouterr().err
-    has = {"up-split4-two": fmt != "fp8", "up-wide8": fmt != "fp8", "down-split4-two": fmt != "fp8", "up-wide-deep": fmt == "fp8",
-           "down-split1-two": fmt == "fp8", "down-wide16-deep": fmt == "fp8"}
+    has = {"up-split2": fmt != "fp8", "up-wide8": fmt != "fp8", "down-split4-two": fmt != "fp8", "up-wide-deep": fmt == "fp8",
+           "down-wide16-deep": fmt == "fp8"}
     if has.get(plan.split(",")[0], True):
         assert ran.count(plan.split(",")[0] + " ") >= len(sizes)
 
