@@ -581,8 +581,10 @@ fg_status int4_cast_per_group_bf16(const uint16_t* w, int64_t ldw, uint8_t* q, u
  *   A   device [M, K] bf16, row stride lda elements (lda >= K, lda % 8 == 0, 16-byte aligned, rows of at most 4 MiB)
  *   B, sb, zb  4-bit weights [N, K] as above (zb may be NULL)
  *   D   device [M, N] bf16, row stride ldd elements (ldd >= N); only D[0:M, 0:N] is written
+ *   workspace  NULL, or device, 256-byte aligned, fg_int4_workspace_bytes(M, N, K) bytes (0 for
+ *       most sizes); needs no initialisation; in use until the call's work has finished
  * Made for M <= 64, where the weights are read once; more rows are taken 64 at a
- * time.  M, N <= 2^30, K % 32 == 0, K <= 2^20.  K == 0 writes zeros.  Sums are in
+ * time.  M <= 2^20, N <= 2^26, K % 32 == 0, K <= 2^20.  K == 0 writes zeros.  Sums are in
  * fp32, the zero point is taken out of a group's sum once, and the result is
  * rounded once.  A row of A with an infinity or a NaN gives a row of D that holds
  * infinities or NaN.  Sums have a fixed order, which depends on the sizes only.
@@ -613,7 +615,7 @@ typedef enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 } fg_scoring;
  * An expert whose logit (or bias) is -infinity is no candidate; places that no
  * candidate is left for hold id -1 and weight 0.  A NaN is chosen after all
  * numbers and gives NaN weights: under softmax all of its row's.
- * 1 <= k <= min(E, 64), E <= 1024, groups <= 64 divides E.  Scores and what they
+ * T <= 2^25, 1 <= k <= min(E, 64), E <= 1024, groups <= 64 divides E.  Scores and what they
  * are compared by are computed in 64 bits, weights are rounded once.
  */
 fg_status moe_route(const float* logits, int64_t ld, const float* bias, int32_t* ids, float* weights, int T, int E, int k,
@@ -625,8 +627,8 @@ fg_status moe_route_bf16(const uint16_t* logits, int64_t ld, const float* bias, 
  * Its gradient: dlogits (device, the logits' type, [T, E], row stride ld_dl;
  * every element is written) from dweights (device fp32 [T, k]), the logits and
  * the forward call's ids, scoring, normalize and scale.  Places whose id is not
- * in [0, E) have no gradient; the choice itself and the bias have none.  With an
- * id in two places of a row both add up.
+ * in [0, E) have no gradient, and their dweights are not read; the choice itself
+ * and the bias have none.  With an id in two places of a row both add up.
  */
 fg_status moe_route_backward(const float* dweights, const float* logits, int64_t ld, const int32_t* ids, float* dlogits,
                              int64_t ld_dl, int T, int E, int k, int scoring, int normalize, float scale, void* stream);
@@ -635,7 +637,7 @@ fg_status moe_route_backward_bf16(const float* dweights, const uint16_t* logits,
                                   float scale, void* stream);
 
 /*
- * A whole expert layer for a few tokens, in two kernels:
+ * A whole expert layer for a few tokens, in two kernels (three for more tokens):
  *     D[t] = bf16( sum_j weights[t,j] * W2[e] . h ),  e = ids[t,j],
  *     h = act(g) * u,  g = W1[e][0:F] . X[t],  u = W1[e][F:2F] . X[t].
  *   X    device [T, K] bf16, row stride ldx elements (ldx >= K, ldx % 8 == 0, 16-byte aligned, rows of at most 4 MiB)

@@ -42,35 +42,61 @@ struct Int4Plan {
   int k_parts;  // wide: parts of the reduction, joined by a second kernel
 };
 
+// What a plan takes, in microseconds, for more than eight rows: fitted to 16
+// weights of 512 x 512 to 7168 x 16384 with 12 to 256 rows, where it is within
+// 20% of most times.  A workgroup's start and end, a chunk of 256 columns, and
+// rounds of 256 workgroups; parts are added by a second kernel, which reads what
+// the first has written.
+inline double split16_cost(int M, int N, int chunks) {
+  const double rounds = ceil_div((int64_t)ceil_div(N, 16) * ceil_div(M, 16), 256);
+  return 1.5 + rounds * (2.0 + 0.65 * ceil_div(chunks, 4));
+}
+inline double wide_cost(Int4Kind kind, int M, int N, int chunks, int parts) {
+  const int rows = kind == kWide64 ? 64 : kind == kWide32 ? 32 : 16;
+  const double start = kind == kWide64 ? 3.6 : kind == kWide32 ? 3.4 : 3.0, chunk = kind == kWide64 ? 1.9 : kind == kWide32 ? 1.23 : 1.03;
+  const double rounds = ceil_div((int64_t)ceil_div(N, 128) * ceil_div(M, rows) * parts, 256);
+  const double join = parts > 1 ? 2.5 + 0.1 * parts + 2e-6 * parts * M * N : 0.0;
+  return rounds * (start + chunk * ceil_div(chunks, parts)) + join;
+}
+// Parts of the reduction: at most one round of workgroups, two chunks each at least.
+inline int wide_parts(Int4Kind kind, int M, int N, int chunks) {
+  const int rows = kind == kWide64 ? 64 : kind == kWide32 ? 32 : 16;
+  const int64_t tiles = (int64_t)ceil_div(N, 128) * ceil_div(M, rows);
+  const int most = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, chunks / 2, 16}));
+  int best = 1;
+  for (int n = 2; n <= most; ++n)
+    if (wide_cost(kind, M, N, chunks, n) < wide_cost(kind, M, N, chunks, best)) best = n;
+  return best;
+}
+
 inline Int4Plan plan_int4(int M, int N, int K, const char* forced) {
   const int chunks = ceil_div(K, 256);
-  const int64_t weights = (int64_t)N * K;
   // The reduction of a 16-column tile over eight waves instead of four where the
-  // tiles are few or the reduction is long (1 x 2112 x 7168: 6.6 for 8.9; 1 x
-  // 7168 x 16384: 13.4 for 16.3; 1 x 24576 x 1536: 9.5 for 7.7).
+  // tiles are few or the reduction is long (1 x 2112 x 7168: 5.8 for 6.7; 1 x
+  // 7168 x 16384: 13.7 for 15.1; 1 x 24576 x 1536: 10.6 for 8.3).
   const bool deep = chunks >= 16 && N <= 4096;
   Int4Kind kind;
   if (M <= 2)
     kind = deep || chunks >= 32 ? kSplit2Deep : kSplit2;
-  else if (M <= 4)
-    kind = deep ? kSplit8Deep : kSplit8;
-  else if (M <= 16 && weights < (1 << 25))
-    // 16 x 4096 x 4096: 5.7, 9.5 wide; 16 x 24576 x 1536: 13 or more, 8.5 wide
-    kind = M <= 8 ? (deep ? kSplit8Deep : kSplit8) : deep && N < 4096 ? kSplit16Deep : kSplit16;
-  else if (weights < (1 << 23))
-    kind = kSplit16;  // 64 x 1000 x 1024: 3.7, 5.5 wide
-  else if (weights < (1 << 25))
-    kind = M <= 32 ? kWide16 : kWide32;  // 32 x 2112 x 7168: 12.9 on 16 rows, 14.3 on 32; 64 rows: 17.2 and 16.0
-  else
-    // 32 x 7168 x 16384: 28 on 16 rows, 26 on 32; 64 rows: 48, 45, and 39 on 64
-    kind = M <= 16 ? kWide16 : M <= 32 ? kWide32 : kWide64;
+  else if (M <= 8)
+    // 4 x 24576 x 1536: 11.4, 8.9 wide; 4 x 16384 x 4096: 12.1, 13.0 wide
+    kind = ceil_div(N, 16) > 1024 ? kWide16 : deep ? kSplit8Deep : kSplit8;
+  else {
+    kind = deep && N < 4096 ? kSplit16Deep : kSplit16;
+    double least = split16_cost(M, N, chunks);
+    for (Int4Kind wide : {kWide16, kWide32, kWide64}) {
+      const double cost = wide_cost(wide, M, N, chunks, wide_parts(wide, M, N, chunks));
+      if (cost < least) {
+        least = cost;
+        kind = wide;
+      }
+    }
+  }
   for (int k = 0; k < kInt4Kinds; ++k)
     if (names(forced, kInt4Names[k])) kind = (Int4Kind)k;
   Int4Plan p{kind, 1};
   if (kind >= kWide16) {
-    // one round of workgroups on 256 CUs, two chunks each at least
-    const int64_t tiles = (int64_t)ceil_div(N, 128) * ceil_div(M, kind == kWide64 ? 64 : kind == kWide32 ? 32 : 16);
-    p.k_parts = (int)std::max<int64_t>(1, std::min<int64_t>({256 / tiles, chunks / 2, 16}));
+    p.k_parts = wide_parts(kind, M, N, chunks);
     for (int n = 1; n <= 8 && n <= std::max(1, chunks); ++n) {
       const char word[] = {'k', 'p', 'a', 'r', 't', 's', (char)('0' + n), 0};
       if (names(forced, word)) p.k_parts = n;

@@ -21,7 +21,7 @@
 namespace fg {
 namespace {
 
-constexpr int kMaxTokens = 1 << 20;
+constexpr int kMaxTokens = 1 << 20, kMaxRouted = 1 << 25;  // the router's threads in 32 bits
 constexpr int kMaxWidth = 1 << 16;  // K and F of a layer: offsets of 64 tokens' rows and of a weight tile in 32 bits
 constexpr int64_t kMaxLd = (int64_t)1 << 21;
 
@@ -36,7 +36,7 @@ fg_status launched(const char* what) {
 
 template <typename L, int SLOTS>
 fg_status launch_route(const RouteParams& p, void* stream) {
-  const dim3 grid((unsigned)(((int64_t)p.T + kRouteWaves - 1) / kRouteWaves)), threads(64 * kRouteWaves);
+  const dim3 grid(ceil_div(p.T, kRouteWaves)), threads(64 * kRouteWaves);
   if (p.bias || p.groups > 1)
     hipLaunchKernelGGL((route_kernel<L, SLOTS, true>), grid, threads, 0, (hipStream_t)stream, p);
   else
@@ -55,7 +55,7 @@ fg_status launch_route(const RouteParams& p, void* stream) {
 
 template <typename L, int SLOTS>
 fg_status launch_route_backward(const RouteGradParams& p, void* stream) {
-  const dim3 grid((unsigned)(((int64_t)p.T + kRouteWaves - 1) / kRouteWaves));
+  const dim3 grid(ceil_div(p.T, kRouteWaves));
   hipLaunchKernelGGL((route_backward_kernel<L, SLOTS>), grid, dim3(64 * kRouteWaves), 0, (hipStream_t)stream, p);
   return launched("moe_route_backward");
 }
@@ -71,6 +71,7 @@ fg_status launch_route_backward(const RouteGradParams& p, void* stream) {
 
 fg_status check_route(int T, int E, int k, int scoring) {
   if (T < 0) return set_error(FG_EINVAL, "negative size T=%d", T);
+  if (T > kMaxRouted) return set_error(FG_EUNSUPPORTED, "T=%d: more than 2^25 tokens", T);
   if (E <= 0) return set_error(FG_EINVAL, "E=%d experts", E);
   if (k <= 0 || k > E) return set_error(FG_EINVAL, "k=%d of %d experts", k, E);
   if (scoring != FG_SCORE_SOFTMAX && scoring != FG_SCORE_SIGMOID)
@@ -126,6 +127,7 @@ fg_status route_backward(const float* dw, const L* logits, int64_t ld, const int
 // More than 64 KiB of dynamic LDS has to be asked for.
 fg_status allow_lds(const void* kernel, int bytes, const char* what) {
   if (bytes > 160 * 1024) return set_error(FG_EUNSUPPORTED, "%s: %d bytes of LDS", what, bytes);
+  if (bytes <= 64 * 1024) return FG_OK;
   const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return set_error(FG_EHIP, "%s: %d bytes of LDS: %s", what, bytes, hipGetErrorString(e));
   return FG_OK;

@@ -78,7 +78,8 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[S::MT][S::CF]) {
 // h of token t's place j and hidden unit f, as the sum of two bf16.
 __device__ __forceinline__ void store_hidden(const ExpertParams& p, int t, int j, int f, float g, float u) {
   const float h = p.act == kActSilu ? gated_value<kActSilu>(g, u) : gated_value<kActGeluTanh>(g, u);
-  const uint16_t top = bf16_bits(h);
+  uint16_t top = bf16_bits(h);
+  if ((top & 0x7fff) == 0x7f80 && __builtin_fabsf(h) < __builtin_inff()) --top;  // no infinity by rounding
   // the rest of an infinity or a NaN would be a NaN
   const float rest = (top & 0x7f80) == 0x7f80 ? 0.f : h - to_f32(top);
   uint16_t* dst = p.H + ((int64_t)t * p.k + j) * 2 * p.F + f;

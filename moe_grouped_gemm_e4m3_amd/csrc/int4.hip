@@ -28,7 +28,7 @@ fg_status check_group(int group) {
 namespace {
 
 constexpr int kMaxK = 1 << 20;   // rows of activations of 2 MiB, offsets of a tile's rows in 32 bits
-constexpr int kMaxRows = 1 << 30;
+constexpr int kMaxM = 1 << 20, kMaxN = 1 << 26;  // a grid's threads in 32 bits
 
 fg_status launched(const char* what) {
   const hipError_t e = hipGetLastError();
@@ -78,7 +78,7 @@ struct ProductLaunch {
   fg_status split() const {
     const int64_t tiles = ceil_div(p.N, C::COLS);
     p.parts = ceil_div(p.M, C::ROWS);
-    if (tiles * p.parts >= (1 << 30)) return set_error(FG_EUNSUPPORTED, "gemm_int4_nt: too many output tiles");
+    if (tiles * p.parts * C::THREADS > 0xffffffff) return set_error(FG_EUNSUPPORTED, "gemm_int4_nt: too many output tiles");
     print();
     hipLaunchKernelGGL((int4_product_kernel<C>), dim3((unsigned)(tiles * p.parts)), dim3(C::THREADS), 0, (hipStream_t)stream, p);
     return launched("gemm_int4_nt");
@@ -150,7 +150,8 @@ fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const u
   if (K % 32) return set_error(FG_EALIGN, "K=%d is not a multiple of 32", K);
   FG_TRY(check_group(group));
   if (M == 0 || N == 0) return FG_OK;
-  if (M > kMaxRows || N > kMaxRows) return set_error(FG_EUNSUPPORTED, "M=%d N=%d: more than 2^30", M, N);
+  if (M > kMaxM) return set_error(FG_EUNSUPPORTED, "M=%d: more than 2^20 rows", M);
+  if (N > kMaxN) return set_error(FG_EUNSUPPORTED, "N=%d: more than 2^26 columns", N);
   if (K > kMaxK) return set_error(FG_EUNSUPPORTED, "K=%d above 2^20", K);
   const Int4Plan plan = planned(M, N, K);
   const int64_t need = int4_partial_bytes(M, N, plan);
@@ -178,7 +179,7 @@ fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const u
 }
 
 int64_t fg_int4_workspace_bytes(int M, int N, int K) {
-  if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K > kMaxK) return -1;
+  if (M < 0 || N < 0 || K < 0 || M > kMaxM || N > kMaxN || K > kMaxK) return -1;
   return M > 0 && N > 0 ? int4_partial_bytes(M, N, planned(M, N, K)) : 0;
 }
 

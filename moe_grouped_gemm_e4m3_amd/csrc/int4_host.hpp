@@ -10,7 +10,7 @@ namespace fg {
 // 32, 64 or a multiple of 128.
 fg_status check_group(int group);
 
-inline int int4_groups(int K, int group) { return (K + group - 1) / group; }
+inline int int4_groups(int K, int group) { return K / group + (K % group != 0); }
 // Rows are padded to whole chunks of 128 codes.
 inline int int4_row_bytes(int K) { return (K + 127) / 128 * 64; }
 

@@ -166,14 +166,14 @@ struct ScaleLoads {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const int x = g + 8 * y + (lane & 7), row = (t % S::PER) * 16 + h * 8 + r8;
-          const int at = x < g_end ? row * src.groups + x : 0x3fffffff;  // out of every range
+          const int x = min(g + 8 * y + (lane & 7), g_end - 1), row = (t % S::PER) * 16 + h * 8 + r8;
+          const int at = row * src.groups + x;
           s[t][h][y] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(src.s[t / S::PER], 2 * at, 0, 0);
           if (S::Z) z[t][h][y] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(src.z[t / S::PER], at, 0, 0);
         }
   }
   // scales: of a row's group g
-  __device__ __forceinline__ void store(uint32_t* scales) const {
+  __device__ __forceinline__ void store(uint32_t* scales, int g, int g_end) const {
     const int lane = threadIdx.x & 63, r8 = lane >> 3;
 #pragma unroll
     for (int t = 0; t < S::CF; ++t)
@@ -181,7 +181,8 @@ struct ScaleLoads {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-          scales[(t * 16 + h * 8 + r8) * S::SCALE_LD + 8 * y + (lane & 7)] = s[t][h][y] << 16 | (S::Z ? z[t][h][y] : 8u);
+          scales[(t * 16 + h * 8 + r8) * S::SCALE_LD + 8 * y + (lane & 7)] =
+              g + 8 * y + (lane & 7) < g_end ? s[t][h][y] << 16 | (S::Z ? z[t][h][y] : 8u) : 0u;
   }
 };
 
@@ -356,7 +357,7 @@ __device__ __forceinline__ void stream_chunks(f32x4 (&acc)[S::MT][S::CF], const 
       const int all = min(S::SCALES, g_last + 1 - g0);
       for (int g = 0; g < all; g += 16) {
         if (g > 0 || !first_are_here) loads.load(src, g0 + g, g_all);
-        loads.store(scales + g);
+        loads.store(scales + g, g0 + g, g_all);
       }
     }
   };

@@ -219,7 +219,7 @@ def product_call(lib, A=0x10000, lda=512, B=0x10000, s=0x10000, z=None, D=0x1000
     (dict(A=None), 1, "A is NULL"), (dict(B=None), 1, "B is NULL"), (dict(s=None), 1, "sb is NULL"), (dict(D=None), 1, "D is NULL"),
     (dict(A=0x10008), 2, "A is not"), (dict(B=0x10008), 2, "B is not"), (dict(s=0x10001), 2, "sb"), (dict(D=0x10001), 2, "D"),
     (dict(lda=511), 1, "lda=511"), (dict(lda=516), 2, "lda=516"), (dict(ldd=63), 1, "ldd=63"),
-    (dict(lda=(1 << 21) + 8), 3, "4 MiB"), (dict(K=(1 << 20) + 32, lda=1 << 21), 3, "K="), (dict(M=(1 << 30) + 1), 3, "2^30"),
+    (dict(lda=(1 << 21) + 8), 3, "4 MiB"), (dict(K=(1 << 20) + 32, lda=1 << 21), 3, "K="), (dict(M=(1 << 20) + 1), 3, "2^20 rows"), (dict(N=(1 << 26) + 1, ldd=1 << 27), 3, "2^26 columns"),
     (dict(nbytes=-1), 1, "negative"), (dict(nbytes=64), 1, "workspace is NULL"), (dict(ws=0x10010, nbytes=64), 2, "256-byte"),
     (dict(M=32, N=512, ldd=512, K=24576, lda=24576), 1, "smaller than the"),
     (dict(M=0, A=None, B=None, s=None, D=None), 0, ""), (dict(N=0, A=None, B=None, s=None, D=None), 0, "")])

@@ -208,6 +208,21 @@ def test_large_and_small_hidden_units(gpu_lib):
 
 
 @pytest.mark.gpu
+def test_hidden_units_next_to_the_largest_number(gpu_lib):
+    """A finite h that bf16 alone would round to an infinity."""
+    announce("layer largest h")
+    one = Layer("fp8", 1, 16, 16)
+    one.W1.codes[:], one.W1.s[:] = 0, 1.0
+    one.W1.codes[0, 0, 0] = one.W1.codes[0, 16, 1] = 0x38  # 1: g = x_0 and u = x_1, for the first unit
+    one.W2.codes[:], one.W2.s[:] = 0x38, 2.0 ** -64
+    X = torch.zeros(1, 16, dtype=torch.bfloat16)
+    X[0, 0], X[0, 1] = 181 * 2.0 ** 56, 181 * 2.0 ** 57  # 32761 / 16384 2^127, for bf16's largest of 32640 / 16384
+    ids, w, D = torch.zeros(1, 1, dtype=torch.int32), torch.ones(1, 1), Output(1, 16)
+    one.call(gpu_lib, X.cuda(), ids.cuda(), w.cuda(), D.t)
+    assert_within(D.f64(), *one.want(f64(X), ids.numpy(), w.numpy()), "largest h")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["fp8", ("int4", 128, False)], ids=str)
 def test_offsets_past_32_bits(gpu_lib, fmt):
     """The last expert's weights lie past 4 GiB."""

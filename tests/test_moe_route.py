@@ -243,7 +243,7 @@ def route_call(lib, x=0x10000, ld=64, bias=None, ids=0x10000, w=0x10000, T=4, E=
     (dict(ids=None), 1, "ids is NULL"), (dict(w=None), 1, "weights is NULL"), (dict(x=0x10002), 2, "logits"),
     (dict(ids=0x10002), 2, "ids"), (dict(bias=0x10001), 2, "bias"), (dict(ld=63), 1, "ld=63"),
     (dict(E=1025, ld=1025), 3, "E=1025"), (dict(E=128, ld=128, k=65), 3, "k=65"),
-    (dict(E=130, ld=130, groups=65), 3, "groups=65"), (dict(T=0, x=None, ids=None, w=None), 0, "")])
+    (dict(E=130, ld=130, groups=65), 3, "groups=65"), (dict(T=(1 << 25) + 1), 3, "2^25"), (dict(T=0, x=None, ids=None, w=None), 0, "")])
 def test_route_refusals(kw, status, needle):
     import moe_grouped_gemm_e4m3_amd as fg
 
