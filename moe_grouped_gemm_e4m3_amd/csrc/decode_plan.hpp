@@ -126,38 +126,48 @@ struct LayerPlan {
 inline int pairs_bytes(int E, int T, int k) { return E * 12 + T * k * 6 + 4; }
 inline bool wide_down(DownKind k) { return k >= kDownWide16; }
 
+// The rules are simple ones that lose least over 2600 layers of 1 to 68 tokens, 4
+// to 128 experts and weights of 256 to 2048 x 1024 to 7168: 1 to 2% of a layer's
+// time on average against the best kernel of each, for either half and format.
 inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const char* forced) {
   T = std::min(T, kLayerTokens);
   const int pairs = T * k, active = std::min(E, pairs);  // experts with tokens, at most
-  const int64_t wide4 = (int64_t)ceil_div(F, 64) * active, wide8 = (int64_t)ceil_div(F, 128) * active;
+  const int64_t wide8 = (int64_t)ceil_div(F, 128) * active;  // workgroups of 128 hidden units
   LayerPlan p{};
-  // up.  E4m3 weights (T=16, 16 of 16 experts of 2048 x 7168: wide 81, split 88;
-  // 8 of 2048 x 1024: wide 12.3, split 8.3; 32 of 2048 x 4096: wide 90, a deeper
-  // ring 82).  4-bit weights cost more arithmetic and LDS for each byte, so that
-  // sharing pays from four tokens on (T=4, 16 experts of 2048 x 7168: 49 for 56).
-  if (fp8)
-    p.up = T <= 4 ? kUpSplit4 : wide4 < 256 ? kUpSplit16 : K >= 4096 ? kUpWideDeep : kUpWide;
-  else if (T >= 4 && wide8 >= 384)
-    p.up = kUpWide8;
-  else if (T <= 4)
+  // up, by an expert's tokens.  Few of them want many small workgroups (e4m3, T=7,
+  // 64 experts of 1024 x 4096: split 37, wide 45; 4 bits, T=9, 16 of 2048 x 7168:
+  // split 95, wide 109); more of them, with work for every CU, waves that share
+  // their columns (4 bits, T=67, 8 of 1408 x 1024: wide 47, split 61; e4m3, T=38,
+  // 64 of 256 x 2048: wide 34, split 35), which long rows give a deeper ring (32
+  // of 2048 x 4096: 82 for 90).
+  if (fp8) {
+    if (2 * pairs < 5 * active || T <= 4)
+      p.up = T > 4 && K < 2048 && wide8 >= 256 ? kUpWide : kUpSplit4;
+    else
+      p.up = wide8 < 88 ? kUpSplit16 : wide8 < 176 || K >= 4096 ? kUpWideDeep : kUpWide;
+  } else if (2 * pairs < 9 * active) {
     // room for two tokens only leaves more workgroups on a CU (T=2, 16 experts of 2048 x 7168: 75 for 79)
-    p.up = T <= 2 ? kUpSplit2 : kUpSplit4;
-  else
-    p.up = wide4 >= 256 ? kUpWide : kUpSplit16;
+    p.up = T <= 2 ? kUpSplit2 : wide8 < 448 ? kUpSplit4 : kUpWide8;
+  } else {
+    p.up = wide8 < 88 ? kUpSplit16 : wide8 < 384 ? kUpWide : kUpWide8;
+  }
   for (int i = 0; i < kUpKinds; ++i)
     if (names(forced, kUpNames[i]) && (fp8 ? i != kUpWide8 && i != kUpSplit2 : i != kUpWideDeep)) p.up = (UpKind)i;
-  // down.  A third kernel costs about 3 us, so that small layers go without
-  // (T=8, 8 experts of 2048 x 1024: 9.7 for 13.0; 64 of 2048 x 704: 26.6 for 21.9).
-  const bool small = T <= 8 && pairs <= 2 * E && (int64_t)active * F * K <= (1 << 25);
+  // down.  A third kernel costs about 3 us, so that few pairs go without (e4m3,
+  // T=8, 8 experts of 512 x 1024: split 12, wide 16; 4 bits, T=9, 64 of 512 x 2048:
+  // 16 and 21), unless there are few outputs for much work (e4m3, T=5, 64 of 2048 x
+  // 1024: split 51, wide 40).
+  const bool few = pairs < (fp8 ? 26 : 22) && (K >= 2048 || (int64_t)active * F * K <= 1 << 24);
   const int tiles = ceil_div(K, 128);
-  if (T == 1)
-    p.down = K > 4096 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
-  else if (T <= 4 || small)
+  const bool one = 8 * pairs < 9 * active && (!fp8 || (int64_t)active * F * K < 43000000);  // a token for each expert
+  if (T == 1 || (few && one))
+    p.down = K > 4096 && T <= 16 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
+  else if (few)
     p.down = !fp8 && K > 4096 ? kDownSplit4Two : kDownSplit4;  // T=2, 4-bit, 7168 x 2048: 38 for 43; 4096 x 2048: 24 for 15
-  else if (pairs > 8 * E && (fp8 || pairs_bytes(E, T, k) <= 12 << 10))  // (4 bits: the rest of LDS is taken)
+  else if (pairs >= 14 * active && (fp8 || pairs_bytes(E, T, k) <= 12 << 10))  // (4 bits: the rest of LDS is taken)
     p.down = kDownWide32;  // T=64, 32 tokens an expert: 122 for 149; 6 tokens: 43 for 40
   else
-    p.down = fp8 && T > 16 ? kDownWide16Deep : kDownWide16;  // T=64, 8 tokens an expert: 66 for 83
+    p.down = fp8 && T >= 26 ? kDownWide16Deep : kDownWide16;  // T=64, 8 tokens an expert: 66 for 83
   for (int i = 0; i < kDownKinds; ++i)
     if (names(forced, kDownNames[i]) && (fp8 ? i != kDownSplit4Two : i != kDownWide16Deep) &&
         (i != kDownSplit1Two || T <= 16))  // its sums of more tokens do not fit LDS
