@@ -37,7 +37,8 @@
  * synchronises, so every call can be captured into a HIP graph (the masked
  * form, whose counts the host never learns, is made for that).  Scratch
  * memory, where a plan needs it, comes from the caller as a `workspace`
- * argument (gemm_fp8_nt_ws, the NN/TN/TT layouts, the K-grouped GEMM).  The
+ * argument (gemm_fp8_nt_ws, the NN/TN/TT layouts, the K-grouped GEMM, the gated
+ * backward pass, gemm_int4_nt, the expert layers).  The
  * one exception is the opt-in debug check FG_CHECK_DEVICE (see the grouped
  * calls), which reads a result back.
  *
@@ -583,12 +584,13 @@ fg_status int4_cast_per_group_bf16(const uint16_t* w, int64_t ldw, uint8_t* q, u
  *   D   device [M, N] bf16, row stride ldd elements (ldd >= N); only D[0:M, 0:N] is written
  *   workspace  NULL, or device, 256-byte aligned, fg_int4_workspace_bytes(M, N, K) bytes (0 for
  *       most sizes); needs no initialisation; in use until the call's work has finished
- * Made for M <= 64, where the weights are read once; more rows are taken 64 at a
- * time.  M <= 2^20, N <= 2^26, K % 32 == 0, K <= 2^20.  K == 0 writes zeros.  Sums are in
- * fp32, the zero point is taken out of a group's sum once, and the result is
- * rounded once.  A row of A with an infinity or a NaN gives a row of D that holds
- * infinities or NaN.  Sums have a fixed order, which depends on the sizes only.
- * D may not overlap an input.  Allocates nothing.
+ * Made for M <= 64, where HBM is read for the weights once; more rows are taken
+ * 16 to 64 at a time.  M <= 2^20, N <= 2^26, K % 32 == 0, K <= 2^20.  K == 0
+ * writes zeros.  Sums are in fp32, the zero point is taken out of a group's sum
+ * once, and the result is rounded once.  A row of A with an infinity or a NaN
+ * gives a row of D that holds infinities or NaN.  Sums have a fixed order, which
+ * depends on the sizes only.  The workspace and D may not overlap anything else.
+ * Allocates nothing.  Runs as one kernel, or two where the reduction is split.
  */
 fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const uint16_t* sb, const uint8_t* zb,
                        uint16_t* D, int64_t ldd, int M, int N, int K, int group, void* workspace,
@@ -615,8 +617,9 @@ typedef enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 } fg_scoring;
  * An expert whose logit (or bias) is -infinity is no candidate; places that no
  * candidate is left for hold id -1 and weight 0.  A NaN is chosen after all
  * numbers and gives NaN weights: under softmax all of its row's.
- * T <= 2^25, 1 <= k <= min(E, 64), E <= 1024, groups <= 64 divides E.  Scores and what they
- * are compared by are computed in 64 bits, weights are rounded once.
+ * T <= 2^25, 1 <= k <= min(E, 64), E <= 1024, groups <= 64 divides E.  Scores and
+ * what they are compared by are computed in 64 bits, weights are rounded once.
+ * One kernel, no workspace.
  */
 fg_status moe_route(const float* logits, int64_t ld, const float* bias, int32_t* ids, float* weights, int T, int E, int k,
                     int scoring, int groups, int top_groups, int normalize, float scale, void* stream);
@@ -637,7 +640,8 @@ fg_status moe_route_backward_bf16(const float* dweights, const uint16_t* logits,
                                   float scale, void* stream);
 
 /*
- * A whole expert layer for a few tokens, in two kernels (three for more tokens):
+ * A whole expert layer for a few tokens, in two kernels (for more of them a third
+ * adds partial sums):
  *     D[t] = bf16( sum_j weights[t,j] * W2[e] . h ),  e = ids[t,j],
  *     h = act(g) * u,  g = W1[e][0:F] . X[t],  u = W1[e][F:2F] . X[t].
  *   X    device [T, K] bf16, row stride ldx elements (ldx >= K, ldx % 8 == 0, 16-byte aligned, rows of at most 4 MiB)
@@ -654,11 +658,14 @@ fg_status moe_route_backward_bf16(const float* dweights, const uint16_t* logits,
  * Activations are not quantised: products are of bf16 X (or of h, kept as the sum
  * of two bf16) with the exact values of the codes, summed in fp32; D is rounded
  * once.  A token that names an expert twice has the sum of both weights.  The
- * weights of every named expert are read once for each 64 tokens; with many
- * tokens for each expert the grouped GEMMs are faster.  Sums have a fixed order,
+ * weights of every named expert are read once for each 64 tokens and, with more
+ * than 16 or 32 tokens of one expert, once more from cache for each as many;
+ * with hundreds of tokens the grouped GEMMs are faster.  Sums have a fixed order,
  * which depends on the sizes and ids only.
  * T <= 2^20, 1 <= k <= 32, 1 <= E <= 1024, K and F multiples of 16 up to 2^16.
- * F == 0 writes zeros.  D may not overlap an input.  Allocates nothing.
+ * F == 0 writes zeros.  The workspace and D may not overlap anything else; calls
+ * that may run at the same time (two streams, two graphs) need a workspace each.
+ * Allocates nothing.
  */
 fg_status moe_ffn_fp8(const uint16_t* X, int64_t ldx, const uint8_t* W1, const float* s1, const uint8_t* W2,
                       const float* s2, const int32_t* ids, const float* weights, uint16_t* D, int64_t ldd, int T, int k,
@@ -667,7 +674,7 @@ fg_status moe_ffn_fp8(const uint16_t* X, int64_t ldx, const uint8_t* W1, const f
 /*
  * The same on 4-bit weights (see int4_cast_per_group):
  *   W1, s1, z1  E matrices of [2F, K], one after the other; W2, s2, z2  E of [K, F]
- *   (z1 and z2 may both be NULL)
+ *   (z1 and z2 are both given, or both NULL: FG_EINVAL otherwise)
  * K and F multiples of 32 up to 2^16.  Everything else as moe_ffn_fp8.
  */
 fg_status moe_ffn_int4(const uint16_t* X, int64_t ldx, const uint8_t* W1, const uint16_t* s1, const uint8_t* z1,
@@ -684,7 +691,7 @@ int fg_get_mk_alignment_for_contiguous_layout(void);
 /* Cap on the compute units the GEMM kernels spread their persistent workgroups
  * over (the digest's set_num_sms); 0 (the default) means all of them.  Kernels
  * without persistent workgroups do not follow it: the few-row (decode) kernels,
- * the casts and copies, and the gated backward pass's gradient pair (from kept
+ * the casts and copies, the router, the 4-bit product and the few-token expert layers, and the gated backward pass's gradient pair (from kept
  * pre-activations or partial sums) and addition of partial sums.
  * Results do not depend on the cap (every tile is computed whole by one
  * workgroup), but for the bf16 gated block and its gradients, whose plan,

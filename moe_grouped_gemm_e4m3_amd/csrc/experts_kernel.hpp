@@ -4,13 +4,27 @@
 //   down  D[t] = bf16( sum_j w[t, j] W2[e] h_(t, j) )
 //
 // Every active expert's weights are read once for each 64 tokens
-// (weight_stream.hpp); that read is the time.  `up` has a workgroup for each
-// expert and 16 hidden units; its tokens are the rows of the matrix product.
-// `down` has a workgroup for each 16 or 32 outputs, which goes through all active
-// experts, so that the sum over experts never leaves it: its waves share out the
-// chunks of all experts' hidden units, evenly, each adds into sums of its own
-// (one for each token and output, in LDS), and these are added in wave order.
-// No sum depends on the order in which workgroups run.
+// (weight_stream.hpp); that read is the time where they are many (one token, 8
+// experts of 2048 x 7168 in e4m3: 352 MB in 69 us, 5.1 TB/s, what a copy reaches;
+// 64 tokens over 16 of them: 706 MB in 166 us, 4.3 TB/s).  `up` has workgroups for
+// each expert and tile of hidden units; an expert's tokens are the rows of the
+// matrix product.  `down` has workgroups for tiles of outputs, which go through
+// all active experts, so that the sum over experts stays inside: sums of its own
+// for each token and output, in LDS.  Both come in two organisations.
+//
+//   split  a tile is 16 units (or 16 or 32 outputs), and its waves share out the
+//          reduction, each with an LDS ring of its own, and are added in wave
+//          order: many independent small streams, for few tokens, where latency
+//          counts (one token, 6 experts of 704 x 2048 in 4 bits: 14.9 us)
+//   wide   a tile is 64 or 128 units (128 outputs), and its waves have rows of
+//          their own and share one copy of the tokens' columns, with a barrier a
+//          chunk: fewer bytes through LDS for a weight.  `down` then splits all
+//          experts' chunks over workgroups, whose sums a third kernel adds in
+//          their order (39 tokens, 64 experts of 2048 x 1024 in 4 bits: 86 us; in
+//          one part 818)
+//
+// No sum depends on the order in which workgroups run, and there are no atomics
+// on results.
 //
 // h passes through the workspace as the sum of two bf16 (16 significant bits):
 // as one its rounding would add as much error as the output's own, and both
@@ -26,8 +40,7 @@
 namespace fg {
 
 static_assert(kLayerTokens == 64, "a lane for each token");
-constexpr int kMaxExperts = 1024;   // `down` keeps a set of tokens for each in LDS
-constexpr int kMaxChoices = 32;
+constexpr int kMaxExperts = 1024, kMaxChoices = 32;  // `down` keeps them in LDS (Pairs): 25 KiB at most
 
 struct ExpertParams {
   const uint16_t* X;
@@ -208,7 +221,9 @@ __global__ __launch_bounds__(C::THREADS) void experts_up_kernel(ExpertParams p) 
   }
 }
 
-// ---- more tokens: the waves of a workgroup share the tokens' columns ----
+// ---- wide: the waves of a workgroup share the tokens' columns ----
+
+// PER: tiles of 16 hidden units of a wave.  MOST: tokens of an expert in one go.
 
 template <class Fmt_, int PER_, int WAVES_, int DEPTH_, int MOST_>
 struct WideUp {
@@ -272,7 +287,8 @@ __global__ __launch_bounds__(C::THREADS) void experts_wide_up_kernel(ExpertParam
   }
 }
 
-// MOST: tokens of an expert in one go (1, 4 or 16).
+// CF: tiles of 16 outputs.  MOST: tokens of an expert in one go (1 or 4).  Two
+// tiles halve the activations' loads for a weight, and the workgroups.
 template <class Fmt_, int CF_, int WAVES_, int DEPTH_, int MOST_>
 struct DownTile {
   using Fmt = Fmt_;
@@ -457,8 +473,9 @@ struct WideDown {
 };
 
 template <class C, int ROWS>
-__device__ __forceinline__ void wide_down_item(const ExpertParams& p, const Pairs& pairs, int t0, int T, int e, int base, int members, int n0, int c0, int c1,
-                                               uint8_t* ring, uint8_t* scales, float* sums) {
+__device__ __forceinline__ void wide_down_item(const ExpertParams& p, const Pairs& pairs, int t0, int T, int e, int base,
+                                               int members, int n0, int c0, int c1, uint8_t* ring, uint8_t* scales,
+                                               float* sums) {
   constexpr int MT = ROWS > 16 ? 2 : 1;
   using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 2>(ROWS), C::CF, 1, 2, C::RING, C::WAVES>;
   const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;

