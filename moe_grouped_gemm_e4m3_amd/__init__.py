@@ -903,7 +903,7 @@ def gemm_int4_nt(A, B, sb, D, zb=None, group=128, stream=None, workspace=None):
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws, ws_bytes = _byte_workspace(workspace, dev)
-    else:
+    elif M > 2:  # (one or two rows need none, and the query is a tenth of their call)
         ws_bytes = int4_workspace_bytes(M, N, K)
         if ws_bytes:
             with _on_stream(stream):

@@ -31,6 +31,7 @@ static void product(int M, int N, int K, const char* forced) {
   CHECK(p.k_parts == 1 || p.k_parts <= ceil_div(K, 256), "%d %d %d: a part without a chunk", M, N, K);
   CHECK(int4_partial_bytes(M, N, p) == (p.k_parts > 1 ? (int64_t)p.k_parts * M * N * 4 : 0), "%d %d %d", M, N, K);
   if (*forced) return;
+  CHECK(M > 2 || p.k_parts == 1, "%d %d %d: the Python binding brings no workspace here", M, N, K);
   // grids that a call without a forced plan has: threads in 32 bits, 2^16 row tiles
   if (p.kind >= kWide16) {
     const int rows = p.kind == kWide64 ? 64 : p.kind == kWide32 ? 32 : 16;
