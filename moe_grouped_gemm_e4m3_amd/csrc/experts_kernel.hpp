@@ -5,8 +5,8 @@
 //
 // Every active expert's weights are read once for each 64 tokens
 // (weight_stream.hpp); that read is the time where they are many (one token, 8
-// experts of 2048 x 7168 in e4m3: 352 MB in 69 us, 5.1 TB/s, what a copy reaches;
-// 64 tokens over 16 of them: 706 MB in 166 us, 4.3 TB/s).  `up` has workgroups for
+// experts of 2048 x 7168 in e4m3: 352 MB in 68 us, 5.2 TB/s, what a copy reaches;
+// 64 tokens over 16 of them: 706 MB in 154 us, 4.6 TB/s).  `up` has workgroups for
 // each expert and tile of hidden units; an expert's tokens are the rows of the
 // matrix product.  `down` has workgroups for tiles of outputs, which go through
 // all active experts, so that the sum over experts stays inside: sums of its own

@@ -193,7 +193,7 @@ __global__ __launch_bounds__(C::THREADS) void int4_product_kernel(Int4Params p) 
 
 // A tile of ROWS rows and 16 CF WAVES columns and a part of K; the waves share
 // the activations' columns ("wide"): a workgroup's X is read once for 128 columns
-// instead of 16.  64 x 7168 x 16384 takes 37 us (64 MB; 410 TFLOP/s) for 78 or
+// instead of 16.  64 x 7168 x 16384 takes 35.4 us (64 MB; 424 TFLOP/s) for 78 or
 // more of the split tiles: a chunk costs its 1.9 us of products, widening and LDS
 // reads, which is what bounds it, not the 13 us of its weights.
 template <class Fmt_, int ROWS_, int CF_, int WAVES_, int DEPTH_>
