@@ -655,9 +655,8 @@ fg_status moe_route_backward_bf16(const float* dweights, const uint16_t* logits,
  *   D    device [T, K] bf16, row stride ldd elements (ldd >= K); a token with no place left gets zeros
  *   workspace  device, 256-byte aligned, fg_moe_ffn_workspace_bytes(T, k, F) bytes; needs no
  *        initialisation; in use until the call's work has finished
- * Activations are not quantised: products are of bf16 X (or of h, kept as the sum
- * of two bf16) with the exact values of the codes, summed in fp32; D is rounded
- * once.  A token that names an expert twice has the sum of both weights.  The
+ * Activations are not quantised: products are of bf16 X (or of h, kept in fp32)
+ * with the exact values of the codes, summed in fp32; D is rounded once.  A token that names an expert twice has the sum of both weights.  The
  * weights of every named expert are read once for each 64 tokens and, with more
  * than 16 or 32 tokens of one expert, once more from cache for each as many;
  * with hundreds of tokens the grouped GEMMs are faster.  Sums have a fixed order,

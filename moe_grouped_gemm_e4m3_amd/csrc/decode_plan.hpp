@@ -122,9 +122,42 @@ struct LayerPlan {
   DownKind down;
   int parts;  // wide down: parts of the experts' chunks, joined by a third kernel
 };
-// LDS bytes of what `down` knows of a pass's pairs (experts_kernel.hpp).
+inline constexpr bool wide_down(DownKind k) { return k >= kDownWide16; }
+
+// The `down` kernels: tiles of 16 outputs of a wave, waves, ring slots, tokens of an
+// expert in one go.  4 bits: the activations of 32 tokens instead of 24 would not
+// leave LDS for the sums of 64.
+struct DownShape {
+  int tiles, waves, depth, rows;
+};
+constexpr DownShape down_shape(bool fp8, DownKind k) {
+  return k == kDownSplit1       ? DownShape{1, 8, 2, 1}
+         : k == kDownSplit1Two  ? DownShape{2, 8, fp8 ? 3 : 2, 1}
+         : k == kDownSplit4     ? DownShape{1, 8, 2, 4}
+         : k == kDownSplit4Two  ? DownShape{2, 4, 3, 4}
+         : k == kDownWide16     ? DownShape{2, 4, 2, 16}
+         : k == kDownWide16Deep ? DownShape{2, 4, 3, 16}
+                                : DownShape{2, 4, fp8 ? 3 : 2, fp8 ? 32 : 24};
+}
+// KiB of `rows` bf16 rows of a chunk's activations.
+constexpr int x_kib(bool fp8, int rows) { return rows * (fp8 ? 256 : 512) > 1024 ? rows * (fp8 ? 256 : 512) / 1024 : 1; }
+// LDS bytes of a wave's scales: 4-bit groups of each row of its tiles, and one word between rows.
+constexpr int scale_bytes(bool fp8, int tiles, int groups = 32) { return fp8 ? 0 : 16 * tiles * (groups + 1) * 4; }
+// LDS bytes of `down`: weights of a split wave or of all wide ones, and three bf16 of each hidden unit of a chunk
+// (where waves share them two times).
+constexpr int down_ring(bool fp8, DownKind k) {
+  const DownShape s = down_shape(fp8, k);
+  return s.depth * (wide_down(k) ? s.waves : 1) * s.tiles * 2048;
+}
+constexpr int down_x(bool fp8, DownKind k) { return down_shape(fp8, k).rows * 3 * (fp8 ? 256 : 512) * (wide_down(k) ? 2 : 1); }
+// What `down` knows of a pass's pairs (experts_kernel.hpp).
 inline int pairs_bytes(int E, int T, int k) { return E * 12 + T * k * 6 + 4; }
-inline bool wide_down(DownKind k) { return k >= kDownWide16; }
+inline int down_lds(bool fp8, DownKind kind, int T, int E, int k) {
+  const DownShape s = down_shape(fp8, kind);
+  const int own = down_ring(fp8, kind) + down_x(fp8, kind), scales = scale_bytes(fp8, s.tiles), sums = T * s.tiles * 64;
+  return (wide_down(kind) ? own + s.waves * (scales + sums) : s.waves * (own + scales + sums)) + pairs_bytes(E, T, k);
+}
+constexpr int kLds = 160 * 1024;
 
 // The rules are simple ones that lose least over 2600 layers of 1 to 68 tokens, 4
 // to 128 experts and weights of 256 to 2048 x 1024 to 7168: 1 to 2% of a layer's
@@ -164,10 +197,12 @@ inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const c
     p.down = K > 4096 && T <= 16 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
   else if (few)
     p.down = !fp8 && K > 4096 ? kDownSplit4Two : kDownSplit4;  // T=2, 4-bit, 7168 x 2048: 38 for 43; 4096 x 2048: 24 for 15
-  else if (pairs >= 14 * active && (fp8 || pairs_bytes(E, T, k) <= 12 << 10))  // (4 bits: the rest of LDS is taken)
+  else if (pairs >= 14 * active)
     p.down = kDownWide32;  // T=64, 32 tokens an expert: 122 for 149; 6 tokens: 43 for 40
   else
     p.down = fp8 && T >= 26 ? kDownWide16Deep : kDownWide16;  // T=64, 8 tokens an expert: 66 for 83
+  // what many experts or pairs leave no LDS for
+  if (down_lds(fp8, p.down, T, E, k) > kLds) p.down = kDownWide16;
   for (int i = 0; i < kDownKinds; ++i)
     if (names(forced, kDownNames[i]) && (fp8 ? i != kDownSplit4Two : i != kDownWide16Deep) &&
         (i != kDownSplit1Two || T <= 16))  // its sums of more tokens do not fit LDS

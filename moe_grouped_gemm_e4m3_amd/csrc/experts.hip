@@ -163,7 +163,7 @@ struct LayerLaunch {
 
   template <class C>
   fg_status down() const {
-    const int T = std::min(p.T, kLayerTokens), lds = C::lds_bytes(T) + pairs_bytes(p.E, T, p.k);
+    const int lds = down_lds(C::Fmt::FP8, plan.down, std::min(p.T, kLayerTokens), p.E, p.k);
     FG_TRY(allow_lds((const void*)experts_down_kernel<C>, lds, what));
     print("down", kDownNames[plan.down], 1);
     hipLaunchKernelGGL((experts_down_kernel<C>), dim3(ceil_div(p.K, C::COLS), passes), dim3(C::THREADS), lds,
@@ -174,7 +174,7 @@ struct LayerLaunch {
   // A pass of tokens at a time: they share the partial sums' place.
   template <class C>
   fg_status down_wide() const {
-    const int most = std::min(p.T, kLayerTokens), lds = C::lds_bytes(most) + pairs_bytes(p.E, most, p.k);
+    const int lds = down_lds(C::Fmt::FP8, plan.down, std::min(p.T, kLayerTokens), p.E, p.k);
     FG_TRY(allow_lds((const void*)experts_wide_down_kernel<C>, lds, what));
     for (int t0 = 0; t0 < p.T; t0 += kLayerTokens) {
       const int T = std::min(kLayerTokens, p.T - t0);
@@ -217,18 +217,18 @@ fg_status launch_layer(const ExpertParams& p, void* stream, const char* what) {
     FG_TRY(st);
   }
   switch (plan.down) {
-    case kDownSplit1: return l.down<DownTile<Fmt, 1, 8, 2, 1>>();
-    case kDownSplit1Two: return l.down<DownTile<Fmt, 2, 8, Fmt::FP8 ? 3 : 2, 1>>();
-    case kDownSplit4: return l.down<DownTile<Fmt, 1, 8, 2, 4>>();
+    case kDownSplit1: return l.down<DownTile<Fmt, kDownSplit1>>();
+    case kDownSplit1Two: return l.down<DownTile<Fmt, kDownSplit1Two>>();
+    case kDownSplit4: return l.down<DownTile<Fmt, kDownSplit4>>();
     case kDownSplit4Two:
-      if constexpr (!Fmt::FP8) return l.down<DownTile<Fmt, 2, 4, 3, 4>>();
+      if constexpr (!Fmt::FP8) return l.down<DownTile<Fmt, kDownSplit4Two>>();
       break;
-    case kDownWide16: return l.down_wide<WideDown<Fmt, 2, 4, 2, 16>>();
+    case kDownWide16: return l.down_wide<WideDown<Fmt, kDownWide16>>();
     case kDownWide16Deep:
-      if constexpr (Fmt::FP8) return l.down_wide<WideDown<Fmt, 2, 4, 3, 16>>();
+      if constexpr (Fmt::FP8) return l.down_wide<WideDown<Fmt, kDownWide16Deep>>();
       break;
     // a third slot (4 bits have no LDS for it): T=64, 16 experts of 2048 x 7168, 32 tokens each: 231 us for 242
-    case kDownWide32: return l.down_wide<WideDown<Fmt, 2, 4, Fmt::FP8 ? 3 : 2, 32>>();
+    case kDownWide32: return l.down_wide<WideDown<Fmt, kDownWide32>>();
     default: break;
   }
   return FG_OK;
@@ -322,7 +322,7 @@ fg_status moe_ffn_fp8(const uint16_t* X, int64_t ldx, const uint8_t* W1, const f
   clear_error();
   ExpertParams p{};
   p.X = X; p.ldx = ldx; p.W1 = W1; p.s1 = s1; p.W2 = W2; p.s2 = s2; p.ids = ids; p.w = weights; p.D = D; p.ldd = ldd;
-  p.H = (uint16_t*)workspace;
+  p.H = (float*)workspace;
   p.T = T; p.k = k; p.E = E; p.F = F; p.K = K; p.act = activation;
   bool empty;
   FG_TRY(check_layer(p, 16, workspace, workspace_bytes, 4, &empty));
@@ -340,7 +340,7 @@ fg_status moe_ffn_int4(const uint16_t* X, int64_t ldx, const uint8_t* W1, const 
   ExpertParams p{};
   p.X = X; p.ldx = ldx; p.W1 = W1; p.s1 = s1; p.z1 = z1; p.W2 = W2; p.s2 = s2; p.z2 = z2; p.ids = ids; p.w = weights;
   p.D = D; p.ldd = ldd;
-  p.H = (uint16_t*)workspace;
+  p.H = (float*)workspace;
   p.T = T; p.k = k; p.E = E; p.F = F; p.K = K; p.act = activation; p.group = group;
   FG_TRY(check_group(group));
   if ((z1 != nullptr) != (z2 != nullptr)) return set_error(FG_EINVAL, "z1 and z2: one of them is NULL");

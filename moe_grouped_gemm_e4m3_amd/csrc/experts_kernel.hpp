@@ -26,9 +26,9 @@
 // No sum depends on the order in which workgroups run, and there are no atomics
 // on results.
 //
-// h passes through the workspace as the sum of two bf16 (16 significant bits):
-// as one its rounding would add as much error as the output's own, and both
-// products of a weight tile cost less than the tile's load.
+// h is held in 32 bits: it passes through the workspace as fp32, and `down` makes
+// three bf16 of it in LDS whose sum it is exactly, three products of a weight tile
+// in the place of one.
 //
 // A token that names an expert twice has one product with the sum of both
 // weights, at the first of the two places.
@@ -52,7 +52,7 @@ struct ExpertParams {
   const float* w;
   uint16_t* D;
   int64_t ldd;
-  uint16_t* H;  // [T k][2][F]: both parts of every pair's h
+  float* H;  // [T k][F]: every pair's h
   int T, k, E, F, K, act;
   int group;
   int row1, row2;        // bytes of a weight row
@@ -88,23 +88,10 @@ __device__ __forceinline__ void clear(f32x4 (&acc)[S::MT][S::CF]) {
     for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 }
 
-// h of token t's place j and hidden unit f, as the sum of two bf16.
+// h of token t's place j and hidden unit f.
 __device__ __forceinline__ void store_hidden(const ExpertParams& p, int t, int j, int f, float g, float u) {
-  const float h = p.act == kActSilu ? gated_value<kActSilu>(g, u) : gated_value<kActGeluTanh>(g, u);
-  uint16_t top = bf16_bits(h);
-  if ((top & 0x7fff) == 0x7f80 && __builtin_fabsf(h) < __builtin_inff()) --top;  // no infinity by rounding
-  // the rest of an infinity or a NaN would be a NaN
-  const float rest = (top & 0x7f80) == 0x7f80 ? 0.f : h - to_f32(top);
-  uint16_t* dst = p.H + ((int64_t)t * p.k + j) * 2 * p.F + f;
-  dst[0] = top;
-  dst[p.F] = bf16_bits(rest);
-}
-
-// KiB of X in a chunk that holds `rows` rows.
-template <class Fmt, int PARTS>
-constexpr int x_kib(int rows) {
-  const int kib = rows * PARTS * (Fmt::FP8 ? 256 : 512) / 1024;
-  return kib > 1 ? kib : 1;
+  p.H[((int64_t)t * p.k + j) * p.F + f] =
+      p.act == kActSilu ? gated_value<kActSilu>(g, u) : gated_value<kActGeluTanh>(g, u);
 }
 
 // PER: tiles of 16 hidden units.  MOST: tokens of an expert in one go (2, 4 or 16).
@@ -113,7 +100,7 @@ struct UpTile {
   using Fmt = Fmt_;
   static constexpr bool WIDE = false;
   static constexpr int PER = PER_, WAVES = WAVES_, MOST = MOST_;
-  static constexpr int RING = DEPTH_ * (2 * PER * 2048 + x_kib<Fmt, 1>(MOST) * 1024);
+  static constexpr int RING = DEPTH_ * (2 * PER * 2048 + x_kib(Fmt::FP8, MOST) * 1024);
   static constexpr int MT = MOST > 16 ? 2 : 1, THREADS = 64 * WAVES, UNITS = 16 * PER;
   static constexpr int WAVE_LDS = RING + scale_lds<Fmt, 2 * PER>();
   static constexpr int BLOCKS = 2 * PER * MT;  // 16 x 16 sums of a wave
@@ -125,7 +112,7 @@ template <class C, int ROWS>
 __device__ __forceinline__ void up_tile(const ExpertParams& p, int e, int t0, int f0, int base, int members,
                                         const int* list, uint8_t* lds) {
   constexpr int MT = ROWS > 16 ? 2 : 1;
-  using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 1>(ROWS), 2 * C::PER, 2, 1, C::RING>;
+  using S = Stream<typename C::Fmt, MT, x_kib(C::Fmt::FP8, ROWS), 2 * C::PER, 2, 0, C::RING>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Sources<S> src;
@@ -142,7 +129,7 @@ __device__ __forceinline__ void up_tile(const ExpertParams& p, int e, int t0, in
   clear<S>(acc);
   uint8_t* mine = lds + wave * C::WAVE_LDS;
   const int chunks = (p.K + S::COLS - 1) / S::COLS;
-  stream_chunks<S>(acc, src, mine, (uint32_t*)(mine + C::RING), chunks * wave / C::WAVES, chunks * (wave + 1) / C::WAVES,
+  stream_chunks<S>(acc, src, mine, nullptr, (uint32_t*)(mine + C::RING), chunks * wave / C::WAVES, chunks * (wave + 1) / C::WAVES,
                    5 * blockIdx.x);
   f32x4* sums = (f32x4*)mine;
 #pragma unroll
@@ -231,7 +218,7 @@ struct WideUp {
   static constexpr bool WIDE = true;
   static constexpr int PER = PER_, WAVES = WAVES_, THREADS = 64 * WAVES, UNITS = 16 * PER * WAVES, MOST = MOST_;
   static constexpr int SCALES = Fmt::GPC == 4 ? 64 : 32;
-  static constexpr int RING = DEPTH_ * (WAVES * PER * 4096 + x_kib<Fmt, 1>(MOST) * 1024);
+  static constexpr int RING = DEPTH_ * (WAVES * PER * 4096 + x_kib(Fmt::FP8, MOST) * 1024);
   static constexpr int SCALE_LDS = scale_lds<Fmt, 2 * PER, SCALES>();  // of a wave
   static constexpr int LDS = RING + WAVES * SCALE_LDS;
 };
@@ -240,7 +227,7 @@ template <class C, int ROWS>
 __device__ __forceinline__ void wide_up_tile(const ExpertParams& p, int e, int t0, int f0, int base, int members,
                                              const int* list, uint8_t* ring, uint8_t* scales) {
   constexpr int MT = ROWS > 16 ? 2 : 1;
-  using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 1>(ROWS), 2 * C::PER, 2, 1, C::RING, C::WAVES, C::SCALES>;
+  using S = Stream<typename C::Fmt, MT, x_kib(C::Fmt::FP8, ROWS), 2 * C::PER, 2, 0, C::RING, C::WAVES, C::SCALES>;
   const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Sources<S> src;
@@ -255,7 +242,7 @@ __device__ __forceinline__ void wide_up_tile(const ExpertParams& p, int e, int t
   for (int i = 0; i < S::X_LOADS; ++i) src.x_off[i] = (list[min(base + x_row_of<S>(i), members - 1)] & 63) * (int)(2 * p.ldx);
   f32x4 acc[MT][2 * C::PER];
   clear<S>(acc);
-  stream_chunks<S>(acc, src, ring, (uint32_t*)(scales + wave * C::SCALE_LDS), 0, (p.K + S::COLS - 1) / S::COLS,
+  stream_chunks<S>(acc, src, ring, nullptr, (uint32_t*)(scales + wave * C::SCALE_LDS), 0, (p.K + S::COLS - 1) / S::COLS,
                    5 * blockIdx.x);
 #pragma unroll
   for (int t = 0; t < MT; ++t)
@@ -288,15 +275,16 @@ __global__ __launch_bounds__(C::THREADS) void experts_wide_up_kernel(ExpertParam
 }
 
 // CF: tiles of 16 outputs.  MOST: tokens of an expert in one go (1 or 4).  Two
-// tiles halve the activations' loads for a weight, and the workgroups.
-template <class Fmt_, int CF_, int WAVES_, int DEPTH_, int MOST_>
+// tiles halve the activations' loads for a weight, and the workgroups.  LDS sizes
+// are those of down_lds.
+template <class Fmt_, DownKind KIND_>
 struct DownTile {
   using Fmt = Fmt_;
-  static constexpr int CF = CF_, WAVES = WAVES_, MOST = MOST_;
-  static constexpr int RING = DEPTH_ * (CF * 2048 + x_kib<Fmt, 2>(MOST) * 1024);
+  static constexpr DownShape SHAPE = down_shape(Fmt::FP8, KIND_);
+  static constexpr int CF = SHAPE.tiles, WAVES = SHAPE.waves, MOST = SHAPE.rows;
+  static constexpr int RING = down_ring(Fmt::FP8, KIND_), X_BYTES = down_x(Fmt::FP8, KIND_);
   static constexpr int THREADS = 64 * WAVES, COLS = 16 * CF;
-  static constexpr int WAVE_LDS = RING + scale_lds<Fmt, CF>();
-  static int lds_bytes(int T) { return WAVES * (WAVE_LDS + T * COLS * 4); }
+  static constexpr int WAVE_LDS = RING + X_BYTES + scale_lds<Fmt, CF>();
 };
 
 // What `down` knows of the pairs, in dynamic LDS: the experts with tokens, and
@@ -391,7 +379,7 @@ __device__ __forceinline__ Member member(const ExpertParams& p, const Pairs& s, 
 
 // Grid: tiles of COLS outputs, passes of 64 tokens.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p) {
+__global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, 4))) void experts_down_kernel(ExpertParams p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -402,7 +390,8 @@ __global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p
   for (int i = tid; i < C::WAVES * T * C::COLS; i += C::THREADS) sums[i] = 0.f;
   sort_pairs(pairs, p, t0, T);
 
-  using S = Stream<typename C::Fmt, 1, x_kib<typename C::Fmt, 2>(C::MOST), C::CF, 1, 2, C::RING>;
+  using S = Stream<typename C::Fmt, 1, 0, C::CF, 1, C::MOST, C::RING>;
+  static_assert(S::X_BYTES == C::X_BYTES, "LDS");
   const int chunks = (p.F + S::COLS - 1) / S::COLS;
   const int items = __builtin_amdgcn_readfirstlane(*pairs.items), total = items * chunks;
   int at = (int)((int64_t)total * wave / C::WAVES), end = (int)((int64_t)total * (wave + 1) / C::WAVES);
@@ -426,16 +415,16 @@ __global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p
       Sources<S> src;
       src.K = p.F;
       set_group(src, p.group);
-      src.x = make_rsrc(p.H + (int64_t)t0 * p.k * 2 * p.F, (int64_t)T * p.k * 4 * p.F);
+      src.x = make_rsrc(p.H + (int64_t)t0 * p.k * p.F, (int64_t)T * p.k * 4 * p.F);
       set_weights(src, 0, p.W2, p.s2, p.z2, e, p.K, n0, p.row2, p.groups2);
 #pragma unroll
       for (int i = 0; i < S::X_LOADS; ++i) {
         const int r = min(x_row_of<S>(i), rows - 1);
-        src.x_off[i] = __shfl(me.pair, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
+        src.x_off[i] = __shfl(me.pair, r) * 4 * p.F;
       }
       f32x4 acc[S::MT][S::CF];
       clear<S>(acc);
-      stream_chunks<S>(acc, src, ring, (uint32_t*)(ring + C::RING), c0, c1, 5 * blockIdx.x);
+      stream_chunks<S>(acc, src, ring, ring + C::RING, (uint32_t*)(ring + C::RING + C::X_BYTES), c0, c1, 5 * blockIdx.x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = 4 * quarter + i;
@@ -462,14 +451,16 @@ __global__ __launch_bounds__(C::THREADS) void experts_down_kernel(ExpertParams p
 // Waves share an item's hidden units; a workgroup does a part of all items'
 // chunks for COLS outputs and, with more than one part, leaves its sums to
 // join_parts_kernel.
-template <class Fmt_, int CF_, int WAVES_, int DEPTH_, int MOST_>
+template <class Fmt_, DownKind KIND_>
 struct WideDown {
   using Fmt = Fmt_;
-  static constexpr int CF = CF_, WAVES = WAVES_, THREADS = 64 * WAVES, COLS = 16 * CF * WAVES, MOST = MOST_;
-  static constexpr int RING = DEPTH_ * (WAVES * CF * 2048 + x_kib<Fmt, 2>(MOST) * 1024);
+  static constexpr DownShape SHAPE = down_shape(Fmt::FP8, KIND_);
+  static constexpr int CF = SHAPE.tiles, WAVES = SHAPE.waves, COLS = 16 * CF * WAVES, MOST = SHAPE.rows;
+  static constexpr int THREADS = 128 * WAVES;  // waves that multiply, then as many that split hidden units
+  static constexpr int RING = down_ring(Fmt::FP8, KIND_), X_BYTES = down_x(Fmt::FP8, KIND_);
+  static constexpr int EU_WAVES = Fmt::FP8 && MOST == 16 ? 4 : 2;  // that LDS leaves room for, at most
   static constexpr int SCALE_LDS = scale_lds<Fmt, CF>();
-  static constexpr int TOKENS_AT = RING + WAVES * SCALE_LDS;
-  static int lds_bytes(int T) { return TOKENS_AT + T * COLS * 4; }
+  static constexpr int TOKENS_AT = RING + X_BYTES + WAVES * SCALE_LDS;
 };
 
 template <class C, int ROWS>
@@ -477,7 +468,8 @@ __device__ __forceinline__ void wide_down_item(const ExpertParams& p, const Pair
                                                int members, int n0, int c0, int c1, uint8_t* ring, uint8_t* scales,
                                                float* sums) {
   constexpr int MT = ROWS > 16 ? 2 : 1;
-  using S = Stream<typename C::Fmt, MT, x_kib<typename C::Fmt, 2>(ROWS), C::CF, 1, 2, C::RING, C::WAVES>;
+  using S = Stream<typename C::Fmt, MT, 0, C::CF, 1, ROWS, C::RING, C::WAVES>;
+  static_assert(2 * S::X_BYTES <= C::X_BYTES, "LDS");
   const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int rows = min(ROWS, members - base);
@@ -485,17 +477,18 @@ __device__ __forceinline__ void wide_down_item(const ExpertParams& p, const Pair
   Sources<S> src;
   src.K = p.F;
   set_group(src, p.group);
-  src.x = make_rsrc(p.H + (int64_t)t0 * p.k * 2 * p.F, (int64_t)T * p.k * 4 * p.F);
+  src.x = make_rsrc(p.H + (int64_t)t0 * p.k * p.F, (int64_t)T * p.k * 4 * p.F);
   set_weights(src, 0, p.W2, p.s2, p.z2, e, p.K, min(n0 + 16 * C::CF * wave, p.K - 16), p.row2,
               p.groups2);  // past K: some rows that are there, for nothing
 #pragma unroll
   for (int i = 0; i < S::X_LOADS; ++i) {
     const int r = min(x_row_of<S>(i), rows - 1);
-    src.x_off[i] = __shfl(me.pair, r) * 4 * p.F + x_part_of<S>() * 2 * p.F;
+    src.x_off[i] = __shfl(me.pair, r) * 4 * p.F;
   }
+  if (wave >= C::WAVES) return split_chunks<S>(src, ring + C::RING, c0, c1, 5 * blockIdx.x);
   f32x4 acc[MT][C::CF];
   clear<S>(acc);
-  stream_chunks<S>(acc, src, ring, (uint32_t*)(scales + wave * C::SCALE_LDS), c0, c1, 5 * blockIdx.x);
+  stream_chunks<S>(acc, src, ring, ring + C::RING, (uint32_t*)(scales + wave * C::SCALE_LDS), c0, c1, 5 * blockIdx.x);
   float* mine = sums + 16 * C::CF * wave + l16;
 #pragma unroll
   for (int t = 0; t < MT; ++t)
@@ -513,12 +506,12 @@ __device__ __forceinline__ void wide_down_item(const ExpertParams& p, const Pair
 
 // Grid: tiles of COLS outputs, parts.  One pass of tokens from t0 on.
 template <class C>
-__global__ __launch_bounds__(C::THREADS) void experts_wide_down_kernel(ExpertParams p, int t0, float* partial) {
+__global__ __launch_bounds__(C::THREADS) __attribute__((amdgpu_waves_per_eu(2, C::EU_WAVES))) void experts_wide_down_kernel(ExpertParams p, int t0, float* partial) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
   const int tid = threadIdx.x;
   const int T = min(kLayerTokens, p.T - t0);
   const int n0 = blockIdx.x * C::COLS;
-  uint8_t* scales = lds + C::RING;
+  uint8_t* scales = lds + C::RING + C::X_BYTES;
   float* sums = (float*)(lds + C::TOKENS_AT);  // [T][COLS]
   const Pairs pairs = pairs_at((uint8_t*)(sums + T * C::COLS), p.E, T * p.k);
   for (int i = tid; i < T * C::COLS; i += C::THREADS) sums[i] = 0.f;

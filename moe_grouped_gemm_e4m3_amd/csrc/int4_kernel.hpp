@@ -145,7 +145,7 @@ struct Int4Tile {
   static constexpr int MT = (ROWS_ + 15) / 16, CF = CF_, WAVES = WAVES_;
   static constexpr int NX = ROWS_ > 2 ? ROWS_ / 2 : 1;
   static constexpr int RING = DEPTH_ * (CF * 2048 + NX * 1024);
-  using S = Stream<Fmt, MT, NX, CF, 1, 1, RING>;
+  using S = Stream<Fmt, MT, NX, CF, 1, 0, RING>;
   static constexpr int THREADS = 64 * WAVES, ROWS = ROWS_, COLS = 16 * CF;
   static constexpr int BLOCKS = MT * CF;
   static constexpr int WAVE_LDS = RING + scale_lds<Fmt, CF>();
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(C::THREADS) void int4_product_kernel(Int4Params p) 
     for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
   uint8_t* mine = lds + wave * C::WAVE_LDS;
   const int chunks = (p.K + S::COLS - 1) / S::COLS;
-  stream_chunks<S>(acc, src, mine, (uint32_t*)(mine + C::RING), chunks * wave / C::WAVES, chunks * (wave + 1) / C::WAVES,
+  stream_chunks<S>(acc, src, mine, nullptr, (uint32_t*)(mine + C::RING), chunks * wave / C::WAVES, chunks * (wave + 1) / C::WAVES,
                    5 * tile);
   f32x4* sums = (f32x4*)mine;
 #pragma unroll
@@ -201,7 +201,7 @@ struct Int4Wide {
   using Fmt = Fmt_;
   static constexpr int MT = ROWS_ / 16, CF = CF_, WAVES = WAVES_, ROWS = ROWS_;
   static constexpr int RING = DEPTH_ * (WAVES * CF * 2048 + ROWS * 512);
-  using S = Stream<Fmt, MT, ROWS / 2, CF, 1, 1, RING, WAVES>;
+  using S = Stream<Fmt, MT, ROWS / 2, CF, 1, 0, RING, WAVES>;
   static constexpr int THREADS = 64 * WAVES, COLS = 16 * CF * WAVES;
   static constexpr int SCALE_LDS = scale_lds<Fmt, CF>(), LDS = RING + WAVES * SCALE_LDS;
 };
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(C::THREADS) void int4_wide_kernel(Int4Params p, flo
     for (int c = 0; c < S::CF; ++c) acc[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int chunks = (p.K + S::COLS - 1) / S::COLS;
   const int first = (int)((int64_t)chunks * blockIdx.z / gridDim.z), end = (int)((int64_t)chunks * (blockIdx.z + 1) / gridDim.z);
-  stream_chunks<S>(acc, src, lds, (uint32_t*)(lds + C::RING + wave * C::SCALE_LDS), first, end, 5 * blockIdx.x);
+  stream_chunks<S>(acc, src, lds, nullptr, (uint32_t*)(lds + C::RING + wave * C::SCALE_LDS), first, end, 5 * blockIdx.x);
 #pragma unroll
   for (int t = 0; t < S::MT; ++t)
 #pragma unroll

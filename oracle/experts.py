@@ -7,7 +7,7 @@ Bounds (eps32 = 2^-24 and eps16 = 2^-8, as in oracle/linear.py):
   of each term (scales, zero points, partial sums of waves) add as many eps32;
 * with a zero point z the kernel sums x q and z x apart, so the terms are
   s |x| (q + z), not s |x| |q - z|;
-* a hidden unit kept as the sum of two bf16 is off by eps16^2 |h|;
+* a hidden unit is kept in fp32;
 * the router computes in 64 bits and rounds once to its output's type.
 """
 
@@ -121,8 +121,7 @@ def layer(X, W1, W2, ids, w, act):
             g, u, dg, du = p[:, :F], p[:, F:], ep[:, :F], ep[:, F:]
             y, _, s, _ = _gate(g, act)
             h = g * s * u
-            dh = ((np.abs(y) + 8) * 2 * EPS32 + EPS16 ** 2) * np.abs(h) + 1.13 * dg * (np.abs(u) + du) \
-                + np.abs(g * s) * du + TINY16
+            dh = (np.abs(y) + 8) * 2 * EPS32 * np.abs(h) + 1.13 * dg * (np.abs(u) + du) + np.abs(g * s) * du + TINY16
             out, _ = product(h, *W2[e])
             terms = (np.abs(h) + dh) @ W2[e][1].T
             D[t] += c * out[0]

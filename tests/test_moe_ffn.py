@@ -223,6 +223,64 @@ def test_hidden_units_next_to_the_largest_number(gpu_lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fmt", ["fp8", ("int4", 32, True), ("int4", 64, True), ("int4", 128, True)], ids=str)
+@pytest.mark.parametrize("T", [1, 3, 20, 64])
+@pytest.mark.parametrize("plan", [""] + DOWNS)
+def test_hidden_units_keep_24_bits(gpu_lib, monkeypatch, fmt, T, plan):
+    """Hidden units of 64 (1 + 2^-10 + 2^-20) and 64 (1 + 2^-10), subtracted: every step of the formula is exact in fp32, and
+    what is left are the 24-bit value's last bits alone.  64 and 2^-14 are bf16: the result has no tolerance."""
+    if T > 16 and plan == "down-split1-two":
+        pytest.skip("sums of 16 tokens at most")
+    announce(f"layer 24 bits {fmt} T={T} {plan}")
+    monkeypatch.setenv("FG_DECODE_PLAN", plan)
+    F, K, a, b = 288, 32, 5, 261  # the hidden units: in different chunks, blocks and groups
+    layer = Layer(fmt, 1, F, K)
+    one = 0x38 if fmt == "fp8" else 1
+    for W in (layer.W1, layer.W2):
+        if fmt == "fp8":
+            W.codes[:], W.s[:] = 0, 1.0
+        else:
+            W.q[:], W.s[:], W.z[:] = 0, 1.0, 0
+    up = layer.W1.codes if fmt == "fp8" else layer.W1.q
+    down = layer.W2.codes if fmt == "fp8" else layer.W2.q
+    for f in (a, b):
+        up[0, f, 0] = one  # g = x_0 = 64, where the gate is 1
+        up[0, F + f, 1] = up[0, F + f, 2] = one
+    up[0, F + a, 3] = one
+    down[0, :, a] = down[0, :, b] = one
+    if fmt == "fp8":
+        layer.W2.codes[0, :, b] |= 0x80
+    else:
+        layer.W2.s[0, :, b // fmt[1]] = -1.0
+    X = torch.zeros(T, K)
+    X[:, 0], X[:, 1], X[:, 2], X[:, 3] = 64.0, 1.0, 2.0 ** -10, 2.0 ** -20
+    X[:, 1:] *= torch.tensor([1.0, -2.0, 0.5, 2.0 ** 40])[torch.arange(T) % 4, None]
+    ids, w, D = torch.zeros(T, 1, dtype=torch.int32), torch.ones(T, 1), Output(T, K)
+    layer.call(gpu_lib, bf16(X).cuda(), ids.cuda(), w.cuda(), D.t)
+    D.check_untouched()
+    assert np.array_equal(D.f64(), np.repeat(f64(64 * X[:, 3:4]), K, axis=1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("plan", [""] + DOWNS)
+def test_infinite_hidden_units_stay_infinite(gpu_lib, monkeypatch, plan):
+    """A hidden unit past fp32 is an infinity and the sum with it one too, of its sign; a NaN stays a NaN."""
+    announce(f"layer infinite h {plan}")
+    monkeypatch.setenv("FG_DECODE_PLAN", plan)
+    layer = Layer("fp8", 1, 16, 16)
+    layer.W1.codes[:], layer.W1.s[:] = 0, 1.0
+    layer.W1.codes[0, 0, 0] = layer.W1.codes[0, 16, 1] = 0x38
+    layer.W2.codes[:], layer.W2.s[:] = 0x38, 1.0
+    X = torch.zeros(4, 16, dtype=torch.bfloat16)
+    X[:, 0] = 2.0 ** 100
+    X[0, 1], X[1, 1], X[2, 1], X[3, 1] = 2.0 ** 100, -2.0 ** 100, float("nan"), 2.0 ** -100
+    ids, w, D = torch.zeros(4, 1, dtype=torch.int32), torch.ones(4, 1), Output(4, 16)
+    layer.call(gpu_lib, X.cuda(), ids.cuda(), w.cuda(), D.t)
+    got = D.f64()
+    assert (got[0] == np.inf).all() and (got[1] == -np.inf).all() and np.isnan(got[2]).all() and (got[3] == 1).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["fp8", ("int4", 128, False)], ids=str)
 def test_offsets_past_32_bits(gpu_lib, fmt):
     """The last expert's weights lie past 4 GiB."""
