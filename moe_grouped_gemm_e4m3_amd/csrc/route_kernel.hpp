@@ -92,9 +92,9 @@ __device__ __forceinline__ double other_group(double v) {
 }
 
 // Integers that order as the numbers do, above 0; a NaN stands in the place of
-// -infinity, below all numbers.
+// -infinity, below all numbers.  -0 + 0 is +0: both zeros are one number.
 __device__ __forceinline__ uint32_t order_of(float v) {
-  const uint32_t b = __float_as_uint(v);
+  const uint32_t b = __float_as_uint(v + 0.f);
   return v != v ? 0x007fffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ uint64_t order_of(double v) {

@@ -112,6 +112,25 @@ def test_ties_go_to_the_lowest_index(gpu_lib, scoring):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_zeros_of_both_signs_are_equal(gpu_lib, scoring, dtype):
+    """-0 and +0 are one logit: rows that mix them, as products with a 0/1 mask do, go by index."""
+    announce(f"route zeros {scoring} {dtype}")
+    ids, _ = check_route(gpu_lib, torch.tensor([[-0.0, 0.0, -1.0], [0.0, -0.0, -1.0], [-1.0, -0.0, 0.0]]).to(dtype), 1, scoring=scoring)
+    assert ids[:, 0].tolist() == [0, 0, 1]
+    for E in (64, 100, 1024):
+        g = torch.Generator().manual_seed(E)
+        l = torch.randn(30, E, generator=g) * (torch.rand(30, E, generator=g) < 0.3)  # zeros of either sign
+        l[::2] = -l[::2].abs()  # zeros above all others
+        assert (torch.signbit(l) & (l == 0)).any() and (~torch.signbit(l) & (l == 0)).any()
+        for norm in (True, False):
+            check_route(gpu_lib, l.to(dtype), min(E, 40), scoring=scoring, normalize=norm)
+            check_route(gpu_lib, l.to(dtype), 7, scoring=scoring, normalize=norm, bias=torch.zeros(E) * -1.0)
+            check_route(gpu_lib, l.to(dtype), 7, scoring=scoring, normalize=norm, groups=2, top_groups=1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("grouped", [False, True])
 def test_values_that_are_not_finite_stay_in_their_row(gpu_lib, scoring, grouped):
     announce(f"route not finite {scoring} {grouped}")
