@@ -329,7 +329,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteG
       scale = sum == 0.0 ? 0.0 : 1.0 / sum;
     }
   }
-  const double s_j = !there ? 0.0 : p.sigmoid ? sigmoid64(x) : exp((double)x - (double)top) * scale;
+  // sigmoid: 1 - s_j without the difference, which cancels (from a logit of 37 on to 0)
+  double s_j = 0.0, rest = 1.0;
+  if (there) {
+    const double u = exp(p.sigmoid ? -(double)x : (double)x - (double)top);
+    s_j = p.sigmoid ? 1.0 / (1.0 + u) : u * scale;
+    rest = x > 0.f ? u * s_j : 1.0 - s_j;
+  }
   double q = s_j;
   if (p.normalize) {
     const double all = wave_sum(s_j);
@@ -338,7 +344,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteG
   const double mean = p.sigmoid && !p.normalize ? 0.0 : wave_sum(g * q);
   // what place j sends to its expert; dense: the part - s_i mean reaches every expert
   double d = dense ? g * q : q * (g - mean);
-  if (p.sigmoid) d *= 1.0 - s_j;
+  if (p.sigmoid) d *= rest;
   L* out = (L*)p.dl + t * p.ld_dl;
   double dl[SLOTS];
 #pragma unroll

@@ -193,5 +193,6 @@ def route_backward(dw, logits, ids, scoring="softmax", normalize=True, scale=1.0
         full = np.zeros(E)
         for j, d in zip(js, ds):
             full[ids[t, j]] += d
-        dl[t] = s * (full - (full * s).sum()) if scoring == "softmax" else full * s * (1 - s)
+        # sigmoid: 1 - s is the sigmoid of -l, which does not cancel
+        dl[t] = s * (full - (full * s).sum()) if scoring == "softmax" else full * s * scores(-l, scoring)
     return dl

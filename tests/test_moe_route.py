@@ -192,6 +192,34 @@ def test_route_backward(gpu_lib, T, E, k, dtype, scoring, normalize):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_sigmoid_gradient_of_large_logits(gpu_lib, dtype, normalize):
+    """s (1 - s) of logits from 20 to 80 either way, where 1 - s rounds to 0 from 37 on: bounds relative to the value alone.
+    Normalised, q (g - mean) is off by a few 64-bit steps of |g|, and 1 - s multiplies that."""
+    announce(f"route backward large logits {dtype} {normalize}")
+    E, k = 61, 3
+    l = torch.stack([torch.arange(20, 81).float(), -torch.arange(20, 81).float(), torch.arange(20, 81).float() * 1.03]).to(dtype)
+    ids = torch.tensor([[0, 30, 60], [0, 30, 60], [9, 18, 55]], dtype=torch.int32)
+    dw = torch.tensor([[1.0, -0.75, 0.5], [0.3, 2.0, -1.0], [-4.0, 0.1, 3.0]])
+    got = f64(gpu_lib.moe_route_backward(dw.cuda(), l.cuda(), ids.cuda(), scoring="sigmoid", normalize=normalize, scale=1.5))
+    x = f64(l)
+    s, rest = 1 / (1 + np.exp(-x)), 1 / (1 + np.exp(x))
+    at = ids.numpy().astype(np.int64)
+    rows = np.arange(3)[:, None]
+    c, g = s[rows, at], 1.5 * f64(dw)
+    q = c / c.sum(1, keepdims=True)
+    d = q * (g - (g * q).sum(1, keepdims=True)) if normalize else g * c
+    want, slack = np.zeros_like(x), np.zeros_like(x)
+    want[rows, at] = d * rest[rows, at]
+    slack[rows, at] = (q if normalize else c) * 16 * 1e-15 * rest[rows, at]
+    assert (np.abs(got - want) <= 1.001 * HALF[dtype] * np.abs(want) + slack + 2.0 ** -149).all()
+    assert np.array_equal(got != 0, want != 0)
+    oracle = ref.route_backward(f64(dw), x, ids.numpy(), scoring="sigmoid", normalize=normalize, scale=1.5)
+    assert (np.abs(oracle - want) <= 1e-13 * np.abs(want) + slack).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_backward_of_given_ids(gpu_lib, scoring, normalize):
