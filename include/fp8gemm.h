@@ -616,7 +616,8 @@ typedef enum { FG_SCORE_SOFTMAX = 0, FG_SCORE_SIGMOID = 1 } fg_scoring;
  *            the sum of the chosen s (0 where that is 0)
  * An expert whose logit (or bias) is -infinity is no candidate; places that no
  * candidate is left for hold id -1 and weight 0.  A NaN is chosen after all
- * numbers and gives NaN weights: under softmax all of its row's.
+ * numbers and gives NaN weights: under softmax all of its row's, and so does
+ * +infinity.
  * T <= 2^25, 1 <= k <= min(E, 64), E <= 1024, groups <= 64 divides E.  Scores and
  * what they are compared by are computed in 64 bits, weights are rounded once.
  * One kernel, no workspace.
@@ -631,7 +632,8 @@ fg_status moe_route_bf16(const uint16_t* logits, int64_t ld, const float* bias, 
  * every element is written) from dweights (device fp32 [T, k]), the logits and
  * the forward call's ids, scoring, normalize and scale.  Places whose id is not
  * in [0, E) have no gradient, and their dweights are not read; the choice itself
- * and the bias have none.  With an id in two places of a row both add up.
+ * and the bias have none.  With an id in two places of a row both add up.  Under
+ * softmax a NaN or +infinity among a row's logits gives NaN for all of the row.
  */
 fg_status moe_route_backward(const float* dweights, const float* logits, int64_t ld, const int32_t* ids, float* dlogits,
                              int64_t ld_dl, int T, int E, int k, int scoring, int normalize, float scale, void* stream);

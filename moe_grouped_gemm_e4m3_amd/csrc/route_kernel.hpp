@@ -301,7 +301,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteG
   const double g = there ? (double)p.dw[t * p.k + lane] * p.scale : 0.0;
   const float x = there ? to_f32(row[id]) : 0.f;
   // softmax: the largest logit and the sum over all experts; normalised, the sum
-  // cancels (but for a NaN)
+  // cancels (but for a NaN, which a NaN or +infinity among the logits makes of all scores)
   double e[SLOTS];
   float top = 0.f;
   double scale = 1.0;
@@ -313,7 +313,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteG
     for (int s = 0; s < SLOTS; ++s) {
       l[s] = lane + 64 * s < p.E ? to_f32(row[lane + 64 * s]) : -__builtin_inff();
       top = s == 0 ? l[0] : fmaxf(top, l[s]);
-      nan |= l[s] != l[s];
+      nan |= !(l[s] < __builtin_inff());
     }
     top = wave_max_logit(top);
     if (top == -__builtin_inff()) top = 0.f;
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteG
   L* out = (L*)p.dl + t * p.ld_dl;
   double dl[SLOTS];
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) dl[s] = dense ? -(e[s] * scale) * mean : 0.0;
+  for (int s = 0; s < SLOTS; ++s) dl[s] = dense ? -(e[s] * scale) * mean : p.sigmoid ? 0.0 : 0.0 * scale;
   for (int j = 0; j < p.k; ++j) {
     const int to = (int)from_lane((uint32_t)id, j) - lane;
     const double v = from_lane(d, j);

@@ -220,6 +220,24 @@ def test_sigmoid_gradient_of_large_logits(gpu_lib, dtype, normalize):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_softmax_gradient_of_rows_that_are_not_finite(gpu_lib, normalize, value):
+    """One infinite or NaN logit makes every share of its row a NaN, chosen or not, and so its gradient."""
+    announce(f"route backward {value} {normalize}")
+    l = make(4, 70, torch.float32, 11)
+    l[1, 5], l[2, 66] = value, value
+    l[3, :65] = -INF
+    ids = torch.tensor([[3, 8], [3, 5], [3, 8], [65, 69]], dtype=torch.int32)
+    dw = torch.randn(4, 2, generator=torch.Generator().manual_seed(1))
+    got = f64(gpu_lib.moe_route_backward(dw.cuda(), l.cuda(), ids.cuda(), normalize=normalize))
+    with np.errstate(invalid="ignore"):
+        want = ref.route_backward(f64(dw), f64(l), ids.numpy(), normalize=normalize)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.isnan(got[1:3]).all() and np.isfinite(got[[0, 3]]).all()
+    check_backward(gpu_lib, dw[[0, 3]], l[[0, 3]], ids[[0, 3]], normalize=normalize)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("normalize", [True, False])
 def test_backward_of_given_ids(gpu_lib, scoring, normalize):
