@@ -570,7 +570,8 @@ fg_status gated_ffn_int8(const int8_t* X, int64_t ldx, const float* sx, const in
  *               q = clamp(rint(x / s) + z, 0, 15)
  * over each group.  w: device [N, K], row stride ldw elements (ldw >= K,
  * 16-byte aligned rows).  Padding words are written as zeros.  Input values must
- * be finite.  K <= 2^20.  N == 0 or K == 0 writes nothing.
+ * be finite; hi - lo may pass the largest fp32 (it is taken of halves).
+ * K <= 2^20.  N == 0 or K == 0 writes nothing.
  */
 fg_status int4_cast_per_group(const float* w, int64_t ldw, uint8_t* q, uint16_t* s, uint8_t* z, int N, int K, int group,
                               void* stream);

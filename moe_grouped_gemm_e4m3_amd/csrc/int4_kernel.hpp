@@ -80,7 +80,8 @@ __global__ __launch_bounds__(256) void int4_cast_kernel(Int4CastParams p) {
       lo = fminf(lo, __shfl_xor(lo, d));
       hi = fmaxf(hi, __shfl_xor(hi, d));
     }
-    const float span = p.z ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f;
+    // half the span over 7.5: the same bits as the span over 15, and no overflow
+    const float span = p.z ? (0.5f * hi - 0.5f * lo) / 7.5f : fmaxf(hi, -lo) / 7.f;
     const uint16_t sb = bf16_bits(fmaxf(span, p.z ? 1e-20f / 15.f : 1e-20f / 7.f));
     const float s = to_f32(sb);
     const float z = p.z ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 8.f;

@@ -65,7 +65,8 @@ def int4_cast(w: np.ndarray, group: int, symmetric: bool):
         if symmetric:
             step = np.maximum(np.maximum(hi, -lo) / f(7), f(1e-20) / f(7))
         else:
-            step = np.maximum((hi - lo) / f(15), f(1e-20) / f(15))
+            # of halves: the same bits, and hi - lo may pass the largest fp32
+            step = np.maximum((f(0.5) * hi - f(0.5) * lo) / f(7.5), f(1e-20) / f(15))
         s[:, g] = bf16_round(step)
         if not symmetric:
             z[:, g] = np.clip(np.rint(-lo / s[:, g]), 0, 15)

@@ -98,6 +98,32 @@ def test_cast(gpu_lib, N, K, group, dtype, symmetric):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("symmetric", [True, False])
+@pytest.mark.parametrize("group", [32, 128, 256])
+def test_cast_of_the_largest_weights(gpu_lib, dtype, symmetric, group):
+    """hi - lo past the largest fp32: scales and codes stay those of the definition, whose span is taken of halves."""
+    announce(f"int4 cast largest {dtype} {symmetric} {group}")
+    top = torch.finfo(dtype).max
+    w = torch.rand(5, 288, generator=torch.Generator().manual_seed(3)).sub(0.5).mul(2.0).double()
+    w[0] *= top
+    w[1] *= 2.0 ** 127
+    w[2, :40] = top
+    w[2, 40:] = -top
+    w[3, 0], w[3, 1] = top, -top
+    w = w.to(dtype)
+    assert torch.isfinite(w).all()
+    q, s, z = gpu_lib.int4_cast_per_group(w.cuda(), group, symmetric)
+    want_q, want_s, want_z = ref.int4_cast(w.float().numpy(), group, symmetric)
+    assert np.isfinite(want_s).all() and np.array_equal(s.float().cpu().numpy(), want_s)
+    assert np.array_equal(q.cpu().numpy(), ref.int4_pack(want_q)) and (symmetric or np.array_equal(z.cpu().numpy(), want_z))
+    # a code's value is within the steps of test_oracle_cast_is_near of its weight
+    back, _ = ref.int4_widen(want_q, want_s, want_z, group)
+    step = np.repeat(want_s.astype(np.float64), group, axis=1)[:, :288]
+    assert (np.abs(back - w.double().numpy()) <= (0.5 + 15 * 2.0 ** -8 + (0.0 if symmetric else 0.5)) * step).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("zeros", [True, False])
 @pytest.mark.parametrize("group", [32, 64, 128, 384])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 32), (1, 40, 96), (2, 17, 128), (15, 33, 160), (16, 100, 1056), (17, 48, 544),
