@@ -95,7 +95,7 @@ inline Int4Plan plan_int4(int M, int N, int K, const char* forced) {
   for (int k = 0; k < kInt4Kinds; ++k)
     if (names(forced, kInt4Names[k])) kind = (Int4Kind)k;
   Int4Plan p{kind, 1};
-  if (kind >= kWide16) {
+  if (kind >= kWide16 && M > 2) {  // one or two rows have no workspace, whatever kernel is asked for
     p.k_parts = wide_parts(kind, M, N, chunks);
     for (int n = 1; n <= 8 && n <= std::max(1, chunks); ++n) {
       const char word[] = {'k', 'p', 'a', 'r', 't', 's', (char)('0' + n), 0};

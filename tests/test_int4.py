@@ -152,6 +152,16 @@ def test_every_plan(gpu_lib, monkeypatch, capfd, plan, group, zeros):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("plan", ["wide16", "wide32", "wide64", "wide16,kparts3", "split2", "split16deep"])
+@pytest.mark.parametrize("M", [1, 2])
+def test_forced_plans_of_one_and_two_rows(gpu_lib, monkeypatch, plan, M):
+    """Many chunks, few tiles: a plan that would split the reduction does without for rows that have no workspace."""
+    monkeypatch.setenv("FG_DECODE_PLAN", plan)
+    assert gpu_lib.int4_workspace_bytes(M, 200, 7168) == 0
+    check_product(gpu_lib, M, 200, 7168, 128, True, seed=8)
+
+
+@pytest.mark.gpu
 def test_workspace(gpu_lib):
     """A product whose reduction is split: with a workspace, with one that holds NaN, with torch's, on another stream;
     one that is too small or misaligned is refused."""
