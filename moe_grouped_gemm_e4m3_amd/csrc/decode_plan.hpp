@@ -8,7 +8,7 @@
 // more rows).  The figures beside the rules are in microseconds, in a HIP graph.
 //
 // FG_DECODE_PLAN names parts of a plan, separated by commas, for tuning and
-// tests; one that a call does not have leaves it its own.
+// tests; one that a call does not have or that does not fit LDS leaves it its own.
 #pragma once
 
 #include <stdint.h>
@@ -205,7 +205,7 @@ inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const c
   if (down_lds(fp8, p.down, T, E, k) > kLds) p.down = kDownWide16;
   for (int i = 0; i < kDownKinds; ++i)
     if (names(forced, kDownNames[i]) && (fp8 ? i != kDownSplit4Two : i != kDownWide16Deep) &&
-        (i != kDownSplit1Two || T <= 16))  // its sums of more tokens do not fit LDS
+        down_lds(fp8, (DownKind)i, T, E, k) <= kLds)
       p.down = (DownKind)i;
   p.parts = 1;
   if (wide_down(p.down)) {

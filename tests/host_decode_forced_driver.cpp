@@ -34,6 +34,23 @@ int main() {
             ++g_plans;
             CHECK(M > 2 || p.k_parts == 1, "%s: %d x %d x %d: %d parts", w.c_str(), M, N, K, p.k_parts);
           }
+  // LDS of `down`, of what is forced and of what is not
+  for (int T : {1, 2, 7, 16, 17, 25, 26, 40, 63, 64, 65, 1 << 20})
+    for (int E : {1, 3, 16, 64, 200, 417, 1000, 1024})
+      for (int k : {1, 2, 8, 31, 32})
+        for (int K : {32, 2048, 4128, 65536})
+          for (int F : {0, 32, 2048, 65536})
+            for (int fp8 = 0; fp8 < 2; ++fp8) {
+              const LayerPlan own = plan_layer(fp8, T, k, E, F, K, "");
+              for (int d = -1; d < kDownKinds; ++d) {
+                const LayerPlan p = d < 0 ? own : plan_layer(fp8, T, k, E, F, K, kDownNames[d]);
+                ++g_plans;
+                const int lds = down_lds(fp8, p.down, std::min(T, kLayerTokens), E, k);
+                CHECK(lds <= 160 * 1024, "%s forced: T=%d E=%d k=%d K=%d fp8=%d: %s takes %d bytes", d < 0 ? "nothing" : kDownNames[d],
+                      T, E, k, K, fp8, kDownNames[p.down], lds);
+                CHECK(p.down == own.down || p.down == d, "%s forced, %s taken", d < 0 ? "nothing" : kDownNames[d], kDownNames[p.down]);
+              }
+            }
   return g_fail ? (std::fprintf(stderr, "%ld of %ld plans wrong\n", g_fail, g_plans), 1)
                 : (std::printf("host forced plans ok: %ld\n", g_plans), 0);
 }
