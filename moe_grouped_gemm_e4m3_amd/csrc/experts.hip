@@ -3,6 +3,7 @@
 // launches.  Nothing is launched after a failed check; nothing is allocated.
 
 #include <algorithm>
+#include <atomic>
 #include <cstdio>
 #include <cstdlib>
 
@@ -124,12 +125,19 @@ fg_status route_backward(const float* dw, const L* logits, int64_t ld, const int
 // ---------------------------------------------------------------------------
 // expert layers
 
-// More than 64 KiB of dynamic LDS has to be asked for.
-fg_status allow_lds(const void* kernel, int bytes, const char* what) {
-  if (bytes > 160 * 1024) return set_error(FG_EUNSUPPORTED, "%s: %d bytes of LDS", what, bytes);
-  if (bytes <= 64 * 1024) return FG_OK;
-  const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != hipSuccess) return set_error(FG_EHIP, "%s: %d bytes of LDS: %s", what, bytes, hipGetErrorString(e));
+// More than 64 KiB of dynamic LDS has to be asked for: once for a kernel and device
+// (a bit of `allowed`), and the most there is, since the limit is the process's and
+// another thread's call may need more than this one.
+fg_status allow_lds(const void* kernel, int bytes, std::atomic<uint64_t>& allowed, const char* what) {
+  if (bytes > kLds) return set_error(FG_EUNSUPPORTED, "%s: %d bytes of LDS", what, bytes);
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return set_error(FG_EHIP, "%s: hipGetDevice: %s", what, hipGetErrorString(e));
+  const uint64_t bit = device < 64 ? (uint64_t)1 << device : 0;
+  if (allowed.load() & bit) return FG_OK;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (e != hipSuccess) return set_error(FG_EHIP, "%s: %d bytes of LDS: %s", what, kLds, hipGetErrorString(e));
+  allowed.fetch_or(bit);
   return FG_OK;
 }
 
@@ -164,7 +172,8 @@ struct LayerLaunch {
   template <class C>
   fg_status down() const {
     const int lds = down_lds(C::Fmt::FP8, plan.down, std::min(p.T, kLayerTokens), p.E, p.k);
-    FG_TRY(allow_lds((const void*)experts_down_kernel<C>, lds, what));
+    static std::atomic<uint64_t> allowed{0};
+    FG_TRY(allow_lds((const void*)experts_down_kernel<C>, lds, allowed, what));
     print("down", kDownNames[plan.down], 1);
     hipLaunchKernelGGL((experts_down_kernel<C>), dim3(ceil_div(p.K, C::COLS), passes), dim3(C::THREADS), lds,
                        (hipStream_t)stream, p);
@@ -175,7 +184,8 @@ struct LayerLaunch {
   template <class C>
   fg_status down_wide() const {
     const int lds = down_lds(C::Fmt::FP8, plan.down, std::min(p.T, kLayerTokens), p.E, p.k);
-    FG_TRY(allow_lds((const void*)experts_wide_down_kernel<C>, lds, what));
+    static std::atomic<uint64_t> allowed{0};
+    FG_TRY(allow_lds((const void*)experts_wide_down_kernel<C>, lds, allowed, what));
     for (int t0 = 0; t0 < p.T; t0 += kLayerTokens) {
       const int T = std::min(kLayerTokens, p.T - t0);
       print("down", kDownNames[plan.down], plan.parts);
