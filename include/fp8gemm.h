@@ -684,7 +684,7 @@ fg_status moe_ffn_int4(const uint16_t* X, int64_t ldx, const uint8_t* W1, const 
                        uint16_t* D, int64_t ldd, int T, int k, int E, int F, int K, int group, int activation,
                        void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of moe_ffn_fp8 and moe_ffn_int4; -1 for sizes that they refuse. */
+/* Workspace bytes of moe_ffn_fp8 and moe_ffn_int4; -1 for sizes that both refuse. */
 int64_t fg_moe_ffn_workspace_bytes(int T, int k, int F);
 
 /* Row alignment of each expert segment in the contiguous layout: 128. */

@@ -892,7 +892,8 @@ def int4_workspace_bytes(M: int, N: int, K: int) -> int:
 def gemm_int4_nt(A, B, sb, D, zb=None, group=128, stream=None, workspace=None):
     """D[M,N] = bf16(A . W^T), W[n,k] = sb[n, k/group] (B[n,k] - zb[n, k/group]), for bf16 A [M, K] and
     4-bit weights as int4_cast_per_group makes them (zb None: zero points of 8).  For few rows: the
-    weights are read once for each 64."""
+    weights are read once for each 64.  The workspace (int4_workspace_bytes, 0 for most sizes) comes
+    from torch's allocator if not given."""
     if A.dim() != 2 or D.dim() != 2:
         raise ValueError("A and D must be matrices")
     M, K = A.shape
@@ -904,7 +905,7 @@ def gemm_int4_nt(A, B, sb, D, zb=None, group=128, stream=None, workspace=None):
     if workspace is not None:
         ws, ws_bytes = _byte_workspace(workspace, dev)
     elif M > 2:  # (one or two rows need none, and the query is a tenth of their call)
-        ws_bytes = int4_workspace_bytes(M, N, K)
+        ws_bytes = max(0, load_library().fg_int4_workspace_bytes(M, N, K))  # (-1: sizes that the call refuses)
         if ws_bytes:
             with _on_stream(stream):
                 workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
@@ -990,8 +991,9 @@ def _layer(X, ids, weights, D, F, workspace, stream, dev):
     ldx, ldd = _matrix(X, "X", torch.bfloat16, T, K, dev), _matrix(D, "D", torch.bfloat16, T, K, dev)
     idp, wp = _packed(ids, "ids", torch.int32, (T, k), dev), _packed(weights, "weights", torch.float32, (T, k), dev)
     if workspace is None:
+        n = max(0, load_library().fg_moe_ffn_workspace_bytes(T, k, F))  # (-1: sizes that the call refuses)
         with _on_stream(stream):
-            workspace = torch.empty(moe_ffn_workspace_bytes(T, k, F), dtype=torch.uint8, device=X.device)
+            workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
     ws, ws_bytes = _byte_workspace(workspace, dev)
     return T, K, k, ldx, ldd, idp, wp, ws, ws_bytes
 

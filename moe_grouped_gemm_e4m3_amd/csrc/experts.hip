@@ -322,7 +322,7 @@ fg_status moe_route_backward_bf16(const float* dweights, const uint16_t* logits,
 }
 
 int64_t fg_moe_ffn_workspace_bytes(int T, int k, int F) {
-  if (T < 0 || k < 0 || F < 0 || T > kMaxTokens || k > kMaxChoices || F > kMaxWidth) return -1;
+  if (T < 0 || k <= 0 || F < 0 || F % 16 || T > kMaxTokens || k > kMaxChoices || F > kMaxWidth) return -1;
   return layer_bytes(T, k, F);
 }
 

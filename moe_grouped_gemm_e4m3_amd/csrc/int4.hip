@@ -179,7 +179,7 @@ fg_status gemm_int4_nt(const uint16_t* A, int64_t lda, const uint8_t* B, const u
 }
 
 int64_t fg_int4_workspace_bytes(int M, int N, int K) {
-  if (M < 0 || N < 0 || K < 0 || M > kMaxM || N > kMaxN || K > kMaxK) return -1;
+  if (M < 0 || N < 0 || K < 0 || K % 32 || M > kMaxM || N > kMaxN || K > kMaxK) return -1;
   return M > 0 && N > 0 ? int4_partial_bytes(M, N, planned(M, N, K)) : 0;
 }
 

@@ -244,6 +244,26 @@ def test_offsets_past_32_bits(gpu_lib, N, K):
     assert (D[:, :-48] == 0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(-1, 8, 64), (8, -1, 64), (8, 8, -32), ((1 << 20) + 1, 8, 64), (8, (1 << 26) + 1, 64),
+                                   (8, 8, (1 << 20) + 32), (30, 512, 24576 + 16), (1, 64, 48)])
+def test_workspace_query_refuses_what_the_product_refuses(M, N, K):
+    import moe_grouped_gemm_e4m3_amd as fg
+
+    lib = fg.load_library()
+    assert lib.fg_int4_workspace_bytes(M, N, K) == -1
+    assert product_call(lib, M=M, N=N, K=K, lda=1 << 20, ldd=1 << 27, ws=0x10000, nbytes=1 << 40) != 0
+    with pytest.raises(ValueError):
+        fg.int4_workspace_bytes(M, N, K)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 8])
+def test_wrapper_leaves_sizes_to_the_library(gpu_lib, M):
+    bf, u8 = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.uint8, device="cuda")
+    with pytest.raises(gpu_lib.FP8GemmError, match="K=48"):
+        gpu_lib.gemm_int4_nt(torch.zeros(M, 48, **bf), torch.zeros(8, 64, **u8), torch.zeros(8, 1, **bf), torch.zeros(M, 8, **bf))
+
+
 def product_call(lib, A=0x10000, lda=512, B=0x10000, s=0x10000, z=None, D=0x10000, ldd=64, M=4, N=64, K=512, group=128, ws=None,
                  nbytes=0):
     return lib.gemm_int4_nt(A, lda, B, s, z, D, ldd, M, N, K, group, ws, nbytes, None)

@@ -470,6 +470,18 @@ def test_group_refusals_and_workspace_query():
             fg.moe_ffn_workspace_bytes(*bad)
 
 
+@pytest.mark.parametrize("T,k,F", [(4, 0, 64), (0, 0, 64), (4, 2, 24), (4, 2, 8), (-1, 2, 64), (4, 33, 64), (4, 2, (1 << 16) + 16)])
+def test_workspace_query_refuses_what_both_layers_refuse(T, k, F):
+    import moe_grouped_gemm_e4m3_amd as fg
+
+    lib = fg.load_library()
+    assert lib.fg_moe_ffn_workspace_bytes(T, k, F) == -1
+    for fmt in ("fp8", "int4"):
+        assert call(lib, fmt, T=T, k=k, F=F, nbytes=1 << 40) != 0
+    with pytest.raises(ValueError):
+        fg.moe_ffn_workspace_bytes(T, k, F)
+
+
 def test_wrapper_refusals():
     import moe_grouped_gemm_e4m3_amd as fg
 
@@ -482,6 +494,16 @@ def test_wrapper_refusals():
             fn(*args)
         with pytest.raises(ValueError):
             fn(args[0][0], *args[1:])
+
+
+@pytest.mark.gpu
+def test_wrapper_leaves_sizes_to_the_library(gpu_lib):
+    bf, u8, f = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.uint8, device="cuda"), dict(device="cuda")
+    for k, F, message in ((0, 32, "k=0"), (33, 32, "k=33"), (2, 24, "F=24")):
+        with pytest.raises(gpu_lib.FP8GemmError, match=message):
+            gpu_lib.moe_ffn_fp8(torch.zeros(2, 32, **bf), torch.zeros(3, 2 * F, 32, **u8), torch.zeros(3, 1, 1, **f), torch.zeros(3, 32, F, **u8),
+                                torch.zeros(3, 1, 1, **f), torch.zeros(2, k, dtype=torch.int32, device="cuda"), torch.zeros(2, k, **f),
+                                torch.zeros(2, 32, **bf))
 
 
 @pytest.mark.gpu
