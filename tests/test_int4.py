@@ -133,6 +133,22 @@ def test_product(gpu_lib, M, N, K, group, zeros):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 1056), (7, 130, 416), (40, 50, 2080)])
+def test_zero_points_up_to_255(gpu_lib, M, N, K, group):
+    """Any uint8 zero point, far outside the codes too."""
+    announce(f"int4 zero points {M}x{N}x{K} group={group}")
+    q, s, z = weights(N, K, group, True, 12)
+    z = np.random.default_rng(M).integers(0, 256, z.shape).astype(np.uint8)
+    z[0, 0], z[-1, -1] = 255, 16
+    A = bf16(torch.randn(M, K, generator=torch.Generator().manual_seed(4)))
+    D = Output(M, N)
+    B, sb, zb = to_gpu(q, s, z, True)
+    gpu_lib.gemm_int4_nt(A.cuda(), B, sb, D.t, zb=zb, group=group)
+    assert_within(D.f64(), *ref.gemm_int4(f64(A), q, s, z, group), f"{M}x{N}x{K}")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K,group", [(1, 2112, 7168, 128), (4, 1024, 2048, 32), (16, 600, 8192, 64), (64, 300, 4096, 128)])
 def test_product_of_whole_layers(gpu_lib, M, N, K, group):
     check_product(gpu_lib, M, N, K, group, True, seed=5)
