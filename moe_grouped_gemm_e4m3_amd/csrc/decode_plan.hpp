@@ -126,7 +126,8 @@ inline constexpr bool wide_down(DownKind k) { return k >= kDownWide16; }
 
 // The `down` kernels: tiles of 16 outputs of a wave, waves, ring slots, tokens of an
 // expert in one go.  4 bits: the activations of 32 tokens instead of 24 would not
-// leave LDS for the sums of 64.
+// leave LDS for the sums of 64.  kDownSplit1Two in e4m3 is for
+// calls that name it.
 struct DownShape {
   int tiles, waves, depth, rows;
 };
@@ -159,9 +160,10 @@ inline int down_lds(bool fp8, DownKind kind, int T, int E, int k) {
 }
 constexpr int kLds = 160 * 1024;
 
-// The rules are simple ones that lose least over 2600 layers of 1 to 68 tokens, 4
-// to 128 experts and weights of 256 to 2048 x 1024 to 7168: 1 to 2% of a layer's
-// time on average against the best kernel of each, for either half and format.
+// The rules are simple ones that lose least over 2700 layers of 1 to 68 tokens, 4
+// to 128 experts, drawn alike, and weights of 256 to 2048 x 1024 to 7168: 1 to 2%
+// of a layer's time on average against the best kernel of each, for either half and
+// format; one layer in 20 loses more than 10%, none more than 40%.
 inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const char* forced) {
   T = std::min(T, kLayerTokens);
   const int pairs = T * k, active = std::min(E, pairs);  // experts with tokens, at most
@@ -187,20 +189,24 @@ inline LayerPlan plan_layer(bool fp8, int T, int k, int E, int F, int K, const c
   for (int i = 0; i < kUpKinds; ++i)
     if (names(forced, kUpNames[i]) && (fp8 ? i != kUpWide8 && i != kUpSplit2 : i != kUpWideDeep)) p.up = (UpKind)i;
   // down.  A third kernel costs about 3 us, so that few pairs go without (e4m3,
-  // T=8, 8 experts of 512 x 1024: split 12, wide 16; 4 bits, T=9, 64 of 512 x 2048:
-  // 16 and 21), unless there are few outputs for much work (e4m3, T=5, 64 of 2048 x
-  // 1024: split 51, wide 40).
+  // T=8, 2 of 8 experts of 512 x 1024: split 13.3, wide 16.1; 4 bits, T=9, 2 of 64 of
+  // 512 x 2048: 20.9 and 21.1), unless there are few outputs for much work (e4m3,
+  // T=5, 4 of 64 of 2048 x 1024: split 48.6, wide 36.6).
   const bool few = pairs < (fp8 ? 26 : 22) && (K >= 2048 || (int64_t)active * F * K <= 1 << 24);
   const int tiles = ceil_div(K, 128);
   const bool one = 8 * pairs < 9 * active && (!fp8 || (int64_t)active * F * K < 43000000);  // a token for each expert
   if (T == 1 || (few && one))
-    p.down = K > 4096 && T <= 16 ? kDownSplit1Two : kDownSplit1;  // 8 of 7168 x 2048: 25.1 for 26.4; 4 of 4096 x 2048: 10.8 for 9.7
+    // two tiles: over 4096 outputs 4 bits are 1.5% faster so (190 layers), e4m3 1% slower (200); up to 4096, 6% and more slower
+    p.down = !fp8 && K > 4096 && T <= 16 ? kDownSplit1Two : kDownSplit1;
   else if (few)
-    p.down = !fp8 && K > 4096 ? kDownSplit4Two : kDownSplit4;  // T=2, 4-bit, 7168 x 2048: 38 for 43; 4096 x 2048: 24 for 15
+    // 4 bits, T=2, 4 experts of 2048 x 7168: 32.5 for 36.5; of 2048 x 4096: 27.3 for 21.7
+    p.down = !fp8 && K > 4096 ? kDownSplit4Two : kDownSplit4;
   else if (pairs >= 14 * active)
-    p.down = kDownWide32;  // T=64, 32 tokens an expert: 122 for 149; 6 tokens: 43 for 40
+    p.down = kDownWide32;  // e4m3, T=64, 8 of 16 experts of 2048 x 4096: 135 for 151; 4 bits no faster and no slower
   else
-    p.down = fp8 && T >= 26 ? kDownWide16Deep : kDownWide16;  // T=64, 8 tokens an expert: 66 for 83
+    // a third slot: 1.5% faster for more than 32 tokens of long reads (48 layers of 100 MB and more); 2 to 9% slower
+    // where it costs a second workgroup on the CU
+    p.down = fp8 && T > 32 && (int64_t)active * F * K >= 100000000 ? kDownWide16Deep : kDownWide16;
   // what many experts or pairs leave no LDS for
   if (down_lds(fp8, p.down, T, E, k) > kLds) p.down = kDownWide16;
   for (int i = 0; i < kDownKinds; ++i)

@@ -237,7 +237,6 @@ fg_status launch_layer(const ExpertParams& p, void* stream, const char* what) {
     case kDownWide16Deep:
       if constexpr (Fmt::FP8) return l.down_wide<WideDown<Fmt, kDownWide16Deep>>();
       break;
-    // a third slot (4 bits have no LDS for it): T=64, 16 experts of 2048 x 7168, 32 tokens each: 231 us for 242
     case kDownWide32: return l.down_wide<WideDown<Fmt, kDownWide32>>();
     default: break;
   }

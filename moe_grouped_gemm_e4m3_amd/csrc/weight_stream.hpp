@@ -329,26 +329,24 @@ __device__ __forceinline__ i32x4 w_piece(const uint8_t* slot, int t, int j) {
 // products (the layer above: 171 us for 162).
 template <class S>
 struct XPieces {
-  static constexpr int STEPS = 4 * S::HALVES, AHEAD = S::WIDE_X ? 1 : 0;
-  i32x4 x[AHEAD + 1][S::PARTS][S::MT];
+  const uint8_t* xs;
+  i32x4 x[2][S::PARTS][S::MT];
 
-  __device__ __forceinline__ void load(const uint8_t* xs, int step) {
-    if (step < STEPS)
+  __device__ __forceinline__ void load(int step) {
+    if (S::WIDE_X && step < 4 * S::HALVES)
 #pragma unroll
       for (int p = 0; p < S::PARTS; ++p)
 #pragma unroll
-        for (int t = 0; t < S::MT; ++t) x[step % (AHEAD + 1)][p][t] = x_piece<S>(xs, t, p, step >> 2, step & 3);
+        for (int t = 0; t < S::MT; ++t) x[step & 1][p][t] = x_piece<S>(xs, t, p, step >> 2, step & 3);
   }
-  __device__ __forceinline__ void start(const uint8_t* xs) {
-#pragma unroll
-    for (int step = 0; step < AHEAD; ++step) load(xs, step);
+  // Before the products of a step.
+  __device__ __forceinline__ void next(int step) {
+    load(step + 1);
+    if (S::WIDE_X) __builtin_amdgcn_sched_barrier(0);
   }
-  // Before the products of a step: what they read is in at(p, t).
-  __device__ __forceinline__ void next(const uint8_t* xs, int step) {
-    load(xs, step + AHEAD);
-    if (AHEAD > 0) __builtin_amdgcn_sched_barrier(0);
+  __device__ __forceinline__ i32x4 at(int step, int p, int t) const {
+    return S::WIDE_X ? x[step & 1][p][t] : x_piece<S>(xs, t, p, step >> 2, step & 3);
   }
-  __device__ __forceinline__ i32x4 at(int step, int p, int t) const { return x[step % (AHEAD + 1)][p][t]; }
 };
 
 // acc += the slot's products.  Products that follow each other are of different
@@ -361,7 +359,8 @@ __device__ __forceinline__ void add_chunk(f32x4 (&acc)[S::MT][S::CF], const Sour
                                           int g0) {
   const f32x4 zero = f32x4{0.f, 0.f, 0.f, 0.f};
   XPieces<S> pieces;
-  pieces.start(xs);
+  pieces.xs = xs;
+  pieces.load(0);
   if constexpr (S::FP8) {
     f32x4 P[S::MT][S::CF];
 #pragma unroll
@@ -376,7 +375,7 @@ __device__ __forceinline__ void add_chunk(f32x4 (&acc)[S::MT][S::CF], const Sour
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int step = 2 * j + h;
-        pieces.next(xs, step);
+        pieces.next(step);
         bf16x8 b[S::CF];
 #pragma unroll
         for (int cf = 0; cf < S::CF; ++cf) b[cf] = widen_bytes(w[cf][2 * h], w[cf][2 * h + 1], 1.f);
@@ -425,7 +424,7 @@ __device__ __forceinline__ void add_chunk(f32x4 (&acc)[S::MT][S::CF], const Sour
 #pragma unroll
         for (int m = in * MPG; m < (in + 1) * MPG; ++m) {
           const int step = 4 * half + m;
-          pieces.next(xs, step);
+          pieces.next(step);
           bf16x8 b[S::CF];
 #pragma unroll
           for (int cf = 0; cf < S::CF; ++cf) b[cf] = widen_int4(w[cf][m]);
