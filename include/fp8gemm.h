@@ -588,7 +588,8 @@ fg_status int4_cast_per_group_bf16(const uint16_t* w, int64_t ldw, uint8_t* q, u
  * Made for M <= 64, where HBM is read for the weights once; more rows are taken
  * 16 to 64 at a time.  M <= 2^20, N <= 2^26, K % 32 == 0, K <= 2^20.  K == 0
  * writes zeros.  Sums are in fp32, the zero point is taken out of a group's sum
- * once, and the result is rounded once.  A row of A with an infinity or a NaN
+ * once (so that sum |A| B and zb sum |A| of a group must stay below fp32's largest
+ * number), and the result is rounded once.  A row of A with an infinity or a NaN
  * gives a row of D that holds infinities or NaN.  Sums have a fixed order, which
  * depends on the sizes only.  The workspace and D may not overlap anything else.
  * Allocates nothing.  Runs as one kernel, or two where the reduction is split.
@@ -659,11 +660,15 @@ fg_status moe_route_backward_bf16(const float* dweights, const uint16_t* logits,
  *   workspace  device, 256-byte aligned, fg_moe_ffn_workspace_bytes(T, k, F) bytes; needs no
  *        initialisation; in use until the call's work has finished
  * Activations are not quantised: products are of bf16 X (or of h, kept in fp32)
- * with the exact values of the codes, summed in fp32; D is rounded once.  A token that names an expert twice has the sum of both weights.  The
- * weights of every named expert are read once for each 64 tokens and, with more
- * than 16 or 32 tokens of one expert, once more from cache for each as many;
- * with hundreds of tokens the grouped GEMMs are faster.  Sums have a fixed order,
- * which depends on the sizes and ids only.
+ * with the exact values of the codes, summed in fp32; D is rounded once.  A token
+ * that names an expert twice has the sum of both weights.  For each 64 tokens the
+ * weights of every named expert are read from HBM once.  A kernel takes 1 to 32
+ * tokens of an expert at a time, by the average over the experts (1 or 2 where most
+ * have a token or none), and streams the expert's weights again for each further so
+ * many, from cache where they fit: ids that crowd on few experts take longer than
+ * ids that are spread over the same ones.  With hundreds of tokens the grouped GEMMs
+ * are faster (e4m3; there are none on 4-bit weights).  Sums have a fixed order, which
+ * depends on the sizes and ids only.
  * T <= 2^20, 1 <= k <= 32, 1 <= E <= 1024, K and F multiples of 16 up to 2^16.
  * F == 0 writes zeros.  The workspace and D may not overlap anything else; calls
  * that may run at the same time (two streams, two graphs) need a workspace each.
@@ -693,8 +698,9 @@ int fg_get_mk_alignment_for_contiguous_layout(void);
 /* Cap on the compute units the GEMM kernels spread their persistent workgroups
  * over (the digest's set_num_sms); 0 (the default) means all of them.  Kernels
  * without persistent workgroups do not follow it: the few-row (decode) kernels,
- * the casts and copies, the router, the 4-bit product and the few-token expert layers, and the gated backward pass's gradient pair (from kept
- * pre-activations or partial sums) and addition of partial sums.
+ * the casts and copies, the router, the 4-bit product and the few-token expert
+ * layers, and the gated backward pass's gradient pair (from kept pre-activations or
+ * partial sums) and addition of partial sums.
  * Results do not depend on the cap (every tile is computed whole by one
  * workgroup), but for the bf16 gated block and its gradients, whose plan,
  * and so the order of their fp32 sums, follows it.  Process-wide, not thread-safe against concurrent launches. */

@@ -72,14 +72,14 @@ inline int wide_parts(Int4Kind kind, int M, int N, int chunks) {
 inline Int4Plan plan_int4(int M, int N, int K, const char* forced) {
   const int chunks = ceil_div(K, 256);
   // The reduction of a 16-column tile over eight waves instead of four where the
-  // tiles are few or the reduction is long (1 x 2112 x 7168: 5.8 for 6.7; 1 x
-  // 7168 x 16384: 13.7 for 15.1; 1 x 24576 x 1536: 10.6 for 8.3).
+  // tiles are few or the reduction is long (1 x 2112 x 7168: eight 5.5, four 6.3; 1 x
+  // 7168 x 16384: 13.0 and 14.2), not elsewhere (1 x 24576 x 1536: 10.0 and 7.7).
   const bool deep = chunks >= 16 && N <= 4096;
   Int4Kind kind;
   if (M <= 2)
     kind = deep || chunks >= 32 ? kSplit2Deep : kSplit2;
   else if (M <= 8)
-    // 4 x 24576 x 1536: 11.4, 8.9 wide; 4 x 16384 x 4096: 12.1, 13.0 wide
+    // 4 x 24576 x 1536: split 10.8, wide 8.2; 4 x 16384 x 4096: 11.3 and 12.1
     kind = ceil_div(N, 16) > 1024 ? kWide16 : deep ? kSplit8Deep : kSplit8;
   else {
     kind = deep && N < 4096 ? kSplit16Deep : kSplit16;

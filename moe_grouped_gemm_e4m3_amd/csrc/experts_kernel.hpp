@@ -5,8 +5,9 @@
 //
 // Every active expert's weights are read once for each 64 tokens
 // (weight_stream.hpp); that read is the time where they are many (one token, 8
-// experts of 2048 x 7168 in e4m3: 352 MB in 68 us, 5.2 TB/s, what a copy reaches;
-// 64 tokens over 16 of them: 706 MB in 154 us, 4.6 TB/s).  `up` has workgroups for
+// experts of 2048 x 7168 in e4m3: 352 MB in 67.7 us, 5.2 TB/s, a little more than a
+// copy's reads and writes together; 64 tokens over 16 of them: 706 MB in 162 us, 4.4
+// TB/s).  `up` has workgroups for
 // each expert and tile of hidden units; an expert's tokens are the rows of the
 // matrix product.  `down` has workgroups for tiles of outputs, which go through
 // all active experts, so that the sum over experts stays inside: sums of its own
@@ -15,13 +16,19 @@
 //   split  a tile is 16 units (or 16 or 32 outputs), and its waves share out the
 //          reduction, each with an LDS ring of its own, and are added in wave
 //          order: many independent small streams, for few tokens, where latency
-//          counts (one token, 6 experts of 704 x 2048 in 4 bits: 14.9 us)
+//          counts (one token, 6 experts of 704 x 2048 in 4 bits: 16.0 us)
 //   wide   a tile is 64 or 128 units (128 outputs), and its waves have rows of
 //          their own and share one copy of the tokens' columns, with a barrier a
 //          chunk: fewer bytes through LDS for a weight.  `down` then splits all
 //          experts' chunks over workgroups, whose sums a third kernel adds in
-//          their order (39 tokens, 64 experts of 2048 x 1024 in 4 bits: 86 us; in
-//          one part 818)
+//          their order (39 tokens, 2 of 64 experts of 2048 x 1024 each in 4 bits: 67
+//          us; in one part 558)
+//
+// A kernel takes so many tokens of an expert at a time: `up` 2, 4 or 16 (split) and
+// 16 or 32 (wide), `down` 1 or 4 and 16, 24 or 32.  For more of them it streams the
+// expert's weights again, one time after the other, from cache where they fit.  The
+// plan goes by the average, so that ids which crowd on one expert cost more (16
+// tokens, one of 16 4-bit experts of 1024 x 2048 each, spread 30 us, all on one 43).
 //
 // No sum depends on the order in which workgroups run, and there are no atomics
 // on results.

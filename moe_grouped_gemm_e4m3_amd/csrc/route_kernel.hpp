@@ -12,10 +12,12 @@
 // A wave takes a token, a lane the experts lane, lane + 64, ...  Scores, what
 // decides between experts, and sums are in 64 bits: the choice is then that of
 // the formula wherever two experts differ by more than 1e-15, and the work is
-// still small (a token's scores are read once).  Bound by latency: two loads, an
-// exponential in 64 bits, the groups and k rounds of finding the largest (8 of 256
-// experts in 8 groups: 5.5 us for one token, of which a launch is about 2; 9.6 for
-// 4096).  Without bias and groups the logits decide, and a sum that the division
+// still small (a token's scores are read once).  A few tokens are bound by latency:
+// two loads, an exponential in 64 bits, the groups and k rounds of finding the
+// largest (8 of 256 experts in 8 groups: 5.6 us for one token, of which a launch is
+// about 2).  Thousands are bound by the vector instructions of a token's wave (the
+// same, 4096 tokens: 9.6 us; 940 of them, 59% of the SIMDs' cycles at four each and
+// more for those on 64 bits).  Without bias and groups the logits decide, and a sum that the division
 // by the chosen scores' sum cancels is not computed (8192 x 128, not normalised,
 // forward and backward: 14 us).
 #pragma once
@@ -288,8 +290,8 @@ __device__ __forceinline__ void store_as(float* p, double v) { *p = (float)v; }
 __device__ __forceinline__ void store_as(uint16_t* p, double v) { *p = bf16_bits((float)v); }
 
 // Every logit's gradient is written once; what the chosen experts get on top is
-// added in the order of their places.  Bound by latency for a few tokens, by
-// exponentials in 64 bits for many.
+// added in the order of their places.  Bound by latency for a few tokens, by vector
+// instructions for many (8192 x 128: 430 a token, 66% of the SIMDs' cycles).
 template <typename L, int SLOTS>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteGradParams p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
