@@ -16,10 +16,12 @@
 // A wave streams chunks of 128 bytes of its weight rows (128 e4m3 or 256 4-bit
 // columns) through an LDS ring that it alone uses, DEPTH - 1 of them in flight,
 // with the same columns of X next to them.  fp32 rows of X are the sums of three
-// bf16, made while the chunk before is multiplied.  Weights loaded into registers in the
-// matrix cores' layout (16 rows by 16 bytes) cost an access of the vector cache
-// for every lane, 64 for 1 KiB, and that rate, about one a clock, bounded the
-// 4-bit layers at 2.3 TB/s; whole rows of 128 bytes cost a quarter of them.
+// bf16, made while the chunk before is multiplied.
+//
+// Weights loaded into registers in the matrix cores' layout (16 rows by 16 bytes)
+// cost an access of the vector cache for every lane, 64 for 1 KiB, and that rate,
+// about one a clock, bounded the 4-bit layers at 2.3 TB/s; whole rows of 128 bytes
+// cost a quarter of them.
 #pragma once
 
 #include "decode_plan.hpp"
